@@ -12,13 +12,14 @@
 #include <stdarg.h>
 #include <stdio.h>
 
-#include "fp8mm.h"
+#include "api_common.hpp"
 #include "launch.hpp"
 #include "quant_launch.hpp"
 
-namespace {
+namespace fp8mm {
+namespace api {
 
-thread_local char g_last_error[512] = "";
+static thread_local char g_last_error[512] = "";
 
 fp8mm_status fail(fp8mm_status st, const char* fmt, ...) {
   va_list ap;
@@ -38,11 +39,21 @@ fp8mm_status from_hip(hipError_t e, const char* what) {
   return fail(FP8MM_ERUNTIME, "%s: HIP error %d (%s)", what, int(e), hipGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+const char* last_error() { return g_last_error; }
+
+}  // namespace api
+}  // namespace fp8mm
+
+namespace {
+
+using fp8mm::api::aligned16;
+using fp8mm::api::fail;
+using fp8mm::api::from_hip;
+using fp8mm::api::kMaxLd;
+using fp8mm::api::ok;
 
 // Offsets are formed in 32-bit buffer descriptors: keep one tile's span of
-// an operand below 2^31 bytes, and a scale array below 2^32 bytes.
-constexpr int64_t kMaxLd = int64_t(1) << 22;
+// an operand below 2^31 bytes (kMaxLd), and a scale array below 2^32 bytes.
 constexpr int64_t kMaxScales = int64_t(1) << 30;   // exclusive: 4 * count must fit in 32 bits
 // Every workgroup of a grouped kernel scans the E offsets to find its expert,
 // and the grouped grids grow with E: cap E so that a call stays a bounded
@@ -78,7 +89,7 @@ bool valid_recipe(int r) { return r >= FP8MM_TENSORWISE && r <= FP8MM_MXFP8; }
 
 extern "C" {
 
-const char* fp8mm_last_error(void) { return g_last_error; }
+const char* fp8mm_last_error(void) { return fp8mm::api::last_error(); }
 
 int fp8mm_recipe_pair_supported(fp8mm_recipe recipe_a, fp8mm_recipe recipe_b, fp8mm_b_layout b_layout) {
   if (b_layout != FP8MM_B_NK && b_layout != FP8MM_B_KN) return 0;
