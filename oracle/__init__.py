@@ -17,10 +17,12 @@ computes, written from the definitions:
   then one matmul" in float64, rounded once to the output dtype; the grouped
   (MoE) variants (forward, input gradient, per-expert weight gradient) and the
   three linear call forms are reductions to it.
+* ``moe``   - the operators around the grouped GEMMs: layer norm, routing,
+  token permutation, gated activation, and their gradients.
 
 It shares no code, tables or constants with the HIP library, and imports
 nothing from it.  Every floating-point step is numpy float32 (where the method
 fixes fp32) or float64.
 """
 
-from . import e4m3, quant, gemm  # noqa: F401
+from . import e4m3, quant, gemm, moe  # noqa: F401
