@@ -1,6 +1,7 @@
 """FP8 scaled matrix multiply for AMD MI355X (gfx950).
 
-Python binding over the C ABI of ``libfp8mm.so`` (include/fp8mm.h).  The
+Python binding over the C ABI of ``libfp8mm.so`` (include/fp8mm.h, and
+include/fp8mm_moe.h in moe.py).  The
 functions carry the C names; they only check and marshal arguments, allocate
 outputs with torch and pass device pointers plus the current HIP stream.
 Every step of the computation runs in the library's HIP kernels.
@@ -453,3 +454,7 @@ def recipe_pair_supported(recipe_a, recipe_b, b_layout="NK"):
 
 from .linear import (FP8BlockwiseLinear, FP8GroupedLinear, fp8_blockwise_linear,  # noqa: E402  (uses the functions above)
                      fp8_grouped_linear)
+from .moe import *  # noqa: E402,F401,F403  (uses the functions above)
+from .moe import __all__ as _moe_all  # noqa: E402
+
+__all__ += _moe_all

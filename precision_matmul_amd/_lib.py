@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/fp8mm.h.
+"""ctypes declarations of the C ABI in include/fp8mm.h and include/fp8mm_moe.h.
 
 Loading fails loudly when ``libfp8mm.so`` has not been built: there is no
 fallback implementation anywhere in this package.
@@ -14,6 +14,8 @@ OK, EINVAL, ENOTIMPL, ERUNTIME = 0, 1, 2, 3
 RECIPES = {"tensorwise": 0, "rowwise": 1, "1x128": 2, "128x128": 3, "128x1": 4, "mxfp8": 5}
 B_LAYOUTS = {"NK": 0, "KN": 1}
 OUT_BF16, OUT_FP32 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
 
 # Every exported entry point: name -> (restype, argtypes).
 _p = ctypes.c_void_p
@@ -39,6 +41,21 @@ SIGNATURES = {
     "fp8_linear_grad_weight": (_i, [_p, _i64, _i64, _p, _p, _i64, _p, _i, _p, _p]),
     "fp8mm_recipe_pair_supported": (_i, [_i, _i, _i]),
     "fp8mm_last_error": (ctypes.c_char_p, []),
+    # include/fp8mm_moe.h
+    "fp8mm_layer_norm": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _i, _f, _p, _i64, _p, _p, _p]),
+    "fp8mm_layer_norm_backward_workspace": (_i64, [_i64, _i64]),
+    "fp8mm_layer_norm_backward": (_i, [_p, _i64, _p, _i64, _i, _i64, _i64, _p, _i, _p, _p, _p, _i64, _p, _p, _p, _i64,
+                                       _p]),
+    "fp8mm_moe_route": (_i, [_p, _i, _i64, _i64, _i64, _p, _i, _i64, _i64, _i64, _i, _i, _f, _p, _p, _p]),
+    "fp8mm_moe_route_backward": (_i, [_p, _p, _i, _i64, _i64, _i64, _p, _i64, _i, _i, _f, _p, _i64, _p]),
+    "fp8mm_moe_plan_workspace": (_i64, [_i64, _i64, _i64]),
+    "fp8mm_moe_plan": (_i, [_p, _i64, _i64, _i64, _p, _p, _p, _i64, _p]),
+    "fp8mm_moe_dispatch": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i64, _p]),
+    "fp8_moe_dispatch": (_i, [_p, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p]),
+    "fp8mm_moe_combine": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _i64, _p, _i64, _p]),
+    "fp8mm_moe_combine_backward": (_i, [_p, _i64, _p, _i64, _i, _i64, _i64, _p, _p, _i64, _p, _i64, _p, _p]),
+    "fp8_swiglu": (_i, [_p, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _p]),
+    "fp8_swiglu_backward": (_i, [_p, _i64, _p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _p]),
 }
 
 _lib = None

@@ -1,0 +1,462 @@
+// Layer norm over the last dimension, forward and backward (gfx950).
+//
+//   mean = sum(x) / C,  var = sum((x - mean)^2) / C,  rstd = 1 / sqrt(var + eps)
+//   y  = (x - mean) rstd w + b
+//   xh = (x - mean) rstd,  a = dy w
+//   dx = rstd (a - sum(a) / C - xh sum(a xh) / C)
+//   dw = sum over rows of dy xh,   db = sum over rows of dy
+//
+// HBM-bound: x (and dy) read once, y (dx) written once.  A row stays in
+// registers, as loaded, between its statistics and its output, so the
+// variance is the sum of centred squares (two passes over registers, not the
+// difference of two large sums).  All sums are float32.
+#include "moe_launch.hpp"
+#include "ops_common.hpp"
+
+namespace fp8mm {
+namespace {
+
+using namespace ops;
+
+// Sum of v over the WPR waves that share a row.  `slot` alternates between
+// calls, so that one barrier a call is enough.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float (&part)[2][WPR], int slot) {
+  v = wave_sum(v);
+  if constexpr (WPR == 1) return v;
+  if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < WPR; ++w) s += part[slot][w];
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// Forward, row in registers: WPR waves a row, NIT chunks a lane.
+// ---------------------------------------------------------------------------
+template <typename T, typename P, int WPR, int NIT>
+__global__ __launch_bounds__(256) void norm_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld_x,
+                                                   const P* __restrict__ weight, const P* __restrict__ bias, float eps,
+                                                   T* __restrict__ y, int64_t ld_y, float* __restrict__ mean_out,
+                                                   float* __restrict__ rstd_out) {
+  constexpr int V = kVec<T>;
+  constexpr int RPB = 4 / WPR;                    // rows of a workgroup
+  __shared__ float part[2][WPR];
+  const int wave = threadIdx.x >> 6;
+  const int64_t c0 = int64_t(WPR == 1 ? threadIdx.x & 63 : threadIdx.x) * V;
+  constexpr int64_t STEP = int64_t(WPR) * 64 * V;
+  // all waves of a row take the same turns
+  for (int64_t row = int64_t(blockIdx.x) * RPB + (WPR == 1 ? wave : 0); row < R; row += int64_t(gridDim.x) * RPB) {
+    Chunk v[NIT];
+    float s = 0.0f;
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) v[it] = load_row(x + row * ld_x, c0 + it * STEP, C);
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      float f[V];
+      unpack<T>(v[it], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += f[i];
+    }
+    const float mean = row_sum<WPR>(s, part, 0) / float(C);
+    float ss = 0.0f;
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      const int64_t c = c0 + it * STEP;
+      float f[V];
+      unpack<T>(v[it], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = f[i] - mean;
+        ss += c + i < C ? d * d : 0.0f;
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<WPR>(ss, part, 1) / float(C) + eps);
+    if ((WPR == 1 ? threadIdx.x & 63 : threadIdx.x) == 0) {
+      if (mean_out) mean_out[row] = mean;
+      if (rstd_out) rstd_out[row] = rstd;
+    }
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      const int64_t c = c0 + it * STEP;
+      float f[V], w[V], b[V];
+      unpack<T>(v[it], f);
+      load_params<P, V>(weight, c, C, 1.0f, w);
+      load_params<P, V>(bias, c, C, 0.0f, b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * w[i] + b[i];
+      store_row(y + row * ld_y, c, C, pack<T>(f));
+    }
+  }
+}
+
+// Forward, rows too long for registers: one workgroup a row, the row read
+// three times (from L2 after the first).
+template <typename T, typename P>
+__global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld_x,
+                                                        const P* __restrict__ weight, const P* __restrict__ bias,
+                                                        float eps, T* __restrict__ y, int64_t ld_y,
+                                                        float* __restrict__ mean_out, float* __restrict__ rstd_out) {
+  constexpr int V = kVec<T>;
+  __shared__ float part[2][4];
+  for (int64_t row = blockIdx.x; row < R; row += gridDim.x) {
+    const T* xr = x + row * ld_x;
+    float s = 0.0f;
+    for (int64_t c = int64_t(threadIdx.x) * V; c < C; c += 256 * V) {
+      float f[V];
+      unpack<T>(load_row(xr, c, C), f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += f[i];
+    }
+    const float mean = row_sum<4>(s, part, 0) / float(C);
+    float ss = 0.0f;
+    for (int64_t c = int64_t(threadIdx.x) * V; c < C; c += 256 * V) {
+      float f[V];
+      unpack<T>(load_row(xr, c, C), f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = f[i] - mean;
+        ss += c + i < C ? d * d : 0.0f;
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<4>(ss, part, 1) / float(C) + eps);
+    if (threadIdx.x == 0) {
+      if (mean_out) mean_out[row] = mean;
+      if (rstd_out) rstd_out[row] = rstd;
+    }
+    for (int64_t c = int64_t(threadIdx.x) * V; c < C; c += 256 * V) {
+      float f[V], w[V], b[V];
+      unpack<T>(load_row(xr, c, C), f);
+      load_params<P, V>(weight, c, C, 1.0f, w);
+      load_params<P, V>(bias, c, C, 0.0f, b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * w[i] + b[i];
+      store_row(y + row * ld_y, c, C, pack<T>(f));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward, row in registers.  A workgroup takes rows blockIdx, blockIdx +
+// gridDim, ... and keeps its share of dw and db in registers over all of them
+// (lane columns are the same for every row); each workgroup then writes one
+// partial row of the workspace, [2][gridDim][C], which column_sum_kernel adds
+// up in workgroup order: no atomics, the same bits every time.
+// ---------------------------------------------------------------------------
+template <typename T, typename P, int WPR, int NIT>
+__global__ __launch_bounds__(256) void norm_backward_kernel(
+    const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ x, int64_t ld_x, int64_t R, int64_t C,
+    const P* __restrict__ weight, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
+    T* __restrict__ dx, int64_t ld_dx, float* __restrict__ partial) {
+  constexpr int V = kVec<T>;
+  constexpr int RPB = 4 / WPR;
+  constexpr int64_t STEP = int64_t(WPR) * 64 * V;
+  __shared__ float part[2][2][4];
+  __shared__ float acc[WPR == 1 ? 2 * NIT * int(STEP) : 1];
+  const int wave = threadIdx.x >> 6;
+  const int64_t c0 = int64_t(WPR == 1 ? threadIdx.x & 63 : threadIdx.x) * V;
+  const float inv_c = 1.0f / float(C);
+  float dw[NIT][V], db[NIT][V];
+#pragma unroll
+  for (int it = 0; it < NIT; ++it)
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[it][i] = db[it][i] = 0.0f;
+  int slot = 0;
+  for (int64_t row = int64_t(blockIdx.x) * RPB + (WPR == 1 ? wave : 0); row < R; row += int64_t(gridDim.x) * RPB) {
+    Chunk vx[NIT], vg[NIT];
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      vx[it] = load_row(x + row * ld_x, c0 + it * STEP, C);
+      vg[it] = load_row(dy + row * ld_dy, c0 + it * STEP, C);
+    }
+    const float mean = mean_in[row], rstd = rstd_in[row];
+    float sa = 0.0f, sax = 0.0f;
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      const int64_t c = c0 + it * STEP;
+      float f[V], g[V], w[V];
+      unpack<T>(vx[it], f);
+      unpack<T>(vg[it], g);
+      load_params<P, V>(weight, c, C, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float xh = (f[i] - mean) * rstd;    // dy is 0 past the row's end
+        const float a = g[i] * w[i];
+        sa += a;
+        sax += a * xh;
+        dw[it][i] += g[i] * xh;
+        db[it][i] += g[i];
+      }
+    }
+    if constexpr (WPR == 1) {
+      sa = wave_sum(sa);
+      sax = wave_sum(sax);
+    } else {
+      sa = wave_sum(sa);
+      sax = wave_sum(sax);
+      if ((threadIdx.x & 63) == 0) {
+        part[slot][0][wave] = sa;
+        part[slot][1][wave] = sax;
+      }
+      __syncthreads();
+      sa = part[slot][0][0] + part[slot][0][1] + part[slot][0][2] + part[slot][0][3];
+      sax = part[slot][1][0] + part[slot][1][1] + part[slot][1][2] + part[slot][1][3];
+      slot ^= 1;
+    }
+    sa *= inv_c;
+    sax *= inv_c;
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      const int64_t c = c0 + it * STEP;
+      float f[V], g[V], w[V];
+      unpack<T>(vx[it], f);
+      unpack<T>(vg[it], g);
+      load_params<P, V>(weight, c, C, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float xh = (f[i] - mean) * rstd;
+        f[i] = rstd * (g[i] * w[i] - sa - xh * sax);
+      }
+      if (dx) store_row(dx + row * ld_dx, c, C, pack<T>(f));
+    }
+  }
+  if (!partial) return;
+  float* pw = partial + int64_t(blockIdx.x) * C;
+  float* pb = pw + int64_t(gridDim.x) * C;
+  if constexpr (WPR == 1) {
+    // the four waves' shares, added in wave order
+    for (int w = 0; w < 4; ++w) {
+      if (wave == w) {
+#pragma unroll
+        for (int it = 0; it < NIT; ++it)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int at = int(c0 + it * STEP) + i;
+            acc[at] = (w ? acc[at] : 0.0f) + dw[it][i];
+            acc[NIT * STEP + at] = (w ? acc[NIT * STEP + at] : 0.0f) + db[it][i];
+          }
+      }
+      __syncthreads();
+    }
+    for (int64_t c = threadIdx.x; c < C; c += 256) {
+      pw[c] = acc[c];
+      pb[c] = acc[NIT * STEP + c];
+    }
+  } else {
+#pragma unroll
+    for (int it = 0; it < NIT; ++it)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int64_t c = c0 + it * STEP + i;
+        if (c < C) {
+          pw[c] = dw[it][i];
+          pb[c] = db[it][i];
+        }
+      }
+  }
+}
+
+// Backward of rows too long for registers: dx by one workgroup a row ...
+template <typename T, typename P>
+__global__ __launch_bounds__(256) void norm_backward_long_kernel(
+    const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ x, int64_t ld_x, int64_t R, int64_t C,
+    const P* __restrict__ weight, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
+    T* __restrict__ dx, int64_t ld_dx) {
+  constexpr int V = kVec<T>;
+  __shared__ float part[2][4];
+  for (int64_t row = blockIdx.x; row < R; row += gridDim.x) {
+    const float mean = mean_in[row], rstd = rstd_in[row];
+    float sa = 0.0f, sax = 0.0f;
+    for (int64_t c = int64_t(threadIdx.x) * V; c < C; c += 256 * V) {
+      float f[V], g[V], w[V];
+      unpack<T>(load_row(x + row * ld_x, c, C), f);
+      unpack<T>(load_row(dy + row * ld_dy, c, C), g);
+      load_params<P, V>(weight, c, C, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        sa += g[i] * w[i];
+        sax += g[i] * w[i] * ((f[i] - mean) * rstd);
+      }
+    }
+    sa = row_sum<4>(sa, part, 0) / float(C);
+    sax = row_sum<4>(sax, part, 1) / float(C);
+    for (int64_t c = int64_t(threadIdx.x) * V; c < C; c += 256 * V) {
+      float f[V], g[V], w[V];
+      unpack<T>(load_row(x + row * ld_x, c, C), f);
+      unpack<T>(load_row(dy + row * ld_dy, c, C), g);
+      load_params<P, V>(weight, c, C, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = rstd * (g[i] * w[i] - sa - (f[i] - mean) * rstd * sax);
+      store_row(dx + row * ld_dx, c, C, pack<T>(f));
+    }
+  }
+}
+
+// ... and the columns' partial sums over rows blockIdx.y, blockIdx.y +
+// gridDim.y, ... by one thread a column.
+template <typename T>
+__global__ __launch_bounds__(256) void norm_columns_kernel(const T* __restrict__ dy, int64_t ld_dy,
+                                                           const T* __restrict__ x, int64_t ld_x, int64_t R, int64_t C,
+                                                           const float* __restrict__ mean_in,
+                                                           const float* __restrict__ rstd_in,
+                                                           float* __restrict__ partial) {
+  const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= C) return;
+  float dw = 0.0f, db = 0.0f;
+  for (int64_t row = blockIdx.y; row < R; row += gridDim.y) {
+    const float g = to_float(dy[row * ld_dy + c]);
+    dw += g * ((to_float(x[row * ld_x + c]) - mean_in[row]) * rstd_in[row]);
+    db += g;
+  }
+  partial[int64_t(blockIdx.y) * C + c] = dw;
+  partial[(int64_t(gridDim.y) + blockIdx.y) * C + c] = db;
+}
+
+// Sums the n partial rows of dw (blockIdx.y 0) or db (1): 64 columns and 16
+// row slices a workgroup, the slices added in order.
+template <typename P>
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ partial, int n, int64_t C,
+                                                          P* __restrict__ dweight, P* __restrict__ dbias) {
+  __shared__ float part[16][64];
+  P* out = blockIdx.y ? dbias : dweight;
+  if (!out) return;
+  const float* p = partial + int64_t(blockIdx.y) * n * C;
+  const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  const int64_t c = int64_t(blockIdx.x) * 64 + lane;
+  float s = 0.0f;
+  if (c < C) {
+#pragma unroll 8
+    for (int r = slice; r < n; r += 16) s += p[int64_t(r) * C + c];
+  }
+  part[slice][lane] = s;
+  __syncthreads();
+  if (slice == 0 && c < C) {
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += part[i][lane];
+    out[c] = from_float<P>(s);
+  }
+}
+
+constexpr int kBackwardGrid = 512;      // partial rows at most
+constexpr int64_t kRegisterCols = 8192; // longest row kept in registers
+
+// Workgroups of the row kernels, which take further rows in turns past this.
+dim3 row_grid(int64_t blocks) { return dim3(unsigned(blocks < (1 << 20) ? blocks : (1 << 20))); }
+
+int backward_grid(int64_t R, int64_t C, int vec) {
+  const int64_t rows_a_block = C <= 256 * vec ? 4 : 1;
+  const int64_t blocks = (R + rows_a_block - 1) / rows_a_block;
+  return int(blocks < kBackwardGrid ? blocks : kBackwardGrid);
+}
+
+template <typename T, typename P, int WPR, int NIT>
+hipError_t run_norm(const NormProblem& p, hipStream_t st) {
+  constexpr int RPB = 4 / WPR;
+  hipLaunchKernelGGL((norm_kernel<T, P, WPR, NIT>), row_grid((p.R + RPB - 1) / RPB), dim3(256), 0, st,
+                     static_cast<const T*>(p.x), p.R, p.C, p.ld_x, static_cast<const P*>(p.weight),
+                     static_cast<const P*>(p.bias), p.eps, static_cast<T*>(p.out), p.ld_out, p.mean, p.rstd);
+  return hipGetLastError();
+}
+
+template <typename T, typename P>
+hipError_t norm_typed(const NormProblem& p, hipStream_t st) {
+  constexpr int64_t S = 64 * kVec<T>;   // columns of one wave chunk
+  if (p.C <= S) return run_norm<T, P, 1, 1>(p, st);
+  if (p.C <= 2 * S) return run_norm<T, P, 1, 2>(p, st);
+  if (p.C <= 4 * S) return run_norm<T, P, 1, 4>(p, st);
+  if (p.C <= 8 * S) return run_norm<T, P, 4, 2>(p, st);
+  if (p.C <= 12 * S) return run_norm<T, P, 4, 3>(p, st);
+  if (p.C <= 16 * S) return run_norm<T, P, 4, 4>(p, st);
+  if constexpr (sizeof(T) == 4) {   // 16 S is 8192 columns of bf16, 4096 of fp32
+    if (p.C <= kRegisterCols) return run_norm<T, P, 4, 8>(p, st);
+  }
+  hipLaunchKernelGGL((norm_long_kernel<T, P>), row_grid(p.R), dim3(256), 0, st, static_cast<const T*>(p.x), p.R,
+                     p.C, p.ld_x, static_cast<const P*>(p.weight), static_cast<const P*>(p.bias), p.eps,
+                     static_cast<T*>(p.out), p.ld_out, p.mean, p.rstd);
+  return hipGetLastError();
+}
+
+template <typename T, typename P, int WPR, int NIT>
+hipError_t run_backward(const NormProblem& p, int grid, float* partial, hipStream_t st) {
+  hipLaunchKernelGGL((norm_backward_kernel<T, P, WPR, NIT>), dim3(grid), dim3(256), 0, st,
+                     static_cast<const T*>(p.dy), p.ld_dy, static_cast<const T*>(p.x), p.ld_x, p.R, p.C,
+                     static_cast<const P*>(p.weight), p.mean, p.rstd, static_cast<T*>(p.out), p.ld_out, partial);
+  return hipGetLastError();
+}
+
+template <typename T, typename P>
+hipError_t backward_typed(const NormProblem& p, hipStream_t st) {
+  constexpr int64_t S = 64 * kVec<T>;
+  const int grid = backward_grid(p.R, p.C, kVec<T>);
+  float* partial = p.dweight || p.dbias ? p.workspace : nullptr;
+  hipError_t e = hipSuccess;
+  if (p.C <= S) {
+    e = run_backward<T, P, 1, 1>(p, grid, partial, st);
+  } else if (p.C <= 2 * S) {
+    e = run_backward<T, P, 1, 2>(p, grid, partial, st);
+  } else if (p.C <= 4 * S) {
+    e = run_backward<T, P, 1, 4>(p, grid, partial, st);
+  } else if (p.C <= 8 * S) {
+    e = run_backward<T, P, 4, 2>(p, grid, partial, st);
+  } else if (p.C <= 12 * S) {
+    e = run_backward<T, P, 4, 3>(p, grid, partial, st);
+  } else if (p.C <= 16 * S) {
+    e = run_backward<T, P, 4, 4>(p, grid, partial, st);
+  } else if (sizeof(T) == 4 && p.C <= kRegisterCols) {
+    if constexpr (sizeof(T) == 4) e = run_backward<T, P, 4, 8>(p, grid, partial, st);
+  } else {
+    if (p.out) {
+      hipLaunchKernelGGL((norm_backward_long_kernel<T, P>), row_grid(p.R), dim3(256), 0, st,
+                         static_cast<const T*>(p.dy), p.ld_dy, static_cast<const T*>(p.x), p.ld_x, p.R, p.C,
+                         static_cast<const P*>(p.weight), p.mean, p.rstd, static_cast<T*>(p.out), p.ld_out);
+      e = hipGetLastError();
+    }
+    if (e == hipSuccess && partial) {
+      hipLaunchKernelGGL((norm_columns_kernel<T>), dim3(unsigned((p.C + 255) / 256), grid), dim3(256), 0, st,
+                         static_cast<const T*>(p.dy), p.ld_dy, static_cast<const T*>(p.x), p.ld_x, p.R, p.C, p.mean,
+                         p.rstd, partial);
+      e = hipGetLastError();
+    }
+  }
+  if (e != hipSuccess || !partial) return e;
+  hipLaunchKernelGGL((column_sum_kernel<P>), dim3(unsigned((p.C + 63) / 64), 2), dim3(1024), 0, st, partial, grid, p.C,
+                     static_cast<P*>(p.dweight), static_cast<P*>(p.dbias));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t norm_backward_workspace(int64_t R, int64_t C) {
+  // the partial rows of the type with the smaller chunks need no more
+  const int64_t n = R < kBackwardGrid ? R : kBackwardGrid;
+  return 2 * n * C * int64_t(sizeof(float));
+}
+
+hipError_t launch_norm(const NormProblem& p, hipStream_t st) {
+  if (p.R == 0) return hipSuccess;
+  if (p.fp32)
+    return p.param_fp32 ? norm_typed<float, float>(p, st) : norm_typed<float, uint16_t>(p, st);
+  return p.param_fp32 ? norm_typed<uint16_t, float>(p, st) : norm_typed<uint16_t, uint16_t>(p, st);
+}
+
+hipError_t launch_norm_backward(const NormProblem& p, hipStream_t st) {
+  // no rows: column_sum_kernel over no partial rows writes the zero gradients
+  if (p.R == 0) {
+    if (!p.dweight && !p.dbias) return hipSuccess;
+    const dim3 grid(unsigned((p.C + 63) / 64), 2);
+    if (p.param_fp32)
+      hipLaunchKernelGGL((column_sum_kernel<float>), grid, dim3(1024), 0, st, nullptr, 0, p.C,
+                         static_cast<float*>(p.dweight), static_cast<float*>(p.dbias));
+    else
+      hipLaunchKernelGGL((column_sum_kernel<uint16_t>), grid, dim3(1024), 0, st, nullptr, 0, p.C,
+                         static_cast<uint16_t*>(p.dweight), static_cast<uint16_t*>(p.dbias));
+    return hipGetLastError();
+  }
+  if (p.fp32)
+    return p.param_fp32 ? backward_typed<float, float>(p, st) : backward_typed<float, uint16_t>(p, st);
+  return p.param_fp32 ? backward_typed<uint16_t, float>(p, st) : backward_typed<uint16_t, uint16_t>(p, st);
+}
+
+}  // namespace fp8mm

@@ -1,0 +1,216 @@
+// Device pieces of the operators around the grouped GEMMs: 16-byte chunks of
+// bf16 or fp32 rows, reductions of a wave in the data-parallel primitives
+// (no LDS traffic), workgroup order.
+//
+// bf16 values are uint16_t in memory and float in registers; results go back
+// through one round-to-nearest-even conversion.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp8mm {
+namespace ops {
+
+template <typename T>
+constexpr int kVec = 16 / int(sizeof(T));   // elements of a 16-byte chunk
+
+// A chunk in registers.  Memory accesses assume the alignment of one element
+// only (rows of odd length start anywhere); the hardware takes the full-width
+// access at any address, and an aligned one costs nothing extra.
+struct Chunk {
+  uint32_t w[4];
+};
+
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) ChunkAt {
+  uint32_t w[4];
+};
+
+template <typename T>
+__device__ __forceinline__ Chunk load_chunk(const T* p) {
+  const ChunkAt<T> c = *reinterpret_cast<const ChunkAt<T>*>(p);
+  return Chunk{{c.w[0], c.w[1], c.w[2], c.w[3]}};
+}
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* p, const Chunk& v) {
+  *reinterpret_cast<ChunkAt<T>*>(p) = ChunkAt<T>{{v.w[0], v.w[1], v.w[2], v.w[3]}};
+}
+
+// The first n < kVec<T> elements of a row's last chunk, zeros after them.
+template <typename T>
+__device__ __forceinline__ Chunk load_part(const T* p, int n) {
+  Chunk c{{0u, 0u, 0u, 0u}};
+  constexpr int per = int(4 / sizeof(T));
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) {
+    if (i < n) {
+      uint32_t v;
+      if constexpr (sizeof(T) == 2)
+        v = p[i];
+      else
+        v = __float_as_uint(p[i]);
+      c.w[i / per] |= v << ((i % per) * 16);
+    }
+  }
+  return c;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_part(T* p, const Chunk& v, int n) {
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) {
+    if (i < n) {
+      if constexpr (sizeof(T) == 2)
+        p[i] = uint16_t(v.w[i / 2] >> ((i % 2) * 16));
+      else
+        p[i] = __uint_as_float(v.w[i]);
+    }
+  }
+}
+
+// Chunk at column c of a row of C elements; zeros past the row.
+template <typename T>
+__device__ __forceinline__ Chunk load_row(const T* row, int64_t c, int64_t C) {
+  if (c + kVec<T> <= C) return load_chunk(row + c);
+  if (c < C) return load_part(row + c, int(C - c));
+  return Chunk{{0u, 0u, 0u, 0u}};
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row(T* row, int64_t c, int64_t C, const Chunk& v) {
+  if (c + kVec<T> <= C)
+    store_chunk(row + c, v);
+  else if (c < C)
+    store_part(row + c, v, int(C - c));
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Chunk& c, float (&f)[kVec<T>]) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(c.w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(c.w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(c.w[i]);
+  }
+}
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two floats to packed bf16, nearest even (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+__device__ __forceinline__ uint16_t to_bf16(float v) { return uint16_t(pack_bf16(v, v)); }
+
+template <typename T>
+__device__ __forceinline__ Chunk pack(const float (&f)[kVec<T>]) {
+  Chunk c;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.w[i] = __float_as_uint(f[i]);
+  }
+  return c;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_float(T v) {
+  if constexpr (sizeof(T) == 2)
+    return __uint_as_float(uint32_t(v) << 16);
+  else
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ T from_float(float v) {
+  if constexpr (sizeof(T) == 2)
+    return to_bf16(v);
+  else
+    return v;
+}
+
+// N consecutive parameters of type P at column c of C, as floats; `none`
+// where there is no parameter vector or the column is past its end.
+template <typename P, int N>
+__device__ __forceinline__ void load_params(const P* p, int64_t c, int64_t C, float none, float (&f)[N]) {
+  struct __attribute__((packed, aligned(sizeof(P)))) At {
+    P v[N];
+  };
+  if (p && c + N <= C) {
+    const At a = *reinterpret_cast<const At*>(p + c);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = to_float(a.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = p && c + i < C ? to_float(p[c + i]) : none;
+  }
+}
+
+// ---------------------------------------------------------------- reductions
+
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __uint_as_float(uint32_t(
+      __builtin_amdgcn_update_dpp(int(__float_as_uint(old)), int(__float_as_uint(v)), CTRL, ROWS, 0xF, false)));
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(v)), lane)));
+}
+
+// Sum over the 64 lanes, in every lane (a scalar).  Row shifts by 1, 2, 4 and
+// 8 sum each row of 16 into its last lane, the two row broadcasts carry the
+// row sums on to lane 63: a fixed order, so results repeat bit for bit.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0x111>(0.0f, v);
+  v += dpp<0x112>(0.0f, v);
+  v += dpp<0x114>(0.0f, v);
+  v += dpp<0x118>(0.0f, v);
+  v += dpp<0x142, 0xA>(0.0f, v);
+  v += dpp<0x143, 0xC>(0.0f, v);
+  return lane_value(v, 63);
+}
+
+// Maximum over the 64 lanes; NaN lanes do not count.
+__device__ __forceinline__ float wave_max_f(float v) {
+  const float lo = -__builtin_inff();
+  v = fmaxf(v, dpp<0x111>(lo, v));
+  v = fmaxf(v, dpp<0x112>(lo, v));
+  v = fmaxf(v, dpp<0x114>(lo, v));
+  v = fmaxf(v, dpp<0x118>(lo, v));
+  v = fmaxf(v, dpp<0x142, 0xA>(lo, v));
+  v = fmaxf(v, dpp<0x143, 0xC>(lo, v));
+  return lane_value(v, 63);
+}
+
+// Maximum of unsigned integers over aligned groups of 8 lanes, in all 8.
+__device__ __forceinline__ uint32_t group8_max(uint32_t v) {
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, false)));   // lane i with 7 - i
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, false)));    // xor 2
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, false)));    // xor 1
+  return v;
+}
+
+// ------------------------------------------------------------ workgroup order
+
+// Position of this workgroup when each of the 8 XCDs takes one contiguous
+// range of them (workgroup ids go round the XCDs in turn, and each XCD has
+// its own L2): neighbouring rows are then written through one L2.  The grid
+// is a multiple of 8; positions at or past the work's end do nothing.
+__device__ __forceinline__ uint32_t xcd_position() { return blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8; }
+
+inline unsigned xcd_grid(int64_t blocks) { return unsigned((blocks + 7) / 8 * 8); }
+
+}  // namespace ops
+}  // namespace fp8mm

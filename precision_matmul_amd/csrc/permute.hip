@@ -1,0 +1,343 @@
+// Token permutation of an expert layer (gfx950): the plan that puts every
+// (token, slot) into expert order, the move of token rows there (dispatch, as
+// rows or as 1x128 FP8 codes) and the weighted sum back (combine), with its
+// backward pass.
+//
+// Slot n = t k + j of token t goes to the row that a stable sort of the slots
+// by expert gives it; slots without an expert (id outside [0, E)) take the
+// rows after the last expert's.  row_of_slot holds the row, or ~row for a slot
+// without an expert, so that its values are all different rows and the
+// dispatch writes every row: zeros (code 0, scale 1) where there is no expert.
+#include "moe_launch.hpp"
+#include "ops_common.hpp"
+#include "quant_cast.hpp"
+
+namespace fp8mm {
+namespace {
+
+using namespace ops;
+
+// ---------------------------------------------------------------------------
+// Plan: a counting sort.  The slots are cut into chunks; a first launch counts
+// each chunk's slots per expert, a second one adds up the counts before each
+// chunk and places its slots, 64 at a time in order (a lane's rank among the
+// lanes of its wave with the same expert by ballots over the expert's bits).
+// Counts are integers and every slot's row is its rank, so the result does not
+// depend on the order of the LDS atomics.  One chunk alone needs no first
+// launch.  Latency-bound: 8 bytes a slot.
+// ---------------------------------------------------------------------------
+constexpr int kPlanSingle = 4096;    // slots that one workgroup places alone
+constexpr int kPlanChunks = 128;     // chunks at most: the second launch reads all their counts
+
+__device__ __forceinline__ int plan_key(int32_t id, int E) { return id >= 0 && id < E ? id : E; }
+
+// Counts of the wave's slots [a, b) into cnt (LDS, this wave's own).
+__device__ __forceinline__ void count_slots(const int32_t* ids, int64_t a, int64_t b, int E, int* cnt) {
+  for (int64_t n = a + (threadIdx.x & 63); n < b; n += 64) atomicAdd(&cnt[plan_key(ids[n], E)], 1);
+}
+
+__global__ __launch_bounds__(256) void plan_count_kernel(const int32_t* __restrict__ ids, int64_t n, int chunk, int E,
+                                                         int* __restrict__ hist) {
+  extern __shared__ int cnt[];         // [E + 1]
+  for (int e = threadIdx.x; e <= E; e += 256) cnt[e] = 0;
+  __syncthreads();
+  const int64_t c0 = int64_t(blockIdx.x) * chunk;
+  const int64_t end = min(n, c0 + chunk);
+  for (int64_t i = c0 + threadIdx.x; i < end; i += 256) atomicAdd(&cnt[plan_key(ids[i], E)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += 256) hist[int64_t(blockIdx.x) * (E + 1) + e] = cnt[e];
+}
+
+// LDS: cnt [4][E + 1] counts, then places, of the four waves; total [E + 1].
+__global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restrict__ ids, int64_t n, int chunk, int E,
+                                                         int bits, const int* __restrict__ hist,
+                                                         int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {
+  extern __shared__ int lds[];
+  __shared__ int wave_total[4];
+  const int E1 = E + 1;
+  int* total = lds + 4 * E1;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int* cnt = lds + wave * E1;
+  for (int i = t; i < 4 * E1; i += 256) lds[i] = 0;
+  __syncthreads();
+  const int64_t c0 = int64_t(blockIdx.x) * chunk;
+  const int quarter = chunk / 4;
+  const int64_t a = min(n, c0 + int64_t(wave) * quarter);
+  const int64_t b = min(n, a + quarter);
+  count_slots(ids, a, b, E, cnt);
+  __syncthreads();
+  // before: slots of expert e in earlier chunks; total: in all chunks
+  for (int e = t; e < E1; e += 256) {
+    int before = 0, all = 0;
+    if (hist) {
+#pragma unroll 8
+      for (int c = 0; c < int(gridDim.x); ++c) {
+        const int h = hist[int64_t(c) * E1 + e];
+        all += h;
+        before += c < int(blockIdx.x) ? h : 0;
+      }
+    } else {
+      all = lds[e] + lds[E1 + e] + lds[2 * E1 + e] + lds[3 * E1 + e];
+    }
+    total[e] = all;
+    // the waves' first places relative to the expert's first row
+    int at = before;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int h = lds[w * E1 + e];
+      lds[w * E1 + e] = at;
+      at += h;
+    }
+  }
+  __syncthreads();
+  // exclusive scan of total: thread t owns `per` consecutive experts
+  const int per = (E1 + 255) / 256;
+  const int s0 = min(E1, t * per), s1 = min(E1, s0 + per);
+  int sum = 0;
+  for (int e = s0; e < s1; ++e) sum += total[e];
+  int incl = sum;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int v = __shfl_up(incl, off, 64);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 63) wave_total[wave] = incl;
+  __syncthreads();
+  int start = incl - sum;
+  for (int w = 0; w < wave; ++w) start += wave_total[w];
+  for (int e = s0; e < s1; ++e) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) lds[w * E1 + e] += start;
+    start += total[e];
+    if (blockIdx.x == 0 && e < E) offsets[e] = start;
+  }
+  __syncthreads();
+  for (int64_t i0 = a; i0 < b; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const bool here = i < b;
+    const int key = here ? plan_key(ids[i], E) : 0;
+    uint64_t peers = __ballot(here);
+    for (int bit = 0; bit < bits; ++bit) {
+      const bool set = (key >> bit) & 1;
+      const uint64_t with = __ballot(set);
+      peers &= set ? with : ~with;
+    }
+    const uint64_t lower = peers & ((1ull << lane) - 1);
+    if (here) {
+      const int row = cnt[key] + __popcll(lower);
+      rows[i] = key == E ? ~row : row;
+    }
+    // every lane has read its expert's place before its last peer moves it on
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (here && (peers >> lane) == 1) cnt[key] += __popcll(peers);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+// This wave's item: the host keeps items below 2^26 (a launch's threads below
+// 2^32), and one item is a wave's, so its arithmetic is scalar and 32-bit.
+__device__ __forceinline__ uint32_t wave_item() {
+  return uint32_t(__builtin_amdgcn_readfirstlane(int(xcd_position() * 4 + (threadIdx.x >> 6))));
+}
+
+struct Slot {
+  int64_t row;
+  bool used;
+};
+
+__device__ __forceinline__ Slot slot_row(int32_t v) { return Slot{int64_t(v < 0 ? ~v : v), v >= 0}; }
+
+// ---------------------------------------------------------------------------
+// Dispatch: one wave an item of 64 chunks of one token, read once and written
+// to the token's k rows.  HBM-bound: (1 + k) rows a token.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(256) void dispatch_kernel(const PermuteProblem p, int strips) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t item = wave_item();
+  const uint32_t token = item / uint32_t(strips);
+  if (token >= p.T) return;
+  const int64_t c = (int64_t(item - token * uint32_t(strips)) * 64 + lane) * kVec<T>;
+  const int64_t M = p.T * p.k;
+  const Chunk v = load_row(static_cast<const T*>(p.x) + int64_t(token) * p.ld_x, c, p.C);
+  for (int j = 0; j < p.k; ++j) {
+    const Slot s = slot_row(p.row_of_slot[int64_t(token) * p.k + j]);
+    if (s.row >= M) continue;
+    store_row(static_cast<T*>(p.out) + s.row * p.ld_out, c, p.C, s.used ? v : Chunk{{0u, 0u, 0u, 0u}});
+  }
+}
+
+// FP8: a wave covers 1024 columns of one token, 16 consecutive ones a lane, 8
+// lanes a group of 128; codes and scales as the 1x128 quantizer makes them.
+__global__ __launch_bounds__(256) void dispatch_fp8_kernel(const PermuteProblem p, int strips) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t item = wave_item();
+  const uint32_t token = item / uint32_t(strips);
+  if (token >= p.T) return;
+  const int64_t c = (int64_t(item - token * uint32_t(strips)) * 64 + lane) * 16;
+  if (c >= p.C) return;                  // C % 128 == 0: whole groups of 8 lanes leave
+  const int64_t M = p.T * p.k;
+  const uint16_t* x = static_cast<const uint16_t*>(p.x) + int64_t(token) * p.ld_x + c;
+  const U16x8 v0 = load16(x), v1 = load16(x + 8);
+  const uint32_t m = group8_max(max(absmax8(v0), absmax8(v1)));
+  const float s = scale_from_amax(bf16_to_f32(uint16_t(m)), 0.0f, false);
+  const CastScale cs = make_cast_scale(s);
+  const uint2 q0 = cast8(v0, cs), q1 = cast8(v1, cs);
+  const uint4 q = make_uint4(q0.x, q0.y, q1.x, q1.y);
+  for (int j = 0; j < p.k; ++j) {
+    const Slot slot = slot_row(p.row_of_slot[int64_t(token) * p.k + j]);
+    if (slot.row >= M) continue;
+    *reinterpret_cast<uint4*>(p.q + slot.row * p.ld_q + c) = slot.used ? q : make_uint4(0u, 0u, 0u, 0u);
+    if ((lane & 7) == 0) p.scale[(c / 128) * M + slot.row] = slot.used ? s : 1.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combine: one wave an item of 64 chunks of one token; its k rows are added in
+// slot order in float32.  HBM-bound: (k + 1) rows a token.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, int strips) {
+  constexpr int V = kVec<T>;
+  const int lane = threadIdx.x & 63;
+  const uint32_t item = wave_item();
+  const uint32_t token = item / uint32_t(strips);
+  if (token >= p.T) return;
+  const int64_t c = (int64_t(item - token * uint32_t(strips)) * 64 + lane) * V;
+  const int64_t M = p.T * p.k;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+  for (int j = 0; j < p.k; ++j) {
+    const Slot s = slot_row(p.row_of_slot[int64_t(token) * p.k + j]);
+    if (!s.used || s.row >= M) continue;
+    const float w = p.weights ? p.weights[int64_t(token) * p.k + j] : 1.0f;
+    float f[V];
+    unpack<T>(load_row(static_cast<const T*>(p.rows) + s.row * p.ld_rows, c, p.C), f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += w * f[i];
+  }
+  store_row(static_cast<T*>(p.out) + int64_t(token) * p.ld_out, c, p.C, pack<T>(acc));
+}
+
+// Combine's backward: grad_rows[row] = w g, grad_weights[t, j] = <g, rows[row]>.
+// One wave a token; slot j's dot product is kept by lane j.
+template <typename T>
+__global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProblem p) {
+  constexpr int V = kVec<T>;
+  constexpr int U = 4;                   // chunks a lane holds of the gradient
+  const int lane = threadIdx.x & 63;
+  const uint32_t token = wave_item();
+  if (token >= p.T) return;
+  const int64_t M = p.T * p.k;
+  const T* g_row = static_cast<const T*>(p.x) + int64_t(token) * p.ld_x;
+  float dots = 0.0f;
+  for (int64_t c0 = int64_t(lane) * V; c0 < (p.C + 64 * V - 1) / (64 * V) * (64 * V); c0 += 64 * V * U) {
+    float g[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) unpack<T>(load_row(g_row, c0 + u * 64 * V, p.C), g[u]);
+    for (int j = 0; j < p.k; ++j) {
+      const Slot s = slot_row(p.row_of_slot[int64_t(token) * p.k + j]);
+      if (s.row >= M) continue;
+      const float w = p.weights ? p.weights[int64_t(token) * p.k + j] : 1.0f;
+      float dot = 0.0f;
+      if (s.used && p.grad_weights) {
+        const T* r = static_cast<const T*>(p.rows) + s.row * p.ld_rows;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[V];
+          unpack<T>(load_row(r, c0 + u * 64 * V, p.C), f);
+#pragma unroll
+          for (int i = 0; i < V; ++i) dot += g[u][i] * f[i];
+        }
+        dot = wave_sum(dot);
+      }
+      dots += lane == j ? dot : 0.0f;
+      if (p.out) {
+        T* o = static_cast<T*>(p.out) + s.row * p.ld_out;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) f[i] = s.used ? w * g[u][i] : 0.0f;
+          store_row(o, c0 + u * 64 * V, p.C, pack<T>(f));
+        }
+      }
+    }
+  }
+  if (p.grad_weights && lane < p.k) p.grad_weights[int64_t(token) * p.k + lane] = dots;
+}
+
+int plan_chunk(int64_t n) {
+  if (n <= kPlanSingle) return int((n + 255) / 256 * 256);
+  const int64_t c = (n + kPlanChunks - 1) / kPlanChunks;
+  return int((c + 1023) / 1024 * 1024);
+}
+
+}  // namespace
+
+int64_t plan_workspace(int64_t n, int64_t E) {
+  if (n <= kPlanSingle) return 0;
+  const int64_t chunk = plan_chunk(n);
+  return (n + chunk - 1) / chunk * (E + 1) * int64_t(sizeof(int32_t));
+}
+
+hipError_t launch_plan(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* row_of_slot,
+                       int32_t* workspace, hipStream_t st) {
+  const int chunk = n ? plan_chunk(n) : 256;
+  const unsigned chunks = unsigned(n ? (n + chunk - 1) / chunk : 1);
+  const bool single = n <= kPlanSingle;
+  if (!single) {
+    hipLaunchKernelGGL(plan_count_kernel, dim3(chunks), dim3(256), size_t(E + 1) * 4, st, ids, n, chunk, E, workspace);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int bits = 32 - __builtin_clz(unsigned(E));    // of keys 0 .. E
+  hipLaunchKernelGGL(plan_place_kernel, dim3(chunks), dim3(256), size_t(5) * (E + 1) * 4, st, ids, n, chunk, E, bits,
+                     single ? nullptr : workspace, offsets, row_of_slot);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch(const PermuteProblem& p, hipStream_t st) {
+  if (p.T == 0 || p.C == 0) return hipSuccess;
+  const int vec = p.fp32 ? 4 : 8;
+  const int strips = int((p.C + 64 * vec - 1) / (64 * vec));
+  const dim3 grid(xcd_grid((p.T * strips + 3) / 4));
+  if (p.fp32)
+    hipLaunchKernelGGL((dispatch_kernel<float>), grid, dim3(256), 0, st, p, strips);
+  else
+    hipLaunchKernelGGL((dispatch_kernel<uint16_t>), grid, dim3(256), 0, st, p, strips);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch_fp8(const PermuteProblem& p, hipStream_t st) {
+  if (p.T == 0 || p.C == 0) return hipSuccess;
+  const int strips = int((p.C + 1023) / 1024);
+  hipLaunchKernelGGL(dispatch_fp8_kernel, dim3(xcd_grid((p.T * strips + 3) / 4)), dim3(256), 0, st, p, strips);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const PermuteProblem& p, hipStream_t st) {
+  if (p.T == 0 || p.C == 0) return hipSuccess;
+  const int vec = p.fp32 ? 4 : 8;
+  const int strips = int((p.C + 64 * vec - 1) / (64 * vec));
+  const dim3 grid(xcd_grid((p.T * strips + 3) / 4));
+  if (p.fp32)
+    hipLaunchKernelGGL((combine_kernel<float>), grid, dim3(256), 0, st, p, strips);
+  else
+    hipLaunchKernelGGL((combine_kernel<uint16_t>), grid, dim3(256), 0, st, p, strips);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_backward(const PermuteProblem& p, hipStream_t st) {
+  if (p.T == 0) return hipSuccess;
+  const dim3 grid(xcd_grid((p.T + 3) / 4));
+  if (p.fp32)
+    hipLaunchKernelGGL((combine_backward_kernel<float>), grid, dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((combine_backward_kernel<uint16_t>), grid, dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace fp8mm

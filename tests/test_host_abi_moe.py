@@ -1,0 +1,201 @@
+"""Host-side checks of the C ABI in include/fp8mm_moe.h (no GPU): every symbol
+is exported and bound, queries answer, and bad arguments are refused before any
+launch.  Every call below fails a check or has nothing to do, so nothing is
+ever enqueued (the fake non-null pointers are never dereferenced)."""
+
+import os
+import re
+
+import pytest
+
+from precision_matmul_amd import _lib
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "fp8mm_moe.h")
+FAKE = 0x1000
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.fail("libfp8mm.so is not built (run __graft_entry__.build())")
+    return _lib.load()
+
+
+def test_every_declared_symbol_is_exported(lib):
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(fp8_\w+|fp8mm_\w+)\s*\(", text)))
+    assert len(names) == 13, names
+    for n in names:
+        assert hasattr(lib, n) and n in _lib.SIGNATURES, n
+
+
+def _call(lib, name, order, defaults, kw):
+    a = dict(defaults)
+    a.update(kw)
+    return getattr(lib, name)(*[a[k] for k in order.split()])
+
+
+NORM = "x dt R C ldx w b pd eps y ldy mean rstd st"
+NORM_D = dict(x=FAKE, dt=0, R=4, C=64, ldx=64, w=FAKE, b=FAKE, pd=0, eps=1e-5, y=FAKE, ldy=64, mean=None, rstd=None,
+              st=None)
+
+
+@pytest.mark.parametrize("kw", [dict(dt=2), dict(pd=7), dict(R=-1), dict(C=0), dict(C=2 ** 22 + 1, ldx=2 ** 23, ldy=2 ** 23),
+                                dict(R=2 ** 31), dict(ldx=63), dict(ldy=1), dict(eps=-1.0), dict(eps=NAN),
+                                dict(eps=INF), dict(x=None), dict(y=None), dict(x=FAKE + 1), dict(dt=1, y=FAKE + 2),
+                                dict(pd=1, w=FAKE + 2)])
+def test_layer_norm_refusals(lib, kw):
+    assert _call(lib, "fp8mm_layer_norm", NORM, NORM_D, kw) == _lib.EINVAL
+    assert lib.fp8mm_last_error().decode()
+
+
+def test_calls_with_nothing_to_do(lib):
+    assert _call(lib, "fp8mm_layer_norm", NORM, NORM_D, dict(R=0, x=None, y=None)) == _lib.OK
+    assert _call(lib, "fp8mm_moe_route", ROUTE, ROUTE_D, dict(T=0, l=None, ids=None, wt=None)) == _lib.OK
+    assert _call(lib, "fp8mm_moe_dispatch", DISP, DISP_D, dict(T=0, x=None, out=None, rows=None)) == _lib.OK
+    assert _call(lib, "fp8mm_moe_combine", COMB, COMB_D, dict(C=0, ldr=0, ldo=0)) == _lib.OK
+    assert _call(lib, "fp8_swiglu", SWI, SWI_D, dict(R=0, x=None)) == _lib.OK
+    assert _call(lib, "fp8_swiglu", SWI, SWI_D, dict(h=None, q=None, c=None)) == _lib.OK
+
+
+NORMB = "dy lddy x ldx dt R C w pd mean rstd dx lddx dw db ws wsb st"
+NORMB_D = dict(dy=FAKE, lddy=64, x=FAKE, ldx=64, dt=0, R=4, C=64, w=None, pd=0, mean=FAKE, rstd=FAKE, dx=FAKE, lddx=64,
+               dw=FAKE, db=None, ws=FAKE, wsb=1 << 20, st=None)
+
+
+@pytest.mark.parametrize("kw", [dict(lddy=10), dict(ldx=10), dict(lddx=10), dict(dy=None), dict(x=None), dict(mean=None),
+                                dict(rstd=None), dict(ws=None), dict(wsb=2 * 4 * 64 * 4 - 1), dict(ws=FAKE + 4),
+                                dict(dt=3), dict(C=-1), dict(dw=FAKE + 1), dict(dx=FAKE + 1)])
+def test_layer_norm_backward_refusals(lib, kw):
+    assert _call(lib, "fp8mm_layer_norm_backward", NORMB, NORMB_D, kw) == _lib.EINVAL
+
+
+def test_workspace_queries(lib):
+    assert lib.fp8mm_layer_norm_backward_workspace(4, 64) == 2 * 4 * 64 * 4
+    assert lib.fp8mm_layer_norm_backward_workspace(0, 64) == 0
+    assert lib.fp8mm_layer_norm_backward_workspace(-1, 64) == -1
+    big = lib.fp8mm_layer_norm_backward_workspace(2 ** 30, 64)
+    assert 0 < big <= 2 * 4096 * 64 * 4                      # bounded in the rows
+    assert lib.fp8mm_moe_plan_workspace(16, 6, 64) == 0
+    assert lib.fp8mm_moe_plan_workspace(16384, 6, 64) > 0
+    assert lib.fp8mm_moe_plan_workspace(-1, 6, 64) == -1
+    assert lib.fp8mm_moe_plan_workspace(2 ** 31, 6, 64) == -1
+
+
+ROUTE = "l dt T E ld b score k g gk gs rn scale ids wt st"
+ROUTE_D = dict(l=FAKE, dt=0, T=4, E=64, ld=64, b=None, score=0, k=6, g=1, gk=1, gs=0, rn=1, scale=1.0, ids=FAKE,
+               wt=FAKE, st=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=2), _lib.EINVAL), (dict(score=2), _lib.EINVAL), (dict(gs=5), _lib.EINVAL), (dict(rn=2), _lib.EINVAL),
+    (dict(T=-1), _lib.EINVAL), (dict(E=0), _lib.EINVAL), (dict(k=0), _lib.EINVAL), (dict(k=65), _lib.EINVAL),
+    (dict(g=0), _lib.EINVAL), (dict(g=3), _lib.EINVAL), (dict(g=4, gk=0), _lib.EINVAL), (dict(g=4, gk=5), _lib.EINVAL),
+    (dict(ld=63), _lib.EINVAL), (dict(scale=NAN), _lib.EINVAL), (dict(scale=-INF), _lib.EINVAL),
+    (dict(l=None), _lib.EINVAL), (dict(ids=None), _lib.EINVAL), (dict(wt=None), _lib.EINVAL),
+    (dict(l=FAKE + 1), _lib.EINVAL),
+    (dict(E=2048, ld=2048), _lib.ENOTIMPL), (dict(E=128, ld=128, k=65), _lib.ENOTIMPL),
+    (dict(E=128, ld=128, g=128), _lib.ENOTIMPL),
+])
+def test_route_refusals(lib, kw, code):
+    assert _call(lib, "fp8mm_moe_route", ROUTE, ROUTE_D, kw) == code
+
+
+ROUTEB = "g l dt T E ld ids k score rn scale out ldg st"
+ROUTEB_D = dict(g=FAKE, l=FAKE, dt=1, T=4, E=64, ld=64, ids=FAKE, k=6, score=0, rn=1, scale=1.0, out=FAKE, ldg=64,
+                st=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(g=None), _lib.EINVAL), (dict(out=None), _lib.EINVAL), (dict(ids=None), _lib.EINVAL), (dict(ldg=1), _lib.EINVAL),
+    (dict(k=0), _lib.EINVAL), (dict(score=-1), _lib.EINVAL), (dict(rn=3), _lib.EINVAL), (dict(out=FAKE + 2), _lib.EINVAL),
+    (dict(E=1025, ld=1025, ldg=1025), _lib.ENOTIMPL),
+])
+def test_route_backward_refusals(lib, kw, code):
+    assert _call(lib, "fp8mm_moe_route_backward", ROUTEB, ROUTEB_D, kw) == code
+
+
+PLAN = "ids T k E offs rows ws wsb st"
+PLAN_D = dict(ids=FAKE, T=9000, k=2, E=64, offs=FAKE, rows=FAKE, ws=FAKE, wsb=1 << 24, st=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(ids=None), _lib.EINVAL), (dict(offs=None), _lib.EINVAL), (dict(rows=None), _lib.EINVAL), (dict(T=-1), _lib.EINVAL),
+    (dict(k=0), _lib.EINVAL), (dict(E=0), _lib.EINVAL), (dict(T=2 ** 30), _lib.EINVAL), (dict(ws=None), _lib.EINVAL),
+    (dict(wsb=16), _lib.EINVAL), (dict(ws=FAKE + 8), _lib.EINVAL), (dict(E=1025), _lib.ENOTIMPL),
+])
+def test_plan_refusals(lib, kw, code):
+    assert _call(lib, "fp8mm_moe_plan", PLAN, PLAN_D, kw) == code
+
+
+DISP = "x dt T C ldx rows k out ldo st"
+DISP_D = dict(x=FAKE, dt=0, T=8, C=64, ldx=64, rows=FAKE, k=2, out=FAKE, ldo=64, st=None)
+COMB = "r dt T C ldr rows w k out ldo st"
+COMB_D = dict(r=FAKE, dt=0, T=8, C=64, ldr=64, rows=FAKE, w=None, k=2, out=FAKE, ldo=64, st=None)
+COMBB = "go ldgo r ldr dt T C rows w k gr ldgr gw st"
+COMBB_D = dict(go=FAKE, ldgo=64, r=FAKE, ldr=64, dt=0, T=8, C=64, rows=FAKE, w=FAKE, k=2, gr=FAKE, ldgr=64, gw=FAKE,
+               st=None)
+FDISP = "x T C ldx rows k q ldq s st"
+FDISP_D = dict(x=FAKE, T=8, C=128, ldx=128, rows=FAKE, k=2, q=FAKE, ldq=128, s=FAKE, st=None)
+
+
+@pytest.mark.parametrize("name,order,base,kw,code", [
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(x=None), _lib.EINVAL),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(out=None), _lib.EINVAL),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(rows=None), _lib.EINVAL),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(ldx=63), _lib.EINVAL),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(ldo=63), _lib.EINVAL),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(dt=4), _lib.EINVAL),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(k=0), _lib.EINVAL),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(k=65), _lib.ENOTIMPL),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(T=2 ** 27), _lib.EINVAL),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(x=FAKE + 1), _lib.EINVAL),
+    ("fp8mm_moe_combine", COMB, COMB_D, dict(r=None), _lib.EINVAL),
+    ("fp8mm_moe_combine", COMB, COMB_D, dict(ldr=3), _lib.EINVAL),
+    ("fp8mm_moe_combine", COMB, COMB_D, dict(T=-1), _lib.EINVAL),
+    ("fp8mm_moe_combine_backward", COMBB, COMBB_D, dict(go=None), _lib.EINVAL),
+    ("fp8mm_moe_combine_backward", COMBB, COMBB_D, dict(r=None), _lib.EINVAL),
+    ("fp8mm_moe_combine_backward", COMBB, COMBB_D, dict(ldgr=3), _lib.EINVAL),
+    ("fp8mm_moe_combine_backward", COMBB, COMBB_D, dict(dt=1, gr=FAKE + 2), _lib.EINVAL),
+    ("fp8_moe_dispatch", FDISP, FDISP_D, dict(C=192, ldx=192, ldq=192), _lib.EINVAL),
+    ("fp8_moe_dispatch", FDISP, FDISP_D, dict(ldx=132), _lib.EINVAL),
+    ("fp8_moe_dispatch", FDISP, FDISP_D, dict(ldq=136), _lib.EINVAL),
+    ("fp8_moe_dispatch", FDISP, FDISP_D, dict(q=FAKE + 8), _lib.EINVAL),
+    ("fp8_moe_dispatch", FDISP, FDISP_D, dict(s=None), _lib.EINVAL),
+])
+def test_permutation_refusals(lib, name, order, base, kw, code):
+    assert _call(lib, name, order, base, kw) == code
+    assert lib.fp8mm_last_error().decode()
+
+
+SWI = "x R F ldx h ldh q ldq s c ldc cs st"
+SWI_D = dict(x=FAKE, R=4, F=128, ldx=256, h=FAKE, ldh=128, q=FAKE, ldq=128, s=FAKE, c=FAKE, ldc=256, cs=FAKE, st=None)
+SWIB = "g ldg c ldc cs R F gx ldgx h ldh st"
+SWIB_D = dict(g=FAKE, ldg=128, c=FAKE, ldc=256, cs=FAKE, R=4, F=128, gx=FAKE, ldgx=256, h=None, ldh=0, st=None)
+
+
+@pytest.mark.parametrize("name,order,base,kw", [
+    ("fp8_swiglu", SWI, SWI_D, dict(F=100)),
+    ("fp8_swiglu", SWI, SWI_D, dict(R=-1)),
+    ("fp8_swiglu", SWI, SWI_D, dict(x=None)),
+    ("fp8_swiglu", SWI, SWI_D, dict(ldx=128)),
+    ("fp8_swiglu", SWI, SWI_D, dict(ldx=260)),
+    ("fp8_swiglu", SWI, SWI_D, dict(ldh=120)),
+    ("fp8_swiglu", SWI, SWI_D, dict(ldq=136)),
+    ("fp8_swiglu", SWI, SWI_D, dict(ldc=128)),
+    ("fp8_swiglu", SWI, SWI_D, dict(s=None)),
+    ("fp8_swiglu", SWI, SWI_D, dict(cs=None)),
+    ("fp8_swiglu", SWI, SWI_D, dict(h=FAKE + 2)),
+    ("fp8_swiglu", SWI, SWI_D, dict(R=2 ** 31 - 1, F=2 ** 20, ldx=2 ** 21, ldh=2 ** 20, ldq=2 ** 20, ldc=2 ** 21)),
+    ("fp8_swiglu_backward", SWIB, SWIB_D, dict(g=None)),
+    ("fp8_swiglu_backward", SWIB, SWIB_D, dict(c=None)),
+    ("fp8_swiglu_backward", SWIB, SWIB_D, dict(cs=None)),
+    ("fp8_swiglu_backward", SWIB, SWIB_D, dict(gx=None)),
+    ("fp8_swiglu_backward", SWIB, SWIB_D, dict(ldgx=128)),
+    ("fp8_swiglu_backward", SWIB, SWIB_D, dict(h=FAKE, ldh=64)),
+])
+def test_swiglu_refusals(lib, name, order, base, kw):
+    assert _call(lib, name, order, base, kw) == _lib.EINVAL
+    assert lib.fp8mm_last_error().decode()
