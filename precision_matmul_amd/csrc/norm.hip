@@ -33,9 +33,14 @@ __device__ __forceinline__ float row_sum(float v, float (&part)[2][WPR], int slo
 }
 
 // ---------------------------------------------------------------------------
-// Forward, row in registers: WPR waves a row, NIT chunks a lane.
+// Forward, row in registers: WPR waves a row, NIT chunks a lane.  A workgroup
+// takes rows blockIdx, blockIdx + gridDim, ...; a lane's columns are the same
+// in all of them, so it keeps its parameters in registers, and the next row is
+// loaded while this one is reduced and written.  16640 x 5120 bf16: 61.5 us,
+// 5.5 TB/s, what a plain copy reaches (one row a workgroup, parameters read
+// again for each: 85 us; one wave a row: 102 us; plain stores: 66 us).
 // ---------------------------------------------------------------------------
-template <typename T, typename P, int WPR, int NIT>
+template <typename T, typename P, int WPR, int NIT, bool NT>
 __global__ __launch_bounds__(256) void norm_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld_x,
                                                    const P* __restrict__ weight, const P* __restrict__ bias, float eps,
                                                    T* __restrict__ y, int64_t ld_y, float* __restrict__ mean_out,
@@ -43,15 +48,30 @@ __global__ __launch_bounds__(256) void norm_kernel(const T* __restrict__ x, int6
   constexpr int V = kVec<T>;
   constexpr int RPB = 4 / WPR;                    // rows of a workgroup
   __shared__ float part[2][WPR];
-  const int wave = threadIdx.x >> 6;
-  const int64_t c0 = int64_t(WPR == 1 ? threadIdx.x & 63 : threadIdx.x) * V;
+  const int in_row = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t c0 = int64_t(in_row) * V;
   constexpr int64_t STEP = int64_t(WPR) * 64 * V;
-  // all waves of a row take the same turns
-  for (int64_t row = int64_t(blockIdx.x) * RPB + (WPR == 1 ? wave : 0); row < R; row += int64_t(gridDim.x) * RPB) {
-    Chunk v[NIT];
-    float s = 0.0f;
+  Params<P, V> w[NIT], b[NIT];
 #pragma unroll
-    for (int it = 0; it < NIT; ++it) v[it] = load_row(x + row * ld_x, c0 + it * STEP, C);
+  for (int it = 0; it < NIT; ++it) {
+    w[it].load(weight, c0 + it * STEP, C, 1.0f);
+    b[it].load(bias, c0 + it * STEP, C, 0.0f);
+  }
+  const int64_t stride = int64_t(gridDim.x) * RPB;
+  int64_t row = int64_t(blockIdx.x) * RPB + (WPR == 1 ? threadIdx.x >> 6 : 0);
+  Chunk next[NIT];
+#pragma unroll
+  for (int it = 0; it < NIT; ++it)
+    if (row < R) next[it] = load_row(x + row * ld_x, c0 + it * STEP, C);
+  for (; row < R; row += stride) {                // all waves of a row take the same turns
+    Chunk v[NIT];
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) v[it] = next[it];
+    if (row + stride < R) {
+#pragma unroll
+      for (int it = 0; it < NIT; ++it) next[it] = load_row(x + (row + stride) * ld_x, c0 + it * STEP, C);
+    }
+    float s = 0.0f;
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
       float f[V];
@@ -73,20 +93,17 @@ __global__ __launch_bounds__(256) void norm_kernel(const T* __restrict__ x, int6
       }
     }
     const float rstd = 1.0f / sqrtf(row_sum<WPR>(ss, part, 1) / float(C) + eps);
-    if ((WPR == 1 ? threadIdx.x & 63 : threadIdx.x) == 0) {
+    if (in_row == 0) {
       if (mean_out) mean_out[row] = mean;
       if (rstd_out) rstd_out[row] = rstd;
     }
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
-      const int64_t c = c0 + it * STEP;
-      float f[V], w[V], b[V];
+      float f[V];
       unpack<T>(v[it], f);
-      load_params<P, V>(weight, c, C, 1.0f, w);
-      load_params<P, V>(bias, c, C, 0.0f, b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * w[i] + b[i];
-      store_row(y + row * ld_y, c, C, pack<T>(f));
+      for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * w[it][i] + b[it][i];
+      store_row<T, NT>(y + row * ld_y, c0 + it * STEP, C, pack<T>(f));
     }
   }
 }
@@ -126,10 +143,11 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
       if (rstd_out) rstd_out[row] = rstd;
     }
     for (int64_t c = int64_t(threadIdx.x) * V; c < C; c += 256 * V) {
-      float f[V], w[V], b[V];
+      float f[V];
+      Params<P, V> w, b;
       unpack<T>(load_row(xr, c, C), f);
-      load_params<P, V>(weight, c, C, 1.0f, w);
-      load_params<P, V>(bias, c, C, 0.0f, b);
+      w.load(weight, c, C, 1.0f);
+      b.load(bias, c, C, 0.0f);
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * w[i] + b[i];
       store_row(y + row * ld_y, c, C, pack<T>(f));
@@ -138,19 +156,28 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
 }
 
 // ---------------------------------------------------------------------------
-// Backward, row in registers.  A workgroup takes rows blockIdx, blockIdx +
-// gridDim, ... and keeps its share of dw and db in registers over all of them
-// (lane columns are the same for every row); each workgroup then writes one
-// partial row of the workspace, [2][gridDim][C], which column_sum_kernel adds
-// up in workgroup order: no atomics, the same bits every time.
+// Backward, row in registers.  A workgroup takes rows in turns like the
+// forward's, the next row in flight while this one is worked on, and keeps its
+// share of dw and db in registers over all of them; it then writes one partial
+// row of the workspace, [2][gridDim][C], which column_sum_kernel adds up in
+// workgroup order: no atomics, the same bits every time.  The partial rows are
+// traffic of their own (8 gridDim C bytes each way), so there are no more
+// workgroups than run at once: 256 of eight waves with a row each, or, above
+// 4 chunks a lane, 512 of four waves that share a row (256 above 12 chunks of
+// a wave, where the registers leave room for one workgroup a compute unit).
+// 16384 x 2048 bf16: 47 us with the column sums, 4.3 TB/s of x, dy and dx (512
+// partial rows of eight-wave workgroups 56 us; no row in flight ahead 55 us);
+// 10000 x 5120: 72 us (1024 partial rows 88 us); 10000 x 8192: 99 us (512: 111).
 // ---------------------------------------------------------------------------
-template <typename T, typename P, int WPR, int NIT>
-__global__ __launch_bounds__(256) void norm_backward_kernel(
+constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
+
+template <typename T, typename P, int WPR, int NIT, bool NT>
+__global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward_kernel(
     const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ x, int64_t ld_x, int64_t R, int64_t C,
     const P* __restrict__ weight, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
     T* __restrict__ dx, int64_t ld_dx, float* __restrict__ partial) {
   constexpr int V = kVec<T>;
-  constexpr int RPB = 4 / WPR;
+  constexpr int RPB = WPR == 1 ? kRowWaves : 1;
   constexpr int64_t STEP = int64_t(WPR) * 64 * V;
   __shared__ float part[2][2][4];
   __shared__ float acc[WPR == 1 ? 2 * NIT * int(STEP) : 1];
@@ -162,39 +189,59 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(
   for (int it = 0; it < NIT; ++it)
 #pragma unroll
     for (int i = 0; i < V; ++i) dw[it][i] = db[it][i] = 0.0f;
+  Params<P, V> w[NIT];
+#pragma unroll
+  for (int it = 0; it < NIT; ++it) w[it].load(weight, c0 + it * STEP, C, 1.0f);
   int slot = 0;
-  for (int64_t row = int64_t(blockIdx.x) * RPB + (WPR == 1 ? wave : 0); row < R; row += int64_t(gridDim.x) * RPB) {
+  const int64_t stride = int64_t(gridDim.x) * RPB;
+  int64_t row = int64_t(blockIdx.x) * RPB + (WPR == 1 ? wave : 0);
+  Chunk nx[NIT], ng[NIT];
+  float nmean = 0.0f, nrstd = 0.0f;
+  if (row < R) {
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      nx[it] = load_row(x + row * ld_x, c0 + it * STEP, C);
+      ng[it] = load_row(dy + row * ld_dy, c0 + it * STEP, C);
+    }
+    nmean = mean_in[row];
+    nrstd = rstd_in[row];
+  }
+  for (; row < R; row += stride) {
     Chunk vx[NIT], vg[NIT];
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
-      vx[it] = load_row(x + row * ld_x, c0 + it * STEP, C);
-      vg[it] = load_row(dy + row * ld_dy, c0 + it * STEP, C);
+      vx[it] = nx[it];
+      vg[it] = ng[it];
     }
-    const float mean = mean_in[row], rstd = rstd_in[row];
+    const float mean = nmean, rstd = nrstd;
+    if (row + stride < R) {
+#pragma unroll
+      for (int it = 0; it < NIT; ++it) {
+        nx[it] = load_row(x + (row + stride) * ld_x, c0 + it * STEP, C);
+        ng[it] = load_row(dy + (row + stride) * ld_dy, c0 + it * STEP, C);
+      }
+      nmean = mean_in[row + stride];
+      nrstd = rstd_in[row + stride];
+    }
     float sa = 0.0f, sax = 0.0f;
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
-      const int64_t c = c0 + it * STEP;
-      float f[V], g[V], w[V];
+      float f[V], g[V];
       unpack<T>(vx[it], f);
       unpack<T>(vg[it], g);
-      load_params<P, V>(weight, c, C, 1.0f, w);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float xh = (f[i] - mean) * rstd;    // dy is 0 past the row's end
-        const float a = g[i] * w[i];
+        const float a = g[i] * w[it][i];
         sa += a;
         sax += a * xh;
         dw[it][i] += g[i] * xh;
         db[it][i] += g[i];
       }
     }
-    if constexpr (WPR == 1) {
-      sa = wave_sum(sa);
-      sax = wave_sum(sax);
-    } else {
-      sa = wave_sum(sa);
-      sax = wave_sum(sax);
+    sa = wave_sum(sa);
+    sax = wave_sum(sax);
+    if constexpr (WPR > 1) {
       if ((threadIdx.x & 63) == 0) {
         part[slot][0][wave] = sa;
         part[slot][1][wave] = sax;
@@ -206,27 +253,27 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(
     }
     sa *= inv_c;
     sax *= inv_c;
+    if (dx) {
 #pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-      const int64_t c = c0 + it * STEP;
-      float f[V], g[V], w[V];
-      unpack<T>(vx[it], f);
-      unpack<T>(vg[it], g);
-      load_params<P, V>(weight, c, C, 1.0f, w);
+      for (int it = 0; it < NIT; ++it) {
+        float f[V], g[V];
+        unpack<T>(vx[it], f);
+        unpack<T>(vg[it], g);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float xh = (f[i] - mean) * rstd;
-        f[i] = rstd * (g[i] * w[i] - sa - xh * sax);
+        for (int i = 0; i < V; ++i) {
+          const float xh = (f[i] - mean) * rstd;
+          f[i] = rstd * (g[i] * w[it][i] - sa - xh * sax);
+        }
+        store_row<T, NT>(dx + row * ld_dx, c0 + it * STEP, C, pack<T>(f));
       }
-      if (dx) store_row(dx + row * ld_dx, c, C, pack<T>(f));
     }
   }
   if (!partial) return;
   float* pw = partial + int64_t(blockIdx.x) * C;
   float* pb = pw + int64_t(gridDim.x) * C;
   if constexpr (WPR == 1) {
-    // the four waves' shares, added in wave order
-    for (int w = 0; w < 4; ++w) {
+    // the waves' shares, added in wave order
+    for (int w = 0; w < kRowWaves; ++w) {
       if (wave == w) {
 #pragma unroll
         for (int it = 0; it < NIT; ++it)
@@ -239,7 +286,7 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(
       }
       __syncthreads();
     }
-    for (int64_t c = threadIdx.x; c < C; c += 256) {
+    for (int64_t c = threadIdx.x; c < C; c += 64 * kRowWaves) {
       pw[c] = acc[c];
       pb[c] = acc[NIT * STEP + c];
     }
@@ -269,10 +316,11 @@ __global__ __launch_bounds__(256) void norm_backward_long_kernel(
     const float mean = mean_in[row], rstd = rstd_in[row];
     float sa = 0.0f, sax = 0.0f;
     for (int64_t c = int64_t(threadIdx.x) * V; c < C; c += 256 * V) {
-      float f[V], g[V], w[V];
+      float f[V], g[V];
+      Params<P, V> w;
       unpack<T>(load_row(x + row * ld_x, c, C), f);
       unpack<T>(load_row(dy + row * ld_dy, c, C), g);
-      load_params<P, V>(weight, c, C, 1.0f, w);
+      w.load(weight, c, C, 1.0f);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         sa += g[i] * w[i];
@@ -282,10 +330,11 @@ __global__ __launch_bounds__(256) void norm_backward_long_kernel(
     sa = row_sum<4>(sa, part, 0) / float(C);
     sax = row_sum<4>(sax, part, 1) / float(C);
     for (int64_t c = int64_t(threadIdx.x) * V; c < C; c += 256 * V) {
-      float f[V], g[V], w[V];
+      float f[V], g[V];
+      Params<P, V> w;
       unpack<T>(load_row(x + row * ld_x, c, C), f);
       unpack<T>(load_row(dy + row * ld_dy, c, C), g);
-      load_params<P, V>(weight, c, C, 1.0f, w);
+      w.load(weight, c, C, 1.0f);
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = rstd * (g[i] * w[i] - sa - (f[i] - mean) * rstd * sax);
       store_row(dx + row * ld_dx, c, C, pack<T>(f));
@@ -339,25 +388,38 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
   }
 }
 
+constexpr int64_t kForwardGrid = 1024;  // four workgroups a compute unit
 constexpr int kBackwardGrid = 512;      // partial rows at most
 constexpr int64_t kRegisterCols = 8192; // longest row kept in registers
 
 // Workgroups of the row kernels, which take further rows in turns past this.
 dim3 row_grid(int64_t blocks) { return dim3(unsigned(blocks < (1 << 20) ? blocks : (1 << 20))); }
 
+// Whether the result is larger than the L2s together (8 x 4 MiB): then no next
+// kernel finds it there, and streaming stores leave the L2s to the inputs.
+bool streams(const NormProblem& p, size_t size) { return p.R * p.C * int64_t(size) > (int64_t(32) << 20); }
+
+// Workgroups of the backward (one partial row each): as many as run at once.
 int backward_grid(int64_t R, int64_t C, int vec) {
-  const int64_t rows_a_block = C <= 256 * vec ? 4 : 1;
-  const int64_t blocks = (R + rows_a_block - 1) / rows_a_block;
-  return int(blocks < kBackwardGrid ? blocks : kBackwardGrid);
+  const int64_t one_wave = 256 * vec;         // rows of up to this many columns: a wave each
+  const int64_t rows = C <= one_wave ? kRowWaves : 1;
+  const int64_t most = C <= one_wave ? 256 : C <= 3 * one_wave ? 512 : 256;
+  const int64_t blocks = (R + rows - 1) / rows;
+  return int(blocks < most ? blocks : most);
 }
 
 template <typename T, typename P, int WPR, int NIT>
 hipError_t run_norm(const NormProblem& p, hipStream_t st) {
   constexpr int RPB = 4 / WPR;
-  hipLaunchKernelGGL((norm_kernel<T, P, WPR, NIT>), row_grid((p.R + RPB - 1) / RPB), dim3(256), 0, st,
-                     static_cast<const T*>(p.x), p.R, p.C, p.ld_x, static_cast<const P*>(p.weight),
-                     static_cast<const P*>(p.bias), p.eps, static_cast<T*>(p.out), p.ld_out, p.mean, p.rstd);
-  return hipGetLastError();
+  const int64_t blocks = (p.R + RPB - 1) / RPB;
+  const dim3 grid(unsigned(blocks < kForwardGrid ? blocks : kForwardGrid));
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, static_cast<const T*>(p.x), p.R, p.C, p.ld_x,
+                       static_cast<const P*>(p.weight), static_cast<const P*>(p.bias), p.eps, static_cast<T*>(p.out),
+                       p.ld_out, p.mean, p.rstd);
+    return hipGetLastError();
+  };
+  return streams(p, sizeof(T)) ? run(norm_kernel<T, P, WPR, NIT, true>) : run(norm_kernel<T, P, WPR, NIT, false>);
 }
 
 template <typename T, typename P>
@@ -380,10 +442,14 @@ hipError_t norm_typed(const NormProblem& p, hipStream_t st) {
 
 template <typename T, typename P, int WPR, int NIT>
 hipError_t run_backward(const NormProblem& p, int grid, float* partial, hipStream_t st) {
-  hipLaunchKernelGGL((norm_backward_kernel<T, P, WPR, NIT>), dim3(grid), dim3(256), 0, st,
-                     static_cast<const T*>(p.dy), p.ld_dy, static_cast<const T*>(p.x), p.ld_x, p.R, p.C,
-                     static_cast<const P*>(p.weight), p.mean, p.rstd, static_cast<T*>(p.out), p.ld_out, partial);
-  return hipGetLastError();
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(WPR == 1 ? 64 * kRowWaves : 256), 0, st,
+                       static_cast<const T*>(p.dy), p.ld_dy, static_cast<const T*>(p.x), p.ld_x, p.R, p.C,
+                       static_cast<const P*>(p.weight), p.mean, p.rstd, static_cast<T*>(p.out), p.ld_out, partial);
+    return hipGetLastError();
+  };
+  return streams(p, sizeof(T)) ? run(norm_backward_kernel<T, P, WPR, NIT, true>)
+                               : run(norm_backward_kernel<T, P, WPR, NIT, false>);
 }
 
 template <typename T, typename P>

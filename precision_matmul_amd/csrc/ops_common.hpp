@@ -38,6 +38,14 @@ __device__ __forceinline__ void store_chunk(T* p, const Chunk& v) {
   *reinterpret_cast<ChunkAt<T>*>(p) = ChunkAt<T>{{v.w[0], v.w[1], v.w[2], v.w[3]}};
 }
 
+// Streaming store, for results larger than the L2s together hold.
+template <typename T>
+__device__ __forceinline__ void store_chunk_nt(T* p, const Chunk& v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  typedef u32x4 __attribute__((aligned(2))) u32x4_at;
+  __builtin_nontemporal_store(u32x4{v.w[0], v.w[1], v.w[2], v.w[3]}, reinterpret_cast<u32x4_at*>(p));
+}
+
 // The first n < kVec<T> elements of a row's last chunk, zeros after them.
 template <typename T>
 __device__ __forceinline__ Chunk load_part(const T* p, int n) {
@@ -78,10 +86,10 @@ __device__ __forceinline__ Chunk load_row(const T* row, int64_t c, int64_t C) {
   return Chunk{{0u, 0u, 0u, 0u}};
 }
 
-template <typename T>
+template <typename T, bool NT = false>
 __device__ __forceinline__ void store_row(T* row, int64_t c, int64_t C, const Chunk& v) {
   if (c + kVec<T> <= C)
-    store_chunk(row + c, v);
+    NT ? store_chunk_nt(row + c, v) : store_chunk(row + c, v);
   else if (c < C)
     store_part(row + c, v, int(C - c));
 }
@@ -140,22 +148,41 @@ __device__ __forceinline__ T from_float(float v) {
     return v;
 }
 
-// N consecutive parameters of type P at column c of C, as floats; `none`
-// where there is no parameter vector or the column is past its end.
+// N consecutive parameters of type P at column c of C, kept in registers as
+// they are stored; `none` where there is no parameter vector or the column is
+// past its end.
 template <typename P, int N>
-__device__ __forceinline__ void load_params(const P* p, int64_t c, int64_t C, float none, float (&f)[N]) {
+struct Params {
   struct __attribute__((packed, aligned(sizeof(P)))) At {
-    P v[N];
+    uint32_t w[N * sizeof(P) / 4];
   };
-  if (p && c + N <= C) {
-    const At a = *reinterpret_cast<const At*>(p + c);
+  uint32_t w[N * sizeof(P) / 4];
+
+  __device__ __forceinline__ void load(const P* p, int64_t c, int64_t C, float none) {
+    if (p && c + N <= C) {
+      const At a = *reinterpret_cast<const At*>(p + c);
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = to_float(a.v[i]);
-  } else {
+      for (int i = 0; i < int(N * sizeof(P) / 4); ++i) w[i] = a.w[i];
+    } else {
+      float f[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = p && c + i < C ? to_float(p[c + i]) : none;
+      for (int i = 0; i < N; ++i) f[i] = p && c + i < C ? to_float(p[c + i]) : none;
+#pragma unroll
+      for (int i = 0; i < int(N * sizeof(P) / 4); ++i) {
+        if constexpr (sizeof(P) == 2)
+          w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+        else
+          w[i] = __float_as_uint(f[i]);
+      }
+    }
   }
-}
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(P) == 2)
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    else
+      return __uint_as_float(w[i]);
+  }
+};
 
 // ---------------------------------------------------------------- reductions
 
