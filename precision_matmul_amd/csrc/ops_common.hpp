@@ -221,6 +221,29 @@ __device__ __forceinline__ float wave_max_f(float v) {
   return lane_value(v, 63);
 }
 
+// Maximum of unsigned integers over the 64 lanes (a scalar): one instruction a
+// step within the rows of 16 (lanes that a shift leaves empty read 0), then the
+// rows' maxima in scalars.
+__device__ __forceinline__ uint32_t wave_max_u(uint32_t v) {
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, true)));
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, true)));
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, true)));
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, true)));
+  const int i = int(v);
+  return max(max(uint32_t(__builtin_amdgcn_readlane(i, 15)), uint32_t(__builtin_amdgcn_readlane(i, 31))),
+             max(uint32_t(__builtin_amdgcn_readlane(i, 47)), uint32_t(__builtin_amdgcn_readlane(i, 63))));
+}
+
+// A lane's value as a scalar; a scalar put into one lane.
+__device__ __forceinline__ uint32_t read_lane(uint32_t v, int lane) {
+  return uint32_t(__builtin_amdgcn_readlane(int(v), lane));
+}
+// (This compiler has the instruction's intrinsic but no builtin for it.)
+extern "C" __device__ int fp8mm_writelane(int value, int lane, int v) __asm("llvm.amdgcn.writelane.i32");
+__device__ __forceinline__ uint32_t write_lane(uint32_t value, int lane, uint32_t v) {
+  return uint32_t(fp8mm_writelane(int(value), lane, int(v)));
+}
+
 // Maximum of unsigned integers over aligned groups of 8 lanes, in all 8.
 __device__ __forceinline__ uint32_t group8_max(uint32_t v) {
   v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, false)));   // lane i with 7 - i

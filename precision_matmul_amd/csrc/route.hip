@@ -28,7 +28,7 @@ using namespace ops;
 constexpr float kInf = __builtin_inff();
 
 template <typename T, int N>
-__device__ __forceinline__ void load_logits(const T* row, int e0, int E, float (&x)[N]) {
+__device__ __forceinline__ void load_row_of(const T* row, int e0, int E, float (&x)[N]) {
   struct __attribute__((packed, aligned(sizeof(T)))) At {
     T v[N];
   };
@@ -42,151 +42,246 @@ __device__ __forceinline__ void load_logits(const T* row, int e0, int E, float (
   }
 }
 
-// Scores of a row: softmax(x) = exp(x - shift) * inv, sigmoid(x).
+// exp(-a) for a >= 0, to an ulp or two: the hardware's exp2 with the rounding
+// error of a log2(e) put back (its part above 2^-24 and log2(e)'s own low part).
+// From a = 104 on the result is 0, as float32's would be.
+__device__ __forceinline__ float exp_neg(float a) {
+  constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;
+  a = fminf(a, 104.0f);
+  const float t = a * -kLog2e;
+  const float low = __builtin_fmaf(a, -kLog2e, -t) - a * kLog2eLow;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, low * 0.693147182464599609375f, e);
+}
+
+// 1 / d by the hardware's reciprocal and one Newton step; d in [1, 2].
+__device__ __forceinline__ float reciprocal(float d) {
+  const float r = __builtin_amdgcn_rcpf(d);
+  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+
+// Scores of a row: sigmoid(x), or softmax(x) = exp(x - shift) * inv, shift >= x.
+template <bool SIGMOID>
 struct Scores {
-  bool sigmoid;
-  float shift, inv;
+  float shift = 0.0f, inv = 1.0f;
+
+  template <int N>
+  __device__ __forceinline__ explicit Scores(const float (&x)[N]) {
+    if constexpr (!SIGMOID) {
+      float m = x[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+      m = wave_max_f(m);
+      shift = m == -kInf ? 0.0f : m;             // a row of -inf alone: every score 0
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum += exp_neg(shift - x[i]);
+      sum = wave_sum(sum);
+      inv = sum == 0.0f ? 1.0f : 1.0f / sum;
+    }
+  }
+
   __device__ __forceinline__ float operator()(float x) const {
-    return sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - shift) * inv;
+    if constexpr (!SIGMOID) return exp_neg(shift - x) * inv;
+    const float e = exp_neg(fabsf(x));
+    return (x < 0.0f ? e : 1.0f) * reciprocal(1.0f + e);
   }
 };
 
-template <int N>
-__device__ __forceinline__ Scores row_scores(const float (&x)[N], bool sigmoid) {
-  Scores s{sigmoid, 0.0f, 1.0f};
-  if (!sigmoid) {
-    float m = x[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
-    m = wave_max_f(m);
-    s.shift = m == -kInf ? 0.0f : m;           // a row of -inf alone: every score 0
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) sum += expf(x[i] - s.shift);
-    sum = wave_sum(sum);
-    s.inv = sum == 0.0f ? 1.0f : 1.0f / sum;
+// Group selection: keys of experts outside the chosen groups become -inf.  L
+// lanes work on each group: where a group is a power of two of whole lanes,
+// those that hold it; else 64 / G rounded down to a power of two, which read its
+// values from LDS.  They merge their two best by butterfly and compare the
+// group's score with the others', L groups at a time.
+struct Groups {
+  int count, size;     // groups, experts in each
+  int shift;           // L = 1 << shift
+  bool whole;          // the L lanes are the group's own
+  float inv_size;
+
+  Groups(const RouteProblem& p, int per_lane) : count(p.groups), size(p.E / p.groups), inv_size(1.0f / float(size)) {
+    const int lanes = size / per_lane;
+    whole = size % per_lane == 0 && (lanes & (lanes - 1)) == 0;
+    shift = 31 - __builtin_clz(unsigned(whole ? lanes : 64 / count));
   }
-  return s;
+  // e / size: half an expert from the next integer at least, far more than
+  // the float product can be off for e < 1024
+  __device__ __forceinline__ int of(int e) const { return int((float(e) + 0.5f) * inv_size); }
+};
+
+// One butterfly step of (best, second) over lanes that differ in `CTRL`'s bit;
+// pairs of lanes already agree below it, so that mirrors serve as well.
+template <int CTRL>
+__device__ __forceinline__ void merge_dpp(float& best, float& second) {
+  const float b = dpp<CTRL>(0.0f, best), s = dpp<CTRL>(0.0f, second);
+  second = fmaxf(fmaxf(second, s), fminf(best, b));
+  best = fmaxf(best, b);
 }
 
-// Group selection: keys of experts outside the chosen groups become -inf.
-// L = 64 / G rounded down to a power of two lanes work on each group, reading
-// its values from LDS, then merge their two best by butterfly.
+__device__ __forceinline__ void merge_far(float& best, float& second, int off) {
+  const float b = __shfl_xor(best, off, 64), s = __shfl_xor(second, off, 64);
+  second = fmaxf(fmaxf(second, s), fminf(best, b));
+  best = fmaxf(best, b);
+}
+
 template <int N>
-__device__ __forceinline__ void keep_groups(float (&key)[N], const float (&value)[N], int e0, const RouteProblem& p,
-                                            float* lds) {
+__device__ __forceinline__ void keep_groups(float (&key)[N], const float (&value)[N], int e0, const Groups& groups,
+                                            bool top2, int topk, int E, float* lds) {
   const int lane = threadIdx.x & 63;
-  const int gs = p.E / p.groups;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (e0 + i < p.E) lds[e0 + i] = p.group_top2 ? value[i] : key[i];
-  // the wave reads what its own lanes wrote: in order, no barrier needed
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  const int shift = 31 - __builtin_clz(unsigned(64 / p.groups));
-  const int L = 1 << shift;
-  const int g = lane >> shift;
+  const int L = 1 << groups.shift;
+  const int g = lane >> groups.shift;
   float best = -kInf, second = -kInf;
-  if (g < p.groups) {
-    for (int j = lane & (L - 1); j < gs; j += L) {
-      const float v = lds[g * gs + j];
-      second = fmaxf(second, fminf(best, v));
-      best = fmaxf(best, v);
-    }
-  }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  for (int off = 1; off < L; off <<= 1) {
-    const float b = __shfl_xor(best, off, 64), s = __shfl_xor(second, off, 64);
-    second = fmaxf(fmaxf(second, s), fminf(best, b));
-    best = fmaxf(best, b);
-  }
-  float score = best;
-  if (p.group_top2 && second != -kInf) score = best + second;
-  int rank = 0;
-  for (int o = 0; o < p.groups; ++o) {
-    const float other = lane_value(score, o << shift);
-    rank += other > score || (other == score && o < g) ? 1 : 0;
-  }
-  const uint64_t kept = __ballot(g < p.groups && rank < p.group_topk);
+  if (groups.whole) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = e0 + i;
-    if (e < p.E && !((kept >> ((e / gs) << shift)) & 1)) key[i] = -kInf;
+    for (int i = 0; i < N; ++i) {
+      second = fmaxf(second, fminf(best, value[i]));
+      best = fmaxf(best, value[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (e0 + i < E) lds[e0 + i] = value[i];
+    // the wave reads what its own lanes wrote: in order, no barrier needed
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (g < groups.count) {
+      for (int j = lane & (L - 1); j < groups.size; j += L) {
+        const float v = lds[g * groups.size + j];
+        second = fmaxf(second, fminf(best, v));
+        best = fmaxf(best, v);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  if (L > 1) merge_dpp<0xB1>(best, second);      // lane ^ 1
+  if (L > 2) merge_dpp<0x4E>(best, second);      // lane ^ 2
+  if (L > 4) merge_dpp<0x141>(best, second);     // 7 - lane in each 8
+  if (L > 8) merge_dpp<0x140>(best, second);     // 15 - lane in each 16
+  if (L > 16) merge_far(best, second, 16);
+  if (L > 32) merge_far(best, second, 32);
+  float score = best;
+  if (top2) score = second == -kInf ? best : best + second;
+  // rank: groups that come before this one
+  const uint64_t mine = (L == 64 ? ~0ull : (1ull << L) - 1) << (g << groups.shift);
+  int rank = 0;
+  for (int o0 = 0; o0 < groups.count; o0 += L) {
+    const int o = o0 + (lane & (L - 1));
+    const float other = __shfl(score, o << groups.shift, 64);
+    const bool first = (other > score) | ((other == score) & (o < g));
+    rank += __popcll(__ballot(first & (o < groups.count)) & mine);
+  }
+  const bool keep = g < groups.count && rank < topk;
+  if (groups.whole) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = keep ? key[i] : -kInf;
+  } else {
+    const uint64_t kept = __ballot(keep);
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = (kept >> (groups.of(min(e0 + i, E - 1)) << groups.shift)) & 1 ? key[i] : -kInf;
   }
 }
 
-template <typename T, int N, bool BIAS>
-__global__ __launch_bounds__(256) void route_kernel(const RouteProblem p) {
+// Floats as unsigned integers of the same order (-0 as +0), so that a wave
+// maximum is six fused data-parallel steps; -inf and what is out are at most
+// kNone.
+constexpr uint32_t kNone = 0x007FFFFFu;
+
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
+template <int N>
+__device__ __forceinline__ void load_logits(const RouteProblem& p, int64_t row, int e0, float (&x)[N]) {
+  if (p.fp32)
+    load_row_of(static_cast<const float*>(p.logits) + row * p.ld, e0, p.E, x);
+  else
+    load_row_of(static_cast<const uint16_t*>(p.logits) + row * p.ld, e0, p.E, x);
+}
+
+template <int N, bool SIGMOID, bool BIAS, bool GROUPS>
+__global__ __launch_bounds__(256) void route_kernel(const RouteProblem p, const Groups groups) {
   extern __shared__ float lds_all[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int e0 = lane * N;
   float b[N];
-  if constexpr (BIAS) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = e0 + i < p.E ? p.bias[e0 + i] : 0.0f;
-  }
+  if constexpr (BIAS) load_row_of(p.bias, e0, p.E, b);
   for (int64_t row = int64_t(blockIdx.x) * 4 + wave; row < p.T; row += int64_t(gridDim.x) * 4) {
     float x[N], key[N];
-    load_logits<T, N>(static_cast<const T*>(p.logits) + row * p.ld, e0, p.E, x);
+    load_logits(p, row, e0, x);
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < N; ++i) bad |= x[i] != x[i] || (!p.sigmoid && x[i] == kInf);
-    const Scores score = row_scores(x, p.sigmoid);
-    const bool by_groups = p.group_topk < p.groups;
-    if constexpr (BIAS) {
+    for (int i = 0; i < N; ++i) bad |= SIGMOID ? x[i] != x[i] : !(x[i] < kInf);
+    const Scores<SIGMOID> score(x);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        key[i] = x[i] == -kInf ? -kInf : score(x[i]) + b[i];
+    for (int i = 0; i < N; ++i) {
+      key[i] = x[i];
+      if constexpr (BIAS) {
+        const float k = score(x[i]) + b[i];
+        key[i] = x[i] == -kInf ? -kInf : k;
         bad |= key[i] != key[i];
       }
-      if (by_groups) {
-        const float (&value)[N] = key;
-        float keep[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) keep[i] = value[i];
-        keep_groups(key, keep, e0, p, lds_all + wave * p.E);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) key[i] = x[i];
-      if (by_groups) {
-        float value[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) value[i] = p.group_top2 && x[i] != -kInf ? score(x[i]) : -kInf;
-        keep_groups(key, value, e0, p, lds_all + wave * p.E);
-      }
     }
-    const bool none_defined = __ballot(bad) != 0;
-    int id = -1;            // lane j: slot j's expert and its logit
-    float logit = 0.0f;
-    for (int j = 0; j < p.k; ++j) {
-      float local = key[0];
+    if constexpr (GROUPS) {
+      float value[N];
 #pragma unroll
-      for (int i = 1; i < N; ++i) local = fmaxf(local, key[i]);
-      const float m = wave_max_f(local);
-      if (m == -kInf) break;
-      // the lowest lane with the maximum, and its lowest element with it
+      for (int i = 0; i < N; ++i) {
+        value[i] = key[i];
+        if constexpr (!BIAS) {
+          const float s = score(x[i]);
+          value[i] = p.group_top2 && x[i] != -kInf ? s : x[i];
+        }
+      }
+      keep_groups(key, value, e0, groups, p.group_top2, p.group_topk, p.E, lds_all + wave * p.E);
+    }
+    const bool undefined = __ballot(bad) != 0;
+    uint32_t u[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = ordered(key[i]);
+    int id = -1;                 // lane j: slot j's expert and its key
+    uint32_t best = 0;
+    for (int j = 0; j < p.k; ++j) {
+      uint32_t local = u[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) local = max(local, u[i]);
+      const uint32_t m = wave_max_u(local);
+      if (m <= kNone) break;
+      // the lowest lane with the maximum, and its lowest place with it; all of
+      // this in scalars, written back to the one lane that it changes
       const int from = int(__builtin_ctzll(__ballot(local == m) | (1ull << 63)));
       int at = 0;
-      float xl = x[0];
-      bool found = key[0] == m;
+      if constexpr (N == 1) {
+        u[0] = write_lane(0u, from, u[0]);
+      } else {
+        bool found = false;
 #pragma unroll
-      for (int i = 1; i < N; ++i) {
-        const bool here = !found && key[i] == m;
-        at = here ? i : at;
-        if constexpr (BIAS) xl = here ? x[i] : xl;
-        found |= here;
+        for (int i = 0; i < N; ++i) {
+          const uint32_t v = read_lane(u[i], from);
+          const bool here = !found && v == m;
+          at = here ? i : at;
+          found |= here;
+          u[i] = write_lane(here ? 0u : v, from, u[i]);
+        }
       }
-      const int e = from * N + __builtin_amdgcn_readlane(at, from);
-      const float xe = BIAS ? lane_value(xl, from) : m;
-      id = lane == j ? e : id;
-      logit = lane == j ? xe : logit;
-#pragma unroll
-      for (int i = 0; i < N; ++i) key[i] = lane == from && at == i ? -kInf : key[i];
+      id = int(write_lane(uint32_t(from * N + at), j, uint32_t(id)));
+      best = write_lane(m, j, best);
     }
-    float w = id < 0 ? 0.0f : score(logit);
+    float chosen = from_ordered(best);
+    if constexpr (BIAS) {        // the key holds the bias too
+      chosen = 0.0f;
+      if (id >= 0)
+        chosen = p.fp32 ? static_cast<const float*>(p.logits)[row * p.ld + id]
+                        : to_float(static_cast<const uint16_t*>(p.logits)[row * p.ld + id]);
+    }
+    float w = score(chosen);
+    w = id < 0 ? 0.0f : w;
     if (p.renorm) w = w / (wave_sum(w) + kRenormEps);
     w *= p.scale;
-    if (none_defined) {
+    if (undefined) {
       id = lane;
       w = __builtin_nanf("");
     }
@@ -202,27 +297,29 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteProblem p) {
 //   d_j = scale (g_j - sum_l g_l s_l / S) / S, S = sum_l s_l + 1e-20   (renormalised)
 // the logits get  softmax: s_e (d_e - sum_l s_l d_l),  sigmoid: s_e (1 - s_e) d_e
 // (d_e = 0 for experts not chosen).  The choice itself has no gradient.
-template <typename T, int N>
+template <typename T, int N, bool SIGMOID>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int e0 = lane * N;
   for (int64_t row = int64_t(blockIdx.x) * 4 + wave; row < p.T; row += int64_t(gridDim.x) * 4) {
     const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
-    float x[N];
-    load_logits<T, N>(logits, e0, p.E, x);
     const int id = lane < p.k ? p.ids[row * p.k + lane] : -1;
     const bool used = id >= 0 && id < p.E;
     float d = used ? p.grad_weights[row * p.k + lane] * p.scale : 0.0f;
     const float xj = used ? to_float(logits[id]) : -kInf;
-    const Scores score = row_scores(x, p.sigmoid);
-    const float sj = used ? score(xj) : 0.0f;
+    float x[N];
+    load_row_of(logits, e0, p.E, x);
+    const Scores<SIGMOID> score(x);
+    float sj = score(xj);
+    sj = used ? sj : 0.0f;
     if (p.renorm) {
       // the sums take every lane: outside the choice of d
       const float total = wave_sum(sj) + kRenormEps;
       const float mean = wave_sum(d * sj) / total;
       d = used ? (d - mean) / total : 0.0f;
     }
-    const float dot = p.sigmoid ? 0.0f : wave_sum(sj * d);
+    const float dot = SIGMOID ? 0.0f : wave_sum(sj * d);
     float de[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) de[i] = 0.0f;
@@ -237,7 +334,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float s = score(x[i]);
-      g[i] = p.sigmoid ? s * (1.0f - s) * de[i] : s * (de[i] - dot);
+      g[i] = SIGMOID ? s * (1.0f - s) * de[i] : s * (de[i] - dot);
     }
     struct __attribute__((packed, aligned(sizeof(T)))) At {
       T v[N];
@@ -258,44 +355,50 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
 // Workgroups of four tokens, which take further tokens in turns past this.
 dim3 token_grid(int64_t T) {
   const int64_t blocks = (T + 3) / 4;
-  return dim3(unsigned(blocks < (1 << 20) ? blocks : (1 << 20)));
+  return dim3(unsigned(blocks < 4096 ? blocks : 4096));
 }
 
-template <typename T, int N>
+template <int N, bool SIGMOID>
 hipError_t run_route(const RouteProblem& p, hipStream_t st) {
-  const size_t lds = p.group_topk < p.groups ? size_t(4) * p.E * sizeof(float) : 0;
-  if (p.bias)
-    hipLaunchKernelGGL((route_kernel<T, N, true>), token_grid(p.T), dim3(256), lds, st, p);
-  else
-    hipLaunchKernelGGL((route_kernel<T, N, false>), token_grid(p.T), dim3(256), lds, st, p);
-  return hipGetLastError();
+  const bool groups = p.group_topk < p.groups;
+  const Groups g(p, N);
+  const auto run = [&](auto kernel) {
+    const size_t lds = groups && !g.whole ? size_t(4) * p.E * sizeof(float) : 0;
+    hipLaunchKernelGGL(kernel, token_grid(p.T), dim3(256), lds, st, p, g);
+    return hipGetLastError();
+  };
+  if (p.bias) return groups ? run(route_kernel<N, SIGMOID, true, true>) : run(route_kernel<N, SIGMOID, true, false>);
+  return groups ? run(route_kernel<N, SIGMOID, false, true>) : run(route_kernel<N, SIGMOID, false, false>);
 }
 
-template <typename T, int N>
+template <int N, bool SIGMOID>
 hipError_t run_route_backward(const RouteProblem& p, hipStream_t st) {
-  hipLaunchKernelGGL((route_backward_kernel<T, N>), token_grid(p.T), dim3(256), 0, st, p);
+  if (p.fp32)
+    hipLaunchKernelGGL((route_backward_kernel<float, N, SIGMOID>), token_grid(p.T), dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((route_backward_kernel<uint16_t, N, SIGMOID>), token_grid(p.T), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t route_typed(const RouteProblem& p, bool backward, hipStream_t st) {
-  if (p.E <= 64) return backward ? run_route_backward<T, 1>(p, st) : run_route<T, 1>(p, st);
-  if (p.E <= 128) return backward ? run_route_backward<T, 2>(p, st) : run_route<T, 2>(p, st);
-  if (p.E <= 256) return backward ? run_route_backward<T, 4>(p, st) : run_route<T, 4>(p, st);
-  if (p.E <= 512) return backward ? run_route_backward<T, 8>(p, st) : run_route<T, 8>(p, st);
-  return backward ? run_route_backward<T, 16>(p, st) : run_route<T, 16>(p, st);
+template <int N>
+hipError_t route_of(const RouteProblem& p, bool backward, hipStream_t st) {
+  if (backward) return p.sigmoid ? run_route_backward<N, true>(p, st) : run_route_backward<N, false>(p, st);
+  return p.sigmoid ? run_route<N, true>(p, st) : run_route<N, false>(p, st);
+}
+
+hipError_t route_any(const RouteProblem& p, bool backward, hipStream_t st) {
+  if (p.T == 0) return hipSuccess;
+  if (p.E <= 64) return route_of<1>(p, backward, st);
+  if (p.E <= 128) return route_of<2>(p, backward, st);
+  if (p.E <= 256) return route_of<4>(p, backward, st);
+  if (p.E <= 512) return route_of<8>(p, backward, st);
+  return route_of<16>(p, backward, st);
 }
 
 }  // namespace
 
-hipError_t launch_route(const RouteProblem& p, hipStream_t st) {
-  if (p.T == 0) return hipSuccess;
-  return p.fp32 ? route_typed<float>(p, false, st) : route_typed<uint16_t>(p, false, st);
-}
+hipError_t launch_route(const RouteProblem& p, hipStream_t st) { return route_any(p, false, st); }
 
-hipError_t launch_route_backward(const RouteProblem& p, hipStream_t st) {
-  if (p.T == 0) return hipSuccess;
-  return p.fp32 ? route_typed<float>(p, true, st) : route_typed<uint16_t>(p, true, st);
-}
+hipError_t launch_route_backward(const RouteProblem& p, hipStream_t st) { return route_any(p, true, st); }
 
 }  // namespace fp8mm
