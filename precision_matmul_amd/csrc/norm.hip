@@ -395,9 +395,7 @@ constexpr int64_t kRegisterCols = 8192; // longest row kept in registers
 // Workgroups of the row kernels, which take further rows in turns past this.
 dim3 row_grid(int64_t blocks) { return dim3(unsigned(blocks < (1 << 20) ? blocks : (1 << 20))); }
 
-// Whether the result is larger than the L2s together (8 x 4 MiB): then no next
-// kernel finds it there, and streaming stores leave the L2s to the inputs.
-bool streams(const NormProblem& p, size_t size) { return p.R * p.C * int64_t(size) > (int64_t(32) << 20); }
+bool streams(const NormProblem& p, size_t size) { return p.R * p.C * int64_t(size) > kL2Bytes; }
 
 // Workgroups of the backward (one partial row each): as many as run at once.
 int backward_grid(int64_t R, int64_t C, int vec) {

@@ -38,7 +38,10 @@ __device__ __forceinline__ void store_chunk(T* p, const Chunk& v) {
   *reinterpret_cast<ChunkAt<T>*>(p) = ChunkAt<T>{{v.w[0], v.w[1], v.w[2], v.w[3]}};
 }
 
-// Streaming store, for results larger than the L2s together hold.
+// The eight L2s together.  A result larger than this is not found there by the
+// next kernel: it goes out by streaming stores, which leave the L2s to inputs.
+constexpr int64_t kL2Bytes = int64_t(32) << 20;
+
 template <typename T>
 __device__ __forceinline__ void store_chunk_nt(T* p, const Chunk& v) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));

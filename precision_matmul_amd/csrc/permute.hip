@@ -26,72 +26,78 @@ using namespace ops;
 // depend on the order of the LDS atomics.  One chunk alone needs no first
 // launch.  Latency-bound: 8 bytes a slot.
 // ---------------------------------------------------------------------------
-constexpr int kPlanSingle = 4096;    // slots that one workgroup places alone
-constexpr int kPlanChunks = 128;     // chunks at most: the second launch reads all their counts
+constexpr int64_t kPlanSingle = 4096;    // slots that one workgroup places alone
+constexpr int64_t kPlanChunks = 64;      // chunks at most: the second launch reads all their counts
 
+// A slot's key: its expert, or E without one.
 __device__ __forceinline__ int plan_key(int32_t id, int E) { return id >= 0 && id < E ? id : E; }
 
-// Counts of the wave's slots [a, b) into cnt (LDS, this wave's own).
-__device__ __forceinline__ void count_slots(const int32_t* ids, int64_t a, int64_t b, int E, int* cnt) {
-  for (int64_t n = a + (threadIdx.x & 63); n < b; n += 64) atomicAdd(&cnt[plan_key(ids[n], E)], 1);
-}
-
-__global__ __launch_bounds__(256) void plan_count_kernel(const int32_t* __restrict__ ids, int64_t n, int chunk, int E,
-                                                         int* __restrict__ hist) {
+__global__ __launch_bounds__(1024) void plan_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk,
+                                                          int E, int* __restrict__ hist) {
   extern __shared__ int cnt[];         // [E + 1]
-  for (int e = threadIdx.x; e <= E; e += 256) cnt[e] = 0;
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
   const int64_t c0 = int64_t(blockIdx.x) * chunk;
   const int64_t end = min(n, c0 + chunk);
-  for (int64_t i = c0 + threadIdx.x; i < end; i += 256) atomicAdd(&cnt[plan_key(ids[i], E)], 1);
+  for (int64_t i = c0 + threadIdx.x; i < end; i += blockDim.x) atomicAdd(&cnt[plan_key(ids[i], E)], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += 256) hist[int64_t(blockIdx.x) * (E + 1) + e] = cnt[e];
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) hist[int64_t(blockIdx.x) * (E + 1) + e] = cnt[e];
 }
 
-// LDS: cnt [4][E + 1] counts, then places, of the four waves; total [E + 1].
-__global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restrict__ ids, int64_t n, int chunk, int E,
-                                                         int bits, const int* __restrict__ hist,
-                                                         int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {
+// W waves a workgroup.  LDS: cnt [W][E + 1] counts, then places, of each wave;
+// total and before [E + 1] slots of an expert in all chunks and in the earlier
+// ones.
+template <int W>
+__global__ __launch_bounds__(64 * W) void plan_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk,
+                                                          int E, int bits, const int* __restrict__ hist,
+                                                          int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {
   extern __shared__ int lds[];
-  __shared__ int wave_total[4];
+  __shared__ int wave_total[W];
+  constexpr int threads = 64 * W;
   const int E1 = E + 1;
-  int* total = lds + 4 * E1;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   int* cnt = lds + wave * E1;
-  for (int i = t; i < 4 * E1; i += 256) lds[i] = 0;
+  int* total = lds + W * E1;
+  int* before = total + E1;
+  for (int i = t; i < (W + 2) * E1; i += threads) lds[i] = 0;
+  const int64_t part = chunk / W;
+  const int64_t a = min(n, int64_t(blockIdx.x) * chunk + int64_t(wave) * part);
+  const int64_t b = min(n, a + part);
   __syncthreads();
-  const int64_t c0 = int64_t(blockIdx.x) * chunk;
-  const int quarter = chunk / 4;
-  const int64_t a = min(n, c0 + int64_t(wave) * quarter);
-  const int64_t b = min(n, a + quarter);
-  count_slots(ids, a, b, E, cnt);
-  __syncthreads();
-  // before: slots of expert e in earlier chunks; total: in all chunks
-  for (int e = t; e < E1; e += 256) {
-    int before = 0, all = 0;
-    if (hist) {
-#pragma unroll 8
-      for (int c = 0; c < int(gridDim.x); ++c) {
+  for (int64_t i = a + lane; i < b; i += 64) atomicAdd(&cnt[plan_key(ids[i], E)], 1);
+  if (hist) {
+    // the chunks dealt out to threads / E1 threads an expert
+    const int sets = max(1, threads / E1);
+    for (int i = t; i < sets * E1; i += threads) {
+      const int set = i / E1, e = i - set * E1;
+      int all = 0, early = 0;
+#pragma unroll 4
+      for (int c = set; c < int(gridDim.x); c += sets) {
         const int h = hist[int64_t(c) * E1 + e];
         all += h;
-        before += c < int(blockIdx.x) ? h : 0;
+        early += c < int(blockIdx.x) ? h : 0;
       }
-    } else {
-      all = lds[e] + lds[E1 + e] + lds[2 * E1 + e] + lds[3 * E1 + e];
-    }
-    total[e] = all;
-    // the waves' first places relative to the expert's first row
-    int at = before;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int h = lds[w * E1 + e];
-      lds[w * E1 + e] = at;
-      at += h;
+      atomicAdd(&total[e], all);
+      atomicAdd(&before[e], early);
     }
   }
   __syncthreads();
+  for (int e = t; e < E1; e += threads) {
+    int at = before[e];
+    // the waves' first places relative to the expert's first row
+    int h[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) h[w] = lds[w * E1 + e];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      lds[w * E1 + e] = at;
+      at += h[w];
+    }
+    if (!hist) total[e] = at;
+  }
+  __syncthreads();
   // exclusive scan of total: thread t owns `per` consecutive experts
-  const int per = (E1 + 255) / 256;
+  const int per = (E1 + threads - 1) / threads;
   const int s0 = min(E1, t * per), s1 = min(E1, s0 + per);
   int sum = 0;
   for (int e = s0; e < s1; ++e) sum += total[e];
@@ -104,10 +110,10 @@ __global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restri
   if (lane == 63) wave_total[wave] = incl;
   __syncthreads();
   int start = incl - sum;
-  for (int w = 0; w < wave; ++w) start += wave_total[w];
-  for (int e = s0; e < s1; ++e) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) lds[w * E1 + e] += start;
+  for (int w = 0; w < W; ++w) start += w < wave ? wave_total[w] : 0;
+  for (int e = s0; e < s1; ++e) {
+    before[e] = start;                 // from here on: the expert's first row
     start += total[e];
     if (blockIdx.x == 0 && e < E) offsets[e] = start;
   }
@@ -124,7 +130,7 @@ __global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restri
     }
     const uint64_t lower = peers & ((1ull << lane) - 1);
     if (here) {
-      const int row = cnt[key] + __popcll(lower);
+      const int row = before[key] + cnt[key] + __popcll(lower);
       rows[i] = key == E ? ~row : row;
     }
     // every lane has read its expert's place before its last peer moves it on
@@ -136,8 +142,8 @@ __global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restri
 
 // This wave's item: the host keeps items below 2^26 (a launch's threads below
 // 2^32), and one item is a wave's, so its arithmetic is scalar and 32-bit.
-__device__ __forceinline__ uint32_t wave_item() {
-  return uint32_t(__builtin_amdgcn_readfirstlane(int(xcd_position() * 4 + (threadIdx.x >> 6))));
+__device__ __forceinline__ uint32_t wave_item(uint32_t workgroup) {
+  return uint32_t(__builtin_amdgcn_readfirstlane(int(workgroup * 4 + (threadIdx.x >> 6))));
 }
 
 struct Slot {
@@ -154,7 +160,7 @@ __device__ __forceinline__ Slot slot_row(int32_t v) { return Slot{int64_t(v < 0 
 template <typename T>
 __global__ __launch_bounds__(256) void dispatch_kernel(const PermuteProblem p, int strips) {
   const int lane = threadIdx.x & 63;
-  const uint32_t item = wave_item();
+  const uint32_t item = wave_item(blockIdx.x);
   const uint32_t token = item / uint32_t(strips);
   if (token >= p.T) return;
   const int64_t c = (int64_t(item - token * uint32_t(strips)) * 64 + lane) * kVec<T>;
@@ -169,9 +175,10 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const PermuteProblem p, i
 
 // FP8: a wave covers 1024 columns of one token, 16 consecutive ones a lane, 8
 // lanes a group of 128; codes and scales as the 1x128 quantizer makes them.
+template <bool NT>
 __global__ __launch_bounds__(256) void dispatch_fp8_kernel(const PermuteProblem p, int strips) {
   const int lane = threadIdx.x & 63;
-  const uint32_t item = wave_item();
+  const uint32_t item = wave_item(xcd_position());
   const uint32_t token = item / uint32_t(strips);
   if (token >= p.T) return;
   const int64_t c = (int64_t(item - token * uint32_t(strips)) * 64 + lane) * 16;
@@ -183,11 +190,13 @@ __global__ __launch_bounds__(256) void dispatch_fp8_kernel(const PermuteProblem 
   const float s = scale_from_amax(bf16_to_f32(uint16_t(m)), 0.0f, false);
   const CastScale cs = make_cast_scale(s);
   const uint2 q0 = cast8(v0, cs), q1 = cast8(v1, cs);
-  const uint4 q = make_uint4(q0.x, q0.y, q1.x, q1.y);
+  const Chunk q{{q0.x, q0.y, q1.x, q1.y}};
   for (int j = 0; j < p.k; ++j) {
     const Slot slot = slot_row(p.row_of_slot[int64_t(token) * p.k + j]);
     if (slot.row >= M) continue;
-    *reinterpret_cast<uint4*>(p.q + slot.row * p.ld_q + c) = slot.used ? q : make_uint4(0u, 0u, 0u, 0u);
+    const Chunk codes = slot.used ? q : Chunk{{0u, 0u, 0u, 0u}};
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.q + slot.row * p.ld_q + c);
+    NT ? store_chunk_nt(out, codes) : store_chunk(out, codes);
     if ((lane & 7) == 0) p.scale[(c / 128) * M + slot.row] = slot.used ? s : 1.0f;
   }
 }
@@ -200,7 +209,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, int strips) {
   constexpr int V = kVec<T>;
   const int lane = threadIdx.x & 63;
-  const uint32_t item = wave_item();
+  const uint32_t item = wave_item(blockIdx.x);
   const uint32_t token = item / uint32_t(strips);
   if (token >= p.T) return;
   const int64_t c = (int64_t(item - token * uint32_t(strips)) * 64 + lane) * V;
@@ -228,7 +237,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProb
   constexpr int V = kVec<T>;
   constexpr int U = 4;                   // chunks a lane holds of the gradient
   const int lane = threadIdx.x & 63;
-  const uint32_t token = wave_item();
+  const uint32_t token = wave_item(blockIdx.x);
   if (token >= p.T) return;
   const int64_t M = p.T * p.k;
   const T* g_row = static_cast<const T*>(p.x) + int64_t(token) * p.ld_x;
@@ -269,10 +278,9 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProb
   if (p.grad_weights && lane < p.k) p.grad_weights[int64_t(token) * p.k + lane] = dots;
 }
 
-int plan_chunk(int64_t n) {
-  if (n <= kPlanSingle) return int((n + 255) / 256 * 256);
-  const int64_t c = (n + kPlanChunks - 1) / kPlanChunks;
-  return int((c + 1023) / 1024 * 1024);
+int64_t plan_chunk(int64_t n) {
+  const int64_t c = n <= kPlanSingle ? n : (n + kPlanChunks - 1) / kPlanChunks;
+  return (c + 1023) / 1024 * 1024;
 }
 
 }  // namespace
@@ -285,25 +293,31 @@ int64_t plan_workspace(int64_t n, int64_t E) {
 
 hipError_t launch_plan(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* row_of_slot,
                        int32_t* workspace, hipStream_t st) {
-  const int chunk = n ? plan_chunk(n) : 256;
-  const unsigned chunks = unsigned(n ? (n + chunk - 1) / chunk : 1);
   const bool single = n <= kPlanSingle;
+  const int64_t chunk = n ? plan_chunk(n) : 1024;
+  const unsigned chunks = unsigned(n ? (n + chunk - 1) / chunk : 1);
   if (!single) {
-    hipLaunchKernelGGL(plan_count_kernel, dim3(chunks), dim3(256), size_t(E + 1) * 4, st, ids, n, chunk, E, workspace);
+    hipLaunchKernelGGL(plan_count_kernel, dim3(chunks), dim3(1024), size_t(E + 1) * 4, st, ids, n, chunk, E, workspace);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const int bits = 32 - __builtin_clz(unsigned(E));    // of keys 0 .. E
-  hipLaunchKernelGGL(plan_place_kernel, dim3(chunks), dim3(256), size_t(5) * (E + 1) * 4, st, ids, n, chunk, E, bits,
-                     single ? nullptr : workspace, offsets, row_of_slot);
-  return hipGetLastError();
+  const auto place = [&](auto kernel, int W) {
+    hipLaunchKernelGGL(kernel, dim3(chunks), dim3(64 * W), size_t(W + 2) * (E + 1) * 4, st, ids, n, chunk, E, bits,
+                       single ? nullptr : workspace, offsets, row_of_slot);
+    return hipGetLastError();
+  };
+  // waves that share a chunk: fewer for few slots, and where their counts in
+  // LDS would pass 64 KiB
+  if (n <= 512) return place(plan_place_kernel<4>, 4);
+  return E > 512 ? place(plan_place_kernel<8>, 8) : place(plan_place_kernel<16>, 16);
 }
 
 hipError_t launch_dispatch(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0 || p.C == 0) return hipSuccess;
   const int vec = p.fp32 ? 4 : 8;
   const int strips = int((p.C + 64 * vec - 1) / (64 * vec));
-  const dim3 grid(xcd_grid((p.T * strips + 3) / 4));
+  const dim3 grid(unsigned((p.T * strips + 3) / 4));
   if (p.fp32)
     hipLaunchKernelGGL((dispatch_kernel<float>), grid, dim3(256), 0, st, p, strips);
   else
@@ -314,7 +328,11 @@ hipError_t launch_dispatch(const PermuteProblem& p, hipStream_t st) {
 hipError_t launch_dispatch_fp8(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0 || p.C == 0) return hipSuccess;
   const int strips = int((p.C + 1023) / 1024);
-  hipLaunchKernelGGL(dispatch_fp8_kernel, dim3(xcd_grid((p.T * strips + 3) / 4)), dim3(256), 0, st, p, strips);
+  const dim3 grid(xcd_grid((p.T * strips + 3) / 4));
+  if (p.T * p.k * p.C > kL2Bytes)
+    hipLaunchKernelGGL((dispatch_fp8_kernel<true>), grid, dim3(256), 0, st, p, strips);
+  else
+    hipLaunchKernelGGL((dispatch_fp8_kernel<false>), grid, dim3(256), 0, st, p, strips);
   return hipGetLastError();
 }
 
@@ -322,7 +340,7 @@ hipError_t launch_combine(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0 || p.C == 0) return hipSuccess;
   const int vec = p.fp32 ? 4 : 8;
   const int strips = int((p.C + 64 * vec - 1) / (64 * vec));
-  const dim3 grid(xcd_grid((p.T * strips + 3) / 4));
+  const dim3 grid(unsigned((p.T * strips + 3) / 4));
   if (p.fp32)
     hipLaunchKernelGGL((combine_kernel<float>), grid, dim3(256), 0, st, p, strips);
   else
@@ -332,7 +350,7 @@ hipError_t launch_combine(const PermuteProblem& p, hipStream_t st) {
 
 hipError_t launch_combine_backward(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  const dim3 grid(xcd_grid((p.T + 3) / 4));
+  const dim3 grid(unsigned((p.T + 3) / 4));
   if (p.fp32)
     hipLaunchKernelGGL((combine_backward_kernel<float>), grid, dim3(256), 0, st, p);
   else

@@ -10,9 +10,17 @@
 //     d_gate = d_h up' sig (1 + gate' (1 - sig)),  d_up = d_h gate' sig
 //     and h again, for the weight gradient of the second product
 //
-// HBM-bound.  A thread holds 16 consecutive columns of one row's gate and up,
-// 8 lanes a group of 128; a workgroup holds 32 rows of one column block, so
-// that a block's 32 scales are one contiguous 128-byte store ([blocks, R]).
+// HBM-bound.  8 lanes hold a group of 128 columns of one row's gate and up, lane
+// l columns 8 l .. and 64 + 8 l .., so that every load and store of theirs is
+// one contiguous piece (16 neighbouring columns a lane leave holes in each
+// 16-byte store: the backward took 274 us against 240, and 640 with streaming
+// stores, which write the holes' lines twice).  A workgroup holds 32 rows of one
+// column block, so that a block's 32 scales are one contiguous 128-byte store
+// ([blocks, R]); the column blocks of the same rows follow each other.  Results
+// larger than the L2s go out by streaming stores.
+// 98304 x 1408: forward with codes and checkpoint 176 us, 5.6 TB/s; backward
+// with the activation again 233 us, 6.0 TB/s (rows before column blocks 304 us,
+// a contiguous range of workgroups an XCD 254, plain stores 240).
 #include "moe_launch.hpp"
 #include "ops_common.hpp"
 #include "quant_cast.hpp"
@@ -28,14 +36,35 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
 }
 
-__device__ __forceinline__ uint4 codes16(const uint2& a, const uint2& b) { return make_uint4(a.x, a.y, b.x, b.y); }
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// 1x128 quantization of a thread's 16 bf16 values.
+// A lane's two pieces of 8 codes; of 8 bf16 values.
+template <bool NT>
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint2& a, const uint2& b) {
+  u32x2* at = reinterpret_cast<u32x2*>(p);
+  const u32x2 va = {a.x, a.y}, vb = {b.x, b.y};
+  if constexpr (NT) {
+    __builtin_nontemporal_store(va, at);
+    __builtin_nontemporal_store(vb, at + 8);
+  } else {
+    at[0] = va;
+    at[8] = vb;
+  }
+}
+
+template <bool NT>
+__device__ __forceinline__ void store8_bf16(uint16_t* p, const float (&f)[8]) {
+  uint32_t* at = reinterpret_cast<uint32_t*>(p);
+  NT ? store_chunk_nt(at, pack<uint16_t>(f)) : store_chunk(at, pack<uint16_t>(f));
+}
+
+// 1x128 quantization of a lane's 16 bf16 values.
+template <bool NT>
 __device__ __forceinline__ void quantize16(const U16x8& v0, const U16x8& v1, uint8_t* q, float* scale, bool first) {
   const uint32_t m = group8_max(max(absmax8(v0), absmax8(v1)));
   const float s = scale_from_amax(bf16_to_f32(uint16_t(m)), 0.0f, false);
   const CastScale cs = make_cast_scale(s);
-  *reinterpret_cast<uint4*>(q) = codes16(cast8(v0, cs), cast8(v1, cs));
+  store_codes<NT>(q, cast8(v0, cs), cast8(v1, cs));
   if (first) *scale = s;
 }
 
@@ -46,25 +75,21 @@ __device__ __forceinline__ uint2 cast8_f32(const float (&x)[8], const CastScale&
   return make_uint2(pack4(y, x), pack4(y + 4, x + 4));
 }
 
-__device__ __forceinline__ void store8_bf16(uint16_t* p, const float (&f)[8]) {
-  store_chunk<uint32_t>(reinterpret_cast<uint32_t*>(p), pack<uint16_t>(f));
-}
-
-template <bool H, bool HQ, bool CKPT>
+template <bool H, bool HQ, bool CKPT, bool NT>
 __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluProblem p, int blocks) {
   const int t = threadIdx.x;
   const int64_t rb = blockIdx.x / unsigned(blocks);
   const int kb = int(blockIdx.x - rb * blocks);
   const int64_t row = rb * 32 + (t >> 3);
   if (row >= p.R) return;                // whole groups of 8 lanes leave
-  const int64_t c = int64_t(kb) * 128 + (t & 7) * 16;
+  const int64_t c = int64_t(kb) * 128 + (t & 7) * 8;
   const bool first = (t & 7) == 0;
   const uint16_t* x = p.x + row * p.ld_x + c;
-  const U16x8 g0 = load16(x), g1 = load16(x + 8), u0 = load16(x + p.F), u1 = load16(x + p.F + 8);
+  const U16x8 g0 = load16(x), g1 = load16(x + 64), u0 = load16(x + p.F), u1 = load16(x + p.F + 64);
   if constexpr (CKPT) {
     uint8_t* q = p.ckpt + row * p.ld_ckpt + c;
-    quantize16(g0, g1, q, p.ckpt_scale + int64_t(kb) * p.R + row, first);
-    quantize16(u0, u1, q + p.F, p.ckpt_scale + (int64_t(kb) + p.F / 128) * p.R + row, first);
+    quantize16<NT>(g0, g1, q, p.ckpt_scale + int64_t(kb) * p.R + row, first);
+    quantize16<NT>(u0, u1, q + p.F, p.ckpt_scale + (int64_t(kb) + p.F / 128) * p.R + row, first);
   }
   float g[2][8], u[2][8];
   unpack8(g0, g[0]);
@@ -77,8 +102,8 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluProblem p, int 
     for (int i = 0; i < 8; ++i) g[a][i] = g[a][i] * fast_sigmoid(g[a][i]) * u[a][i];
   if constexpr (H) {
     uint16_t* h = p.h + row * p.ld_h + c;
-    store8_bf16(h, g[0]);
-    store8_bf16(h + 8, g[1]);
+    store8_bf16<NT>(h, g[0]);
+    store8_bf16<NT>(h + 64, g[1]);
   }
   if constexpr (HQ) {
     uint32_t m = 0;                      // |h| orders like its bits; NaN above everything
@@ -89,7 +114,7 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluProblem p, int 
     m = group8_max(m);
     const float s = scale_from_amax(__uint_as_float(m), 0.0f, false);
     const CastScale cs = make_cast_scale(s);
-    *reinterpret_cast<uint4*>(p.h_q + row * p.ld_hq + c) = codes16(cast8_f32(g[0], cs), cast8_f32(g[1], cs));
+    store_codes<NT>(p.h_q + row * p.ld_hq + c, cast8_f32(g[0], cs), cast8_f32(g[1], cs));
     if (first) p.h_scale[int64_t(kb) * p.R + row] = s;
   }
 }
@@ -107,27 +132,28 @@ __device__ __forceinline__ void decode8(uint32_t lo, uint32_t hi, float s, float
   }
 }
 
-template <bool H>
+template <bool H, bool NT>
 __global__ __launch_bounds__(256) void swiglu_backward_kernel(const SwigluProblem p, int blocks) {
   const int t = threadIdx.x;
   const int64_t rb = blockIdx.x / unsigned(blocks);
   const int kb = int(blockIdx.x - rb * blocks);
   const int64_t row = rb * 32 + (t >> 3);
   if (row >= p.R) return;
-  const int64_t c = int64_t(kb) * 128 + (t & 7) * 16;
+  const int64_t c = int64_t(kb) * 128 + (t & 7) * 8;
   const uint8_t* q = p.ckpt + row * p.ld_ckpt + c;
-  const uint4 qg = *reinterpret_cast<const uint4*>(q), qu = *reinterpret_cast<const uint4*>(q + p.F);
+  const uint2 qg[2] = {*reinterpret_cast<const uint2*>(q), *reinterpret_cast<const uint2*>(q + 64)};
+  const uint2 qu[2] = {*reinterpret_cast<const uint2*>(q + p.F), *reinterpret_cast<const uint2*>(q + p.F + 64)};
   const float sg = p.ckpt_scale[int64_t(kb) * p.R + row];
   const float su = p.ckpt_scale[(int64_t(kb) + p.F / 128) * p.R + row];
   const uint16_t* gh = p.grad_h + row * p.ld_gh + c;
-  const U16x8 d0 = load16(gh), d1 = load16(gh + 8);
+  const U16x8 dv[2] = {load16(gh), load16(gh + 64)};
   uint16_t* gx = p.grad_x + row * p.ld_gx + c;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
     float g[8], u[8], d[8], h[8];
-    decode8(a ? qg.z : qg.x, a ? qg.w : qg.y, sg, g);
-    decode8(a ? qu.z : qu.x, a ? qu.w : qu.y, su, u);
-    unpack8(a ? d1 : d0, d);
+    decode8(qg[a].x, qg[a].y, sg, g);
+    decode8(qu[a].x, qu[a].y, su, u);
+    unpack8(dv[a], d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float sig = fast_sigmoid(g[i]);
@@ -136,18 +162,32 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const SwigluProble
       g[i] = d[i] * u[i] * (sig + silu * (1.0f - sig));
       u[i] = d[i] * silu;
     }
-    store8_bf16(gx + 8 * a, g);
-    store8_bf16(gx + p.F + 8 * a, u);
-    if constexpr (H) store8_bf16(p.h + row * p.ld_h + c + 8 * a, h);
+    store8_bf16<NT>(gx + 64 * a, g);
+    store8_bf16<NT>(gx + p.F + 64 * a, u);
+    if constexpr (H) store8_bf16<NT>(p.h + row * p.ld_h + c + 64 * a, h);
   }
 }
 
+int64_t workgroups(const SwigluProblem& p) { return (p.R + 31) / 32 * (p.F / 128); }
+
 template <bool H, bool HQ, bool CKPT>
 hipError_t run_swiglu(const SwigluProblem& p, hipStream_t st) {
-  const int blocks = int(p.F / 128);
-  hipLaunchKernelGGL((swiglu_kernel<H, HQ, CKPT>), dim3(unsigned((p.R + 31) / 32 * blocks)), dim3(256), 0, st, p,
-                     blocks);
-  return hipGetLastError();
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned(workgroups(p))), dim3(256), 0, st, p, int(p.F / 128));
+    return hipGetLastError();
+  };
+  const int64_t bytes = p.R * p.F * (H ? 2 : 0) + p.R * p.F * (HQ ? 1 : 0) + p.R * p.F * (CKPT ? 2 : 0);
+  return bytes > kL2Bytes ? run(swiglu_kernel<H, HQ, CKPT, true>) : run(swiglu_kernel<H, HQ, CKPT, false>);
+}
+
+template <bool H>
+hipError_t run_swiglu_backward(const SwigluProblem& p, hipStream_t st) {
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned(workgroups(p))), dim3(256), 0, st, p, int(p.F / 128));
+    return hipGetLastError();
+  };
+  const int64_t bytes = p.R * p.F * (H ? 6 : 4);
+  return bytes > kL2Bytes ? run(swiglu_backward_kernel<H, true>) : run(swiglu_backward_kernel<H, false>);
 }
 
 }  // namespace
@@ -169,13 +209,7 @@ hipError_t launch_swiglu(const SwigluProblem& p, hipStream_t st) {
 
 hipError_t launch_swiglu_backward(const SwigluProblem& p, hipStream_t st) {
   if (p.R == 0 || p.F == 0) return hipSuccess;
-  const int blocks = int(p.F / 128);
-  const dim3 grid(unsigned((p.R + 31) / 32 * blocks));
-  if (p.h)
-    hipLaunchKernelGGL((swiglu_backward_kernel<true>), grid, dim3(256), 0, st, p, blocks);
-  else
-    hipLaunchKernelGGL((swiglu_backward_kernel<false>), grid, dim3(256), 0, st, p, blocks);
-  return hipGetLastError();
+  return p.h ? run_swiglu_backward<true>(p, st) : run_swiglu_backward<false>(p, st);
 }
 
 }  // namespace fp8mm
