@@ -44,7 +44,7 @@ fp8mm_status check_permute(fp8mm_dtype dtype, int64_t T, int64_t C, int64_t k, c
   if (T < 0 || C < 0 || k < 1) return fail(FP8MM_EINVAL, "need T >= 0, C >= 0 and k >= 1");
   if (k > fp8mm::kRouteMaxK) return fail(FP8MM_ENOTIMPL, "k (%lld) above %d", (long long)k, fp8mm::kRouteMaxK);
   if (T > kMaxInt / k || C > kMaxInt) return fail(FP8MM_EINVAL, "T k and C must be < 2^31");
-  if (T > kMaxWaves || T * ((C + 255) / 256) > kMaxWaves)
+  if (T * k > kMaxWaves || T * ((C + 255) / 256) > kMaxWaves)
     return fail(FP8MM_EINVAL, "[%lld, %lld] is too large for one launch", (long long)T, (long long)C);
   if (T > 0 && !row_of_slot) return fail(FP8MM_EINVAL, "row_of_slot must not be NULL");
   return FP8MM_OK;

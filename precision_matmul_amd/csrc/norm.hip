@@ -36,9 +36,10 @@ __device__ __forceinline__ float row_sum(float v, float (&part)[2][WPR], int slo
 // Forward, row in registers: WPR waves a row, NIT chunks a lane.  A workgroup
 // takes rows blockIdx, blockIdx + gridDim, ...; a lane's columns are the same
 // in all of them, so it keeps its parameters in registers, and the next row is
-// loaded while this one is reduced and written.  16640 x 5120 bf16: 61.5 us,
-// 5.5 TB/s, what a plain copy reaches (one row a workgroup, parameters read
-// again for each: 85 us; one wave a row: 102 us; plain stores: 66 us).
+// loaded while this one is reduced and written.  Results larger than the L2s
+// are read and written by streaming accesses (NT).  16640 x 5120 bf16: 60 us,
+// 5.6 TB/s, more than a plain copy reaches (one row a workgroup, parameters
+// read again for each: 85 us; one wave a row: 102 us; plain accesses: 66 us).
 // ---------------------------------------------------------------------------
 template <typename T, typename P, int WPR, int NIT, bool NT>
 __global__ __launch_bounds__(256) void norm_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld_x,
@@ -62,14 +63,14 @@ __global__ __launch_bounds__(256) void norm_kernel(const T* __restrict__ x, int6
   Chunk next[NIT];
 #pragma unroll
   for (int it = 0; it < NIT; ++it)
-    if (row < R) next[it] = load_row(x + row * ld_x, c0 + it * STEP, C);
+    if (row < R) next[it] = load_row<T, NT>(x + row * ld_x, c0 + it * STEP, C);
   for (; row < R; row += stride) {                // all waves of a row take the same turns
     Chunk v[NIT];
 #pragma unroll
     for (int it = 0; it < NIT; ++it) v[it] = next[it];
     if (row + stride < R) {
 #pragma unroll
-      for (int it = 0; it < NIT; ++it) next[it] = load_row(x + (row + stride) * ld_x, c0 + it * STEP, C);
+      for (int it = 0; it < NIT; ++it) next[it] = load_row<T, NT>(x + (row + stride) * ld_x, c0 + it * STEP, C);
     }
     float s = 0.0f;
 #pragma unroll
@@ -165,7 +166,7 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
 // workgroups than run at once: 256 of eight waves with a row each, or, above
 // 4 chunks a lane, 512 of four waves that share a row (256 above 12 chunks of
 // a wave, where the registers leave room for one workgroup a compute unit).
-// 16384 x 2048 bf16: 47 us with the column sums, 4.3 TB/s of x, dy and dx (512
+// 16384 x 2048 bf16: 45 us with the column sums, 4.5 TB/s of x, dy and dx (512
 // partial rows of eight-wave workgroups 56 us; no row in flight ahead 55 us);
 // 10000 x 5120: 72 us (1024 partial rows 88 us); 10000 x 8192: 99 us (512: 111).
 // ---------------------------------------------------------------------------
@@ -200,8 +201,8 @@ __global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward
   if (row < R) {
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
-      nx[it] = load_row(x + row * ld_x, c0 + it * STEP, C);
-      ng[it] = load_row(dy + row * ld_dy, c0 + it * STEP, C);
+      nx[it] = load_row<T, NT>(x + row * ld_x, c0 + it * STEP, C);
+      ng[it] = load_row<T, NT>(dy + row * ld_dy, c0 + it * STEP, C);
     }
     nmean = mean_in[row];
     nrstd = rstd_in[row];
@@ -217,8 +218,8 @@ __global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward
     if (row + stride < R) {
 #pragma unroll
       for (int it = 0; it < NIT; ++it) {
-        nx[it] = load_row(x + (row + stride) * ld_x, c0 + it * STEP, C);
-        ng[it] = load_row(dy + (row + stride) * ld_dy, c0 + it * STEP, C);
+        nx[it] = load_row<T, NT>(x + (row + stride) * ld_x, c0 + it * STEP, C);
+        ng[it] = load_row<T, NT>(dy + (row + stride) * ld_dy, c0 + it * STEP, C);
       }
       nmean = mean_in[row + stride];
       nrstd = rstd_in[row + stride];

@@ -49,6 +49,15 @@ __device__ __forceinline__ void store_chunk_nt(T* p, const Chunk& v) {
   __builtin_nontemporal_store(u32x4{v.w[0], v.w[1], v.w[2], v.w[3]}, reinterpret_cast<u32x4_at*>(p));
 }
 
+// Streaming load, of what is read once and is larger than the L2s.
+template <typename T>
+__device__ __forceinline__ Chunk load_chunk_nt(const T* p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  typedef u32x4 __attribute__((aligned(2))) u32x4_at;
+  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_at*>(p));
+  return Chunk{{v.x, v.y, v.z, v.w}};
+}
+
 // The first n < kVec<T> elements of a row's last chunk, zeros after them.
 template <typename T>
 __device__ __forceinline__ Chunk load_part(const T* p, int n) {
@@ -82,9 +91,9 @@ __device__ __forceinline__ void store_part(T* p, const Chunk& v, int n) {
 }
 
 // Chunk at column c of a row of C elements; zeros past the row.
-template <typename T>
+template <typename T, bool NT = false>
 __device__ __forceinline__ Chunk load_row(const T* row, int64_t c, int64_t C) {
-  if (c + kVec<T> <= C) return load_chunk(row + c);
+  if (c + kVec<T> <= C) return NT ? load_chunk_nt(row + c) : load_chunk(row + c);
   if (c < C) return load_part(row + c, int(C - c));
   return Chunk{{0u, 0u, 0u, 0u}};
 }

@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256) void dispatch_fp8_kernel(const PermuteProblem 
 // Combine: one wave an item of 64 chunks of one token; its k rows are added in
 // slot order in float32.  HBM-bound: (k + 1) rows a token.
 // ---------------------------------------------------------------------------
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, int strips) {
   constexpr int V = kVec<T>;
   const int lane = threadIdx.x & 63;
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, in
     if (!s.used || s.row >= M) continue;
     const float w = p.weights ? p.weights[int64_t(token) * p.k + j] : 1.0f;
     float f[V];
-    unpack<T>(load_row(static_cast<const T*>(p.rows) + s.row * p.ld_rows, c, p.C), f);
+    unpack<T>(load_row<T, NT>(static_cast<const T*>(p.rows) + s.row * p.ld_rows, c, p.C), f);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] += w * f[i];
   }
@@ -231,51 +231,49 @@ __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, in
 }
 
 // Combine's backward: grad_rows[row] = w g, grad_weights[t, j] = <g, rows[row]>.
-// One wave a token; slot j's dot product is kept by lane j.
-template <typename T>
+// One wave a slot, four chunks a lane in flight: a token's k waves are
+// neighbours and share its gradient through the caches.  HBM-bound: (1 + 2 k)
+// rows a token.  16384 x 2048, k = 6: 156 us, 5.6 TB/s (one wave a token, which
+// reads the gradient once: 160 us, and 27 against 10 us for 64 tokens of 5120
+// columns; without streaming loads 172 us).
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProblem p) {
   constexpr int V = kVec<T>;
-  constexpr int U = 4;                   // chunks a lane holds of the gradient
+  constexpr int U = 4;
   const int lane = threadIdx.x & 63;
-  const uint32_t token = wave_item(blockIdx.x);
-  if (token >= p.T) return;
+  const uint32_t slot = wave_item(blockIdx.x);
   const int64_t M = p.T * p.k;
+  if (slot >= M) return;
+  const uint32_t token = slot / uint32_t(p.k);
   const T* g_row = static_cast<const T*>(p.x) + int64_t(token) * p.ld_x;
-  float dots = 0.0f;
-  for (int64_t c0 = int64_t(lane) * V; c0 < (p.C + 64 * V - 1) / (64 * V) * (64 * V); c0 += 64 * V * U) {
-    float g[U][V];
+  const Slot s = slot_row(p.row_of_slot[slot]);
+  const bool inside = s.row < M;
+  const float w = p.weights && s.used ? p.weights[slot] : 1.0f;
+  const T* r = s.used && inside && p.grad_weights ? static_cast<const T*>(p.rows) + s.row * p.ld_rows : nullptr;
+  T* o = inside && p.out ? static_cast<T*>(p.out) + s.row * p.ld_out : nullptr;
+  float dot = 0.0f;
+  for (int64_t c0 = int64_t(lane) * V; c0 < p.C; c0 += 64 * V * U) {
+    Chunk vg[U], vr[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) unpack<T>(load_row(g_row, c0 + u * 64 * V, p.C), g[u]);
-    for (int j = 0; j < p.k; ++j) {
-      const Slot s = slot_row(p.row_of_slot[int64_t(token) * p.k + j]);
-      if (s.row >= M) continue;
-      const float w = p.weights ? p.weights[int64_t(token) * p.k + j] : 1.0f;
-      float dot = 0.0f;
-      if (s.used && p.grad_weights) {
-        const T* r = static_cast<const T*>(p.rows) + s.row * p.ld_rows;
+    for (int u = 0; u < U; ++u) {
+      vg[u] = load_row(g_row, c0 + u * 64 * V, p.C);
+      vr[u] = r ? load_row<T, NT>(r, c0 + u * 64 * V, p.C) : Chunk{{0u, 0u, 0u, 0u}};
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float f[V];
-          unpack<T>(load_row(r, c0 + u * 64 * V, p.C), f);
+    for (int u = 0; u < U; ++u) {
+      float g[V], f[V];
+      unpack<T>(vg[u], g);
+      unpack<T>(vr[u], f);
 #pragma unroll
-          for (int i = 0; i < V; ++i) dot += g[u][i] * f[i];
-        }
-        dot = wave_sum(dot);
+      for (int i = 0; i < V; ++i) {
+        if (r) dot += g[i] * f[i];
+        f[i] = s.used ? w * g[i] : 0.0f;
       }
-      dots += lane == j ? dot : 0.0f;
-      if (p.out) {
-        T* o = static_cast<T*>(p.out) + s.row * p.ld_out;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float f[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) f[i] = s.used ? w * g[u][i] : 0.0f;
-          store_row(o, c0 + u * 64 * V, p.C, pack<T>(f));
-        }
-      }
+      if (o) store_row(o, c0 + u * 64 * V, p.C, pack<T>(f));
     }
   }
-  if (p.grad_weights && lane < p.k) p.grad_weights[int64_t(token) * p.k + lane] = dots;
+  dot = wave_sum(dot);
+  if (p.grad_weights && lane == 0) p.grad_weights[slot] = dot;
 }
 
 int64_t plan_chunk(int64_t n) {
@@ -336,26 +334,36 @@ hipError_t launch_dispatch_fp8(const PermuteProblem& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Whether the expert-order rows are more than half of the 256 MiB cache behind
+// the L2s, so that little of them is still there: then they are read by
+// streaming loads (16384 x 2048 x 6: combine 92 -> 80 us, its backward 172 ->
+// 156; at 50 MB of rows plain loads are the faster ones, 18 against 20 us, and
+// at 100 MB both take 36).
+static bool rows_stream(const PermuteProblem& p) {
+  return p.T * p.k * p.C * (p.fp32 ? 4 : 2) > (int64_t(128) << 20);
+}
+
 hipError_t launch_combine(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0 || p.C == 0) return hipSuccess;
   const int vec = p.fp32 ? 4 : 8;
   const int strips = int((p.C + 64 * vec - 1) / (64 * vec));
-  const dim3 grid(unsigned((p.T * strips + 3) / 4));
-  if (p.fp32)
-    hipLaunchKernelGGL((combine_kernel<float>), grid, dim3(256), 0, st, p, strips);
-  else
-    hipLaunchKernelGGL((combine_kernel<uint16_t>), grid, dim3(256), 0, st, p, strips);
-  return hipGetLastError();
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned((p.T * strips + 3) / 4)), dim3(256), 0, st, p, strips);
+    return hipGetLastError();
+  };
+  if (p.fp32) return rows_stream(p) ? run(combine_kernel<float, true>) : run(combine_kernel<float, false>);
+  return rows_stream(p) ? run(combine_kernel<uint16_t, true>) : run(combine_kernel<uint16_t, false>);
 }
 
 hipError_t launch_combine_backward(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  const dim3 grid(unsigned((p.T + 3) / 4));
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned((p.T * p.k + 3) / 4)), dim3(256), 0, st, p);
+    return hipGetLastError();
+  };
   if (p.fp32)
-    hipLaunchKernelGGL((combine_backward_kernel<float>), grid, dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((combine_backward_kernel<uint16_t>), grid, dim3(256), 0, st, p);
-  return hipGetLastError();
+    return rows_stream(p) ? run(combine_backward_kernel<float, true>) : run(combine_backward_kernel<float, false>);
+  return rows_stream(p) ? run(combine_backward_kernel<uint16_t, true>) : run(combine_backward_kernel<uint16_t, false>);
 }
 
 }  // namespace fp8mm

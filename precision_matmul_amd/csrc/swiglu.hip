@@ -17,8 +17,8 @@
 // stores, which write the holes' lines twice).  A workgroup holds 32 rows of one
 // column block, so that a block's 32 scales are one contiguous 128-byte store
 // ([blocks, R]); the column blocks of the same rows follow each other.  Results
-// larger than the L2s go out by streaming stores.
-// 98304 x 1408: forward with codes and checkpoint 176 us, 5.6 TB/s; backward
+// larger than the L2s go out by streaming stores, the forward's input comes in so.
+// 98304 x 1408: forward with codes and checkpoint 170 us, 5.8 TB/s; backward
 // with the activation again 233 us, 6.0 TB/s (rows before column blocks 304 us,
 // a contiguous range of workgroups an XCD 254, plain stores 240).
 #include "moe_launch.hpp"
@@ -50,6 +50,13 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const uint2& a, const ui
     at[0] = va;
     at[8] = vb;
   }
+}
+
+template <bool NT>
+__device__ __forceinline__ U16x8 load8_bf16(const uint16_t* p) {
+  if constexpr (!NT) return load16(p);
+  const Chunk c = load_chunk_nt(p);
+  return U16x8{{c.w[0], c.w[1], c.w[2], c.w[3]}};
 }
 
 template <bool NT>
@@ -85,7 +92,8 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluProblem p, int 
   const int64_t c = int64_t(kb) * 128 + (t & 7) * 8;
   const bool first = (t & 7) == 0;
   const uint16_t* x = p.x + row * p.ld_x + c;
-  const U16x8 g0 = load16(x), g1 = load16(x + 64), u0 = load16(x + p.F), u1 = load16(x + p.F + 64);
+  const U16x8 g0 = load8_bf16<NT>(x), g1 = load8_bf16<NT>(x + 64);
+  const U16x8 u0 = load8_bf16<NT>(x + p.F), u1 = load8_bf16<NT>(x + p.F + 64);
   if constexpr (CKPT) {
     uint8_t* q = p.ckpt + row * p.ld_ckpt + c;
     quantize16<NT>(g0, g1, q, p.ckpt_scale + int64_t(kb) * p.R + row, first);
