@@ -246,6 +246,24 @@ __device__ __forceinline__ uint32_t wave_max_u(uint32_t v) {
              max(uint32_t(__builtin_amdgcn_readlane(i, 47)), uint32_t(__builtin_amdgcn_readlane(i, 63))));
 }
 
+// The same within each row of 16 lanes, in all 16: rotations by 8, 4, 2 and 1.
+template <int BY>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + BY, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t row_max_u(uint32_t v) {
+  v = max(v, row_ror<8>(v));
+  v = max(v, row_ror<4>(v));
+  v = max(v, row_ror<2>(v));
+  return max(v, row_ror<1>(v));
+}
+__device__ __forceinline__ float row_sum_f(float v) {
+  v += __uint_as_float(row_ror<8>(__float_as_uint(v)));
+  v += __uint_as_float(row_ror<4>(__float_as_uint(v)));
+  v += __uint_as_float(row_ror<2>(__float_as_uint(v)));
+  return v + __uint_as_float(row_ror<1>(__float_as_uint(v)));
+}
+
 // A lane's value as a scalar; a scalar put into one lane.
 __device__ __forceinline__ uint32_t read_lane(uint32_t v, int lane) {
   return uint32_t(__builtin_amdgcn_readlane(int(v), lane));

@@ -13,10 +13,14 @@
 // under softmax, has no defined choice: ids 0 .. k-1 with NaN weights, so that
 // the fault shows in the token's output.
 //
-// One wave a token, N = ceil(E / 64) consecutive experts a lane, everything in
-// registers.  The logits are read once (T E values against T k results), so a
-// large batch is bound by instructions: k selection rounds of a wave maximum
-// (six data-parallel steps), a ballot and a lane read.
+// Everything stays in registers and the logits are read once (T E values against
+// T k results), so a large batch is bound by instructions, most of them in the k
+// selection rounds: a maximum over lanes, the first lane that has it, the first
+// place in that lane.  Two forms: 16 lanes a token, four tokens a wave (E <= 256,
+// k <= 16), and one wave a token.  16384 tokens in us, the calls of the other
+// form in brackets: 256 experts in 8 groups, sigmoid and bias, k = 8: 12.6 (17.8);
+// 256 experts, softmax and bias: 10.8 (15.3); 128 experts 7.7 (11.5); 64 experts,
+// k = 6: 7.6 (8.4), about what a call takes the host.
 #include "moe_launch.hpp"
 #include "ops_common.hpp"
 
@@ -60,8 +64,23 @@ __device__ __forceinline__ float reciprocal(float d) {
   return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
 }
 
+// Floats as unsigned integers of the same order (-0 as +0), so that a wave
+// maximum is six fused data-parallel steps; -inf and what is out are at most
+// kNone.
+constexpr uint32_t kNone = 0x007FFFFFu;
+
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
 // Scores of a row: sigmoid(x), or softmax(x) = exp(x - shift) * inv, shift >= x.
-template <bool SIGMOID>
+// A token's logits lie in 64 lanes, or (ROW) in 16.
+template <bool SIGMOID, bool ROW = false>
 struct Scores {
   float shift = 0.0f, inv = 1.0f;
 
@@ -71,12 +90,12 @@ struct Scores {
       float m = x[0];
 #pragma unroll
       for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
-      m = wave_max_f(m);
+      m = ROW ? from_ordered(row_max_u(ordered(m))) : wave_max_f(m);
       shift = m == -kInf ? 0.0f : m;             // a row of -inf alone: every score 0
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < N; ++i) sum += exp_neg(shift - x[i]);
-      sum = wave_sum(sum);
+      sum = ROW ? row_sum_f(sum) : wave_sum(sum);
       inv = sum == 0.0f ? 1.0f : 1.0f / sum;
     }
   }
@@ -180,20 +199,6 @@ __device__ __forceinline__ void keep_groups(float (&key)[N], const float (&value
   }
 }
 
-// Floats as unsigned integers of the same order (-0 as +0), so that a wave
-// maximum is six fused data-parallel steps; -inf and what is out are at most
-// kNone.
-constexpr uint32_t kNone = 0x007FFFFFu;
-
-__device__ __forceinline__ uint32_t ordered(float f) {
-  const uint32_t u = __float_as_uint(f + 0.0f);
-  return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
-}
-
-__device__ __forceinline__ float from_ordered(uint32_t u) {
-  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
-}
-
 template <int N>
 __device__ __forceinline__ void load_logits(const RouteProblem& p, int64_t row, int e0, float (&x)[N]) {
   if (p.fp32)
@@ -202,6 +207,7 @@ __device__ __forceinline__ void load_logits(const RouteProblem& p, int64_t row, 
     load_row_of(static_cast<const uint16_t*>(p.logits) + row * p.ld, e0, p.E, x);
 }
 
+// One wave a token, N = ceil(E / 64) consecutive experts a lane.
 template <int N, bool SIGMOID, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(256) void route_kernel(const RouteProblem p, const Groups groups) {
   extern __shared__ float lds_all[];
@@ -292,6 +298,117 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteProblem p, const 
   }
 }
 
+// ---------------------------------------------------------------------------
+// The same for at most 256 experts and 16 slots, groups (if any) of whole lanes:
+// four tokens a wave, 16 lanes each with V consecutive experts, so that the
+// rounds' lane steps serve four tokens at once.
+// ---------------------------------------------------------------------------
+template <int V, bool SIGMOID, bool BIAS, bool GROUPS>
+__global__ __launch_bounds__(256) void route16_kernel(const RouteProblem p, const Groups groups) {
+  const int lane = threadIdx.x & 63;
+  const int l16 = lane & 15, first = lane & 48;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int e0 = l16 * V;
+  float b[V];
+  if constexpr (BIAS) load_row_of(p.bias, e0, p.E, b);
+  for (int64_t row0 = (int64_t(blockIdx.x) * 4 + wave) * 4; row0 < p.T; row0 += int64_t(gridDim.x) * 16) {
+    const int64_t own = row0 + (lane >> 4);
+    const int64_t row = min(own, p.T - 1);       // lanes past the last token repeat it and write nothing
+    float x[V], key[V];
+    load_logits(p, row, e0, x);
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) bad |= SIGMOID ? x[i] != x[i] : !(x[i] < kInf);
+    const Scores<SIGMOID, true> score(x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      key[i] = x[i];
+      if constexpr (BIAS) {
+        const float k = score(x[i]) + b[i];
+        key[i] = x[i] == -kInf ? -kInf : k;
+        bad |= key[i] != key[i];
+      }
+    }
+    if constexpr (GROUPS) {
+      float best = -kInf, second = -kInf;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float value = key[i];
+        if constexpr (!BIAS) {
+          const float s = score(x[i]);
+          value = p.group_top2 && x[i] != -kInf ? s : x[i];
+        }
+        second = fmaxf(second, fminf(best, value));
+        best = fmaxf(best, value);
+      }
+      const int L = 1 << groups.shift;
+      if (L > 1) merge_dpp<0xB1>(best, second);
+      if (L > 2) merge_dpp<0x4E>(best, second);
+      if (L > 4) merge_dpp<0x141>(best, second);
+      if (L > 8) merge_dpp<0x140>(best, second);
+      float value = best;
+      if (p.group_top2) value = second == -kInf ? best : best + second;
+      const int g = l16 >> groups.shift;
+      int rank = 0;
+      for (int o = 0; o < groups.count; ++o) {
+        const float other = __shfl(value, first + (o << groups.shift), 64);
+        rank += (other > value) | ((other == value) & (o < g)) ? 1 : 0;
+      }
+      const bool keep = rank < p.group_topk;
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = keep ? key[i] : -kInf;
+    }
+    const bool undefined = row_max_u(bad ? 1u : 0u) != 0;
+    uint32_t u[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) u[i] = ordered(key[i]);
+    int id = -1;                 // lane j of a token: slot j's expert and its key
+    uint32_t chosen_key = 0;
+    for (int j = 0; j < p.k; ++j) {
+      uint32_t local = u[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) local = max(local, u[i]);
+      const uint32_t m = row_max_u(local);
+      if (__ballot(m > kNone) == 0) break;
+      // the token's lowest lane with the maximum, and its lowest place with it
+      const uint32_t with = uint32_t(__ballot(local == m) >> first) & 0xFFFFu;
+      bool take = l16 == __builtin_ctz(with | 0x10000u) && m > kNone;
+      uint32_t e = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const bool here = take && u[i] == m;
+        e = here ? uint32_t(e0 + i) : e;
+        u[i] = here ? 0u : u[i];
+        take = take && !here;
+      }
+      e = row_max_u(e);
+      if (l16 == j && m > kNone) {
+        id = int(e);
+        chosen_key = m;
+      }
+    }
+    float chosen = from_ordered(chosen_key);
+    if constexpr (BIAS) {        // the key holds the bias too
+      chosen = 0.0f;
+      if (id >= 0)
+        chosen = p.fp32 ? static_cast<const float*>(p.logits)[row * p.ld + id]
+                        : to_float(static_cast<const uint16_t*>(p.logits)[row * p.ld + id]);
+    }
+    float w = score(chosen);
+    w = id < 0 ? 0.0f : w;
+    if (p.renorm) w = w / (row_sum_f(w) + kRenormEps);
+    w *= p.scale;
+    if (undefined) {
+      id = l16;
+      w = __builtin_nanf("");
+    }
+    if (l16 < p.k && own < p.T) {
+      p.ids[own * p.k + l16] = id;
+      p.weights[own * p.k + l16] = w;
+    }
+  }
+}
+
 // Backward.  With d_j the gradient of the chosen score s_j,
 //   d_j = scale g_j                                     (weights as they are)
 //   d_j = scale (g_j - sum_l g_l s_l / S) / S, S = sum_l s_l + 1e-20   (renormalised)
@@ -371,6 +488,29 @@ hipError_t run_route(const RouteProblem& p, hipStream_t st) {
   return groups ? run(route_kernel<N, SIGMOID, false, true>) : run(route_kernel<N, SIGMOID, false, false>);
 }
 
+template <int V, bool SIGMOID>
+hipError_t run_route16(const RouteProblem& p, hipStream_t st) {
+  const bool groups = p.group_topk < p.groups;
+  const Groups g(p, V);
+  const auto run = [&](auto kernel) {
+    const int64_t blocks = (p.T + 15) / 16;
+    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, p, g);
+    return hipGetLastError();
+  };
+  if (p.bias) return groups ? run(route16_kernel<V, SIGMOID, true, true>) : run(route16_kernel<V, SIGMOID, true, false>);
+  return groups ? run(route16_kernel<V, SIGMOID, false, true>) : run(route16_kernel<V, SIGMOID, false, false>);
+}
+
+template <int V>
+hipError_t route16_of(const RouteProblem& p, hipStream_t st) {
+  return p.sigmoid ? run_route16<V, true>(p, st) : run_route16<V, false>(p, st);
+}
+
+// Whether the four-tokens form serves: V experts a lane of 16.
+bool takes_route16(const RouteProblem& p, int V) {
+  return p.E <= 16 * V && p.k <= 16 && (p.group_topk == p.groups || Groups(p, V).whole);
+}
+
 template <int N, bool SIGMOID>
 hipError_t run_route_backward(const RouteProblem& p, hipStream_t st) {
   if (p.fp32)
@@ -388,6 +528,11 @@ hipError_t route_of(const RouteProblem& p, bool backward, hipStream_t st) {
 
 hipError_t route_any(const RouteProblem& p, bool backward, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
+  if (!backward) {
+    if (takes_route16(p, 4)) return route16_of<4>(p, st);
+    if (takes_route16(p, 8)) return route16_of<8>(p, st);
+    if (takes_route16(p, 16)) return route16_of<16>(p, st);
+  }
   if (p.E <= 64) return route_of<1>(p, backward, st);
   if (p.E <= 128) return route_of<2>(p, backward, st);
   if (p.E <= 256) return route_of<4>(p, backward, st);

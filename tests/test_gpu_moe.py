@@ -183,6 +183,13 @@ ROUTE = [
     (5, 300, 12, "softmax", True, 3, 2, "top2"),
     (4, 1000, 64, "sigmoid", True, 1, 1, "max"),
     (3, 1024, 16, "softmax", False, 16, 2, "max"),
+    (18, 64, 8, "sigmoid", True, 8, 2, "top2"),
+    (19, 240, 8, "sigmoid", True, 15, 4, "top2"),
+    (35, 256, 16, "softmax", False, 2, 1, "max"),
+    (6, 200, 40, "sigmoid", True, 1, 1, "max"),
+    (5, 128, 20, "softmax", False, 8, 4, "max"),
+    (4, 60, 17, "softmax", True, 1, 1, "max"),
+    (64, 9, 3, "sigmoid", False, 3, 2, "top2"),
 ]
 
 
