@@ -164,11 +164,12 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
 // workgroup order: no atomics, the same bits every time.  The partial rows are
 // traffic of their own (8 gridDim C bytes each way), so there are no more
 // workgroups than run at once: 256 of eight waves with a row each, or, above
-// 4 chunks a lane, 512 of four waves that share a row (256 above 12 chunks of
-// a wave, where the registers leave room for one workgroup a compute unit).
+// 4 chunks a lane, 512 of four waves that share a row (256 above 6144 columns,
+// where the registers leave room for one workgroup a compute unit).
 // 16384 x 2048 bf16: 45 us with the column sums, 4.5 TB/s of x, dy and dx (512
-// partial rows of eight-wave workgroups 56 us; no row in flight ahead 55 us);
-// 10000 x 5120: 72 us (1024 partial rows 88 us); 10000 x 8192: 99 us (512: 111).
+// partial rows of eight-wave workgroups 55 us; no row in flight ahead 55 us);
+// 16000 x 5120: 101 us (1024 partial rows 116 us); 10000 x 8192: 99 us (512:
+// 111); 7534 x 3560 fp32: 69 us (256: 90, 1024: 85).
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 
@@ -402,7 +403,7 @@ bool streams(const NormProblem& p, size_t size) { return p.R * p.C * int64_t(siz
 int backward_grid(int64_t R, int64_t C, int vec) {
   const int64_t one_wave = 256 * vec;         // rows of up to this many columns: a wave each
   const int64_t rows = C <= one_wave ? kRowWaves : 1;
-  const int64_t most = C <= one_wave ? 256 : C <= 3 * one_wave ? 512 : 256;
+  const int64_t most = C <= one_wave || C > 6144 ? 256 : 512;
   const int64_t blocks = (R + rows - 1) / rows;
   return int(blocks < most ? blocks : most);
 }

@@ -24,7 +24,8 @@ using namespace ops;
 // lanes of its wave with the same expert by ballots over the expert's bits).
 // Counts are integers and every slot's row is its rank, so the result does not
 // depend on the order of the LDS atomics.  One chunk alone needs no first
-// launch.  Latency-bound: 8 bytes a slot.
+// launch.  Latency-bound: 8 bytes a slot.  98304 slots, 64 experts: 5 and 6 us;
+// 96 slots: 3.5 us (four ids in flight a lane: no faster).
 // ---------------------------------------------------------------------------
 constexpr int64_t kPlanSingle = 4096;    // slots that one workgroup places alone
 constexpr int64_t kPlanChunks = 64;      // chunks at most: the second launch reads all their counts
@@ -155,9 +156,10 @@ __device__ __forceinline__ Slot slot_row(int32_t v) { return Slot{int64_t(v < 0 
 
 // ---------------------------------------------------------------------------
 // Dispatch: one wave an item of 64 chunks of one token, read once and written
-// to the token's k rows.  HBM-bound: (1 + k) rows a token.
+// to the token's k rows.  HBM-bound: (1 + k) rows a token.  16384 x 2048 x 6
+// bf16 with the plan: 87 us, 5.4 TB/s (plain stores 100 us).
 // ---------------------------------------------------------------------------
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void dispatch_kernel(const PermuteProblem p, int strips) {
   const int lane = threadIdx.x & 63;
   const uint32_t item = wave_item(blockIdx.x);
@@ -169,12 +171,17 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const PermuteProblem p, i
   for (int j = 0; j < p.k; ++j) {
     const Slot s = slot_row(p.row_of_slot[int64_t(token) * p.k + j]);
     if (s.row >= M) continue;
-    store_row(static_cast<T*>(p.out) + s.row * p.ld_out, c, p.C, s.used ? v : Chunk{{0u, 0u, 0u, 0u}});
+    store_row<T, NT>(static_cast<T*>(p.out) + s.row * p.ld_out, c, p.C, s.used ? v : Chunk{{0u, 0u, 0u, 0u}});
   }
 }
 
 // FP8: a wave covers 1024 columns of one token, 16 consecutive ones a lane, 8
-// lanes a group of 128; codes and scales as the 1x128 quantizer makes them.
+// lanes a group of 128; codes and scales as the 1x128 quantizer makes them, each
+// token quantized once.  A slot's scales are single floats a whole row of slots
+// apart: with a contiguous range of tokens an XCD, neighbouring rows of an
+// expert meet in one L2 before they go out.  16384 x 2048 x 6: 41 us, 6.7 TB/s
+// of x, codes and scales (plain code stores 53, tokens in launch order 58 with
+// the streaming ones).
 template <bool NT>
 __global__ __launch_bounds__(256) void dispatch_fp8_kernel(const PermuteProblem p, int strips) {
   const int lane = threadIdx.x & 63;
@@ -203,7 +210,8 @@ __global__ __launch_bounds__(256) void dispatch_fp8_kernel(const PermuteProblem 
 
 // ---------------------------------------------------------------------------
 // Combine: one wave an item of 64 chunks of one token; its k rows are added in
-// slot order in float32.  HBM-bound: (k + 1) rows a token.
+// slot order in float32.  HBM-bound: (k + 1) rows a token.  16384 x 2048 x 6: 80
+// us, 5.9 TB/s; 4099 x 2048 x 6, 1 of 20 slots empty: 21 us, 5.2 TB/s.
 // ---------------------------------------------------------------------------
 template <typename T, bool NT>
 __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, int strips) {
@@ -233,10 +241,10 @@ __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, in
 // Combine's backward: grad_rows[row] = w g, grad_weights[t, j] = <g, rows[row]>.
 // One wave a slot, four chunks a lane in flight: a token's k waves are
 // neighbours and share its gradient through the caches.  HBM-bound: (1 + 2 k)
-// rows a token.  16384 x 2048, k = 6: 156 us, 5.6 TB/s (one wave a token, which
-// reads the gradient once: 160 us, and 27 against 10 us for 64 tokens of 5120
-// columns; without streaming loads 172 us).
-template <typename T, bool NT>
+// rows a token.  16384 x 2048, k = 6: 154 us, 5.7 TB/s (plain stores 169; one
+// wave a token, which reads the gradient once, 4 us more, and 27 against 9 us for
+// 64 tokens of 5120 columns).
+template <typename T, bool LD, bool ST>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProblem p) {
   constexpr int V = kVec<T>;
   constexpr int U = 4;
@@ -257,7 +265,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProb
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       vg[u] = load_row(g_row, c0 + u * 64 * V, p.C);
-      vr[u] = r ? load_row<T, NT>(r, c0 + u * 64 * V, p.C) : Chunk{{0u, 0u, 0u, 0u}};
+      vr[u] = r ? load_row<T, LD>(r, c0 + u * 64 * V, p.C) : Chunk{{0u, 0u, 0u, 0u}};
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -269,12 +277,19 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProb
         if (r) dot += g[i] * f[i];
         f[i] = s.used ? w * g[i] : 0.0f;
       }
-      if (o) store_row(o, c0 + u * 64 * V, p.C, pack<T>(f));
+      if (o) store_row<T, ST>(o, c0 + u * 64 * V, p.C, pack<T>(f));
     }
   }
   dot = wave_sum(dot);
   if (p.grad_weights && lane == 0) p.grad_weights[slot] = dot;
 }
+
+int64_t rows_bytes(const PermuteProblem& p) { return p.T * p.k * p.C * (p.fp32 ? 4 : 2); }
+
+// Expert-order rows of more than twice the L2s are read by streaming loads:
+// combine of 16384 x 2048 x 6 (403 MB) 80 against 92 us, of 134 MB 30 against 34,
+// of 100 MB 21.2 against 21.9; of 25 MB 7.1 against 6.8.
+bool rows_stream(const PermuteProblem& p) { return rows_bytes(p) > 2 * kL2Bytes; }
 
 int64_t plan_chunk(int64_t n) {
   const int64_t c = n <= kPlanSingle ? n : (n + kPlanChunks - 1) / kPlanChunks;
@@ -315,12 +330,13 @@ hipError_t launch_dispatch(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0 || p.C == 0) return hipSuccess;
   const int vec = p.fp32 ? 4 : 8;
   const int strips = int((p.C + 64 * vec - 1) / (64 * vec));
-  const dim3 grid(unsigned((p.T * strips + 3) / 4));
-  if (p.fp32)
-    hipLaunchKernelGGL((dispatch_kernel<float>), grid, dim3(256), 0, st, p, strips);
-  else
-    hipLaunchKernelGGL((dispatch_kernel<uint16_t>), grid, dim3(256), 0, st, p, strips);
-  return hipGetLastError();
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned((p.T * strips + 3) / 4)), dim3(256), 0, st, p, strips);
+    return hipGetLastError();
+  };
+  const bool nt = rows_bytes(p) > kL2Bytes;
+  if (p.fp32) return nt ? run(dispatch_kernel<float, true>) : run(dispatch_kernel<float, false>);
+  return nt ? run(dispatch_kernel<uint16_t, true>) : run(dispatch_kernel<uint16_t, false>);
 }
 
 hipError_t launch_dispatch_fp8(const PermuteProblem& p, hipStream_t st) {
@@ -332,15 +348,6 @@ hipError_t launch_dispatch_fp8(const PermuteProblem& p, hipStream_t st) {
   else
     hipLaunchKernelGGL((dispatch_fp8_kernel<false>), grid, dim3(256), 0, st, p, strips);
   return hipGetLastError();
-}
-
-// Whether the expert-order rows are more than half of the 256 MiB cache behind
-// the L2s, so that little of them is still there: then they are read by
-// streaming loads (16384 x 2048 x 6: combine 92 -> 80 us, its backward 172 ->
-// 156; at 50 MB of rows plain loads are the faster ones, 18 against 20 us, and
-// at 100 MB both take 36).
-static bool rows_stream(const PermuteProblem& p) {
-  return p.T * p.k * p.C * (p.fp32 ? 4 : 2) > (int64_t(128) << 20);
 }
 
 hipError_t launch_combine(const PermuteProblem& p, hipStream_t st) {
@@ -361,9 +368,13 @@ hipError_t launch_combine_backward(const PermuteProblem& p, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(unsigned((p.T * p.k + 3) / 4)), dim3(256), 0, st, p);
     return hipGetLastError();
   };
-  if (p.fp32)
-    return rows_stream(p) ? run(combine_backward_kernel<float, true>) : run(combine_backward_kernel<float, false>);
-  return rows_stream(p) ? run(combine_backward_kernel<uint16_t, true>) : run(combine_backward_kernel<uint16_t, false>);
+  const auto typed = [&](auto zero) {
+    using T = decltype(zero);
+    if (rows_stream(p)) return run(combine_backward_kernel<T, true, true>);
+    return rows_bytes(p) > kL2Bytes ? run(combine_backward_kernel<T, false, true>)
+                                    : run(combine_backward_kernel<T, false, false>);
+  };
+  return p.fp32 ? typed(0.0f) : typed(uint16_t(0));
 }
 
 }  // namespace fp8mm
