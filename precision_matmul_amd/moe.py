@@ -12,6 +12,7 @@ RuntimeError.
 """
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (_ld, _lib, _need, _out_code, _ptr, fp8_grouped_linear_grad_weight, fp8_quantize_blockwise,
                fp8_quantize_grouped_128x1, fp8_quantize_grouped_dual, fp8_scaled_grouped_mm_v2)
@@ -58,7 +59,7 @@ def _need_float(t, name):
 
 def _need_dense(t, dtype, shape, device, name):
     _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+    if t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {device}, got {list(t.shape)}")
 
 
@@ -142,6 +143,7 @@ class _LayerNorm(torch.autograd.Function):
         return y.view(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -216,6 +218,7 @@ class _Route(torch.autograd.Function):
         return ids, weights
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _, grad_weights):
         logits, ids = ctx.saved_tensors
         grad = moe_route_backward(grad_weights.contiguous(), logits, ids, *ctx.args)
@@ -338,6 +341,7 @@ class _Dispatch(torch.autograd.Function):
         return moe_dispatch_forward(x.contiguous(), row_of_slot)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         row_of_slot, = ctx.saved_tensors
         return moe_combine_forward(grad.contiguous(), row_of_slot), None
@@ -356,6 +360,7 @@ class _Combine(torch.autograd.Function):
         return moe_combine_forward(rows, row_of_slot, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         rows, row_of_slot, weights = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -430,6 +435,7 @@ class _Swiglu(torch.autograd.Function):
         return h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_h):
         return fp8_swiglu_backward(grad_h.to(torch.bfloat16).contiguous(), *ctx.saved_tensors)[0]
 
@@ -466,7 +472,8 @@ class FP8MoE(torch.autograd.Function):
                 first product's two gradients; dispatch's
 
     Kept for the backward: x once per token, the checkpoint (2 F bytes a row in
-    place of 4 F), the rows before combine for the gradient of the weights."""
+    place of 4 F), the rows before combine (for the gradient of the weights) and
+    the weights' codes."""
 
     @staticmethod
     def forward(ctx, x, w_in, w_out, ids, weights):
@@ -491,6 +498,7 @@ class FP8MoE(torch.autograd.Function):
         return moe_combine_forward(rows, row_of_slot, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         x, q_in, s_in, q_out, s_out, codes, scale, rows, offsets, row_of_slot, weights = ctx.saved_tensors
         need_x, need_in, need_out, _, need_w = ctx.needs_input_grad
@@ -504,7 +512,6 @@ class FP8MoE(torch.autograd.Function):
                 qg, sg, qgt, sgt = fp8_quantize_grouped_dual(grad_rows, offsets)
             else:
                 qg, sg = fp8_quantize_blockwise(grad_rows, (1, 128))
-            # the input gradient; out is needed for the recomputed activation's backward call only
             grad_h = fp8_scaled_grouped_mm_v2(qg, q_out, offsets, sg, "1x128", s_out, "128x128", b_layout="KN")
             grad_gate_up, h = fp8_swiglu_backward(grad_h, codes, scale, recompute=need_out)
             if need_out:

@@ -593,6 +593,135 @@ def test_expert_layer_graph_follows_new_routing():
             assert float(eager[2].float().abs().max()) > 0
 
 
+def test_no_tokens_and_tokens_without_experts():
+    E, C, F, k = 4, 256, 128, 2
+    w_in = torch.randn((E, 2 * F, C), device=DEV).bfloat16().requires_grad_(True)
+    w_out = torch.randn((E, C, F), device=DEV).bfloat16().requires_grad_(True)
+    for T in (0, 1, 5):
+        logits = torch.full((T, E), float("-inf"), device=DEV)
+        ids, w = fp8mm.moe_route_forward(logits, k)
+        assert ids.shape == (T, k) and bool((ids == -1).all()) and not bool(w.any())
+        assert fp8mm.moe_route_backward(w, logits, ids).shape == (T, E)
+        offsets, slots = fp8mm.moe_plan(ids, E)
+        assert offsets.tolist() == [0] * E and bool((slots < 0).all())
+        x = torch.randn((T, C), device=DEV).bfloat16().requires_grad_(True)
+        rows = fp8mm.moe_dispatch_forward(x.detach(), slots)
+        q, s = fp8mm.fp8_moe_dispatch(x.detach(), slots)
+        assert rows.shape == (T * k, C) and not bool(rows.any()) and not bool(q.any()) and bool((s == 1).all())
+        gr, gw = fp8mm.moe_combine_backward(x.detach(), rows, slots, w)
+        assert not bool(gr.any()) and not bool(gw.any())
+        w_in.grad = w_out.grad = None
+        y = fp8mm.fp8_moe(x, w_in, w_out, ids, w)
+        y.backward(torch.ones_like(y))
+        assert y.shape == (T, C) and not bool(y.any())
+        for g in (x.grad, w_in.grad, w_out.grad):
+            assert not bool(g.any())
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements (4 GiB of bf16) in every large operand."""
+    T, k, C, E = 280000, 4, 2048, 16
+    assert T * k * C > 2 ** 31
+    say("dispatch and combine of 1.1 million rows")
+    ids = (torch.arange(T * k, device=DEV, dtype=torch.int64) * 7919 % E).to(torch.int32).view(T, k)
+    slots = fp8mm.moe_plan(ids, E)[1]
+    x = torch.randn((T, C), device=DEV, dtype=torch.bfloat16)
+    rows = fp8mm.moe_dispatch_forward(x, slots)
+    assert torch.equal(fp8mm.moe_combine_forward(rows, slots), x * 4)       # four equal bf16 values: exact
+    last = slots[-1].tolist()
+    gr, gw = fp8mm.moe_combine_backward(x, rows, slots)
+    assert torch.equal(gr[last], x[-1:].expand(k, C))
+    assert torch.equal(gw[:, :1].expand(T, k), gw)
+    del gr, rows
+    q, s = fp8mm.fp8_moe_dispatch(x, slots)
+    q1, s1 = fp8mm.fp8_quantize_blockwise(x[-3:].contiguous(), (1, 128))
+    assert torch.equal(q[slots[-3:].flatten().long()], q1.repeat_interleave(k, 0))
+    assert torch.equal(s[:, slots[-3:].flatten().long()], s1.repeat_interleave(k, 1))
+    del q, s
+    say("layer norm and gated activation of 2.2e9 elements")
+    big = x.repeat(4, 1)
+    y, mean, rstd = fp8mm.layer_norm_forward(big)
+    y1, m1, r1 = fp8mm.layer_norm_forward(x[-5:].contiguous())
+    assert torch.equal(y[-5:], y1) and torch.equal(mean[-5:], m1) and torch.equal(rstd[-5:], r1)
+    dx = fp8mm.layer_norm_backward(y, big, None, mean, rstd, need_params=False)[0]
+    assert torch.equal(dx[-5:], fp8mm.layer_norm_backward(y1, x[-5:].contiguous(), None, m1, r1, need_params=False)[0])
+    del y, dx
+    (hq, hs), (c, cs) = fp8mm.fp8_swiglu_forward(big, "fp8")
+    (hq1, hs1), (c1, cs1) = fp8mm.fp8_swiglu_forward(x[-5:].contiguous(), "fp8")
+    assert torch.equal(hq[-5:], hq1) and torch.equal(hs[:, -5:], hs1)
+    assert torch.equal(c[-5:], c1) and torch.equal(cs[:, -5:], cs1)
+    grad = torch.ones((T * 4, C // 2), device=DEV, dtype=torch.bfloat16)
+    gx, h = fp8mm.fp8_swiglu_backward(grad, c, cs, recompute=True)
+    gx1, h1 = fp8mm.fp8_swiglu_backward(grad[:5].contiguous(), c1, cs1.contiguous(), recompute=True)
+    assert torch.equal(gx[-5:], gx1) and torch.equal(h[-5:], h1)
+
+
+def test_strided_outputs_leave_the_padding_alone():
+    """The C calls take a row stride for each output: columns past the row stay."""
+    lib = fp8mm._lib.load()
+    st = torch.cuda.current_stream().cuda_stream
+    T, k, C = 9, 2, 200
+    x = torch.randn((T, C), device=DEV).bfloat16()
+    slots = fp8mm.moe_plan((torch.arange(T * k, device=DEV, dtype=torch.int32) % 4).view(T, k), 4)[1]
+
+    def padded(rows, cols, pad=24, dtype=torch.bfloat16):
+        return torch.full((rows, cols + pad), 7, device=DEV, dtype=dtype)
+
+    def untouched(t, cols, ref):
+        torch.cuda.synchronize()
+        assert bool((t[:, cols:] == 7).all()) and torch.equal(t[:, :cols], ref)
+
+    y = padded(T, C)
+    assert lib.fp8mm_layer_norm(x.data_ptr(), 0, T, C, C, None, None, 0, 1e-5, y.data_ptr(), C + 24, None, None, st) == 0
+    yr, mean, rstd = fp8mm.layer_norm_forward(x)
+    untouched(y, C, yr)
+    dx = padded(T, C)
+    assert lib.fp8mm_layer_norm_backward(yr.data_ptr(), C, x.data_ptr(), C, 0, T, C, None, 0, mean.data_ptr(),
+                                         rstd.data_ptr(), dx.data_ptr(), C + 24, None, None, None, 0, st) == 0
+    untouched(dx, C, fp8mm.layer_norm_backward(yr, x, None, mean, rstd)[0])
+    rows = padded(T * k, C)
+    assert lib.fp8mm_moe_dispatch(x.data_ptr(), 0, T, C, C, slots.data_ptr(), k, rows.data_ptr(), C + 24, st) == 0
+    r = fp8mm.moe_dispatch_forward(x, slots)
+    untouched(rows, C, r)
+    out = padded(T, C)
+    assert lib.fp8mm_moe_combine(r.data_ptr(), 0, T, C, C, slots.data_ptr(), None, k, out.data_ptr(), C + 24, st) == 0
+    untouched(out, C, fp8mm.moe_combine_forward(r, slots))
+    gr = padded(T * k, C)
+    assert lib.fp8mm_moe_combine_backward(x.data_ptr(), C, None, 0, 0, T, C, slots.data_ptr(), None, k, gr.data_ptr(),
+                                          C + 24, None, st) == 0
+    untouched(gr, C, r)
+    logits = torch.randn((T, 50), device=DEV)
+    ids, w = fp8mm.moe_route_forward(logits, k)
+    gl = padded(T, 50, dtype=torch.float32)
+    assert lib.fp8mm_moe_route_backward(w.data_ptr(), logits.data_ptr(), 1, T, 50, 50, ids.data_ptr(), k, 0, 1, 1.0,
+                                        gl.data_ptr(), 74, st) == 0
+    untouched(gl, 50, fp8mm.moe_route_backward(w, logits, ids))
+    u = torch.randn((T, 512), device=DEV).bfloat16()
+    h, q, c = padded(T, 256), padded(T, 256, 32, torch.uint8), padded(T, 512, 32, torch.uint8)
+    s, cs = torch.empty((2, T), device=DEV), torch.empty((4, T), device=DEV)
+    assert lib.fp8_swiglu(u.data_ptr(), T, 256, 512, h.data_ptr(), 280, q.data_ptr(), 288, s.data_ptr(), c.data_ptr(),
+                          544, cs.data_ptr(), st) == 0
+    (qr, sr), (cr, csr) = fp8mm.fp8_swiglu_forward(u, "fp8")
+    untouched(h, 256, fp8mm.fp8_swiglu_forward(u)[0])
+    untouched(q, 256, qr)
+    untouched(c, 512, cr)
+    assert torch.equal(s, sr) and torch.equal(cs, csr)
+    gx, h2 = padded(T, 512), padded(T, 256)
+    g = torch.randn((T, 256), device=DEV).bfloat16()
+    assert lib.fp8_swiglu_backward(g.data_ptr(), 256, c.data_ptr(), 544, cs.data_ptr(), T, 256, gx.data_ptr(), 536,
+                                   h2.data_ptr(), 280, st) == 0
+    gxr, hr = fp8mm.fp8_swiglu_backward(g, cr, csr, recompute=True)
+    untouched(gx, 512, gxr)
+    untouched(h2, 256, hr)
+    xd = torch.randn((T, 256), device=DEV).bfloat16()
+    qd, sd = padded(T * k, 256, 32, torch.uint8), torch.empty((2, T * k), device=DEV)
+    assert lib.fp8_moe_dispatch(xd.data_ptr(), T, 256, 256, slots.data_ptr(), k, qd.data_ptr(), 288, sd.data_ptr(),
+                                st) == 0
+    qdr, sdr = fp8mm.fp8_moe_dispatch(xd, slots)
+    untouched(qd, 256, qdr)
+    assert torch.equal(sd, sdr)
+
+
 # -------------------------------------------------------------------- refusals
 
 def test_refusals():
