@@ -17,7 +17,8 @@
 // stores, which write the holes' lines twice).  A workgroup holds 32 rows of one
 // column block, so that a block's 32 scales are one contiguous 128-byte store
 // ([blocks, R]); the column blocks of the same rows follow each other.  Results
-// larger than the L2s go out by streaming stores, the forward's input comes in so.
+// larger than the L2s go out by streaming stores; the forward's input comes in by
+// streaming loads where it is larger than twice the L2s.
 // 98304 x 1408: forward with codes and checkpoint 170 us, 5.8 TB/s; backward
 // with the activation again 233 us, 6.0 TB/s (rows before column blocks 304 us,
 // a contiguous range of workgroups an XCD 254, plain stores 240).
@@ -82,7 +83,7 @@ __device__ __forceinline__ uint2 cast8_f32(const float (&x)[8], const CastScale&
   return make_uint2(pack4(y, x), pack4(y + 4, x + 4));
 }
 
-template <bool H, bool HQ, bool CKPT, bool NT>
+template <bool H, bool HQ, bool CKPT, bool LD, bool ST>
 __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluProblem p, int blocks) {
   const int t = threadIdx.x;
   const int64_t rb = blockIdx.x / unsigned(blocks);
@@ -92,12 +93,12 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluProblem p, int 
   const int64_t c = int64_t(kb) * 128 + (t & 7) * 8;
   const bool first = (t & 7) == 0;
   const uint16_t* x = p.x + row * p.ld_x + c;
-  const U16x8 g0 = load8_bf16<NT>(x), g1 = load8_bf16<NT>(x + 64);
-  const U16x8 u0 = load8_bf16<NT>(x + p.F), u1 = load8_bf16<NT>(x + p.F + 64);
+  const U16x8 g0 = load8_bf16<LD>(x), g1 = load8_bf16<LD>(x + 64);
+  const U16x8 u0 = load8_bf16<LD>(x + p.F), u1 = load8_bf16<LD>(x + p.F + 64);
   if constexpr (CKPT) {
     uint8_t* q = p.ckpt + row * p.ld_ckpt + c;
-    quantize16<NT>(g0, g1, q, p.ckpt_scale + int64_t(kb) * p.R + row, first);
-    quantize16<NT>(u0, u1, q + p.F, p.ckpt_scale + (int64_t(kb) + p.F / 128) * p.R + row, first);
+    quantize16<ST>(g0, g1, q, p.ckpt_scale + int64_t(kb) * p.R + row, first);
+    quantize16<ST>(u0, u1, q + p.F, p.ckpt_scale + (int64_t(kb) + p.F / 128) * p.R + row, first);
   }
   float g[2][8], u[2][8];
   unpack8(g0, g[0]);
@@ -110,8 +111,8 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluProblem p, int 
     for (int i = 0; i < 8; ++i) g[a][i] = g[a][i] * fast_sigmoid(g[a][i]) * u[a][i];
   if constexpr (H) {
     uint16_t* h = p.h + row * p.ld_h + c;
-    store8_bf16<NT>(h, g[0]);
-    store8_bf16<NT>(h + 64, g[1]);
+    store8_bf16<ST>(h, g[0]);
+    store8_bf16<ST>(h + 64, g[1]);
   }
   if constexpr (HQ) {
     uint32_t m = 0;                      // |h| orders like its bits; NaN above everything
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluProblem p, int 
     m = group8_max(m);
     const float s = scale_from_amax(__uint_as_float(m), 0.0f, false);
     const CastScale cs = make_cast_scale(s);
-    store_codes<NT>(p.h_q + row * p.ld_hq + c, cast8_f32(g[0], cs), cast8_f32(g[1], cs));
+    store_codes<ST>(p.h_q + row * p.ld_hq + c, cast8_f32(g[0], cs), cast8_f32(g[1], cs));
     if (first) p.h_scale[int64_t(kb) * p.R + row] = s;
   }
 }
@@ -185,7 +186,8 @@ hipError_t run_swiglu(const SwigluProblem& p, hipStream_t st) {
     return hipGetLastError();
   };
   const int64_t bytes = p.R * p.F * (H ? 2 : 0) + p.R * p.F * (HQ ? 1 : 0) + p.R * p.F * (CKPT ? 2 : 0);
-  return bytes > kL2Bytes ? run(swiglu_kernel<H, HQ, CKPT, true>) : run(swiglu_kernel<H, HQ, CKPT, false>);
+  if (p.R * p.F * 4 > 2 * kL2Bytes) return run(swiglu_kernel<H, HQ, CKPT, true, true>);
+  return bytes > kL2Bytes ? run(swiglu_kernel<H, HQ, CKPT, false, true>) : run(swiglu_kernel<H, HQ, CKPT, false, false>);
 }
 
 template <bool H>

@@ -123,9 +123,10 @@ def layer_norm_backward(dy, x, weight, mean, rstd, need_dx=True, need_params=Tru
     size = 0
     if need_params:
         dweight = x.new_empty((C,), dtype=param_dtype)
-        dbias = x.new_empty((C,), dtype=param_dtype)
-        size = max(0, lib.fp8mm_layer_norm_backward_workspace(R, C))
-        workspace = x.new_empty((size,), dtype=torch.uint8)
+        dbias = torch.empty_like(dweight)
+        size = lib.fp8mm_layer_norm_backward_workspace(R, C)
+        if size > 0:
+            workspace = x.new_empty((size,), dtype=torch.uint8)
     st = lib.fp8mm_layer_norm_backward(dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, dtype, R, C, _ptr(weight),
                                        _out_code(param_dtype), mean.data_ptr(), rstd.data_ptr(), _ptr(dx), C,
                                        _ptr(dweight), _ptr(dbias), _ptr(workspace), size, _stream(x))

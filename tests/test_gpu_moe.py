@@ -60,6 +60,45 @@ NORM_SHAPES = [(1, 1), (3, 7), (5, 64), (4, 513), (9, 1024), (2, 1413), (7, 2048
                (2, 6200), (3, 8192), (2, 8193), (2, 20001)]
 
 
+def _check_norm_backward(x, xv, dy, dyv, w, wv, mean, rstd, dtype, params):
+    """layer_norm_backward against the formula with the same mean and rstd."""
+    R, C = xv.shape
+    half, D = BF16 if dtype == "bf16" else U, _depth(C) + 4
+    wa = np.ones(C) if wv is None else np.abs(wv)
+    m32, r32 = mean.double().cpu().numpy(), rstd.double().cpu().numpy()
+    dx, dw, db = fp8mm.layer_norm_backward(dy, x, w, mean, rstd)
+    rdx, rdw, rdb = moe.layer_norm_backward(dyv, xv, wv, m32, r32)
+    a = np.abs(dyv) * wa
+    xh = np.abs((xv - m32[:, None]) * r32[:, None])
+    mx = (a * xh).mean(1, keepdims=True)
+    tol = r32[:, None] * (6 * U * a + D * U * a.mean(1, keepdims=True) + (D + 10) * U * xh * mx + 6 * U * xh * mx)
+    _within(_f64(dx), rdx, tol + half * np.abs(rdx) * (1 + half) + half * tol + TINY, "dx")
+    p_half = BF16 if params == "bf16" else U
+    n = R + 24            # rows of one workgroup, its waves, the partial rows: at most R + 24 in a chain
+    tol = (n + 4) * U * (np.abs(dyv) * xh).sum(0)
+    _within(_f64(dw), rdw, tol + p_half * np.abs(rdw) + p_half * tol + TINY, "dweight")
+    tol = n * U * np.abs(dyv).sum(0)
+    _within(_f64(db), rdb, tol + p_half * np.abs(rdb) + p_half * tol + TINY, "dbias")
+    return dx, dw, db
+
+
+@pytest.mark.parametrize("params", ["bf16", "fp32"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("R,C", [(512, 100), (513, 100), (600, 513), (530, 1024), (521, 2047), (519, 2049), (520, 3560),
+                                 (515, 4104), (514, 6200), (516, 8190)])
+def test_layer_norm_backward_of_many_rows(R, C, dtype, params):
+    """Both sides of the step from one launch to partial sums, in every width."""
+    say(f"layer norm backward {R}x{C} {dtype} params {params}")
+    r = np.random.default_rng(R + C)
+    x, xv = _dev(r.standard_normal((R, C)) + r.standard_normal((R, 1)), DT[dtype])
+    dy, dyv = _dev(r.standard_normal((R, C)), DT[dtype])
+    w, wv = _dev(1 + 0.3 * r.standard_normal(C), DT[params])
+    _, mean, rstd = fp8mm.layer_norm_forward(x, w)
+    out = _check_norm_backward(x, xv, dy, dyv, w, wv, mean, rstd, dtype, params)
+    for got, want in zip(fp8mm.layer_norm_backward(_strided(dy, 1, 2), _strided(x), w, mean, rstd), out):
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("params", ["bf16", "fp32", None])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("R,C", NORM_SHAPES)
@@ -87,20 +126,7 @@ def test_layer_norm(R, C, dtype, params):
     tol = wa * (rrstd * e_mean)[:, None] + np.abs(xh) * wa * (e_rstd / rrstd + 6 * U)[:, None] + 4 * U * ba
     _within(_f64(y), ref, tol + half * np.abs(ref) * (1 + half) + half * tol + TINY, "y")
 
-    m32, r32 = mean.double().cpu().numpy(), rstd.double().cpu().numpy()
-    dx, dw, db = fp8mm.layer_norm_backward(dy, x, w, mean, rstd)
-    rdx, rdw, rdb = moe.layer_norm_backward(dyv, xv, wv, m32, r32)
-    a = np.abs(dyv) * wa
-    xh = np.abs((xv - m32[:, None]) * r32[:, None])
-    mx = (a * xh).mean(1, keepdims=True)
-    tol = r32[:, None] * (6 * U * a + D * U * a.mean(1, keepdims=True) + (D + 10) * U * xh * mx + 6 * U * xh * mx)
-    _within(_f64(dx), rdx, tol + half * np.abs(rdx) * (1 + half) + half * tol + TINY, "dx")
-    p_half = BF16 if params == "bf16" else U
-    n = R + 24            # rows of one workgroup, its waves, the partial rows: at most R + 24 in a chain
-    tol = (n + 4) * U * (np.abs(dyv) * xh).sum(0)
-    _within(_f64(dw), rdw, tol + p_half * np.abs(rdw) + p_half * tol + TINY, "dweight")
-    tol = n * U * np.abs(dyv).sum(0)
-    _within(_f64(db), rdb, tol + p_half * np.abs(rdb) + p_half * tol + TINY, "dbias")
+    dx, dw, db = _check_norm_backward(x, xv, dy, dyv, w, wv, mean, rstd, dtype, params)
     # rows at any stride and start: the same bits
     ys, _, _ = fp8mm.layer_norm_forward(_strided(x), w, b, eps)
     assert torch.equal(ys, y)
