@@ -231,8 +231,9 @@ fp8mm_status fp8mm_moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E,
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return fail(FP8MM_EINVAL, "workspace must be 16-byte aligned and hold %lld bytes, has %lld", (long long)need,
                 (long long)(workspace ? workspace_bytes : 0));
-  return from_hip(fp8mm::launch_plan(ids, T * k, int(E), offsets, row_of_slot, static_cast<int32_t*>(workspace), stream),
-                  "fp8mm_moe_plan");
+  return from_hip(
+      fp8mm::launch_plan(ids, T * k, int(E), offsets, row_of_slot, static_cast<int32_t*>(workspace), stream),
+      "fp8mm_moe_plan");
 }
 
 fp8mm_status fp8mm_moe_dispatch(const void* x, fp8mm_dtype dtype, int64_t T, int64_t C, int64_t ld_x,

@@ -497,7 +497,8 @@ hipError_t run_route16(const RouteProblem& p, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, p, g);
     return hipGetLastError();
   };
-  if (p.bias) return groups ? run(route16_kernel<V, SIGMOID, true, true>) : run(route16_kernel<V, SIGMOID, true, false>);
+  if (p.bias)
+    return groups ? run(route16_kernel<V, SIGMOID, true, true>) : run(route16_kernel<V, SIGMOID, true, false>);
   return groups ? run(route16_kernel<V, SIGMOID, false, true>) : run(route16_kernel<V, SIGMOID, false, false>);
 }
 

@@ -187,7 +187,8 @@ hipError_t run_swiglu(const SwigluProblem& p, hipStream_t st) {
   };
   const int64_t bytes = p.R * p.F * (H ? 2 : 0) + p.R * p.F * (HQ ? 1 : 0) + p.R * p.F * (CKPT ? 2 : 0);
   if (p.R * p.F * 4 > 2 * kL2Bytes) return run(swiglu_kernel<H, HQ, CKPT, true, true>);
-  return bytes > kL2Bytes ? run(swiglu_kernel<H, HQ, CKPT, false, true>) : run(swiglu_kernel<H, HQ, CKPT, false, false>);
+  if (bytes > kL2Bytes) return run(swiglu_kernel<H, HQ, CKPT, false, true>);
+  return run(swiglu_kernel<H, HQ, CKPT, false, false>);
 }
 
 template <bool H>

@@ -37,11 +37,15 @@ def _stream(t):
 
 
 def _rows(t, name):
-    """Row stride of a 2-D tensor with unit column stride; at least its width
-    where there is one row or none."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    """Row stride of a 2-D tensor with unit column stride; its width where there
+    is one row or none."""
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D row-major tensor")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    row, column = t.stride()
+    if column != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must be a 2-D row-major tensor")
+    return row if shape[0] > 1 else shape[1]
 
 
 def _need_float(t, name):
@@ -57,10 +61,15 @@ def _need_float(t, name):
     raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
 
 
+def _like(t):
+    """A dense tensor of t's shape and type (empty_like, where it is one, costs the host less)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _need_dense(t, dtype, shape, device, name):
     _need(t, dtype, name)
-    if t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {device}, got {list(t.shape)}")
+    if t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on device {device}, got {list(t.shape)}")
 
 
 def _code(table, value, name):
@@ -71,19 +80,22 @@ def _code(table, value, name):
 
 # ------------------------------------------------------------------ layer norm
 
+def _param(x, t, name):
+    """Type code of a parameter vector of x's columns."""
+    code = _need_float(t, name)
+    if t.shape != x.shape[1:] or not t.is_contiguous() or t.get_device() != x.get_device():
+        raise ValueError(f"{name} must be a contiguous [{x.shape[1]}] tensor on {x.device}, got {list(t.shape)}")
+    return code
+
+
 def _params(x, weight, bias):
-    """(code, weight, bias) of the parameters: both [C], of one type."""
-    code = None
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            continue
-        c = _need_float(t, name)
-        if tuple(t.shape) != (x.shape[1],) or not t.is_contiguous() or t.device != x.device:
-            raise ValueError(f"{name} must be a contiguous [{x.shape[1]}] tensor on {x.device}")
-        if code is not None and c != code:
-            raise ValueError("weight and bias must have the same dtype")
-        code = c
-    return _lib.OUT_FP32 if code is None else code
+    """Type code of the parameters, which are of one type."""
+    if weight is None:
+        return _lib.OUT_FP32 if bias is None else _param(x, bias, "bias")
+    code = _param(x, weight, "weight")
+    if bias is not None and _param(x, bias, "bias") != code:
+        raise ValueError("weight and bias must have the same dtype")
+    return code
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps=1e-5):
@@ -93,7 +105,7 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5):
     ld = _rows(x, "x")
     params = _params(x, weight, bias)
     R, C = x.shape
-    y = x.new_empty((R, C))
+    y = _like(x)
     mean, rstd = x.new_empty((2, R), dtype=torch.float32).unbind(0)
     st = _lib.load().fp8mm_layer_norm(x.data_ptr(), dtype, R, C, ld, _ptr(weight), _ptr(bias), params, eps,
                                       y.data_ptr(), C, mean.data_ptr(), rstd.data_ptr(), _stream(x))
@@ -106,19 +118,19 @@ def layer_norm_backward(dy, x, weight, mean, rstd, need_dx=True, need_params=Tru
     rstd.  dweight and dbias have the weight's type (param_dtype, or float32,
     where there is no weight); None where not needed."""
     dtype = _need_float(x, "x")
-    if _need_float(dy, "dy") != dtype or dy.shape != x.shape or dy.device != x.device:
+    if _need_float(dy, "dy") != dtype or dy.shape != x.shape or dy.get_device() != x.get_device():
         raise ValueError("dy must have the dtype, shape and device of x")
     ld_dy, ld_x = _rows(dy, "dy"), _rows(x, "x")
     R, C = x.shape
     _params(x, weight, None)
     for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _need_dense(t, torch.float32, (R,), x.device, name)
+        _need_dense(t, torch.float32, (R,), x.get_device(), name)
     if weight is not None:
         param_dtype = weight.dtype
     elif param_dtype is None:
         param_dtype = torch.float32
     lib = _lib.load()
-    dx = x.new_empty((R, C)) if need_dx else None
+    dx = _like(x) if need_dx else None
     dweight = dbias = workspace = None
     size = 0
     if need_params:
@@ -176,7 +188,7 @@ def moe_route_forward(logits, k, score="softmax", bias=None, groups=1, group_top
     ld = _rows(logits, "logits")
     T, E = logits.shape
     if bias is not None:
-        _need_dense(bias, torch.float32, (E,), logits.device, "bias")
+        _need_dense(bias, torch.float32, (E,), logits.get_device(), "bias")
     k = int(k)
     slots = max(k, 0)
     ids = logits.new_empty((T, slots), dtype=torch.int32)
@@ -198,9 +210,9 @@ def moe_route_backward(grad_weights, logits, ids, score="softmax", renormalize=T
     T, E = logits.shape
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError(f"ids must be [{T}, k], got {list(ids.shape)}")
-    _need_dense(ids, torch.int32, ids.shape, logits.device, "ids")
-    _need_dense(grad_weights, torch.float32, ids.shape, logits.device, "grad_weights")
-    grad = logits.new_empty((T, E))
+    _need_dense(ids, torch.int32, ids.shape, logits.get_device(), "ids")
+    _need_dense(grad_weights, torch.float32, ids.shape, logits.get_device(), "grad_weights")
+    grad = _like(logits)
     st = _lib.load().fp8mm_moe_route_backward(grad_weights.data_ptr(), logits.data_ptr(), dtype, T, E, ld,
                                               ids.data_ptr(), ids.shape[1], _code(_lib.SCORES, score, "score"),
                                               1 if renormalize else 0, scale, grad.data_ptr(), E, _stream(logits))
@@ -246,8 +258,8 @@ def moe_plan(ids, experts):
     lib = _lib.load()
     size = lib.fp8mm_moe_plan_workspace(T, k, experts)
     workspace = ids.new_empty((size,), dtype=torch.uint8) if size > 0 else None
-    offsets = torch.empty((max(int(experts), 0),), dtype=torch.int32, device=ids.device)
-    row_of_slot = ids.new_empty((T, k), dtype=torch.int32)
+    offsets = ids.new_empty((max(int(experts), 0),))
+    row_of_slot = torch.empty_like(ids)
     st = lib.fp8mm_moe_plan(ids.data_ptr(), T, k, experts, offsets.data_ptr(), row_of_slot.data_ptr(), _ptr(workspace),
                             max(size, 0), _stream(ids))
     _lib.check(st, "fp8mm_moe_plan")
@@ -257,7 +269,7 @@ def moe_plan(ids, experts):
 def _need_slots(row_of_slot, tokens, device):
     _need(row_of_slot, torch.int32, "row_of_slot")
     if (row_of_slot.dim() != 2 or (tokens is not None and row_of_slot.shape[0] != tokens) or
-            not row_of_slot.is_contiguous() or row_of_slot.device != device):
+            not row_of_slot.is_contiguous() or row_of_slot.get_device() != device):
         raise ValueError("row_of_slot must be a contiguous [T, k] tensor on the rows' device")
     return row_of_slot.shape
 
@@ -267,7 +279,7 @@ def moe_dispatch_forward(x, row_of_slot):
     of slots without an expert)."""
     dtype = _need_float(x, "x")
     ld = _rows(x, "x")
-    T, k = _need_slots(row_of_slot, x.shape[0], x.device)
+    T, k = _need_slots(row_of_slot, x.shape[0], x.get_device())
     C = x.shape[1]
     out = x.new_empty((T * k, C))
     st = _lib.load().fp8mm_moe_dispatch(x.data_ptr(), dtype, T, C, ld, row_of_slot.data_ptr(), k, out.data_ptr(), C,
@@ -282,7 +294,7 @@ def fp8_moe_dispatch(x, row_of_slot):
     quantized once.  Rows of slots without an expert: codes 0, scales 1."""
     _need(x, torch.bfloat16, "x")
     ld = _ld(x, "x")
-    T, k = _need_slots(row_of_slot, x.shape[0], x.device)
+    T, k = _need_slots(row_of_slot, x.shape[0], x.get_device())
     C = x.shape[1]
     q = x.new_empty((T * k, C), dtype=torch.uint8)
     scale = x.new_empty((C // 128, T * k), dtype=torch.float32)
@@ -297,11 +309,11 @@ def moe_combine_forward(rows, row_of_slot, weights=None):
     (float32 [T, k]; None: 1) and added in slot order."""
     dtype = _need_float(rows, "rows")
     ld = _rows(rows, "rows")
-    T, k = _need_slots(row_of_slot, None, rows.device)
+    T, k = _need_slots(row_of_slot, None, rows.get_device())
     if rows.shape[0] != T * k:
         raise ValueError(f"rows must have T k = {T * k} rows, got {rows.shape[0]}")
     if weights is not None:
-        _need_dense(weights, torch.float32, (T, k), rows.device, "weights")
+        _need_dense(weights, torch.float32, (T, k), rows.get_device(), "weights")
     C = rows.shape[1]
     out = rows.new_empty((T, C))
     st = _lib.load().fp8mm_moe_combine(rows.data_ptr(), dtype, T, C, ld, row_of_slot.data_ptr(), _ptr(weights), k,
@@ -315,17 +327,18 @@ def moe_combine_backward(grad_out, rows, row_of_slot, weights=None, need_rows=Tr
     None where not needed.  rows may be None without need_weights."""
     dtype = _need_float(grad_out, "grad_out")
     ld_go = _rows(grad_out, "grad_out")
-    T, k = _need_slots(row_of_slot, grad_out.shape[0], grad_out.device)
+    T, k = _need_slots(row_of_slot, grad_out.shape[0], grad_out.get_device())
     C = grad_out.shape[1]
     ld = 0
     if rows is not None:
-        if _need_float(rows, "rows") != dtype or tuple(rows.shape) != (T * k, C) or rows.device != grad_out.device:
+        if (_need_float(rows, "rows") != dtype or rows.shape != (T * k, C) or
+                rows.get_device() != grad_out.get_device()):
             raise ValueError(f"rows must be [{T * k}, {C}] of grad_out's dtype and device")
         ld = _rows(rows, "rows")
     elif need_weights:
         raise ValueError("rows are needed for the gradient of the weights")
     if weights is not None:
-        _need_dense(weights, torch.float32, (T, k), grad_out.device, "weights")
+        _need_dense(weights, torch.float32, (T, k), grad_out.get_device(), "weights")
     grad_rows = grad_out.new_empty((T * k, C)) if need_rows else None
     grad_weights = grad_out.new_empty((T, k), dtype=torch.float32) if need_weights else None
     st = _lib.load().fp8mm_moe_combine_backward(grad_out.data_ptr(), ld_go, _ptr(rows), ld, dtype, T, C,
@@ -417,8 +430,8 @@ def fp8_swiglu_backward(grad_h, codes, scale, recompute=False):
     R, F = grad_h.shape
     if F % 128:
         raise ValueError(f"grad_h must have a multiple of 128 columns, got {F}")
-    _need_dense(codes, torch.uint8, (R, 2 * F), grad_h.device, "codes")
-    _need_dense(scale, torch.float32, (2 * F // 128, R), grad_h.device, "scale")
+    _need_dense(codes, torch.uint8, (R, 2 * F), grad_h.get_device(), "codes")
+    _need_dense(scale, torch.float32, (2 * F // 128, R), grad_h.get_device(), "scale")
     grad_x = grad_h.new_empty((R, 2 * F), dtype=torch.bfloat16)
     h = grad_h.new_empty((R, F), dtype=torch.bfloat16) if recompute else None
     st = _lib.load().fp8_swiglu_backward(grad_h.data_ptr(), ld, codes.data_ptr(), 2 * F, scale.data_ptr(), R, F,
@@ -482,7 +495,8 @@ class FP8MoE(torch.autograd.Function):
             _need(t, torch.bfloat16, name)
         E = w_in.shape[0]
         if w_in.dim() != 3 or w_out.dim() != 3 or w_in.shape != (E, 2 * w_out.shape[2], w_out.shape[1]):
-            raise ValueError(f"w_in must be [E, 2 F, C] and w_out [E, C, F], got {list(w_in.shape)}, {list(w_out.shape)}")
+            raise ValueError("w_in must be [E, 2 F, C] and w_out [E, C, F], "
+                             f"got {list(w_in.shape)} and {list(w_out.shape)}")
         if w_out.shape[0] != E:
             raise ValueError(f"w_in has {E} experts, w_out {w_out.shape[0]}")
         x, weights = x.contiguous(), weights.contiguous()

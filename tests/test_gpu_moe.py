@@ -45,7 +45,8 @@ def _f64(t):
 def _within(got, ref, tol, what):
     off = np.abs(got - ref)
     bad = ~(off <= tol)
-    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} outside, worst {np.nanmax(off / np.maximum(tol, 1e-300)):.3g} x"
+    worst = np.nanmax(off / np.maximum(tol, 1e-300)) if off.size else 0.0
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} outside, worst {worst:.3g} x"
 
 
 def _depth(C):
@@ -395,7 +396,8 @@ def test_dispatch_and_combine(T, C, k, E, dtype):
         rgr, rgw = moe.combine_backward(gv, rowsv, rv, weightsv)
         _within(_f64(gr), rgr, (half + 2 * U) * np.abs(rgr) + TINY, "grad_rows")
         depth = C / 64 + 6 + 10
-        _within(_f64(gw), rgw, depth * U * moe.combine_backward(np.abs(gv), np.abs(rowsv), rv)[1] + TINY, "grad_weights")
+        size = moe.combine_backward(np.abs(gv), np.abs(rowsv), rv)[1]
+        _within(_f64(gw), rgw, depth * U * size + TINY, "grad_weights")
         grs, gws = fp8mm.moe_combine_backward(_strided(g), _strided(rows, 1, 1), slots, weights)
         assert torch.equal(grs, gr) and torch.equal(gws, gw)
         assert torch.equal(fp8mm.moe_combine_backward(g, None, slots, weights, need_weights=False)[0], gr)
@@ -468,7 +470,8 @@ def test_swiglu(R, F):
     assert none is None
     amax = np.abs(ref).reshape(R, F // 128, 128).max(2).T
     want = np.where(amax < 448 * 1e-45, 1.0, amax / 448)
-    _within(_f64(s), want, want * (tol.max() / max(np.abs(ref).max(), 1e-30) + (np.abs(xv).max() * 4 + 24) * U), "scale")
+    rel = tol.max() / max(np.abs(ref).max(), 1e-30) + (np.abs(xv).max() * 4 + 24) * U
+    _within(_f64(s), want, want * rel, "scale")
     step = np.maximum(np.abs(ref) * 2.0 ** -4, np.repeat(_f64(s).T, 128, axis=1) * 2.0 ** -10)
     _within(_dequantize(q, s), ref, step * (1 + 1e-4) + 2 * tol, "codes")
     for out in ("bf16", "fp8"):
@@ -698,7 +701,8 @@ def test_strided_outputs_leave_the_padding_alone():
         assert bool((t[:, cols:] == 7).all()) and torch.equal(t[:, :cols], ref)
 
     y = padded(T, C)
-    assert lib.fp8mm_layer_norm(x.data_ptr(), 0, T, C, C, None, None, 0, 1e-5, y.data_ptr(), C + 24, None, None, st) == 0
+    assert lib.fp8mm_layer_norm(x.data_ptr(), 0, T, C, C, None, None, 0, 1e-5, y.data_ptr(), C + 24, None, None,
+                                st) == 0
     yr, mean, rstd = fp8mm.layer_norm_forward(x)
     untouched(y, C, yr)
     dx = padded(T, C)

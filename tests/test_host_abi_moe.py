@@ -42,7 +42,8 @@ NORM_D = dict(x=FAKE, dt=0, R=4, C=64, ldx=64, w=FAKE, b=FAKE, pd=0, eps=1e-5, y
               st=None)
 
 
-@pytest.mark.parametrize("kw", [dict(dt=2), dict(pd=7), dict(R=-1), dict(C=0), dict(C=2 ** 22 + 1, ldx=2 ** 23, ldy=2 ** 23),
+@pytest.mark.parametrize("kw", [dict(dt=2), dict(pd=7), dict(R=-1), dict(C=0),
+                                dict(C=2 ** 22 + 1, ldx=2 ** 23, ldy=2 ** 23),
                                 dict(R=2 ** 31), dict(ldx=63), dict(ldy=1), dict(eps=-1.0), dict(eps=NAN),
                                 dict(eps=INF), dict(x=None), dict(y=None), dict(x=FAKE + 1), dict(dt=1, y=FAKE + 2),
                                 dict(pd=1, w=FAKE + 2)])
@@ -65,8 +66,9 @@ NORMB_D = dict(dy=FAKE, lddy=64, x=FAKE, ldx=64, dt=0, R=4, C=64, w=None, pd=0, 
                dw=FAKE, db=None, ws=FAKE, wsb=1 << 20, st=None)
 
 
-@pytest.mark.parametrize("kw", [dict(lddy=10), dict(ldx=10), dict(lddx=10), dict(dy=None), dict(x=None), dict(mean=None),
-                                dict(rstd=None), dict(R=9000, ws=None), dict(R=9000, wsb=64), dict(R=9000, ws=FAKE + 4),
+@pytest.mark.parametrize("kw", [dict(lddy=10), dict(ldx=10), dict(lddx=10), dict(dy=None), dict(x=None),
+                                dict(mean=None), dict(rstd=None), dict(R=9000, ws=None), dict(R=9000, wsb=64),
+                                dict(R=9000, ws=FAKE + 4),
                                 dict(dt=3), dict(C=-1), dict(dw=FAKE + 1), dict(dx=FAKE + 1)])
 def test_layer_norm_backward_refusals(lib, kw):
     assert _call(lib, "fp8mm_layer_norm_backward", NORMB, NORMB_D, kw) == _lib.EINVAL
@@ -110,8 +112,9 @@ ROUTEB_D = dict(g=FAKE, l=FAKE, dt=1, T=4, E=64, ld=64, ids=FAKE, k=6, score=0, 
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(g=None), _lib.EINVAL), (dict(out=None), _lib.EINVAL), (dict(ids=None), _lib.EINVAL), (dict(ldg=1), _lib.EINVAL),
-    (dict(k=0), _lib.EINVAL), (dict(score=-1), _lib.EINVAL), (dict(rn=3), _lib.EINVAL), (dict(out=FAKE + 2), _lib.EINVAL),
+    (dict(g=None), _lib.EINVAL), (dict(out=None), _lib.EINVAL), (dict(ids=None), _lib.EINVAL),
+    (dict(ldg=1), _lib.EINVAL), (dict(k=0), _lib.EINVAL), (dict(score=-1), _lib.EINVAL), (dict(rn=3), _lib.EINVAL),
+    (dict(out=FAKE + 2), _lib.EINVAL),
     (dict(E=1025, ld=1025, ldg=1025), _lib.ENOTIMPL),
 ])
 def test_route_backward_refusals(lib, kw, code):
@@ -123,8 +126,8 @@ PLAN_D = dict(ids=FAKE, T=9000, k=2, E=64, offs=FAKE, rows=FAKE, ws=FAKE, wsb=1 
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(ids=None), _lib.EINVAL), (dict(offs=None), _lib.EINVAL), (dict(rows=None), _lib.EINVAL), (dict(T=-1), _lib.EINVAL),
-    (dict(k=0), _lib.EINVAL), (dict(E=0), _lib.EINVAL), (dict(T=2 ** 30), _lib.EINVAL), (dict(ws=None), _lib.EINVAL),
+    (dict(ids=None), _lib.EINVAL), (dict(offs=None), _lib.EINVAL), (dict(rows=None), _lib.EINVAL),
+    (dict(T=-1), _lib.EINVAL), (dict(k=0), _lib.EINVAL), (dict(E=0), _lib.EINVAL), (dict(T=2 ** 30), _lib.EINVAL), (dict(ws=None), _lib.EINVAL),
     (dict(wsb=16), _lib.EINVAL), (dict(ws=FAKE + 8), _lib.EINVAL), (dict(E=1025), _lib.ENOTIMPL),
 ])
 def test_plan_refusals(lib, kw, code):
