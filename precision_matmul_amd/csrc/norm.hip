@@ -18,6 +18,10 @@ namespace {
 
 using namespace ops;
 
+__device__ __forceinline__ Chunk pack4f(const float* f) {
+  return Chunk{{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])}};
+}
+
 // Sum of v over the WPR waves that share a row.  `slot` alternates between
 // calls, so that one barrier a call is enough.
 template <int WPR>
@@ -166,10 +170,11 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
 // workgroups than run at once: 256 of eight waves with a row each, or, above
 // 4 chunks a lane, 512 of four waves that share a row (256 above 6144 columns,
 // where the registers leave room for one workgroup a compute unit).
-// 16384 x 2048 bf16: 45 us with the column sums, 4.5 TB/s of x, dy and dx (512
-// partial rows of eight-wave workgroups 55 us; no row in flight ahead 55 us);
-// 16000 x 5120: 101 us (1024 partial rows 116 us); 10000 x 8192: 99 us (512:
-// 111); 7534 x 3560 fp32: 69 us (256: 90, 1024: 85).
+// 16384 x 2048 bf16: 43 us with the column sums, 4.7 TB/s of x, dy and dx; without
+// dw and db 37 us, what a sum of two such matrices takes (512 partial rows of
+// eight-wave workgroups 55 us; no row in flight ahead 55; the waves' shares added
+// one wave after the other 45).  16000 x 4096: 76 us (1024 partial rows 93);
+// 10000 x 8192: 94 us (512: 111); 7534 x 3560 fp32: 68 us (256: 90, 1024: 85).
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 
@@ -182,7 +187,8 @@ __global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward
   constexpr int RPB = WPR == 1 ? kRowWaves : 1;
   constexpr int64_t STEP = int64_t(WPR) * 64 * V;
   __shared__ float part[2][2][4];
-  __shared__ float acc[WPR == 1 ? 2 * NIT * int(STEP) : 1];
+  constexpr int Q = 2 * NIT * V / 4;              // a lane's sums, in fours
+  __shared__ float4 acc[WPR == 1 ? kRowWaves / 2 * Q * 64 : 1];
   const int wave = threadIdx.x >> 6;
   const int64_t c0 = int64_t(WPR == 1 ? threadIdx.x & 63 : threadIdx.x) * V;
   const float inv_c = 1.0f / float(C);
@@ -274,36 +280,42 @@ __global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward
   float* pw = partial + int64_t(blockIdx.x) * C;
   float* pb = pw + int64_t(gridDim.x) * C;
   if constexpr (WPR == 1) {
-    // the waves' shares, added in wave order
-    for (int w = 0; w < kRowWaves; ++w) {
-      if (wave == w) {
+    // the waves' shares, halved three times: the upper half's waves hand theirs
+    // to the lower half's
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int it = 0; it < NIT; ++it)
+    for (int half = kRowWaves / 2; half >= 1; half >>= 1) {
+      if (wave >= half && wave < 2 * half) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int at = int(c0 + it * STEP) + i;
-            acc[at] = (w ? acc[at] : 0.0f) + dw[it][i];
-            acc[NIT * STEP + at] = (w ? acc[NIT * STEP + at] : 0.0f) + db[it][i];
-          }
+        for (int q = 0; q < Q / 2; ++q) {
+          const int it = q * 4 / V, i = q * 4 % V;
+          float4* at = acc + (wave - half) * Q * 64 + lane;
+          at[q * 64] = make_float4(dw[it][i], dw[it][i + 1], dw[it][i + 2], dw[it][i + 3]);
+          at[(Q / 2 + q) * 64] = make_float4(db[it][i], db[it][i + 1], db[it][i + 2], db[it][i + 3]);
+        }
+      }
+      __syncthreads();
+      if (wave < half) {
+#pragma unroll
+        for (int q = 0; q < Q / 2; ++q) {
+          const int it = q * 4 / V, i = q * 4 % V;
+          const float4* at = acc + wave * Q * 64 + lane;
+          const float4 a = at[q * 64], b = at[(Q / 2 + q) * 64];
+          dw[it][i] += a.x, dw[it][i + 1] += a.y, dw[it][i + 2] += a.z, dw[it][i + 3] += a.w;
+          db[it][i] += b.x, db[it][i + 1] += b.y, db[it][i + 2] += b.z, db[it][i + 3] += b.w;
+        }
       }
       __syncthreads();
     }
-    for (int64_t c = threadIdx.x; c < C; c += 64 * kRowWaves) {
-      pw[c] = acc[c];
-      pb[c] = acc[NIT * STEP + c];
-    }
-  } else {
-#pragma unroll
-    for (int it = 0; it < NIT; ++it)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int64_t c = c0 + it * STEP + i;
-        if (c < C) {
-          pw[c] = dw[it][i];
-          pb[c] = db[it][i];
-        }
-      }
+    if (wave != 0) return;
   }
+#pragma unroll
+  for (int it = 0; it < NIT; ++it)
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      store_row(pw, c0 + it * STEP + i, C, pack4f(&dw[it][i]));
+      store_row(pb, c0 + it * STEP + i, C, pack4f(&db[it][i]));
+    }
 }
 
 // ---------------------------------------------------------------------------
