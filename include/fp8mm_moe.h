@@ -95,7 +95,7 @@ fp8mm_status fp8mm_moe_route(const void* logits, fp8mm_dtype dtype, int64_t T, i
  *   1e-20 if renormalize;  softmax: s_e (d_e - sum_l s_l d_l);
  *   sigmoid: s_e (1 - s_e) d_e
  * logits, ids, score, renormalize and scale: as in the forward; ids outside
- * [0, E) are empty slots.  grad_weights: float32 [T, k]; grad_logits: [T, E]
+ * [0, E) are empty slots, a token's others differ.  grad_weights: float32 [T, k]; grad_logits: [T, E]
  * of `dtype`, row stride ld_grad >= E, written whole. */
 fp8mm_status fp8mm_moe_route_backward(const float* grad_weights, const void* logits, fp8mm_dtype dtype, int64_t T,
                                       int64_t E, int64_t ld, const int32_t* ids, int64_t k, fp8mm_score score,

@@ -20,7 +20,8 @@
 // k <= 16), and one wave a token.  16384 tokens in us, the calls of the other
 // form in brackets: 256 experts in 8 groups, sigmoid and bias, k = 8: 12.6 (17.8);
 // 256 experts, softmax and bias: 10.8 (15.3); 128 experts 7.7 (11.5); 64 experts,
-// k = 6: 7.6 (8.4), about what a call takes the host.
+// k = 6: 7.6 (8.4), about what a call takes the host.  Backward of 64 experts: 4.3
+// in the kernel (7.3); of 256, softmax, k = 8: 10.9 (12.7).
 #include "moe_launch.hpp"
 #include "ops_common.hpp"
 
@@ -43,6 +44,23 @@ __device__ __forceinline__ void load_row_of(const T* row, int e0, int E, float (
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = e0 + i < E ? to_float(row[e0 + i]) : -kInf;
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_row_of(T* row, int e0, int E, const float (&g)[N]) {
+  struct __attribute__((packed, aligned(sizeof(T)))) At {
+    T v[N];
+  };
+  if (e0 + N <= E) {
+    At a;
+#pragma unroll
+    for (int i = 0; i < N; ++i) a.v[i] = from_float<T>(g[i]);
+    *reinterpret_cast<At*>(row + e0) = a;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (e0 + i < E) row[e0 + i] = from_float<T>(g[i]);
   }
 }
 
@@ -453,19 +471,63 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
       const float s = score(x[i]);
       g[i] = SIGMOID ? s * (1.0f - s) * de[i] : s * (de[i] - dot);
     }
-    struct __attribute__((packed, aligned(sizeof(T)))) At {
-      T v[N];
-    };
-    if (e0 + N <= p.E) {
-      At a;
+    store_row_of(out, e0, p.E, g);
+  }
+}
+
+// The same for at most 256 experts and 16 slots, four tokens a wave (see
+// route16_kernel).  Scores and gradients of single experts change lanes through
+// LDS, 16 V values a token.
+template <typename T, int V, bool SIGMOID>
+__global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProblem p) {
+  __shared__ __attribute__((aligned(16))) float lds[16][16 * V];
+  const int lane = threadIdx.x & 63;
+  const int l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int e0 = l16 * V;
+  float* values = lds[threadIdx.x >> 4];
+  for (int64_t row0 = (int64_t(blockIdx.x) * 4 + wave) * 4; row0 < p.T; row0 += int64_t(gridDim.x) * 16) {
+    const int64_t own = row0 + (lane >> 4);
+    const int64_t row = min(own, p.T - 1);       // lanes past the last token repeat it and write nothing
+    const int id = l16 < p.k ? p.ids[row * p.k + l16] : -1;
+    const bool used = id >= 0 && id < p.E;
+    float d = l16 < p.k ? p.grad_weights[row * p.k + l16] * p.scale : 0.0f;
+    d = used ? d : 0.0f;
+    float x[V], s[V];
+    load_row_of(static_cast<const T*>(p.logits) + row * p.ld, e0, p.E, x);
+    const Scores<SIGMOID, true> score(x);
 #pragma unroll
-      for (int i = 0; i < N; ++i) a.v[i] = from_float<T>(g[i]);
-      *reinterpret_cast<At*>(out + e0) = a;
-    } else {
+    for (int i = 0; i < V; ++i) s[i] = score(x[i]);
+    float4* mine = reinterpret_cast<float4*>(values + e0);
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (e0 + i < p.E) out[e0 + i] = from_float<T>(g[i]);
+    for (int i = 0; i < V; i += 4) mine[i / 4] = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+    // a wave's LDS accesses are in order: the fences only keep the compiler's
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float sj = values[used ? id : 0];
+    sj = used ? sj : 0.0f;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < V; i += 4) mine[i / 4] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (p.renorm) {
+      // the sums take every lane: outside the choice of d
+      const float total = row_sum_f(sj) + kRenormEps;
+      const float mean = row_sum_f(d * sj) / total;
+      d = used ? (d - mean) / total : 0.0f;
     }
+    const float dot = SIGMOID ? 0.0f : row_sum_f(sj * d);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (used) atomicAdd(&values[id], d);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float g[V];
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 de = mine[i / 4];
+      g[i] = de.x, g[i + 1] = de.y, g[i + 2] = de.z, g[i + 3] = de.w;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = SIGMOID ? s[i] * (1.0f - s[i]) * g[i] : s[i] * (g[i] - dot);
+    if (own < p.T) store_row_of(static_cast<T*>(p.grad_logits) + own * p.ld_grad, e0, p.E, g);
   }
 }
 
@@ -502,8 +564,20 @@ hipError_t run_route16(const RouteProblem& p, hipStream_t st) {
   return groups ? run(route16_kernel<V, SIGMOID, false, true>) : run(route16_kernel<V, SIGMOID, false, false>);
 }
 
+template <int V, bool SIGMOID>
+hipError_t run_route_backward16(const RouteProblem& p, hipStream_t st) {
+  const int64_t blocks = (p.T + 15) / 16;
+  const dim3 grid(unsigned(blocks < 4096 ? blocks : 4096));
+  if (p.fp32)
+    hipLaunchKernelGGL((route_backward16_kernel<float, V, SIGMOID>), grid, dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((route_backward16_kernel<uint16_t, V, SIGMOID>), grid, dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
 template <int V>
-hipError_t route16_of(const RouteProblem& p, hipStream_t st) {
+hipError_t route16_of(const RouteProblem& p, bool backward, hipStream_t st) {
+  if (backward) return p.sigmoid ? run_route_backward16<V, true>(p, st) : run_route_backward16<V, false>(p, st);
   return p.sigmoid ? run_route16<V, true>(p, st) : run_route16<V, false>(p, st);
 }
 
@@ -529,11 +603,9 @@ hipError_t route_of(const RouteProblem& p, bool backward, hipStream_t st) {
 
 hipError_t route_any(const RouteProblem& p, bool backward, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  if (!backward) {
-    if (takes_route16(p, 4)) return route16_of<4>(p, st);
-    if (takes_route16(p, 8)) return route16_of<8>(p, st);
-    if (takes_route16(p, 16)) return route16_of<16>(p, st);
-  }
+  if (takes_route16(p, 4)) return route16_of<4>(p, backward, st);
+  if (takes_route16(p, 8)) return route16_of<8>(p, backward, st);
+  if (takes_route16(p, 16)) return route16_of<16>(p, backward, st);
   if (p.E <= 64) return route_of<1>(p, backward, st);
   if (p.E <= 128) return route_of<2>(p, backward, st);
   if (p.E <= 256) return route_of<4>(p, backward, st);
