@@ -96,7 +96,8 @@ fp8mm_status fp8mm_moe_route(const void* logits, fp8mm_dtype dtype, int64_t T, i
  *   sigmoid: s_e (1 - s_e) d_e
  * logits, ids, score, renormalize and scale: as in the forward; ids outside
  * [0, E) are empty slots, a token's others differ.  grad_weights: float32 [T, k]; grad_logits: [T, E]
- * of `dtype`, row stride ld_grad >= E, written whole. */
+ * of `dtype`, row stride ld_grad >= E, written whole; a row with a NaN logit (or
+ * +inf under softmax) gets NaN. */
 fp8mm_status fp8mm_moe_route_backward(const float* grad_weights, const void* logits, fp8mm_dtype dtype, int64_t T,
                                       int64_t E, int64_t ld, const int32_t* ids, int64_t k, fp8mm_score score,
                                       int renormalize, float scale, void* grad_logits, int64_t ld_grad,

@@ -118,12 +118,29 @@ struct Scores {
     }
   }
 
+  // For the backward: the sigmoid with its division rounded once.  Where one slot
+  // holds nearly all of the renormalised weight, the gradient is a difference of
+  // nearly equal terms and every bit of the score shows in it.
+  __device__ __forceinline__ float rounded(float x) const {
+    if constexpr (!SIGMOID) return (*this)(x);
+    return 1.0f / (1.0f + expf(-x));
+  }
+
   __device__ __forceinline__ float operator()(float x) const {
     if constexpr (!SIGMOID) return exp_neg(shift - x) * inv;
     const float e = exp_neg(fabsf(x));
     return (x < 0.0f ? e : 1.0f) * reciprocal(1.0f + e);
   }
 };
+
+// Whether a lane's logits leave its row without a defined choice.
+template <bool SIGMOID, int N>
+__device__ __forceinline__ bool undefined_logits(const float (&x)[N]) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) bad |= SIGMOID ? x[i] != x[i] : !(x[i] < kInf);
+  return bad;
+}
 
 // Group selection: keys of experts outside the chosen groups become -inf.  L
 // lanes work on each group: where a group is a power of two of whole lanes,
@@ -237,9 +254,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteProblem p, const 
   for (int64_t row = int64_t(blockIdx.x) * 4 + wave; row < p.T; row += int64_t(gridDim.x) * 4) {
     float x[N], key[N];
     load_logits(p, row, e0, x);
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < N; ++i) bad |= SIGMOID ? x[i] != x[i] : !(x[i] < kInf);
+    bool bad = undefined_logits<SIGMOID>(x);
     const Scores<SIGMOID> score(x);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -334,9 +349,7 @@ __global__ __launch_bounds__(256) void route16_kernel(const RouteProblem p, cons
     const int64_t row = min(own, p.T - 1);       // lanes past the last token repeat it and write nothing
     float x[V], key[V];
     load_logits(p, row, e0, x);
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) bad |= SIGMOID ? x[i] != x[i] : !(x[i] < kInf);
+    bool bad = undefined_logits<SIGMOID>(x);
     const Scores<SIGMOID, true> score(x);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -431,7 +444,8 @@ __global__ __launch_bounds__(256) void route16_kernel(const RouteProblem p, cons
 //   d_j = scale g_j                                     (weights as they are)
 //   d_j = scale (g_j - sum_l g_l s_l / S) / S, S = sum_l s_l + 1e-20   (renormalised)
 // the logits get  softmax: s_e (d_e - sum_l s_l d_l),  sigmoid: s_e (1 - s_e) d_e
-// (d_e = 0 for experts not chosen).  The choice itself has no gradient.
+// (d_e = 0 for experts not chosen).  The choice itself has no gradient; a row
+// whose choice is undefined gets NaN.
 template <typename T, int N, bool SIGMOID>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem p) {
   const int lane = threadIdx.x & 63;
@@ -446,7 +460,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
     float x[N];
     load_row_of(logits, e0, p.E, x);
     const Scores<SIGMOID> score(x);
-    float sj = score(xj);
+    float sj = score.rounded(xj);
     sj = used ? sj : 0.0f;
     if (p.renorm) {
       // the sums take every lane: outside the choice of d
@@ -455,6 +469,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
       d = used ? (d - mean) / total : 0.0f;
     }
     const float dot = SIGMOID ? 0.0f : wave_sum(sj * d);
+    const bool undefined = __ballot(undefined_logits<SIGMOID>(x)) != 0;
     float de[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) de[i] = 0.0f;
@@ -468,8 +483,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
     float g[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float s = score(x[i]);
+      const float s = score.rounded(x[i]);
       g[i] = SIGMOID ? s * (1.0f - s) * de[i] : s * (de[i] - dot);
+      g[i] = undefined ? __builtin_nanf("") : g[i];
     }
     store_row_of(out, e0, p.E, g);
   }
@@ -497,7 +513,7 @@ __global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProble
     load_row_of(static_cast<const T*>(p.logits) + row * p.ld, e0, p.E, x);
     const Scores<SIGMOID, true> score(x);
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = score(x[i]);
+    for (int i = 0; i < V; ++i) s[i] = score.rounded(x[i]);
     float4* mine = reinterpret_cast<float4*>(values + e0);
 #pragma unroll
     for (int i = 0; i < V; i += 4) mine[i / 4] = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
@@ -515,6 +531,7 @@ __global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProble
       d = used ? (d - mean) / total : 0.0f;
     }
     const float dot = SIGMOID ? 0.0f : row_sum_f(sj * d);
+    const bool undefined = row_max_u(undefined_logits<SIGMOID>(x) ? 1u : 0u) != 0;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (used) atomicAdd(&values[id], d);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -526,7 +543,10 @@ __global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProble
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int i = 0; i < V; ++i) g[i] = SIGMOID ? s[i] * (1.0f - s[i]) * g[i] : s[i] * (g[i] - dot);
+    for (int i = 0; i < V; ++i) {
+      g[i] = SIGMOID ? s[i] * (1.0f - s[i]) * g[i] : s[i] * (g[i] - dot);
+      g[i] = undefined ? __builtin_nanf("") : g[i];
+    }
     if (own < p.T) store_row_of(static_cast<T*>(p.grad_logits) + own * p.ld_grad, e0, p.E, g);
   }
 }

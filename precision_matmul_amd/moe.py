@@ -469,6 +469,15 @@ def _weight_codes(w):
     return q.view(E, N, K), s.view(E, N // 128, K // 128)
 
 
+def _experts_mm(q, s, w_q, w_s, offsets, layout="NK"):
+    """The grouped product of expert-order rows in the blockwise recipe.  Rows of
+    slots without an expert are left unwritten: nothing that follows lets them
+    into a row that has one (combine and the per-expert quantizers skip them)."""
+    N = w_q.shape[1 if layout == "NK" else 2]
+    out = q.new_empty((q.shape[0], N), dtype=torch.bfloat16)
+    return fp8_scaled_grouped_mm_v2(q, w_q, offsets, s, "1x128", w_s, "128x128", b_layout=layout, out=out)
+
+
 class FP8MoE(torch.autograd.Function):
     """The experts of a mixture-of-experts block on routed tokens,
 
@@ -505,9 +514,9 @@ class FP8MoE(torch.autograd.Function):
         q_in, s_in = _weight_codes(w_in)
         q_out, s_out = _weight_codes(w_out)
         q, s = fp8_moe_dispatch(x, row_of_slot)
-        gate_up = fp8_scaled_grouped_mm_v2(q, q_in, offsets, s, "1x128", s_in, "128x128")
+        gate_up = _experts_mm(q, s, q_in, s_in, offsets)
         (hq, hs), checkpoint = fp8_swiglu_forward(gate_up, "fp8", train)
-        rows = fp8_scaled_grouped_mm_v2(hq, q_out, offsets, hs, "1x128", s_out, "128x128")
+        rows = _experts_mm(hq, hs, q_out, s_out, offsets)
         if train:
             ctx.save_for_backward(x, q_in, s_in, q_out, s_out, *checkpoint, rows, offsets, row_of_slot, weights)
         return moe_combine_forward(rows, row_of_slot, weights)
@@ -527,7 +536,7 @@ class FP8MoE(torch.autograd.Function):
                 qg, sg, qgt, sgt = fp8_quantize_grouped_dual(grad_rows, offsets)
             else:
                 qg, sg = fp8_quantize_blockwise(grad_rows, (1, 128))
-            grad_h = fp8_scaled_grouped_mm_v2(qg, q_out, offsets, sg, "1x128", s_out, "128x128", b_layout="KN")
+            grad_h = _experts_mm(qg, sg, q_out, s_out, offsets, "KN")
             grad_gate_up, h = fp8_swiglu_backward(grad_h, codes, scale, recompute=need_out)
             if need_out:
                 qht, sht = fp8_quantize_grouped_128x1(h, offsets)
@@ -539,7 +548,7 @@ class FP8MoE(torch.autograd.Function):
             elif need_x:
                 qg, sg = fp8_quantize_blockwise(grad_gate_up, (1, 128))
             if need_x:
-                grad_rows = fp8_scaled_grouped_mm_v2(qg, q_in, offsets, sg, "1x128", s_in, "128x128", b_layout="KN")
+                grad_rows = _experts_mm(qg, sg, q_in, s_in, offsets, "KN")
                 grad_x = moe_combine_forward(grad_rows, row_of_slot)
         return grad_x, grad_in, grad_w_out, None, grad_weights
 

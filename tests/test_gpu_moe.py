@@ -314,6 +314,17 @@ def test_route_undefined_rows_show():
     assert torch.isnan(w).any(1).tolist() == [False, True, False, False]
 
 
+@pytest.mark.parametrize("E", [100, 300])
+def test_route_gradients_of_undefined_rows_show(E):
+    logits = torch.zeros((4, E), device=DEV)
+    logits[1, 70], logits[2, E - 1] = float("nan"), float("inf")
+    ids = torch.tensor([[0, 1]] * 4, dtype=torch.int32, device=DEV)
+    g = torch.ones((4, 2), device=DEV)
+    for score, bad in (("softmax", [False, True, True, False]), ("sigmoid", [False, True, False, False])):
+        grad = fp8mm.moe_route_backward(g, logits, ids, score, renormalize=False)
+        assert torch.isnan(grad).all(1).tolist() == bad and torch.isnan(grad).any(1).tolist() == bad
+
+
 def test_route_many_tokens_and_autograd():
     T, E, k = 9001, 64, 6
     logits, lv, _, _ = _route_data(T, E, False, "fp32", 3)
