@@ -322,19 +322,25 @@ __global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward
 // Backward of few rows in one launch and without a workspace.  dw and db need
 // no row sums (mean and rstd are inputs), so the first row_blocks workgroups
 // write dx, a row a wave (WPR = 1) or a workgroup, and the others each add up a
-// strip of 16 chunks of columns over all rows: 16 row slices, added in order.
-// x and dy come from HBM once and from the L2s the second time.  500 x 8192 bf16:
-// 11.6 us against 26.7 in two launches, 300 x 2048 11.3 against 15.5 (the host's
-// part of a call); from 1000 rows on the two launches are the faster form (2000 x
-// 2048 19 against 30 us).
+// strip of columns over all rows, 64 (WPR = 1) or 16 row slices of it, the slices
+// added in a fixed order.  x and dy come from HBM once and from the L2s the second
+// time.  500 x 8192 bf16: 11.5 us against 21.9 in two launches, 455 x 195 10.8
+// against 14.6 (the host's part of a call; 23 with strips of 16 chunks); from 1000
+// rows on the two launches are the faster form (1000 x 300 14 against 20 us).
 // ---------------------------------------------------------------------------
+// Chunks of columns of a strip: narrow where rows are short, so that there are
+// enough strips.
+template <int WPR>
+constexpr int kStripChunks = WPR == 1 ? 4 : 16;
+
 template <typename T, typename P, int WPR, int NIT>
 __global__ __launch_bounds__(256) void norm_backward_few_kernel(
     const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ x, int64_t ld_x, int64_t R, int64_t C,
     const P* __restrict__ weight, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
     T* __restrict__ dx, int64_t ld_dx, P* __restrict__ dweight, P* __restrict__ dbias, unsigned row_blocks) {
   constexpr int V = kVec<T>;
-  __shared__ float part[2][16][16 * V];
+  constexpr int CL = kStripChunks<WPR>, SLICES = 256 / CL;
+  __shared__ float part[2][SLICES][CL * V];
   if (blockIdx.x < row_blocks) {
     constexpr int64_t STEP = int64_t(WPR) * 64 * V;
     const int64_t row = WPR == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
@@ -387,14 +393,14 @@ __global__ __launch_bounds__(256) void norm_backward_few_kernel(
     }
     return;
   }
-  const int chunk = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int64_t strip = int64_t(blockIdx.x - row_blocks) * 16 * V;
+  const int chunk = threadIdx.x % CL, slice = threadIdx.x / CL;
+  const int64_t strip = int64_t(blockIdx.x - row_blocks) * CL * V;
   const int64_t c = strip + chunk * V;
   float dw[V], db[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.0f;
 #pragma unroll 4
-  for (int64_t row = slice; row < R; row += 16) {
+  for (int64_t row = slice; row < R; row += SLICES) {
     float f[V], g[V];
     unpack<T>(load_row(x + row * ld_x, c, C), f);
     unpack<T>(load_row(dy + row * ld_dy, c, C), g);
@@ -411,15 +417,18 @@ __global__ __launch_bounds__(256) void norm_backward_few_kernel(
     part[1][slice][chunk * V + i] = db[i];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * V; i += 256) {
-    const int which = i / (16 * V), col = i - which * 16 * V;
-    P* out = which ? dbias : dweight;
-    if (!out || strip + col >= C) continue;
-    float s = 0.0f;
+  // SHARE neighbouring threads add up a column's slices
+  constexpr int SHARE = 256 / (2 * CL * V);
+  static_assert(SHARE >= 1 && SHARE <= SLICES && (SHARE & (SHARE - 1)) == 0, "a column or more for each thread");
+  const int column = threadIdx.x / SHARE, share = threadIdx.x % SHARE;
+  const int which = column / (CL * V), col = column - which * CL * V;
+  float s = 0.0f;
+#pragma unroll 16
+  for (int r = share; r < SLICES; r += SHARE) s += part[which][r][col];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s += part[which][r][col];
-    out[strip + col] = from_float<P>(s);
-  }
+  for (int off = 1; off < SHARE; off <<= 1) s += __shfl_xor(s, off, 64);
+  P* out = which ? dbias : dweight;
+  if (share == 0 && out && strip + col < C) out[strip + col] = from_float<P>(s);
 }
 
 // Backward of rows too long for registers: dx by one workgroup a row ...
@@ -563,7 +572,7 @@ template <typename T, typename P, int WPR, int NIT>
 hipError_t run_backward(const NormProblem& p, int grid, float* partial, hipStream_t st) {
   if (few_rows(p.R, p.C)) {
     const int64_t rows = p.out ? (WPR == 1 ? (p.R + 3) / 4 : p.R) : 0;
-    const int64_t strips = p.dweight || p.dbias ? (p.C + 16 * kVec<T> - 1) / (16 * kVec<T>) : 0;
+    const int64_t strips = p.dweight || p.dbias ? (p.C + kStripChunks<WPR> * kVec<T> - 1) / (kStripChunks<WPR> * kVec<T>) : 0;
     hipLaunchKernelGGL((norm_backward_few_kernel<T, P, WPR, NIT>), dim3(unsigned(rows + strips)), dim3(256), 0, st,
                        static_cast<const T*>(p.dy), p.ld_dy, static_cast<const T*>(p.x), p.ld_x, p.R, p.C,
                        static_cast<const P*>(p.weight), p.mean, p.rstd, static_cast<T*>(p.out), p.ld_out,
