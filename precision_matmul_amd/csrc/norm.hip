@@ -169,12 +169,14 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
 // traffic of their own (8 gridDim C bytes each way), so there are no more
 // workgroups than run at once: 256 of eight waves with a row each, or, above
 // 4 chunks a lane, 512 of four waves that share a row (256 above 6144 columns,
-// where the registers leave room for one workgroup a compute unit).
+// where the registers leave room for one workgroup a compute unit, and below 2048
+// rows, where a partial row would stand for one or two rows).
 // 16384 x 2048 bf16: 43 us with the column sums, 4.7 TB/s of x, dy and dx; without
 // dw and db 37 us, what a sum of two such matrices takes (512 partial rows of
 // eight-wave workgroups 55 us; no row in flight ahead 55; the waves' shares added
 // one wave after the other 45).  16000 x 4096: 76 us (1024 partial rows 93);
-// 10000 x 8192: 94 us (512: 111); 7534 x 3560 fp32: 68 us (256: 90, 1024: 85).
+// 10000 x 8192: 94 us (512: 111); 7534 x 3560 fp32: 68 us (256: 90, 1024: 85);
+// 700 x 5120: 17.3 us (512: 21.6).
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 
@@ -531,7 +533,7 @@ bool streams(const NormProblem& p, size_t size) { return p.R * p.C * int64_t(siz
 int backward_grid(int64_t R, int64_t C, int vec) {
   const int64_t one_wave = 256 * vec;         // rows of up to this many columns: a wave each
   const int64_t rows = C <= one_wave ? kRowWaves : 1;
-  const int64_t most = C <= one_wave || C > 6144 ? 256 : 512;
+  const int64_t most = C <= one_wave || C > 6144 || R < 2048 ? 256 : 512;
   const int64_t blocks = (R + rows - 1) / rows;
   return int(blocks < most ? blocks : most);
 }
