@@ -36,6 +36,18 @@ __device__ __forceinline__ float row_sum(float v, float (&part)[2][WPR], int slo
   return s;
 }
 
+// The next row's chunks.  PART: the row ends within a chunk, and the four waves
+// that share it would all wait for that chunk's single elements where they are
+// asked for; it is loaded whole and shifted when its turn comes.
+template <typename T, bool NT, bool PART>
+__device__ __forceinline__ Chunk fetch(const T* row, int64_t c, int64_t C) {
+  return PART ? fetch_row<T, NT>(row, c, C) : load_row<T, NT>(row, c, C);
+}
+template <typename T, bool PART>
+__device__ __forceinline__ Chunk settle(const Chunk& v, int64_t c, int64_t C) {
+  return PART ? fetched<T>(v, c, C) : v;
+}
+
 // ---------------------------------------------------------------------------
 // Forward, row in registers: WPR waves a row, NIT chunks a lane.  A workgroup
 // takes rows blockIdx, blockIdx + gridDim, ...; a lane's columns are the same
@@ -45,7 +57,7 @@ __device__ __forceinline__ float row_sum(float v, float (&part)[2][WPR], int slo
 // 5.6 TB/s, more than a plain copy reaches (one row a workgroup, parameters
 // read again for each: 85 us; one wave a row: 102 us; plain accesses: 66 us).
 // ---------------------------------------------------------------------------
-template <typename T, typename P, int WPR, int NIT, bool NT>
+template <typename T, typename P, int WPR, int NIT, bool NT, bool PART>
 __global__ __launch_bounds__(256) void norm_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld_x,
                                                    const P* __restrict__ weight, const P* __restrict__ bias, float eps,
                                                    T* __restrict__ y, int64_t ld_y, float* __restrict__ mean_out,
@@ -67,14 +79,14 @@ __global__ __launch_bounds__(256) void norm_kernel(const T* __restrict__ x, int6
   Chunk next[NIT];
 #pragma unroll
   for (int it = 0; it < NIT; ++it)
-    if (row < R) next[it] = load_row<T, NT>(x + row * ld_x, c0 + it * STEP, C);
+    if (row < R) next[it] = fetch<T, NT, PART>(x + row * ld_x, c0 + it * STEP, C);
   for (; row < R; row += stride) {                // all waves of a row take the same turns
     Chunk v[NIT];
 #pragma unroll
-    for (int it = 0; it < NIT; ++it) v[it] = next[it];
+    for (int it = 0; it < NIT; ++it) v[it] = settle<T, PART>(next[it], c0 + it * STEP, C);
     if (row + stride < R) {
 #pragma unroll
-      for (int it = 0; it < NIT; ++it) next[it] = load_row<T, NT>(x + (row + stride) * ld_x, c0 + it * STEP, C);
+      for (int it = 0; it < NIT; ++it) next[it] = fetch<T, NT, PART>(x + (row + stride) * ld_x, c0 + it * STEP, C);
     }
     float s = 0.0f;
 #pragma unroll
@@ -176,11 +188,11 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
 // eight-wave workgroups 55 us; no row in flight ahead 55; the waves' shares added
 // one wave after the other 45).  16000 x 4096: 76 us (1024 partial rows 93);
 // 10000 x 8192: 94 us (512: 111); 7534 x 3560 fp32: 68 us (256: 90, 1024: 85);
-// 700 x 5120: 17.3 us (512: 21.6).
+// 700 x 5120: 17.3 us (512: 21.6).  7534 x 3559: 49 us (84 without PART).
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 
-template <typename T, typename P, int WPR, int NIT, bool NT>
+template <typename T, typename P, int WPR, int NIT, bool NT, bool PART>
 __global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward_kernel(
     const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ x, int64_t ld_x, int64_t R, int64_t C,
     const P* __restrict__ weight, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
@@ -210,8 +222,8 @@ __global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward
   if (row < R) {
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
-      nx[it] = load_row<T, NT>(x + row * ld_x, c0 + it * STEP, C);
-      ng[it] = load_row<T, NT>(dy + row * ld_dy, c0 + it * STEP, C);
+      nx[it] = fetch<T, NT, PART>(x + row * ld_x, c0 + it * STEP, C);
+      ng[it] = fetch<T, NT, PART>(dy + row * ld_dy, c0 + it * STEP, C);
     }
     nmean = mean_in[row];
     nrstd = rstd_in[row];
@@ -220,15 +232,15 @@ __global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward
     Chunk vx[NIT], vg[NIT];
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
-      vx[it] = nx[it];
-      vg[it] = ng[it];
+      vx[it] = settle<T, PART>(nx[it], c0 + it * STEP, C);
+      vg[it] = settle<T, PART>(ng[it], c0 + it * STEP, C);
     }
     const float mean = nmean, rstd = nrstd;
     if (row + stride < R) {
 #pragma unroll
       for (int it = 0; it < NIT; ++it) {
-        nx[it] = load_row<T, NT>(x + (row + stride) * ld_x, c0 + it * STEP, C);
-        ng[it] = load_row<T, NT>(dy + (row + stride) * ld_dy, c0 + it * STEP, C);
+        nx[it] = fetch<T, NT, PART>(x + (row + stride) * ld_x, c0 + it * STEP, C);
+        ng[it] = fetch<T, NT, PART>(dy + (row + stride) * ld_dy, c0 + it * STEP, C);
       }
       nmean = mean_in[row + stride];
       nrstd = rstd_in[row + stride];
@@ -549,7 +561,12 @@ hipError_t run_norm(const NormProblem& p, hipStream_t st) {
                        p.ld_out, p.mean, p.rstd);
     return hipGetLastError();
   };
-  return streams(p, sizeof(T)) ? run(norm_kernel<T, P, WPR, NIT, true>) : run(norm_kernel<T, P, WPR, NIT, false>);
+  const bool nt = streams(p, sizeof(T));
+  if (WPR > 1 && p.C % kVec<T> != 0) {
+    constexpr bool PART = WPR > 1;
+    return nt ? run(norm_kernel<T, P, WPR, NIT, true, PART>) : run(norm_kernel<T, P, WPR, NIT, false, PART>);
+  }
+  return nt ? run(norm_kernel<T, P, WPR, NIT, true, false>) : run(norm_kernel<T, P, WPR, NIT, false, false>);
 }
 
 template <typename T, typename P>
@@ -587,8 +604,14 @@ hipError_t run_backward(const NormProblem& p, int grid, float* partial, hipStrea
                        static_cast<const P*>(p.weight), p.mean, p.rstd, static_cast<T*>(p.out), p.ld_out, partial);
     return hipGetLastError();
   };
-  return streams(p, sizeof(T)) ? run(norm_backward_kernel<T, P, WPR, NIT, true>)
-                               : run(norm_backward_kernel<T, P, WPR, NIT, false>);
+  const bool nt = streams(p, sizeof(T));
+  if (WPR > 1 && p.C % kVec<T> != 0) {
+    constexpr bool PART = WPR > 1;
+    return nt ? run(norm_backward_kernel<T, P, WPR, NIT, true, PART>)
+              : run(norm_backward_kernel<T, P, WPR, NIT, false, PART>);
+  }
+  return nt ? run(norm_backward_kernel<T, P, WPR, NIT, true, false>)
+            : run(norm_backward_kernel<T, P, WPR, NIT, false, false>);
 }
 
 template <typename T, typename P>
