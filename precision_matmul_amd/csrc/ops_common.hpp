@@ -105,16 +105,15 @@ __device__ __forceinline__ Chunk load_row(const T* row, int64_t c, int64_t C) {
 template <typename T, bool NT = false>
 __device__ __forceinline__ Chunk fetch_row(const T* row, int64_t c, int64_t C) {
   if (C < kVec<T>) return load_row(row, c, C);
+  if (c >= C) return Chunk{{0u, 0u, 0u, 0u}};
   const T* p = row + min(c, C - kVec<T>);
   return NT ? load_chunk_nt(p) : load_chunk(p);
 }
 
 template <typename T>
 __device__ __forceinline__ Chunk fetched(const Chunk& v, int64_t c, int64_t C) {
-  if (C < kVec<T> || c + kVec<T> <= C) return v;
-  const int64_t past = c + kVec<T> - C;         // elements past the end; all of them from kVec on
-  if (past >= kVec<T>) return Chunk{{0u, 0u, 0u, 0u}};
-  const int n = int(past) * int(sizeof(T)) * 8;
+  if (C < kVec<T> || c + kVec<T> <= C || c >= C) return v;
+  const int n = int(c + kVec<T> - C) * int(sizeof(T)) * 8;     // bits of the elements past the end
   const uint64_t lo = uint64_t(v.w[1]) << 32 | v.w[0], hi = uint64_t(v.w[3]) << 32 | v.w[2];
   const uint64_t a = n < 64 ? lo >> n | hi << (64 - n) : hi >> (n - 64), b = n < 64 ? hi >> n : 0;
   return Chunk{{uint32_t(a), uint32_t(a >> 32), uint32_t(b), uint32_t(b >> 32)}};

@@ -211,7 +211,8 @@ __global__ __launch_bounds__(256) void dispatch_fp8_kernel(const PermuteProblem 
 // ---------------------------------------------------------------------------
 // Combine: one wave an item of 64 chunks of one token; its k rows are added in
 // slot order in float32.  HBM-bound: (k + 1) rows a token.  16384 x 2048 x 6: 80
-// us, 5.9 TB/s; 4099 x 2048 x 6, 1 of 20 slots empty: 21 us, 5.2 TB/s.
+// us, 5.9 TB/s; 4099 x 2048 x 6, 1 of 20 slots empty: 21 us, 5.2 TB/s; 8000 x
+// 2375 x 4: 38 us (47 where a row's last elements are loaded one by one).
 // ---------------------------------------------------------------------------
 template <typename T, bool NT>
 __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, int strips) {
@@ -231,7 +232,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, in
     if (!s.used || s.row >= M) continue;
     const float w = p.weights ? p.weights[int64_t(token) * p.k + j] : 1.0f;
     float f[V];
-    unpack<T>(load_row<T, NT>(static_cast<const T*>(p.rows) + s.row * p.ld_rows, c, p.C), f);
+    const T* row = static_cast<const T*>(p.rows) + s.row * p.ld_rows;
+    unpack<T>(fetched<T>(fetch_row<T, NT>(row, c, p.C), c, p.C), f);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] += w * f[i];
   }
