@@ -61,6 +61,24 @@ NORM_SHAPES = [(1, 1), (3, 7), (5, 64), (4, 513), (9, 1024), (2, 1413), (7, 2048
                (2, 6200), (3, 8192), (2, 8193), (2, 20001)]
 
 
+def _check_norm_forward(x, xv, w, wv, b, bv, eps, dtype):
+    R, C = xv.shape
+    half, D = BF16 if dtype == "bf16" else U, _depth(C) + 4
+    y, mean, rstd = fp8mm.layer_norm_forward(x, w, b, eps)
+    ref, rmean, rrstd = moe.layer_norm(xv, wv, bv, eps)
+    wa = np.ones(C) if wv is None else np.abs(wv)
+    ba = np.zeros(C) if bv is None else np.abs(bv)
+    e_mean = D * U * np.abs(xv).mean(1)
+    std = 1 / rrstd
+    e_rstd = rrstd * (2 * e_mean / std + D * U)
+    _within(_f64(mean), rmean, e_mean, "mean")
+    _within(_f64(rstd), rrstd, e_rstd, "rstd")
+    xh = (xv - rmean[:, None]) * rrstd[:, None]
+    tol = wa * (rrstd * e_mean)[:, None] + np.abs(xh) * wa * (e_rstd / rrstd + 6 * U)[:, None] + 4 * U * ba
+    _within(_f64(y), ref, tol + half * np.abs(ref) * (1 + half) + half * tol + TINY, "y")
+    return y, mean, rstd
+
+
 def _check_norm_backward(x, xv, dy, dyv, w, wv, mean, rstd, dtype, params):
     """layer_norm_backward against the formula with the same mean and rstd."""
     R, C = xv.shape
@@ -112,27 +130,28 @@ def test_layer_norm(R, C, dtype, params):
     if params:
         w, wv = _dev(1 + 0.3 * r.standard_normal(C), DT[params])
         b, bv = _dev(r.standard_normal(C), DT[params])
-    half = BF16 if dtype == "bf16" else U
-    D, eps = _depth(C) + 4, 1e-5
-    y, mean, rstd = fp8mm.layer_norm_forward(x, w, b, eps)
-    ref, rmean, rrstd = moe.layer_norm(xv, wv, bv, eps)
-    wa = np.ones(C) if wv is None else np.abs(wv)
-    ba = np.zeros(C) if bv is None else np.abs(bv)
-    e_mean = D * U * np.abs(xv).mean(1)
-    std = 1 / rrstd
-    e_rstd = rrstd * (2 * e_mean / std + D * U)
-    _within(_f64(mean), rmean, e_mean, "mean")
-    _within(_f64(rstd), rrstd, e_rstd, "rstd")
-    xh = (xv - rmean[:, None]) * rrstd[:, None]
-    tol = wa * (rrstd * e_mean)[:, None] + np.abs(xh) * wa * (e_rstd / rrstd + 6 * U)[:, None] + 4 * U * ba
-    _within(_f64(y), ref, tol + half * np.abs(ref) * (1 + half) + half * tol + TINY, "y")
-
+    eps = 1e-5
+    y, mean, rstd = _check_norm_forward(x, xv, w, wv, b, bv, eps, dtype)
     dx, dw, db = _check_norm_backward(x, xv, dy, dyv, w, wv, mean, rstd, dtype, params)
     # rows at any stride and start: the same bits
     ys, _, _ = fp8mm.layer_norm_forward(_strided(x), w, b, eps)
     assert torch.equal(ys, y)
     for got, want in zip(fp8mm.layer_norm_backward(_strided(dy, 1, 2), _strided(x), w, mean, rstd), (dx, dw, db)):
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("R,C,dtype", [(5000, 64, "fp32"), (4500, 1001, "bf16"), (2100, 3557, "bf16"),
+                                       (1500, 5120, "bf16"), (1200, 8191, "fp32"), (17000, 2048, "bf16")])
+def test_layer_norm_of_more_rows_than_workgroups(R, C, dtype):
+    """Workgroups take further rows in turns; the last case is large enough for
+    streaming accesses."""
+    say(f"layer norm {R}x{C} {dtype}")
+    r = np.random.default_rng(C)
+    x, xv = _dev(r.standard_normal((R, C), dtype=np.float32) + r.standard_normal((R, 1), dtype=np.float32), DT[dtype])
+    w, wv = _dev(1 + 0.3 * r.standard_normal(C), torch.float32)
+    _, mean, rstd = _check_norm_forward(x, xv, w, wv, None, None, 1e-5, dtype)
+    dy, dyv = _dev(r.standard_normal((R, C), dtype=np.float32), DT[dtype])
+    _check_norm_backward(x, xv, dy, dyv, w, wv, mean, rstd, dtype, "fp32")
 
 
 @pytest.mark.parametrize("C", [64, 2048, 5120, 9000])
@@ -325,6 +344,23 @@ def test_route_gradients_of_undefined_rows_show(E):
         assert torch.isnan(grad).all(1).tolist() == bad and torch.isnan(grad).any(1).tolist() == bad
 
 
+@pytest.mark.parametrize("T,E,k", [(70001, 8, 2), (70003, 100, 3), (17001, 300, 4)])
+def test_route_more_tokens_than_workgroups(T, E, k):
+    say(f"route {T}x{E}")
+    logits, lv, _, _ = _route_data(T, E, False, "bf16", T)
+    ids, w = fp8mm.moe_route_forward(logits, k)
+    at = np.argsort(-lv, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(ids.cpu().numpy(), at)
+    ref = moe.route_weights(lv, at, "softmax", True, 1.0)
+    _within(_f64(w), ref, 2 * _score_tol(lv) * ref + TINY, "weights")
+    g, gv = _dev(np.random.default_rng(1).standard_normal((T, k)), torch.float32)
+    grad = fp8mm.moe_route_backward(g, logits, ids, renormalize=False)
+    ref = moe.route_backward(gv, lv, at, "softmax", False, 1.0)
+    s = moe.scores(lv, "softmax")
+    tol = s * 2 * np.abs(gv).max(1, keepdims=True) * 2 * 4 * (_score_tol(lv) + 64 * U)
+    _within(_f64(grad), ref, tol + BF16 * np.abs(ref) + TINY, "grad_logits")
+
+
 def test_route_many_tokens_and_autograd():
     T, E, k = 9001, 64, 6
     logits, lv, _, _ = _route_data(T, E, False, "fp32", 3)
@@ -351,7 +387,8 @@ def _ids(T, k, E, seed, empty=0.1):
 
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 5), (1, 1, 1), (7, 3, 4), (16, 6, 64), (65, 2, 64), (511, 8, 8),
-                                   (512, 8, 63), (1000, 4, 256), (2049, 2, 255), (3000, 8, 1024), (20011, 7, 64),
+                                   (512, 8, 63), (100, 8, 1000), (1000, 4, 256), (2049, 2, 255), (3000, 8, 1024),
+                                   (20011, 7, 64),
                                    (40000, 8, 257)])
 def test_plan(T, k, E):
     say(f"plan {T}x{k} E={E}")
