@@ -241,19 +241,20 @@ __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, in
 }
 
 // Combine's backward: grad_rows[row] = w g, grad_weights[t, j] = <g, rows[row]>.
-// One wave a slot, four chunks a lane in flight: a token's k waves are
-// neighbours and share its gradient through the caches.  HBM-bound: (1 + 2 k)
-// rows a token.  16384 x 2048, k = 6: 154 us, 5.7 TB/s (plain stores 169; one
-// wave a token, which reads the gradient once, 4 us more, and 27 against 9 us for
-// 64 tokens of 5120 columns).
-template <typename T, bool LD, bool ST>
+// LANES lanes a slot (a wave, or 16 where a row is no longer than their chunks), U
+// chunks a lane in flight: a token's k slots are neighbours and share its gradient
+// through the caches.  HBM-bound: (1 + 2 k) rows a token.  16384 x 2048, k = 6:
+// 154 us, 5.7 TB/s (plain stores 169; one wave a token, which reads the gradient
+// once, 4 us more, and 27 against 9 us for 64 tokens of 5120 columns).  Short rows
+// with U = 4 and a wave a slot: 16000 x 512 x 4 28.6 us against 24.9, x 128 x 8 52.
+template <typename T, bool LD, bool ST, int LANES, int U>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProblem p) {
   constexpr int V = kVec<T>;
-  constexpr int U = 4;
-  const int lane = threadIdx.x & 63;
-  const uint32_t slot = wave_item(blockIdx.x);
+  const int lane = threadIdx.x & (LANES - 1);
+  uint32_t slot = wave_item(blockIdx.x) * (64 / LANES);
+  if constexpr (LANES < 64) slot += (threadIdx.x & 63) / LANES;
   const int64_t M = p.T * p.k;
-  if (slot >= M) return;
+  if (slot >= M) return;                 // whole groups of LANES leave
   const uint32_t token = slot / uint32_t(p.k);
   const T* g_row = static_cast<const T*>(p.x) + int64_t(token) * p.ld_x;
   const Slot s = slot_row(p.row_of_slot[slot]);
@@ -262,12 +263,12 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProb
   const T* r = s.used && inside && p.grad_weights ? static_cast<const T*>(p.rows) + s.row * p.ld_rows : nullptr;
   T* o = inside && p.out ? static_cast<T*>(p.out) + s.row * p.ld_out : nullptr;
   float dot = 0.0f;
-  for (int64_t c0 = int64_t(lane) * V; c0 < p.C; c0 += 64 * V * U) {
+  for (int64_t c0 = int64_t(lane) * V; c0 < p.C; c0 += LANES * V * U) {
     Chunk vg[U], vr[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      vg[u] = load_row(g_row, c0 + u * 64 * V, p.C);
-      vr[u] = r ? load_row<T, LD>(r, c0 + u * 64 * V, p.C) : Chunk{{0u, 0u, 0u, 0u}};
+      vg[u] = load_row(g_row, c0 + u * LANES * V, p.C);
+      vr[u] = r ? load_row<T, LD>(r, c0 + u * LANES * V, p.C) : Chunk{{0u, 0u, 0u, 0u}};
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -279,10 +280,10 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProb
         if (r) dot += g[i] * f[i];
         f[i] = s.used ? w * g[i] : 0.0f;
       }
-      if (o) store_row<T, ST>(o, c0 + u * 64 * V, p.C, pack<T>(f));
+      if (o) store_row<T, ST>(o, c0 + u * LANES * V, p.C, pack<T>(f));
     }
   }
-  dot = wave_sum(dot);
+  dot = LANES == 64 ? wave_sum(dot) : row_sum_f(dot);
   if (p.grad_weights && lane == 0) p.grad_weights[slot] = dot;
 }
 
@@ -364,19 +365,27 @@ hipError_t launch_combine(const PermuteProblem& p, hipStream_t st) {
   return rows_stream(p) ? run(combine_kernel<uint16_t, true>) : run(combine_kernel<uint16_t, false>);
 }
 
-hipError_t launch_combine_backward(const PermuteProblem& p, hipStream_t st) {
-  if (p.T == 0) return hipSuccess;
+template <typename T, int LANES, int U>
+static hipError_t run_combine_backward(const PermuteProblem& p, hipStream_t st) {
   const auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(unsigned((p.T * p.k + 3) / 4)), dim3(256), 0, st, p);
+    const int64_t slots = 256 / LANES;   // of a workgroup
+    hipLaunchKernelGGL(kernel, dim3(unsigned((p.T * p.k + slots - 1) / slots)), dim3(256), 0, st, p);
     return hipGetLastError();
   };
-  const auto typed = [&](auto zero) {
-    using T = decltype(zero);
-    if (rows_stream(p)) return run(combine_backward_kernel<T, true, true>);
-    return rows_bytes(p) > kL2Bytes ? run(combine_backward_kernel<T, false, true>)
-                                    : run(combine_backward_kernel<T, false, false>);
-  };
-  return p.fp32 ? typed(0.0f) : typed(uint16_t(0));
+  if (rows_stream(p)) return run(combine_backward_kernel<T, true, true, LANES, U>);
+  return rows_bytes(p) > kL2Bytes ? run(combine_backward_kernel<T, false, true, LANES, U>)
+                                  : run(combine_backward_kernel<T, false, false, LANES, U>);
+}
+
+template <typename T>
+static hipError_t combine_backward_of(const PermuteProblem& p, hipStream_t st) {
+  if (p.C <= 16 * kVec<T>) return run_combine_backward<T, 16, 1>(p, st);
+  return p.C <= 64 * kVec<T> ? run_combine_backward<T, 64, 1>(p, st) : run_combine_backward<T, 64, 4>(p, st);
+}
+
+hipError_t launch_combine_backward(const PermuteProblem& p, hipStream_t st) {
+  if (p.T == 0) return hipSuccess;
+  return p.fp32 ? combine_backward_of<float>(p, st) : combine_backward_of<uint16_t>(p, st);
 }
 
 }  // namespace fp8mm
