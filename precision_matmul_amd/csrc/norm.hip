@@ -36,9 +36,9 @@ __device__ __forceinline__ float row_sum(float v, float (&part)[2][WPR], int slo
   return s;
 }
 
-// The next row's chunks.  PART: the row ends within a chunk, and the four waves
-// that share it would all wait for that chunk's single elements where they are
-// asked for; it is loaded whole and shifted when its turn comes.
+// The next row's chunks.  PART: without a path for a row's last elements, for
+// which the waves that share a row would all wait where they ask for them: the
+// last chunk is loaded whole and shifted, if it has to be, when its turn comes.
 template <typename T, bool NT, bool PART>
 __device__ __forceinline__ Chunk fetch(const T* row, int64_t c, int64_t C) {
   return PART ? fetch_row<T, NT>(row, c, C) : load_row<T, NT>(row, c, C);
@@ -56,14 +56,18 @@ __device__ __forceinline__ Chunk settle(const Chunk& v, int64_t c, int64_t C) {
 // are read and written by streaming accesses (NT).  16640 x 5120 bf16: 60 us,
 // 5.6 TB/s, more than a plain copy reaches (one row a workgroup, parameters
 // read again for each: 85 us; one wave a row: 102 us; plain accesses: 66 us).
+// fp32 rows above 4096 columns take eight waves: 4096 x 4764 30 us (four waves 38).
+// PART where rows end within a chunk and, for results larger than the L2s, at
+// eight waves (6000 x 6144 fp32 50 against 54 us; four waves: 16000 x 5128 bf16 65
+// against 62; within the L2s 900 x 8192 fp32 16 against 14).
 // ---------------------------------------------------------------------------
 template <typename T, typename P, int WPR, int NIT, bool NT, bool PART>
-__global__ __launch_bounds__(256) void norm_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld_x,
-                                                   const P* __restrict__ weight, const P* __restrict__ bias, float eps,
-                                                   T* __restrict__ y, int64_t ld_y, float* __restrict__ mean_out,
-                                                   float* __restrict__ rstd_out) {
+__global__ __launch_bounds__(WPR == 8 ? 512 : 256) void norm_kernel(
+    const T* __restrict__ x, int64_t R, int64_t C, int64_t ld_x, const P* __restrict__ weight,
+    const P* __restrict__ bias, float eps, T* __restrict__ y, int64_t ld_y, float* __restrict__ mean_out,
+    float* __restrict__ rstd_out) {
   constexpr int V = kVec<T>;
-  constexpr int RPB = 4 / WPR;                    // rows of a workgroup
+  constexpr int RPB = WPR == 1 ? 4 : 1;           // rows of a workgroup
   __shared__ float part[2][WPR];
   const int in_row = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t c0 = int64_t(in_row) * V;
@@ -181,26 +185,31 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
 // traffic of their own (8 gridDim C bytes each way), so there are no more
 // workgroups than run at once: 256 of eight waves with a row each, or, above
 // 4 chunks a lane, 512 of four waves that share a row (256 above 6144 columns,
-// where the registers leave room for one workgroup a compute unit, and below 2048
-// rows, where a partial row would stand for one or two rows).
+// where the registers leave room for one workgroup a compute unit, above 4096 of
+// fp32, where eight waves share it, and below 2048 rows, where a partial row would
+// stand for one or two rows).
 // 16384 x 2048 bf16: 43 us with the column sums, 4.7 TB/s of x, dy and dx; without
 // dw and db 37 us, what a sum of two such matrices takes (512 partial rows of
 // eight-wave workgroups 55 us; no row in flight ahead 55; the waves' shares added
 // one wave after the other 45).  16000 x 4096: 76 us (1024 partial rows 93);
-// 10000 x 8192: 94 us (512: 111); 7534 x 3560 fp32: 68 us (256: 90, 1024: 85);
-// 700 x 5120: 17.3 us (512: 21.6).  7534 x 3559: 49 us (84 without PART).
+// 10000 x 8192: 94 us (512: 111); 7534 x 3560 fp32: 65 us (68 without PART, and then
+// 90 with 256 and 85 with 1024 partial rows); 700 x 5120: 17.3 us (512: 21.6); 6000
+// x 6144 fp32: 78 us (four waves 103; 512 partial rows 82).  PART wherever rows are
+// shared and stream or end within a chunk: 16000 x 3000 bf16 62 us (85 without),
+// 16000 x 2056 50 (75), 7534 x 3559 48 (84); within the L2s it costs: 1703 x 3000
+// fp32 25 against 22.5.
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 
 template <typename T, typename P, int WPR, int NIT, bool NT, bool PART>
-__global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward_kernel(
+__global__ __launch_bounds__(64 * (WPR == 1 ? kRowWaves : WPR)) void norm_backward_kernel(
     const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ x, int64_t ld_x, int64_t R, int64_t C,
     const P* __restrict__ weight, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
     T* __restrict__ dx, int64_t ld_dx, float* __restrict__ partial) {
   constexpr int V = kVec<T>;
   constexpr int RPB = WPR == 1 ? kRowWaves : 1;
   constexpr int64_t STEP = int64_t(WPR) * 64 * V;
-  __shared__ float part[2][2][4];
+  __shared__ float part[2][2][WPR];
   constexpr int Q = 2 * NIT * V / 4;              // a lane's sums, in fours
   __shared__ float4 acc[WPR == 1 ? kRowWaves / 2 * Q * 64 : 1];
   const int wave = threadIdx.x >> 6;
@@ -269,8 +278,12 @@ __global__ __launch_bounds__(WPR == 1 ? 64 * kRowWaves : 256) void norm_backward
         part[slot][1][wave] = sax;
       }
       __syncthreads();
-      sa = part[slot][0][0] + part[slot][0][1] + part[slot][0][2] + part[slot][0][3];
-      sax = part[slot][1][0] + part[slot][1][1] + part[slot][1][2] + part[slot][1][3];
+      sa = sax = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) {
+        sa += part[slot][0][w];
+        sax += part[slot][1][w];
+      }
       slot ^= 1;
     }
     sa *= inv_c;
@@ -545,28 +558,29 @@ bool streams(const NormProblem& p, size_t size) { return p.R * p.C * int64_t(siz
 int backward_grid(int64_t R, int64_t C, int vec) {
   const int64_t one_wave = 256 * vec;         // rows of up to this many columns: a wave each
   const int64_t rows = C <= one_wave ? kRowWaves : 1;
-  const int64_t most = C <= one_wave || C > 6144 || R < 2048 ? 256 : 512;
+  const int64_t few = vec == 4 ? 4096 : 6144; // longer rows leave room for 256 at a time
+  const int64_t most = C <= one_wave || C > few || R < 2048 ? 256 : 512;
   const int64_t blocks = (R + rows - 1) / rows;
   return int(blocks < most ? blocks : most);
 }
 
 template <typename T, typename P, int WPR, int NIT>
 hipError_t run_norm(const NormProblem& p, hipStream_t st) {
-  constexpr int RPB = 4 / WPR;
+  constexpr int RPB = WPR == 1 ? 4 : 1;
   const int64_t blocks = (p.R + RPB - 1) / RPB;
   const dim3 grid(unsigned(blocks < kForwardGrid ? blocks : kForwardGrid));
   const auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, static_cast<const T*>(p.x), p.R, p.C, p.ld_x,
-                       static_cast<const P*>(p.weight), static_cast<const P*>(p.bias), p.eps, static_cast<T*>(p.out),
-                       p.ld_out, p.mean, p.rstd);
+    hipLaunchKernelGGL(kernel, grid, dim3(WPR == 8 ? 512 : 256), 0, st, static_cast<const T*>(p.x), p.R, p.C,
+                       p.ld_x, static_cast<const P*>(p.weight), static_cast<const P*>(p.bias), p.eps,
+                       static_cast<T*>(p.out), p.ld_out, p.mean, p.rstd);
     return hipGetLastError();
   };
-  const bool nt = streams(p, sizeof(T));
-  if (WPR > 1 && p.C % kVec<T> != 0) {
-    constexpr bool PART = WPR > 1;
-    return nt ? run(norm_kernel<T, P, WPR, NIT, true, PART>) : run(norm_kernel<T, P, WPR, NIT, false, PART>);
-  }
-  return nt ? run(norm_kernel<T, P, WPR, NIT, true, false>) : run(norm_kernel<T, P, WPR, NIT, false, false>);
+  constexpr bool MANY = WPR > 1;
+  const bool part = MANY && p.C % kVec<T> != 0;
+  if (streams(p, sizeof(T)))
+    return part || WPR == 8 ? run(norm_kernel<T, P, WPR, NIT, true, MANY>)
+                            : run(norm_kernel<T, P, WPR, NIT, true, false>);
+  return part ? run(norm_kernel<T, P, WPR, NIT, false, MANY>) : run(norm_kernel<T, P, WPR, NIT, false, false>);
 }
 
 template <typename T, typename P>
@@ -579,7 +593,8 @@ hipError_t norm_typed(const NormProblem& p, hipStream_t st) {
   if (p.C <= 12 * S) return run_norm<T, P, 4, 3>(p, st);
   if (p.C <= 16 * S) return run_norm<T, P, 4, 4>(p, st);
   if constexpr (sizeof(T) == 4) {   // 16 S is 8192 columns of bf16, 4096 of fp32
-    if (p.C <= kRegisterCols) return run_norm<T, P, 4, 8>(p, st);
+    if (p.C <= 24 * S) return run_norm<T, P, 8, 3>(p, st);
+    if (p.C <= kRegisterCols) return run_norm<T, P, 8, 4>(p, st);
   }
   hipLaunchKernelGGL((norm_long_kernel<T, P>), row_grid(p.R), dim3(256), 0, st, static_cast<const T*>(p.x), p.R,
                      p.C, p.ld_x, static_cast<const P*>(p.weight), static_cast<const P*>(p.bias), p.eps,
@@ -591,27 +606,24 @@ template <typename T, typename P, int WPR, int NIT>
 hipError_t run_backward(const NormProblem& p, int grid, float* partial, hipStream_t st) {
   if (few_rows(p.R, p.C)) {
     const int64_t rows = p.out ? (WPR == 1 ? (p.R + 3) / 4 : p.R) : 0;
-    const int64_t strips = p.dweight || p.dbias ? (p.C + kStripChunks<WPR> * kVec<T> - 1) / (kStripChunks<WPR> * kVec<T>) : 0;
-    hipLaunchKernelGGL((norm_backward_few_kernel<T, P, WPR, NIT>), dim3(unsigned(rows + strips)), dim3(256), 0, st,
-                       static_cast<const T*>(p.dy), p.ld_dy, static_cast<const T*>(p.x), p.ld_x, p.R, p.C,
+    constexpr int W = WPR == 1 ? 1 : 4, STRIP = kStripChunks<W> * kVec<T>;
+    const int64_t strips = p.dweight || p.dbias ? (p.C + STRIP - 1) / STRIP : 0;
+    hipLaunchKernelGGL((norm_backward_few_kernel<T, P, W, NIT * WPR / W>), dim3(unsigned(rows + strips)), dim3(256), 0,
+                       st, static_cast<const T*>(p.dy), p.ld_dy, static_cast<const T*>(p.x), p.ld_x, p.R, p.C,
                        static_cast<const P*>(p.weight), p.mean, p.rstd, static_cast<T*>(p.out), p.ld_out,
                        static_cast<P*>(p.dweight), static_cast<P*>(p.dbias), unsigned(rows));
     return hipGetLastError();
   }
   const auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(WPR == 1 ? 64 * kRowWaves : 256), 0, st,
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * (WPR == 1 ? kRowWaves : WPR)), 0, st,
                        static_cast<const T*>(p.dy), p.ld_dy, static_cast<const T*>(p.x), p.ld_x, p.R, p.C,
                        static_cast<const P*>(p.weight), p.mean, p.rstd, static_cast<T*>(p.out), p.ld_out, partial);
     return hipGetLastError();
   };
-  const bool nt = streams(p, sizeof(T));
-  if (WPR > 1 && p.C % kVec<T> != 0) {
-    constexpr bool PART = WPR > 1;
-    return nt ? run(norm_backward_kernel<T, P, WPR, NIT, true, PART>)
-              : run(norm_backward_kernel<T, P, WPR, NIT, false, PART>);
-  }
-  return nt ? run(norm_backward_kernel<T, P, WPR, NIT, true, false>)
-            : run(norm_backward_kernel<T, P, WPR, NIT, false, false>);
+  constexpr bool MANY = WPR > 1;
+  if (streams(p, sizeof(T))) return run(norm_backward_kernel<T, P, WPR, NIT, true, MANY>);
+  return MANY && p.C % kVec<T> != 0 ? run(norm_backward_kernel<T, P, WPR, NIT, false, MANY>)
+                                    : run(norm_backward_kernel<T, P, WPR, NIT, false, false>);
 }
 
 template <typename T, typename P>
@@ -633,7 +645,9 @@ hipError_t backward_typed(const NormProblem& p, hipStream_t st) {
   } else if (p.C <= 16 * S) {
     e = run_backward<T, P, 4, 4>(p, grid, partial, st);
   } else if (sizeof(T) == 4 && p.C <= kRegisterCols) {
-    if constexpr (sizeof(T) == 4) e = run_backward<T, P, 4, 8>(p, grid, partial, st);
+    if constexpr (sizeof(T) == 4)
+      e = p.C <= 24 * S ? run_backward<T, P, 8, 3>(p, grid, partial, st)
+                        : run_backward<T, P, 8, 4>(p, grid, partial, st);
   } else {
     if (p.out) {
       hipLaunchKernelGGL((norm_backward_long_kernel<T, P>), row_grid(p.R), dim3(256), 0, st,

@@ -154,6 +154,26 @@ def test_layer_norm_of_more_rows_than_workgroups(R, C, dtype):
     _check_norm_backward(x, xv, dy, dyv, w, wv, mean, rstd, dtype, "fp32")
 
 
+@pytest.mark.parametrize("R,C,dtype", [(600, 4097, "fp32"), (600, 6144, "fp32"), (1800, 4764, "fp32"),
+                                       (1800, 4762, "fp32"), (1500, 6148, "fp32"), (1100, 8192, "fp32"),
+                                       (1100, 7999, "fp32"), (8200, 2056, "bf16"), (4000, 4104, "bf16"),
+                                       (2400, 7177, "bf16")])
+def test_layer_norm_of_rows_shared_by_waves(R, C, dtype):
+    """Rows of four and of eight waves, whole and ending within a chunk, with
+    plain and (all but the first two) with streaming accesses."""
+    say(f"layer norm {R}x{C} {dtype}")
+    r = np.random.default_rng(R + C)
+    x, xv = _dev(r.standard_normal((R, C), dtype=np.float32) + r.standard_normal((R, 1), dtype=np.float32), DT[dtype])
+    w, wv = _dev(1 + 0.3 * r.standard_normal(C), torch.float32)
+    b, bv = _dev(r.standard_normal(C), torch.float32)
+    y, mean, rstd = _check_norm_forward(x, xv, w, wv, b, bv, 1e-5, dtype)
+    dy, dyv = _dev(r.standard_normal((R, C), dtype=np.float32), DT[dtype])
+    grads = _check_norm_backward(x, xv, dy, dyv, w, wv, mean, rstd, dtype, "fp32")
+    assert torch.equal(fp8mm.layer_norm_forward(_strided(x), w, b, 1e-5)[0], y)
+    for got, want in zip(fp8mm.layer_norm_backward(_strided(dy, 1, 2), _strided(x), w, mean, rstd), grads):
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("C", [64, 2048, 5120, 9000])
 def test_layer_norm_gradients_over_many_rows(C):
     """More rows than one turn of the workgroups; partial results in a fixed
