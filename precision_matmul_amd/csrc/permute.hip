@@ -241,13 +241,15 @@ __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, in
 }
 
 // Combine's backward: grad_rows[row] = w g, grad_weights[t, j] = <g, rows[row]>.
-// LANES lanes a slot (a wave, or 16 where a row is no longer than their chunks), U
-// chunks a lane in flight: a token's k slots are neighbours and share its gradient
+// LANES lanes a slot (a wave, or 16 for rows of at most one chunk a lane of a wave),
+// U chunks a lane in flight: a token's k slots are neighbours and share its gradient
 // through the caches.  HBM-bound: (1 + 2 k) rows a token.  16384 x 2048, k = 6:
 // 154 us, 5.7 TB/s (plain stores 169; one wave a token, which reads the gradient
 // once, 4 us more, and 27 against 9 us for 64 tokens of 5120 columns).  Short rows
-// with U = 4 and a wave a slot: 16000 x 512 x 4 28.6 us against 24.9, x 128 x 8 52.
-template <typename T, bool LD, bool ST, int LANES, int U>
+// with a wave a slot and one chunk in flight: 16000 x 256, k = 4 19 us against 13,
+// 512 columns 25 against 24.  PART, a row's last chunk loaded whole and shifted:
+// 16000 x 339 24 us (30 without); long rows lose by it (4000 x 2048 38 against 34).
+template <typename T, bool LD, bool ST, int LANES, int U, bool PART>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProblem p) {
   constexpr int V = kVec<T>;
   const int lane = threadIdx.x & (LANES - 1);
@@ -267,11 +269,17 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProb
     Chunk vg[U], vr[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      vg[u] = load_row(g_row, c0 + u * LANES * V, p.C);
-      vr[u] = r ? load_row<T, LD>(r, c0 + u * LANES * V, p.C) : Chunk{{0u, 0u, 0u, 0u}};
+      const int64_t c = c0 + u * LANES * V;
+      vg[u] = PART ? fetch_row<T, false>(g_row, c, p.C) : load_row(g_row, c, p.C);
+      vr[u] = Chunk{{0u, 0u, 0u, 0u}};
+      if (r) vr[u] = PART ? fetch_row<T, LD>(r, c, p.C) : load_row<T, LD>(r, c, p.C);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if constexpr (PART) {
+        vg[u] = fetched<T>(vg[u], c0 + u * LANES * V, p.C);
+        if (r) vr[u] = fetched<T>(vr[u], c0 + u * LANES * V, p.C);
+      }
       float g[V], f[V];
       unpack<T>(vg[u], g);
       unpack<T>(vr[u], f);
@@ -365,22 +373,22 @@ hipError_t launch_combine(const PermuteProblem& p, hipStream_t st) {
   return rows_stream(p) ? run(combine_kernel<uint16_t, true>) : run(combine_kernel<uint16_t, false>);
 }
 
-template <typename T, int LANES, int U>
+template <typename T, int LANES, int U, bool PART>
 static hipError_t run_combine_backward(const PermuteProblem& p, hipStream_t st) {
   const auto run = [&](auto kernel) {
     const int64_t slots = 256 / LANES;   // of a workgroup
     hipLaunchKernelGGL(kernel, dim3(unsigned((p.T * p.k + slots - 1) / slots)), dim3(256), 0, st, p);
     return hipGetLastError();
   };
-  if (rows_stream(p)) return run(combine_backward_kernel<T, true, true, LANES, U>);
-  return rows_bytes(p) > kL2Bytes ? run(combine_backward_kernel<T, false, true, LANES, U>)
-                                  : run(combine_backward_kernel<T, false, false, LANES, U>);
+  if (rows_stream(p)) return run(combine_backward_kernel<T, true, true, LANES, U, PART>);
+  return rows_bytes(p) > kL2Bytes ? run(combine_backward_kernel<T, false, true, LANES, U, PART>)
+                                  : run(combine_backward_kernel<T, false, false, LANES, U, PART>);
 }
 
 template <typename T>
 static hipError_t combine_backward_of(const PermuteProblem& p, hipStream_t st) {
-  if (p.C <= 16 * kVec<T>) return run_combine_backward<T, 16, 1>(p, st);
-  return p.C <= 64 * kVec<T> ? run_combine_backward<T, 64, 1>(p, st) : run_combine_backward<T, 64, 4>(p, st);
+  if (p.C > 64 * kVec<T>) return run_combine_backward<T, 64, 4, false>(p, st);
+  return p.C % kVec<T> ? run_combine_backward<T, 16, 2, true>(p, st) : run_combine_backward<T, 16, 2, false>(p, st);
 }
 
 hipError_t launch_combine_backward(const PermuteProblem& p, hipStream_t st) {
