@@ -56,7 +56,8 @@ __device__ __forceinline__ Chunk settle(const Chunk& v, int64_t c, int64_t C) {
 // are read and written by streaming accesses (NT).  16640 x 5120 bf16: 60 us,
 // 5.6 TB/s, more than a plain copy reaches (one row a workgroup, parameters
 // read again for each: 85 us; one wave a row: 102 us; plain accesses: 66 us).
-// fp32 rows above 4096 columns take eight waves: 4096 x 4764 30 us (four waves 38).
+// Rows above 12 chunks of a wave (16 of fp32) take eight waves: 10000 x 8192 bf16 56
+// us (four waves 62), 4096 x 4764 fp32 30 (38), but 16640 x 5120 66.
 // PART where rows end within a chunk and, for results larger than the L2s, at
 // eight waves (6000 x 6144 fp32 50 against 54 us; four waves: 16000 x 5128 bf16 65
 // against 62; within the L2s 900 x 8192 fp32 16 against 14).
@@ -183,21 +184,18 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
 // row of the workspace, [2][gridDim][C], which column_sum_kernel adds up in
 // workgroup order: no atomics, the same bits every time.  The partial rows are
 // traffic of their own (8 gridDim C bytes each way), so there are no more
-// workgroups than run at once: 256 of eight waves with a row each, or, above
-// 4 chunks a lane, 512 of four waves that share a row (256 above 6144 columns,
-// where the registers leave room for one workgroup a compute unit, above 4096 of
-// fp32, where eight waves share it, and below 2048 rows, where a partial row would
-// stand for one or two rows).
+// workgroups than run at once: 256 of eight waves, with a row each or, above 8
+// chunks a lane, sharing one, and 512 of four waves that share a row in between
+// (256 below 2048 rows, where a partial row would stand for one or two rows).
 // 16384 x 2048 bf16: 43 us with the column sums, 4.7 TB/s of x, dy and dx; without
 // dw and db 37 us, what a sum of two such matrices takes (512 partial rows of
 // eight-wave workgroups 55 us; no row in flight ahead 55; the waves' shares added
-// one wave after the other 45).  16000 x 4096: 76 us (1024 partial rows 93);
-// 10000 x 8192: 94 us (512: 111); 7534 x 3560 fp32: 65 us (68 without PART, and then
-// 90 with 256 and 85 with 1024 partial rows); 700 x 5120: 17.3 us (512: 21.6); 6000
-// x 6144 fp32: 78 us (four waves 103; 512 partial rows 82).  PART wherever rows are
-// shared and stream or end within a chunk: 16000 x 3000 bf16 62 us (85 without),
-// 16000 x 2056 50 (75), 7534 x 3559 48 (84); within the L2s it costs: 1703 x 3000
-// fp32 25 against 22.5.
+// one wave after the other 45).  16000 x 4096: 76 us (1024 partial rows 93).  Eight
+// waves a row: 16000 x 6144 101 us (four waves 106, 512 partial rows 107), 2841 x
+// 5127 27 (30, 33), 6000 x 6144 fp32 78 (103, 82).  PART wherever rows are shared
+// and stream or end within a chunk: 16000 x 3000 bf16 62 us (85 without), 16000 x
+// 2056 50 (75), 7534 x 3559 48 (84); within the L2s it costs: 1703 x 3000 fp32 25
+// against 22.5 (four waves).
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 
@@ -558,8 +556,7 @@ bool streams(const NormProblem& p, size_t size) { return p.R * p.C * int64_t(siz
 int backward_grid(int64_t R, int64_t C, int vec) {
   const int64_t one_wave = 256 * vec;         // rows of up to this many columns: a wave each
   const int64_t rows = C <= one_wave ? kRowWaves : 1;
-  const int64_t few = vec == 4 ? 4096 : 6144; // longer rows leave room for 256 at a time
-  const int64_t most = C <= one_wave || C > few || R < 2048 ? 256 : 512;
+  const int64_t most = C <= one_wave || C > 2 * one_wave || R < 2048 ? 256 : 512;
   const int64_t blocks = (R + rows - 1) / rows;
   return int(blocks < most ? blocks : most);
 }
@@ -591,10 +588,12 @@ hipError_t norm_typed(const NormProblem& p, hipStream_t st) {
   if (p.C <= 4 * S) return run_norm<T, P, 1, 4>(p, st);
   if (p.C <= 8 * S) return run_norm<T, P, 4, 2>(p, st);
   if (p.C <= 12 * S) return run_norm<T, P, 4, 3>(p, st);
-  if (p.C <= 16 * S) return run_norm<T, P, 4, 4>(p, st);
-  if constexpr (sizeof(T) == 4) {   // 16 S is 8192 columns of bf16, 4096 of fp32
+  if constexpr (sizeof(T) == 2) {   // 16 S is 8192 columns of bf16, 4096 of fp32
+    if (p.C <= 16 * S) return run_norm<T, P, 8, 2>(p, st);
+  } else {
+    if (p.C <= 16 * S) return run_norm<T, P, 4, 4>(p, st);
     if (p.C <= 24 * S) return run_norm<T, P, 8, 3>(p, st);
-    if (p.C <= kRegisterCols) return run_norm<T, P, 8, 4>(p, st);
+    if (p.C <= 32 * S) return run_norm<T, P, 8, 4>(p, st);
   }
   hipLaunchKernelGGL((norm_long_kernel<T, P>), row_grid(p.R), dim3(256), 0, st, static_cast<const T*>(p.x), p.R,
                      p.C, p.ld_x, static_cast<const P*>(p.weight), static_cast<const P*>(p.bias), p.eps,
@@ -640,10 +639,8 @@ hipError_t backward_typed(const NormProblem& p, hipStream_t st) {
     e = run_backward<T, P, 1, 4>(p, grid, partial, st);
   } else if (p.C <= 8 * S) {
     e = run_backward<T, P, 4, 2>(p, grid, partial, st);
-  } else if (p.C <= 12 * S) {
-    e = run_backward<T, P, 4, 3>(p, grid, partial, st);
   } else if (p.C <= 16 * S) {
-    e = run_backward<T, P, 4, 4>(p, grid, partial, st);
+    e = run_backward<T, P, 8, 2>(p, grid, partial, st);
   } else if (sizeof(T) == 4 && p.C <= kRegisterCols) {
     if constexpr (sizeof(T) == 4)
       e = p.C <= 24 * S ? run_backward<T, P, 8, 3>(p, grid, partial, st)

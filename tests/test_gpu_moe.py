@@ -156,11 +156,12 @@ def test_layer_norm_of_more_rows_than_workgroups(R, C, dtype):
 
 @pytest.mark.parametrize("R,C,dtype", [(600, 4097, "fp32"), (600, 6144, "fp32"), (1800, 4764, "fp32"),
                                        (1800, 4762, "fp32"), (1500, 6148, "fp32"), (1100, 8192, "fp32"),
-                                       (1100, 7999, "fp32"), (8200, 2056, "bf16"), (4000, 4104, "bf16"),
+                                       (1100, 7999, "fp32"), (2800, 3003, "fp32"), (700, 4096, "fp32"), (700, 6152, "bf16"),
+                                       (8200, 2056, "bf16"), (4000, 4104, "bf16"),
                                        (2400, 7177, "bf16")])
 def test_layer_norm_of_rows_shared_by_waves(R, C, dtype):
     """Rows of four and of eight waves, whole and ending within a chunk, with
-    plain and (all but the first two) with streaming accesses."""
+    plain and (more than 32 MiB) with streaming accesses."""
     say(f"layer norm {R}x{C} {dtype}")
     r = np.random.default_rng(R + C)
     x, xv = _dev(r.standard_normal((R, C), dtype=np.float32) + r.standard_normal((R, 1), dtype=np.float32), DT[dtype])
