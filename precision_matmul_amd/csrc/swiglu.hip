@@ -19,7 +19,7 @@
 // ([blocks, R]); the column blocks of the same rows follow each other.  Results
 // larger than the L2s go out by streaming stores; the forward's input comes in by
 // streaming loads where it is larger than twice the L2s.
-// 98304 x 1408: forward with codes and checkpoint 170 us, 5.8 TB/s; backward
+// 98304 x 1408: forward with codes and checkpoint 181 us, 5.4 TB/s; backward
 // with the activation again 233 us, 6.0 TB/s (rows before column blocks 304 us,
 // a contiguous range of workgroups an XCD 254, plain stores 240).
 #include "moe_launch.hpp"
@@ -32,9 +32,22 @@ namespace {
 using namespace ops;
 
 // 1 / (1 + exp(-x)) from the hardware's exp2 and reciprocal (each within an
-// ulp; the product with log2(e) adds |x| 2^-24): results go out in bf16 or E4M3.
+// ulp; the product with log2(e) adds |x| 2^-24): for results that go out in bf16.
 __device__ __forceinline__ float fast_sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
+}
+
+// x / (1 + exp(-x)) as exactly as a float32 quotient, for E4M3 codes that no bf16
+// rounding precedes: exp2 corrected by the rounding of its argument (x + t ln 2),
+// the quotient by its remainder.  Past 126 ln 2 the result is x, or 0 where
+// sig < 2^-126 (NaN at -inf, as inf / inf).  10007 x 1408 with codes and checkpoint
+// 21.3 us against 20.1 with fast_sigmoid, whose last bits put some codes on the
+// other side of their rounding (1e-4 of the codes' norm in all, 2e-8 with this).
+__device__ __forceinline__ float silu(float x) {
+  const float t = x * -1.44269504f, e = __builtin_amdgcn_exp2f(t);
+  const float rest = fmaf(t, -1.90465421e-9f, fmaf(t, 0.693147182f, x));
+  const float d = 1.0f + fmaf(-e, rest, e), inv = __builtin_amdgcn_rcpf(d), q = x * inv;
+  return fabsf(x) < 87.3365402f ? fmaf(fmaf(-q, d, x), inv, q) : fmaf(0.5f, fabsf(x), 0.5f * x);
 }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -108,7 +121,7 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluProblem p, int 
 #pragma unroll
   for (int a = 0; a < 2; ++a)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[a][i] = g[a][i] * fast_sigmoid(g[a][i]) * u[a][i];
+    for (int i = 0; i < 8; ++i) g[a][i] = (HQ ? silu(g[a][i]) : g[a][i] * fast_sigmoid(g[a][i])) * u[a][i];
   if constexpr (H) {
     uint16_t* h = p.h + row * p.ld_h + c;
     store8_bf16<ST>(h, g[0]);

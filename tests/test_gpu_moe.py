@@ -175,6 +175,21 @@ def test_layer_norm_of_rows_shared_by_waves(R, C, dtype):
         assert torch.equal(got, want)
 
 
+def test_swiglu_code_scales_are_those_of_float32_values():
+    """A block's scale is max|h| / 448 of h = gate / (1 + exp(-gate)) up: the
+    hardware's exp2 is within 2 U, its correction, the sum, the product and the
+    scale's division add 1 U each, the quotient less than 2 U: 8 U bounds it."""
+    say("swiglu scales 64x1024")
+    r = np.random.default_rng(12)
+    gate = r.uniform(-60, 60, (64, 1024)) * r.random((64, 1))
+    gate[0] = -np.abs(gate[0])
+    x, xv = _dev(np.concatenate([gate, r.standard_normal((64, 1024))], 1), torch.bfloat16)
+    (_, scale), _ = fp8mm.fp8_swiglu_forward(x, "fp8", checkpoint=False)
+    g, u = xv[:, :1024], xv[:, 1024:]
+    ref = np.abs(g / (1 + np.exp(-g)) * u).reshape(64, 8, 128).max(2) / 448
+    _within(_f64(scale).T, ref, 8 * U * ref, "scale")
+
+
 @pytest.mark.parametrize("C", [64, 2048, 5120, 9000])
 def test_layer_norm_gradients_over_many_rows(C):
     """More rows than one turn of the workgroups; partial results in a fixed
