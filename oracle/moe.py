@@ -110,7 +110,7 @@ def route_backward(grad, logits, ids, score, renormalize, scale):
     de = np.zeros_like(s)
     np.add.at(de, (np.arange(len(s))[:, None], at), d)
     if score == "sigmoid":
-        return s * (1.0 - s) * de
+        return s * scores(-logits, score) * de       # 1 - s, without its cancellation
     return s * (de - (s * de).sum(1, keepdims=True))
 
 

@@ -380,6 +380,26 @@ def test_route_gradients_of_undefined_rows_show(E):
         assert torch.isnan(grad).all(1).tolist() == bad and torch.isnan(grad).any(1).tolist() == bad
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E", [24, 256, 300])
+def test_route_gradients_of_saturated_sigmoids(E, dtype):
+    """Slopes where the sigmoid is near 0 or 1, relative to themselves.  e =
+    exp(-|x|) is off by 4 U (the hardware's exp2 2 U, its correction and the
+    rounding of the sum), 1 + e by 5 U, its reciprocal by 7 U, e r r by 4 + 14 + 2
+    U, the products with scale and gradient by 2 U more: 24 U bounds it."""
+    say(f"route gradients of saturated sigmoids E={E} {dtype}")
+    r = np.random.default_rng(E)
+    size = np.array([0.0, 1.0, 4.0, 8.0, 10.0, 12.0, 16.0, 17.0, 20.0, 30.0, 60.0, 80.0])
+    logits, lv = _dev(r.choice(np.concatenate([size, -size]), (33, E)), DT[dtype])
+    ids = np.argsort(r.random((33, E)), axis=1)[:, :8]
+    ids[3, 5] = -1
+    g, gv = _dev(r.standard_normal((33, 8)), torch.float32)
+    grad = fp8mm.moe_route_backward(g, logits, torch.from_numpy(ids.astype(np.int32)).to(DEV), "sigmoid", False, 2.5)
+    ref = moe.route_backward(gv, lv, ids, "sigmoid", False, 2.5)
+    half = BF16 if dtype == "bf16" else 0.0
+    _within(_f64(grad), ref, (24 * U + half + 24 * U * half) * np.abs(ref), "grad_logits")
+
+
 @pytest.mark.parametrize("T,E,k", [(70001, 8, 2), (70003, 100, 3), (17001, 300, 4)])
 def test_route_more_tokens_than_workgroups(T, E, k):
     say(f"route {T}x{E}")
