@@ -118,27 +118,20 @@ struct Scores {
     }
   }
 
-  // Slope of the sigmoid, s (1 - s) as e / (1 + e)^2 with e = exp(-|x|): 1 - s has
-  // lost its bits where s is near 1 (6 % of it at a logit of 16, all from 17 on).
-  __device__ __forceinline__ float slope(float x) const {
-    const float e = exp_neg(fabsf(x)), r = reciprocal(1.0f + e);
-    return e * r * r;
-  }
-
-  // For the backward: the sigmoid with its division rounded once.  Where one slot
-  // holds nearly all of the renormalised weight, the gradient is a difference of
-  // nearly equal terms and every bit of the score shows in it.
-  __device__ __forceinline__ float rounded(float x) const {
-    if constexpr (!SIGMOID) return (*this)(x);
-    return 1.0f / (1.0f + expf(-x));
-  }
-
   __device__ __forceinline__ float operator()(float x) const {
     if constexpr (!SIGMOID) return exp_neg(shift - x) * inv;
     const float e = exp_neg(fabsf(x));
     return (x < 0.0f ? e : 1.0f) * reciprocal(1.0f + e);
   }
 };
+
+// The sigmoid and its slope, s (1 - s) as e / (1 + e)^2 with e = exp(-|x|): 1 - s
+// has lost its bits where s is near 1 (6 % of it at a logit of 16, all from 17 on).
+__device__ __forceinline__ float sigmoid_slope(float x, float& slope) {
+  const float e = exp_neg(fabsf(x)), r = reciprocal(1.0f + e);
+  slope = e * r * r;
+  return (x < 0.0f ? e : 1.0f) * r;
+}
 
 // Whether a lane's logits leave its row without a defined choice.
 template <bool SIGMOID, int N>
@@ -447,12 +440,16 @@ __global__ __launch_bounds__(256) void route16_kernel(const RouteProblem p, cons
   }
 }
 
-// Backward.  With d_j the gradient of the chosen score s_j,
-//   d_j = scale g_j                                     (weights as they are)
-//   d_j = scale (g_j - sum_l g_l s_l / S) / S, S = sum_l s_l + 1e-20   (renormalised)
+// Backward.  With d_j the gradient of the chosen score s_j and S = sum_l s_l + 1e-20,
+//   d_j = scale g_j                                             (weights as they are)
+//   d_j = scale (sum_l s_l (g_j - g_l) + 1e-20 g_j) / S^2       (renormalised)
 // the logits get  softmax: s_e (d_e - sum_l s_l d_l),  sigmoid: s_e (1 - s_e) d_e
-// (the slope without its subtraction; d_e = 0 for experts not chosen).  The choice itself has no gradient; a row
-// whose choice is undefined gets NaN.
+// (the slope without its subtraction; d_e = 0 for experts not chosen).  The
+// differences of the g come before their sum: g_j - sum_l s_l g_l / S, the same
+// number, is rounding noise where one slot has nearly all of the weight, and for
+// k = 1.  Of sum_l s_l d_l only 1e-20 sum_l s_l g_l scale / S^2 is left when
+// renormalised.  The choice itself has no gradient; a row whose choice is
+// undefined gets NaN.
 template <typename T, int N, bool SIGMOID>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem p) {
   const int lane = threadIdx.x & 63;
@@ -467,15 +464,22 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
     float x[N];
     load_row_of(logits, e0, p.E, x);
     const Scores<SIGMOID> score(x);
-    float sj = score.rounded(xj);
+    float sj, slope = 1.0f;
+    if constexpr (SIGMOID)
+      sj = sigmoid_slope(xj, slope);
+    else
+      sj = score(xj);
     sj = used ? sj : 0.0f;
+    float dot = SIGMOID ? 0.0f : wave_sum(sj * d);
     if (p.renorm) {
       // the sums take every lane: outside the choice of d
       const float total = wave_sum(sj) + kRenormEps;
-      const float mean = wave_sum(d * sj) / total;
-      d = used ? (d - mean) / total : 0.0f;
+      float t = kRenormEps * d;
+      for (int l = 0; l < p.k; ++l) t += lane_value(sj, l) * (d - lane_value(d, l));
+      d = used ? t / total / total : 0.0f;
+      dot = kRenormEps * dot / total / total;
     }
-    const float dot = SIGMOID ? 0.0f : wave_sum(sj * d);
+    if constexpr (SIGMOID) d *= slope;
     const bool undefined = __ballot(undefined_logits<SIGMOID>(x)) != 0;
     float de[N];
 #pragma unroll
@@ -490,16 +494,27 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
     float g[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      g[i] = SIGMOID ? score.slope(x[i]) * de[i] : score(x[i]) * (de[i] - dot);
+      g[i] = SIGMOID ? de[i] : score(x[i]) * (de[i] - dot);
       g[i] = undefined ? __builtin_nanf("") : g[i];
     }
     store_row_of(out, e0, p.E, g);
   }
 }
 
+// sum_l s_l (d_j - d_l) over the 16 lanes of a row: the others' values by rotations.
+template <int BY = 15>
+__device__ __forceinline__ float row_differences(float s, float d) {
+  const float sl = __uint_as_float(row_ror<BY>(__float_as_uint(s)));
+  const float dl = __uint_as_float(row_ror<BY>(__float_as_uint(d)));
+  if constexpr (BY == 1)
+    return sl * (d - dl);
+  else
+    return row_differences<BY - 1>(s, d) + sl * (d - dl);
+}
+
 // The same for at most 256 experts and 16 slots, four tokens a wave (see
-// route16_kernel).  Scores and gradients of single experts change lanes through
-// LDS, 16 V values a token.
+// route16_kernel).  Logits (sigmoid) or scores and gradients of single experts
+// change lanes through LDS, 16 V values a token.
 template <typename T, int V, bool SIGMOID>
 __global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProblem p) {
   __shared__ __attribute__((aligned(16))) float lds[16][16 * V];
@@ -519,24 +534,27 @@ __global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProble
     load_row_of(static_cast<const T*>(p.logits) + row * p.ld, e0, p.E, x);
     const Scores<SIGMOID, true> score(x);
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = score.rounded(x[i]);
+    for (int i = 0; i < V; ++i) s[i] = SIGMOID ? x[i] : score(x[i]);
     float4* mine = reinterpret_cast<float4*>(values + e0);
 #pragma unroll
     for (int i = 0; i < V; i += 4) mine[i / 4] = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
     // a wave's LDS accesses are in order: the fences only keep the compiler's
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    float sj = values[used ? id : 0];
+    float sj = values[used ? id : 0], slope = 1.0f;
+    if constexpr (SIGMOID) sj = sigmoid_slope(sj, slope);
     sj = used ? sj : 0.0f;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < V; i += 4) mine[i / 4] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float dot = SIGMOID ? 0.0f : row_sum_f(sj * d);
     if (p.renorm) {
       // the sums take every lane: outside the choice of d
       const float total = row_sum_f(sj) + kRenormEps;
-      const float mean = row_sum_f(d * sj) / total;
-      d = used ? (d - mean) / total : 0.0f;
+      const float t = row_differences(sj, d) + kRenormEps * d;
+      d = used ? t / total / total : 0.0f;
+      dot = kRenormEps * dot / total / total;
     }
-    const float dot = SIGMOID ? 0.0f : row_sum_f(sj * d);
+    if constexpr (SIGMOID) d *= slope;
     const bool undefined = row_max_u(undefined_logits<SIGMOID>(x) ? 1u : 0u) != 0;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (used) atomicAdd(&values[id], d);
@@ -550,7 +568,7 @@ __global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProble
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      g[i] = SIGMOID ? score.slope(x[i]) * g[i] : s[i] * (g[i] - dot);
+      if constexpr (!SIGMOID) g[i] = s[i] * (g[i] - dot);
       g[i] = undefined ? __builtin_nanf("") : g[i];
     }
     if (own < p.T) store_row_of(static_cast<T*>(p.grad_logits) + own * p.ld_grad, e0, p.E, g);

@@ -400,6 +400,45 @@ def test_route_gradients_of_saturated_sigmoids(E, dtype):
     _within(_f64(grad), ref, (24 * U + half + 24 * U * half) * np.abs(ref), "grad_logits")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E,k", [(24, 1), (24, 2), (60, 6), (256, 8), (256, 16), (300, 1), (300, 12), (60, 40)])
+def test_route_renormalised_gradients_of_a_dominating_slot(E, k, dtype, score):
+    """d_j = scale (sum_l s_l (g_j - g_l) + 1e-20 g_j) / S^2, relative to the sum of
+    its terms' sizes (0 but for 1e-20 with k = 1), against the formula in long double.
+    Scores are off by _score_tol or 8 U each and come in four times (s_l, S twice,
+    s_j or the slope, at most 20 U); differences, products and k additions add 3 + k U,
+    S's sum 2 k U, divisions and products with scale and slope 6 U."""
+    say(f"renormalised route gradients E={E} k={k} {dtype} {score}")
+    r = np.random.default_rng(E + k)
+    T, scale = 21, 2.5
+    grid = np.round(r.standard_normal((T, E)) * 16) / 16 - (6 if score == "sigmoid" else 0)
+    ids = np.argsort(r.random((T, E)), axis=1)[:, :k]
+    grid[np.arange(T), ids[:, 0]] += np.arange(T) * 0.5          # from level with the others to far above
+    logits, lv = _dev(grid, DT[dtype])
+    if k > 1:
+        ids[4, -1] = -1
+    g, gv = _dev(r.standard_normal((T, k)), torch.float32)
+    grad = fp8mm.moe_route_backward(g, logits, torch.from_numpy(ids.astype(np.int32)).to(DEV), score, True, scale)
+    lv, gv = lv.astype(np.longdouble), gv.astype(np.longdouble) * (ids >= 0)
+    ref = moe.route_backward(gv, lv, ids, score, True, scale)
+    s = moe.scores(lv, score)
+    at = np.where(ids >= 0, ids, 0)
+    chosen = np.take_along_axis(s, at, 1) * (ids >= 0)
+    S = chosen.sum(1, keepdims=True) + 1e-20
+    size = (np.abs(gv[:, :, None] - gv[:, None, :]) * chosen[:, None, :]).sum(2) + 1e-20 * np.abs(gv)
+    noise = np.abs(gv).max(1, keepdims=True) * S * 2.0 ** -58    # of the formula's own cancellation in long double
+    terms = np.zeros_like(lv)
+    np.add.at(terms, (np.arange(T)[:, None], at), (size + noise) * (ids >= 0) * scale / S ** 2)
+    if score == "softmax":
+        terms += 1e-20 * (chosen * np.abs(gv)).sum(1, keepdims=True) * scale / S ** 2 + noise * scale / S ** 2
+    factor = s if score == "softmax" else s * moe.scores(-lv, score)
+    half = BF16 if dtype == "bf16" else U
+    tol = factor * terms * (4 * _score_tol(lv) + (20 + 20 + 9 + 3 * k) * U) + factor * noise * scale / S ** 2
+    _within(_f64(grad), ref.astype(np.float64), (tol + half * np.abs(ref) + half * tol).astype(np.float64),
+            "grad_logits")
+
+
 @pytest.mark.parametrize("T,E,k", [(70001, 8, 2), (70003, 100, 3), (17001, 300, 4)])
 def test_route_more_tokens_than_workgroups(T, E, k):
     say(f"route {T}x{E}")
