@@ -448,7 +448,9 @@ __global__ __launch_bounds__(256) void route16_kernel(const RouteProblem p, cons
 // differences of the g come before their sum: g_j - sum_l s_l g_l / S, the same
 // number, is rounding noise where one slot has nearly all of the weight, and for
 // k = 1.  Of sum_l s_l d_l only 1e-20 sum_l s_l g_l scale / S^2 is left when
-// renormalised.  The choice itself has no gradient; a row whose choice is
+// renormalised.  In the same way, without renormalisation a chosen expert of a
+// softmax gets s_j (d_j rest + sum_l s_l (d_j - d_l)), rest the sum of the scores
+// that were not chosen.  The choice itself has no gradient; a row whose choice is
 // undefined gets NaN.
 template <typename T, int N, bool SIGMOID>
 __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem p) {
@@ -459,7 +461,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
     const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
     const int id = lane < p.k ? p.ids[row * p.k + lane] : -1;
     const bool used = id >= 0 && id < p.E;
-    float d = used ? p.grad_weights[row * p.k + lane] * p.scale : 0.0f;
+    float d = used ? p.grad_weights[row * p.k + lane] : 0.0f;
     const float xj = used ? to_float(logits[id]) : -kInf;
     float x[N];
     load_row_of(logits, e0, p.E, x);
@@ -471,30 +473,44 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const RouteProblem 
       sj = score(xj);
     sj = used ? sj : 0.0f;
     float dot = SIGMOID ? 0.0f : wave_sum(sj * d);
-    if (p.renorm) {
-      // the sums take every lane: outside the choice of d
-      const float total = wave_sum(sj) + kRenormEps;
-      float t = kRenormEps * d;
+    // d becomes d_j, for a softmax d_j - dot (the sums take every lane); scale comes
+    // last, since its rounding would show in the differences
+    if (p.renorm || !SIGMOID) {
+      float t = 0.0f;
       for (int l = 0; l < p.k; ++l) t += lane_value(sj, l) * (d - lane_value(d, l));
-      d = used ? t / total / total : 0.0f;
-      dot = kRenormEps * dot / total / total;
+      if (p.renorm) {
+        const float total = wave_sum(sj) + kRenormEps;
+        dot = kRenormEps * dot / total / total;
+        d = (t + kRenormEps * d) / total / total - dot;
+      } else {
+        uint32_t chosen = 0;
+        for (int l = 0; l < p.k; ++l) {
+          const uint32_t at = uint32_t(__builtin_amdgcn_readlane(id, l) - e0);
+          chosen |= at < uint32_t(N) ? 1u << at : 0u;
+        }
+        float rest = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) rest += chosen >> i & 1 ? 0.0f : score(x[i]);
+        d = t + d * wave_sum(rest);
+      }
     }
+    d *= p.scale;
+    dot *= p.scale;
     if constexpr (SIGMOID) d *= slope;
     const bool undefined = __ballot(undefined_logits<SIGMOID>(x)) != 0;
-    float de[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) de[i] = 0.0f;
-    for (int j = 0; j < p.k; ++j) {
-      const int e = __builtin_amdgcn_readlane(id, j);
-      const float dj = lane_value(d, j);
-#pragma unroll
-      for (int i = 0; i < N; ++i) de[i] += e == e0 + i ? dj : 0.0f;
-    }
-    T* out = static_cast<T*>(p.grad_logits) + row * p.ld_grad;
     float g[N];
 #pragma unroll
+    for (int i = 0; i < N; ++i) g[i] = 0.0f - dot;
+    for (int j = 0; j < p.k; ++j) {
+      const int e = __builtin_amdgcn_readlane(used ? id : -1, j);
+      const float dj = lane_value(d, j);
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[i] = e == e0 + i ? dj : g[i];
+    }
+    T* out = static_cast<T*>(p.grad_logits) + row * p.ld_grad;
+#pragma unroll
     for (int i = 0; i < N; ++i) {
-      g[i] = SIGMOID ? de[i] : score(x[i]) * (de[i] - dot);
+      if constexpr (!SIGMOID) g[i] *= score(x[i]);
       g[i] = undefined ? __builtin_nanf("") : g[i];
     }
     store_row_of(out, e0, p.E, g);
@@ -528,7 +544,7 @@ __global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProble
     const int64_t row = min(own, p.T - 1);       // lanes past the last token repeat it and write nothing
     const int id = l16 < p.k ? p.ids[row * p.k + l16] : -1;
     const bool used = id >= 0 && id < p.E;
-    float d = l16 < p.k ? p.grad_weights[row * p.k + l16] * p.scale : 0.0f;
+    float d = l16 < p.k ? p.grad_weights[row * p.k + l16] : 0.0f;
     d = used ? d : 0.0f;
     float x[V], s[V];
     load_row_of(static_cast<const T*>(p.logits) + row * p.ld, e0, p.E, x);
@@ -544,20 +560,34 @@ __global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProble
     if constexpr (SIGMOID) sj = sigmoid_slope(sj, slope);
     sj = used ? sj : 0.0f;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-    for (int i = 0; i < V; i += 4) mine[i / 4] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float dot = SIGMOID ? 0.0f : row_sum_f(sj * d);
+    // d becomes d_j, for a softmax d_j - dot (the sums take every lane); scale comes
+    // last, since its rounding would show in the differences
     if (p.renorm) {
-      // the sums take every lane: outside the choice of d
       const float total = row_sum_f(sj) + kRenormEps;
-      const float t = row_differences(sj, d) + kRenormEps * d;
-      d = used ? t / total / total : 0.0f;
       dot = kRenormEps * dot / total / total;
+      d = (row_differences(sj, d) + kRenormEps * d) / total / total - dot;
+    } else if constexpr (!SIGMOID) {
+      if (used) values[id] = 0.0f;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      float rest = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 v = mine[i / 4];
+        rest += v.x + v.y + (v.z + v.w);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      d = row_differences(sj, d) + d * row_sum_f(rest);
     }
+    d *= p.scale;
+    dot *= p.scale;
     if constexpr (SIGMOID) d *= slope;
     const bool undefined = row_max_u(undefined_logits<SIGMOID>(x) ? 1u : 0u) != 0;
+    const float others = 0.0f - dot;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) mine[i / 4] = make_float4(others, others, others, others);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (used) atomicAdd(&values[id], d);
+    if (used) values[id] = d;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     float g[V];
 #pragma unroll
@@ -568,7 +598,7 @@ __global__ __launch_bounds__(256) void route_backward16_kernel(const RouteProble
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if constexpr (!SIGMOID) g[i] = s[i] * (g[i] - dot);
+      if constexpr (!SIGMOID) g[i] *= s[i];
       g[i] = undefined ? __builtin_nanf("") : g[i];
     }
     if (own < p.T) store_row_of(static_cast<T*>(p.grad_logits) + own * p.ld_grad, e0, p.E, g);

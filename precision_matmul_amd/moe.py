@@ -204,7 +204,8 @@ def moe_route_forward(logits, k, score="softmax", bias=None, groups=1, group_top
 
 def moe_route_backward(grad_weights, logits, ids, score="softmax", renormalize=True, scale=1.0):
     """Gradient of the logits (their type and shape) from the gradient of
-    moe_route_forward's weights, the chosen ids held fixed."""
+    moe_route_forward's weights, the chosen ids (different ones in a token, as
+    the forward gives them) held fixed."""
     dtype = _need_float(logits, "logits")
     ld = _rows(logits, "logits")
     T, E = logits.shape

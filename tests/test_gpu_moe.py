@@ -439,6 +439,44 @@ def test_route_renormalised_gradients_of_a_dominating_slot(E, k, dtype, score):
             "grad_logits")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E,k", [(2, 1), (24, 1), (24, 2), (60, 6), (256, 8), (256, 16), (16, 16), (300, 1), (300, 12),
+                                 (60, 40), (40, 40), (1000, 5)])
+def test_route_softmax_gradients_of_a_dominating_expert(E, k, dtype):
+    """s_j (d_j rest + sum_l s_l (d_j - d_l)) for the chosen, -s_e sum_l s_l d_l for the
+    others, relative to the sum of their terms' sizes.  The scores come in twice and
+    their sum of the rest once (_score_tol each), differences, products and k
+    additions add k + 12 U."""
+    say(f"softmax route gradients E={E} k={k} {dtype}")
+    r = np.random.default_rng(E + k)
+    T, scale = 27, 2.5
+    grid = np.round(r.standard_normal((T, E)) * 16) / 16
+    ids = np.argsort(r.random((T, E)), axis=1)[:, :k]
+    grid[np.arange(T), ids[:, 0]] += np.arange(T)                # from level with the others to far above
+    logits, lv = _dev(grid, DT[dtype])
+    if k > 1:
+        ids[4, -1] = -1
+    g, gv = _dev(r.standard_normal((T, k)), torch.float32)
+    grad = fp8mm.moe_route_backward(g, logits, torch.from_numpy(ids.astype(np.int32)).to(DEV), "softmax", False, scale)
+    used = ids >= 0
+    d = scale * gv * used
+    s = moe.scores(lv, "softmax")
+    chosen = np.take_along_axis(s, np.where(used, ids, 0), 1) * used
+    others = s.copy()
+    np.put_along_axis(others, np.where(used, ids, ids[:, :1]), 0.0, 1)      # an empty slot: the first's again
+    rest = others.sum(1, keepdims=True)
+    ref, size = (-s * (chosen * d).sum(1, keepdims=True), s * (chosen * np.abs(d)).sum(1, keepdims=True))
+    diff = d[:, :, None] - d[:, None, :]
+    for t in range(T):
+        at = ids[t][used[t]]
+        ref[t, at] = (s[t, at] * (d[t] * rest[t] + (chosen[t] * diff[t]).sum(1))[used[t]])
+        size[t, at] = (s[t, at] * (np.abs(d[t]) * rest[t] + (chosen[t] * np.abs(diff[t])).sum(1))[used[t]])
+    assert np.abs(ref - moe.route_backward(gv, lv, ids, "softmax", False, scale)).max() <= 1e-14 * scale * 4
+    half = BF16 if dtype == "bf16" else U
+    tol = size * (3 * _score_tol(lv) + (k + 12) * U)
+    _within(_f64(grad), ref, tol + half * np.abs(ref) + half * tol + TINY, "grad_logits")
+
+
 @pytest.mark.parametrize("T,E,k", [(70001, 8, 2), (70003, 100, 3), (17001, 300, 4)])
 def test_route_more_tokens_than_workgroups(T, E, k):
     say(f"route {T}x{E}")
