@@ -10,6 +10,10 @@
 // registers, as loaded, between its statistics and its output, so the
 // variance is the sum of centred squares (two passes over registers, not the
 // difference of two large sums).  All sums are float32.
+//
+// Lanes past a row's end hold x = dy = 0.  The sum of a xh is rstd times the sum of
+// a (x - mean), which is 0 there; (x - mean) rstd alone can pass float32's range (a
+// row of one large value under a small eps), and 0 times that is NaN.
 #include "moe_launch.hpp"
 #include "ops_common.hpp"
 
@@ -260,11 +264,11 @@ __global__ __launch_bounds__(64 * (WPR == 1 ? kRowWaves : WPR)) void norm_backwa
       unpack<T>(vg[it], g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float xh = (f[i] - mean) * rstd;    // dy is 0 past the row's end
+        const float t = f[i] - mean;
         const float a = g[i] * w[it][i];
         sa += a;
-        sax += a * xh;
-        dw[it][i] += g[i] * xh;
+        sax += a * t;                             // 0 past the row's end
+        dw[it][i] += g[i] * (t * rstd);
         db[it][i] += g[i];
       }
     }
@@ -285,7 +289,7 @@ __global__ __launch_bounds__(64 * (WPR == 1 ? kRowWaves : WPR)) void norm_backwa
       slot ^= 1;
     }
     sa *= inv_c;
-    sax *= inv_c;
+    sax *= rstd * inv_c;
     if (dx) {
 #pragma unroll
       for (int it = 0; it < NIT; ++it) {
@@ -388,9 +392,9 @@ __global__ __launch_bounds__(256) void norm_backward_few_kernel(
       unpack<T>(vg[it], g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float a = g[i] * w[it][i];          // dy is 0 past the row's end
+        const float a = g[i] * w[it][i];
         sa += a;
-        sax += a * ((f[i] - mean) * rstd);
+        sax += a * (f[i] - mean);                 // 0 past the row's end
       }
     }
     sa = wave_sum(sa);
@@ -406,7 +410,7 @@ __global__ __launch_bounds__(256) void norm_backward_few_kernel(
       sax = part[1][0][0] + part[1][0][1] + part[1][0][2] + part[1][0][3];
     }
     sa /= float(C);
-    sax /= float(C);
+    sax = sax * rstd / float(C);
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
       float f[V], g[V];
@@ -476,11 +480,11 @@ __global__ __launch_bounds__(256) void norm_backward_long_kernel(
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         sa += g[i] * w[i];
-        sax += g[i] * w[i] * ((f[i] - mean) * rstd);
+        sax += g[i] * w[i] * (f[i] - mean);       // 0 past the row's end
       }
     }
     sa = row_sum<4>(sa, part, 0) / float(C);
-    sax = row_sum<4>(sax, part, 1) / float(C);
+    sax = row_sum<4>(sax, part, 1) * rstd / float(C);
     for (int64_t c = int64_t(threadIdx.x) * V; c < C; c += 256 * V) {
       float f[V], g[V];
       Params<P, V> w;

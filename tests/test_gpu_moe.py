@@ -211,6 +211,20 @@ def test_layer_norm_gradients_over_many_rows(C):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("R,C", [(5, 1), (6, 100), (3, 1152), (4, 2056), (600, 3), (600, 513), (530, 1152), (520, 2056),
+                                 (515, 4099), (2, 8200), (3, 8203)])
+def test_layer_norm_backward_of_rows_of_one_large_value(R, C, dtype):
+    """x - mean is 0 in the row, and mean rstd = 2^110 1e6 is past float32's range:
+    dx = rstd (dy - mean dy), with the places past the row's end out of the sums."""
+    say(f"layer norm backward of constant rows {R}x{C} {dtype}")
+    x = torch.full((R, C), 2.0 ** 110, dtype=DT[dtype], device=DEV)
+    dy, dyv = _dev(np.random.default_rng(C).standard_normal((R, C)), DT[dtype])
+    _, mean, rstd = fp8mm.layer_norm_forward(x, eps=1e-12)
+    assert bool((mean == 2.0 ** 110).all())                 # the sums of equal powers of two are exact here
+    _check_norm_backward(x, np.full((R, C), 2.0 ** 110), dy, dyv, None, None, mean, rstd, dtype, "fp32")
+
+
 def test_layer_norm_empty_and_partial_results():
     x = torch.empty((0, 130), dtype=torch.bfloat16, device=DEV)
     y, mean, rstd = fp8mm.layer_norm_forward(x)
