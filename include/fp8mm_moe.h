@@ -105,6 +105,10 @@ fp8mm_status fp8mm_moe_route_backward(const float* grad_weights, const void* log
 
 /* ---------------------------------------------------------------------------
  * Permutation of token rows into expert order.
+ * T k < 2^31 and C < 2^31 throughout, and one launch of at most 2^25 waves, else
+ * FP8MM_EINVAL: T ceil(C / 512) waves for bf16 rows, T ceil(C / 256) for fp32
+ * rows and T ceil(C / 1024) for codes in dispatch and combine; in combine's
+ * backward T k, or T k / 4 for rows of at most 512 (bf16) or 256 (fp32) columns.
  * ------------------------------------------------------------------------- */
 
 /* Workspace bytes of fp8mm_moe_plan for T tokens of k slots over E experts (0
@@ -155,7 +159,8 @@ fp8mm_status fp8mm_moe_combine_backward(const void* grad_out, int64_t ld_go, con
 
 /* ---------------------------------------------------------------------------
  * Gated activation with an 8-bit checkpoint:  x = [gate, up] bf16 [R, 2 F],
- * h = gate sigmoid(gate) up, F % 128 == 0.
+ * h = gate sigmoid(gate) up, F % 128 == 0, F <= 2^21, R < 2^31 and
+ * ceil(R / 32) (F / 128) <= 2^23 (one launch), else FP8MM_EINVAL.
  *   h: bf16 [R, F], or NULL.
  *   h_q, h_scale: the 1x128 codes uint8 [R, F] and scales float32 [F / 128, R]
  *     of the float32 values of h (no bf16 rounding in between), or NULL.

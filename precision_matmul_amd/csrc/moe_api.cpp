@@ -16,7 +16,7 @@ using fp8mm::api::ok;
 namespace {
 
 constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
-// waves of one launch: 64 threads each, fewer than 2^32 threads
+// waves of one launch at most: 64 threads each, fewer than 2^32 threads
 constexpr int64_t kMaxWaves = int64_t(1) << 25;
 
 bool valid_dtype(int d) { return d == FP8MM_OUT_BF16 || d == FP8MM_OUT_FP32; }
@@ -39,15 +39,25 @@ fp8mm_status check_ld(int64_t ld, int64_t cols, const char* name) {
   return FP8MM_OK;
 }
 
+// `units` waves of each of `n` tokens or slots.
+fp8mm_status check_waves(int64_t n, int64_t units, int64_t T, int64_t C) {
+  if (n > 0 && units > kMaxWaves / n)
+    return fail(FP8MM_EINVAL, "[%lld, %lld] is too large for one launch", (long long)T, (long long)C);
+  return FP8MM_OK;
+}
+
 fp8mm_status check_permute(fp8mm_dtype dtype, int64_t T, int64_t C, int64_t k, const int32_t* row_of_slot) {
   if (!valid_dtype(dtype)) return fail(FP8MM_EINVAL, "unknown dtype");
   if (T < 0 || C < 0 || k < 1) return fail(FP8MM_EINVAL, "need T >= 0, C >= 0 and k >= 1");
   if (k > fp8mm::kRouteMaxK) return fail(FP8MM_ENOTIMPL, "k (%lld) above %d", (long long)k, fp8mm::kRouteMaxK);
   if (T > kMaxInt / k || C > kMaxInt) return fail(FP8MM_EINVAL, "T k and C must be < 2^31");
-  if (T * k > kMaxWaves || T * ((C + 255) / 256) > kMaxWaves)
-    return fail(FP8MM_EINVAL, "[%lld, %lld] is too large for one launch", (long long)T, (long long)C);
   if (T > 0 && !row_of_slot) return fail(FP8MM_EINVAL, "row_of_slot must not be NULL");
   return FP8MM_OK;
+}
+
+fp8mm_status check_row_waves(int64_t T, int64_t C, fp8mm_dtype dtype) {
+  const int64_t columns = fp8mm::row_columns(dtype == FP8MM_OUT_FP32);
+  return check_waves(T, (C + columns - 1) / columns, T, C);
 }
 
 }  // namespace
@@ -239,6 +249,7 @@ fp8mm_status fp8mm_moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E,
 fp8mm_status fp8mm_moe_dispatch(const void* x, fp8mm_dtype dtype, int64_t T, int64_t C, int64_t ld_x,
                                 const int32_t* row_of_slot, int64_t k, void* out, int64_t ld_out, hipStream_t stream) {
   fp8mm_status st = check_permute(dtype, T, C, k, row_of_slot);
+  if (st == FP8MM_OK) st = check_row_waves(T, C, dtype);
   if (st == FP8MM_OK) st = check_ld(ld_x, C, "ld_x");
   if (st == FP8MM_OK) st = check_ld(ld_out, C, "ld_out");
   if (st != FP8MM_OK) return st;
@@ -262,6 +273,7 @@ fp8mm_status fp8mm_moe_dispatch(const void* x, fp8mm_dtype dtype, int64_t T, int
 fp8mm_status fp8_moe_dispatch(const void* x, int64_t T, int64_t C, int64_t ld_x, const int32_t* row_of_slot, int64_t k,
                               uint8_t* q, int64_t ld_q, float* scale, hipStream_t stream) {
   fp8mm_status st = check_permute(FP8MM_OUT_BF16, T, C, k, row_of_slot);
+  if (st == FP8MM_OK) st = check_waves(T, (C + fp8mm::kCodeColumns - 1) / fp8mm::kCodeColumns, T, C);
   if (st != FP8MM_OK) return st;
   if (C % 128 != 0) return fail(FP8MM_EINVAL, "C (%lld) must be a multiple of 128", (long long)C);
   if (ld_x < C || ld_x % 8 != 0 || ld_x > kMaxLd)
@@ -288,6 +300,7 @@ fp8mm_status fp8mm_moe_combine(const void* rows, fp8mm_dtype dtype, int64_t T, i
                                const int32_t* row_of_slot, const float* weights, int64_t k, void* out, int64_t ld_out,
                                hipStream_t stream) {
   fp8mm_status st = check_permute(dtype, T, C, k, row_of_slot);
+  if (st == FP8MM_OK) st = check_row_waves(T, C, dtype);
   if (st == FP8MM_OK) st = check_ld(ld_rows, C, "ld_rows");
   if (st == FP8MM_OK) st = check_ld(ld_out, C, "ld_out");
   if (st != FP8MM_OK) return st;
@@ -314,6 +327,10 @@ fp8mm_status fp8mm_moe_combine_backward(const void* grad_out, int64_t ld_go, con
                                         const float* weights, int64_t k, void* grad_rows, int64_t ld_gr,
                                         float* grad_weights, hipStream_t stream) {
   fp8mm_status st = check_permute(dtype, T, C, k, row_of_slot);
+  if (st == FP8MM_OK) {
+    const int64_t slots = 64 / fp8mm::slot_lanes(C, dtype == FP8MM_OUT_FP32);    // of a wave
+    st = check_waves((T * k + slots - 1) / slots, 1, T * k, C);
+  }
   if (st == FP8MM_OK) st = check_ld(ld_go, C, "ld_go");
   if (st == FP8MM_OK && grad_weights) st = check_ld(ld_rows, C, "ld_rows");
   if (st == FP8MM_OK && grad_rows) st = check_ld(ld_gr, C, "ld_gr");

@@ -83,6 +83,12 @@ struct PermuteProblem {
   float* scale;                  // FP8 dispatch: [C / 128, T k]
 };
 
+// Columns of one token that a wave of dispatch (rows, codes) and of combine covers.
+constexpr int64_t kCodeColumns = 1024;
+inline int64_t row_columns(bool fp32) { return fp32 ? 256 : 512; }
+// Lanes that share a slot in combine's backward.
+inline int64_t slot_lanes(int64_t C, bool fp32) { return C > row_columns(fp32) ? 64 : 16; }
+
 hipError_t launch_dispatch(const PermuteProblem& p, hipStream_t st);
 hipError_t launch_dispatch_fp8(const PermuteProblem& p, hipStream_t st);
 hipError_t launch_combine(const PermuteProblem& p, hipStream_t st);

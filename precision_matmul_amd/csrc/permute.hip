@@ -339,8 +339,7 @@ hipError_t launch_plan(const int32_t* ids, int64_t n, int E, int32_t* offsets, i
 
 hipError_t launch_dispatch(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0 || p.C == 0) return hipSuccess;
-  const int vec = p.fp32 ? 4 : 8;
-  const int strips = int((p.C + 64 * vec - 1) / (64 * vec));
+  const int strips = int((p.C + row_columns(p.fp32) - 1) / row_columns(p.fp32));
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(unsigned((p.T * strips + 3) / 4)), dim3(256), 0, st, p, strips);
     return hipGetLastError();
@@ -352,7 +351,7 @@ hipError_t launch_dispatch(const PermuteProblem& p, hipStream_t st) {
 
 hipError_t launch_dispatch_fp8(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0 || p.C == 0) return hipSuccess;
-  const int strips = int((p.C + 1023) / 1024);
+  const int strips = int((p.C + kCodeColumns - 1) / kCodeColumns);
   const dim3 grid(xcd_grid((p.T * strips + 3) / 4));
   if (p.T * p.k * p.C > kL2Bytes)
     hipLaunchKernelGGL((dispatch_fp8_kernel<true>), grid, dim3(256), 0, st, p, strips);
@@ -363,8 +362,7 @@ hipError_t launch_dispatch_fp8(const PermuteProblem& p, hipStream_t st) {
 
 hipError_t launch_combine(const PermuteProblem& p, hipStream_t st) {
   if (p.T == 0 || p.C == 0) return hipSuccess;
-  const int vec = p.fp32 ? 4 : 8;
-  const int strips = int((p.C + 64 * vec - 1) / (64 * vec));
+  const int strips = int((p.C + row_columns(p.fp32) - 1) / row_columns(p.fp32));
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(unsigned((p.T * strips + 3) / 4)), dim3(256), 0, st, p, strips);
     return hipGetLastError();
@@ -387,7 +385,7 @@ static hipError_t run_combine_backward(const PermuteProblem& p, hipStream_t st) 
 
 template <typename T>
 static hipError_t combine_backward_of(const PermuteProblem& p, hipStream_t st) {
-  if (p.C > 64 * kVec<T>) return run_combine_backward<T, 64, 4, false>(p, st);
+  if (slot_lanes(p.C, p.fp32) == 64) return run_combine_backward<T, 64, 4, false>(p, st);
   return p.C % kVec<T> ? run_combine_backward<T, 16, 2, true>(p, st) : run_combine_backward<T, 16, 2, false>(p, st);
 }
 

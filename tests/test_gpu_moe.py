@@ -880,6 +880,30 @@ def test_offsets_past_32_bits():
     assert torch.equal(gx[-5:], gx1) and torch.equal(h[-5:], h1)
 
 
+def test_permutation_of_more_slots_than_waves():
+    """More than 2^25 slots: dispatch and combine take a wave a token, combine's
+    backward of short rows a quarter of one a slot."""
+    T, k, C, E = 600011, 64, 128, 16
+    assert T * k > 2 ** 25
+    say("permutation of 38 million slots")
+    ids = (torch.arange(T * k, device=DEV, dtype=torch.int64) * 7919 % E).to(torch.int32).view(T, k)
+    slots = fp8mm.moe_plan(ids, E)[1]
+    x = torch.randn((T, C), device=DEV, dtype=torch.bfloat16)
+    rows = fp8mm.moe_dispatch_forward(x, slots)
+    some = torch.arange(0, T, 9973, device=DEV)
+    at = slots[some].flatten().long()
+    assert torch.equal(rows[at], x[some].repeat_interleave(k, 0))
+    assert torch.equal(fp8mm.moe_combine_forward(rows, slots), x * k)       # 64 equal bf16 values: exact
+    gr, gw = fp8mm.moe_combine_backward(x, rows, slots)
+    assert torch.equal(gr, rows)
+    dot = (x.double() ** 2).sum(1, keepdim=True)
+    assert bool(((gw - dot).abs() <= (128 / 16 + 4 + 10) * U * dot).all())
+    del gr, rows
+    q, s = fp8mm.fp8_moe_dispatch(x, slots)
+    q1, s1 = fp8mm.fp8_quantize_blockwise(x[some].contiguous(), (1, 128))
+    assert torch.equal(q[at], q1.repeat_interleave(k, 0)) and torch.equal(s[:, at], s1.repeat_interleave(k, 1))
+
+
 def test_strided_outputs_leave_the_padding_alone():
     """The C calls take a row stride for each output: columns past the row stay."""
     lib = fp8mm._lib.load()

@@ -203,3 +203,28 @@ SWIB_D = dict(g=FAKE, ldg=128, c=FAKE, ldc=256, cs=FAKE, R=4, F=128, gx=FAKE, ld
 def test_swiglu_refusals(lib, name, order, base, kw):
     assert _call(lib, name, order, base, kw) == _lib.EINVAL
     assert lib.fp8mm_last_error().decode()
+
+
+# Sizes that one launch covers reach the checks behind the launch's own (a null
+# pointer here); larger ones are refused as too large.
+@pytest.mark.parametrize("name,order,base,kw,fits", [
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(T=2 ** 21, C=5120, ldx=5120, ldo=5120, x=None), True),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(T=2 ** 25, k=63, x=None), True),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(T=2 ** 25 + 1, x=None), False),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(T=2 ** 24, C=1025, ldx=1025, ldo=1025, x=None), False),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(dt=1, T=2 ** 24, C=512, ldx=512, ldo=512, x=None), True),
+    ("fp8mm_moe_dispatch", DISP, DISP_D, dict(dt=1, T=2 ** 24, C=513, ldx=513, ldo=513, x=None), False),
+    ("fp8mm_moe_combine", COMB, COMB_D, dict(T=2 ** 21, C=8192, ldr=8192, ldo=8192, r=None), True),
+    ("fp8mm_moe_combine", COMB, COMB_D, dict(T=2 ** 21, C=8193, ldr=8193, ldo=8193, r=None), False),
+    ("fp8mm_moe_combine_backward", COMBB, COMBB_D, dict(T=2 ** 21, k=64, go=None), True),
+    ("fp8mm_moe_combine_backward", COMBB, COMBB_D, dict(T=2 ** 21 + 1, k=64, go=None), False),
+    ("fp8mm_moe_combine_backward", COMBB, COMBB_D, dict(T=2 ** 19, k=64, C=5120, ldgo=5120, ldr=5120, ldgr=5120,
+                                                        go=None), True),
+    ("fp8mm_moe_combine_backward", COMBB, COMBB_D, dict(T=2 ** 19 + 1, k=64, C=513, ldgo=513, ldr=513, ldgr=513,
+                                                        go=None), False),
+    ("fp8_moe_dispatch", FDISP, FDISP_D, dict(T=2 ** 24, C=2048, ldx=2048, ldq=2048, x=None), True),
+    ("fp8_moe_dispatch", FDISP, FDISP_D, dict(T=2 ** 24 + 1, C=2048, ldx=2048, ldq=2048, x=None), False),
+])
+def test_permutation_launch_limits(lib, name, order, base, kw, fits):
+    assert _call(lib, name, order, base, kw) == _lib.EINVAL
+    assert ("too large for one launch" in lib.fp8mm_last_error().decode()) != fits
