@@ -6,7 +6,8 @@ them together.
 Functions named *_forward and *_backward are one call of the library each;
 layer_norm, moe_route, moe_dispatch, moe_combine and fp8_swiglu are the same
 operators as differentiable functions.  Matrices are 2-D and row-major with any
-row stride (the differentiable functions make their inputs so).  Errors are
+row stride, vectors, ids and weights dense (the differentiable functions make
+their inputs so).  Errors are
 those of the rest of the package: ValueError, NotImplementedError,
 RuntimeError.
 """
@@ -150,6 +151,8 @@ class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
         flat = x.contiguous().view(-1, x.shape[-1])
+        weight = None if weight is None else weight.contiguous()
+        bias = None if bias is None else bias.contiguous()
         y, mean, rstd = layer_norm_forward(flat, weight, bias, eps)
         ctx.save_for_backward(flat, weight, mean, rstd)
         ctx.bias_dtype = None if bias is None else bias.dtype
@@ -225,6 +228,7 @@ class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, score, bias, groups, group_topk, group_score, renormalize, scale):
         logits = logits.contiguous()
+        bias = None if bias is None else bias.contiguous()
         ids, weights = moe_route_forward(logits, k, score, bias, groups, group_topk, group_score, renormalize, scale)
         ctx.save_for_backward(logits, ids)
         ctx.args = score, renormalize, scale
@@ -352,6 +356,7 @@ def moe_combine_backward(grad_out, rows, row_of_slot, weights=None, need_rows=Tr
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, row_of_slot):
+        row_of_slot = row_of_slot.contiguous()
         ctx.save_for_backward(row_of_slot)
         return moe_dispatch_forward(x.contiguous(), row_of_slot)
 
@@ -370,7 +375,8 @@ def moe_dispatch(x, row_of_slot):
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, row_of_slot, weights):
-        rows = rows.contiguous()
+        rows, row_of_slot = rows.contiguous(), row_of_slot.contiguous()
+        weights = None if weights is None else weights.contiguous()
         ctx.save_for_backward(rows, row_of_slot, weights)
         return moe_combine_forward(rows, row_of_slot, weights)
 

@@ -634,6 +634,47 @@ def test_permutation_autograd():
     assert torch.allclose(w.grad.double(), dot * used, rtol=1e-4, atol=1e-4)
 
 
+def test_differentiable_functions_take_any_strides():
+    """Transposed, sliced and broadcast inputs give the bits and gradients of dense ones."""
+    T, C, k, E = 33, 256, 4, 16
+    torch.manual_seed(4)
+
+    def strided(t):
+        return t.t().contiguous().t() if t.dim() == 2 else torch.stack([t, t], 1)[:, 0]
+
+    def check(f, *inputs):
+        got = []
+        for change in (strided, lambda t: t):
+            leaves = [t.detach().clone().requires_grad_(t.is_floating_point()) for t in inputs]
+            views = [change(t) for t in leaves]
+            out = f(*views)
+            out.backward(torch.ones_like(out))
+            got.append([out.detach()] + [t.grad for t in leaves if t.is_floating_point()])
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+
+    x, v = torch.randn((T, C), device=DEV), torch.randn((C,), device=DEV)
+    check(fp8mm.layer_norm, x, v, v + 1)
+    balance = strided(torch.randn((E,), device=DEV) * 0.1)
+    assert not balance.is_contiguous()
+    logits = torch.randn((T, E), device=DEV)
+    check(lambda l: fp8mm.moe_route(l, k, "sigmoid", balance)[1], logits)
+    slots = fp8mm.moe_plan(fp8mm.moe_route_forward(logits, k)[0], E)[1]
+    check(lambda x, s: fp8mm.moe_dispatch(x, s), x, slots)
+    check(lambda r, s, w: fp8mm.moe_combine(r, s, w), torch.randn((T * k, C), device=DEV), slots,
+          torch.rand((T, k), device=DEV))
+    check(fp8mm.fp8_swiglu, x.bfloat16())
+    w_in, w_out = (torch.randn(s, device=DEV).bfloat16() for s in ((E, 2 * 128, C), (E, C, 128)))
+    check(lambda x, i, w: fp8mm.fp8_moe(x, w_in, w_out, i, w), x.bfloat16(), torch.arange(
+        T * k, device=DEV, dtype=torch.int32).view(T, k) % E, torch.rand((T, k), device=DEV))
+    g = torch.randn((1, C), device=DEV).expand(T, C)                         # a broadcast gradient
+    leaf = x.clone().requires_grad_(True)
+    fp8mm.layer_norm(leaf).backward(g)
+    again = x.clone().requires_grad_(True)
+    fp8mm.layer_norm(again).backward(g.contiguous())
+    assert torch.equal(leaf.grad, again.grad)
+
+
 # ------------------------------------------------------------ gated activation
 
 def _dequantize(q, s):
