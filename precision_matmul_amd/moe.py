@@ -79,6 +79,13 @@ def _code(table, value, name):
     return table[value]
 
 
+def _differentiates(*tensors):
+    """Whether a gradient of one of the inputs can be asked for later.  (Inside an
+    autograd function it is too late to ask: grad mode is off there, and its
+    needs_input_grad is true of a parameter under no_grad too.)"""
+    return torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in tensors)
+
+
 # ------------------------------------------------------------------ layer norm
 
 def _param(x, t, name):
@@ -463,8 +470,11 @@ class _Swiglu(torch.autograd.Function):
 
 def fp8_swiglu(x):
     """silu(gate) up of x = [gate, up] bf16 [R, 2 F], differentiable; the
-    backward pass reads x in 8 bits (1x128 codes), and x itself is not kept."""
-    return _Swiglu.apply(x)
+    backward pass reads x in 8 bits (1x128 codes), and x itself is not kept.
+    The codes are made only where a gradient can follow."""
+    if _differentiates(x):
+        return _Swiglu.apply(x)
+    return fp8_swiglu_forward(x.contiguous(), "bf16", False)[0]
 
 
 # ---------------------------------------------------------------- expert layer
@@ -483,6 +493,28 @@ def _experts_mm(q, s, w_q, w_s, offsets, layout="NK"):
     N = w_q.shape[1 if layout == "NK" else 2]
     out = q.new_empty((q.shape[0], N), dtype=torch.bfloat16)
     return fp8_scaled_grouped_mm_v2(q, w_q, offsets, s, "1x128", w_s, "128x128", b_layout=layout, out=out)
+
+
+def _experts_forward(x, w_in, w_out, ids, weights, train):
+    """(y, what FP8MoE.backward needs: nothing without train)."""
+    for t, name in ((x, "x"), (w_in, "w_in"), (w_out, "w_out")):
+        _need(t, torch.bfloat16, name)
+    E = w_in.shape[0]
+    if w_in.dim() != 3 or w_out.dim() != 3 or w_in.shape != (E, 2 * w_out.shape[2], w_out.shape[1]):
+        raise ValueError("w_in must be [E, 2 F, C] and w_out [E, C, F], "
+                         f"got {list(w_in.shape)} and {list(w_out.shape)}")
+    if w_out.shape[0] != E:
+        raise ValueError(f"w_in has {E} experts, w_out {w_out.shape[0]}")
+    x, weights = x.contiguous(), weights.contiguous()
+    offsets, row_of_slot = moe_plan(ids.contiguous(), E)
+    q_in, s_in = _weight_codes(w_in)
+    q_out, s_out = _weight_codes(w_out)
+    q, s = fp8_moe_dispatch(x, row_of_slot)
+    gate_up = _experts_mm(q, s, q_in, s_in, offsets)
+    (hq, hs), checkpoint = fp8_swiglu_forward(gate_up, "fp8", train)
+    rows = _experts_mm(hq, hs, q_out, s_out, offsets)
+    saved = (x, q_in, s_in, q_out, s_out, *checkpoint, rows, offsets, row_of_slot, weights) if train else ()
+    return moe_combine_forward(rows, row_of_slot, weights), saved
 
 
 class FP8MoE(torch.autograd.Function):
@@ -507,26 +539,9 @@ class FP8MoE(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w_in, w_out, ids, weights):
-        for t, name in ((x, "x"), (w_in, "w_in"), (w_out, "w_out")):
-            _need(t, torch.bfloat16, name)
-        E = w_in.shape[0]
-        if w_in.dim() != 3 or w_out.dim() != 3 or w_in.shape != (E, 2 * w_out.shape[2], w_out.shape[1]):
-            raise ValueError("w_in must be [E, 2 F, C] and w_out [E, C, F], "
-                             f"got {list(w_in.shape)} and {list(w_out.shape)}")
-        if w_out.shape[0] != E:
-            raise ValueError(f"w_in has {E} experts, w_out {w_out.shape[0]}")
-        x, weights = x.contiguous(), weights.contiguous()
-        train = any(ctx.needs_input_grad)
-        offsets, row_of_slot = moe_plan(ids.contiguous(), E)
-        q_in, s_in = _weight_codes(w_in)
-        q_out, s_out = _weight_codes(w_out)
-        q, s = fp8_moe_dispatch(x, row_of_slot)
-        gate_up = _experts_mm(q, s, q_in, s_in, offsets)
-        (hq, hs), checkpoint = fp8_swiglu_forward(gate_up, "fp8", train)
-        rows = _experts_mm(hq, hs, q_out, s_out, offsets)
-        if train:
-            ctx.save_for_backward(x, q_in, s_in, q_out, s_out, *checkpoint, rows, offsets, row_of_slot, weights)
-        return moe_combine_forward(rows, row_of_slot, weights)
+        y, saved = _experts_forward(x, w_in, w_out, ids, weights, any(ctx.needs_input_grad))
+        ctx.save_for_backward(*saved)
+        return y
 
     @staticmethod
     @once_differentiable
@@ -562,5 +577,8 @@ class FP8MoE(torch.autograd.Function):
 
 def fp8_moe(x, w_in, w_out, ids, weights):
     """The expert layer through FP8MoE (differentiable in x, w_in, w_out and
-    weights; ids and weights from moe_route)."""
-    return FP8MoE.apply(x, w_in, w_out, ids, weights)
+    weights; ids and weights from moe_route).  Where no gradient can follow (no_grad,
+    or no input that needs one), its forward alone, without the 8-bit checkpoint."""
+    if _differentiates(x, w_in, w_out, weights):
+        return FP8MoE.apply(x, w_in, w_out, ids, weights)
+    return _experts_forward(x, w_in, w_out, ids, weights, False)[0]

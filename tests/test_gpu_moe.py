@@ -858,6 +858,36 @@ def test_expert_layer_graph_follows_new_routing():
             assert float(eager[2].float().abs().max()) > 0
 
 
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_no_checkpoint_where_no_gradient_can_follow(mode, monkeypatch):
+    """Parameters need gradients under no_grad too; the activation's codes are not
+    made there, and the results have the same bits."""
+    asked = []
+    forward = fp8mm.moe.fp8_swiglu_forward
+
+    def spy(x, out="bf16", checkpoint=True):
+        asked.append(bool(checkpoint))
+        return forward(x, out, checkpoint)
+
+    monkeypatch.setattr(fp8mm.moe, "fp8_swiglu_forward", spy)
+    E, C, F, k, T = 4, 256, 128, 2, 40
+    torch.manual_seed(2)
+    w_in = torch.nn.Parameter(torch.randn((E, 2 * F, C), device=DEV).bfloat16() / 16)
+    w_out = torch.nn.Parameter(torch.randn((E, C, F), device=DEV).bfloat16() / 11)
+    x = torch.randn((T, C), device=DEV).bfloat16()
+    u = torch.nn.Parameter(torch.randn((T, C), device=DEV).bfloat16())
+    ids, w = fp8mm.moe_route_forward(torch.randn((T, E), device=DEV), k)
+    y, h = fp8mm.fp8_moe(x, w_in, w_out, ids, w), fp8mm.fp8_swiglu(u)
+    assert asked == [True, True] and y.requires_grad and h.requires_grad
+    with mode():
+        assert torch.equal(fp8mm.fp8_moe(x, w_in, w_out, ids, w), y)
+        assert torch.equal(fp8mm.fp8_swiglu(u), h)
+    assert torch.equal(fp8mm.fp8_moe(x, w_in.detach(), w_out.detach(), ids, w), y)
+    assert asked[2:] == [False] * 3
+    y.float().sum().backward()
+    assert bool(w_in.grad.any()) and bool(w_out.grad.any())
+
+
 def test_no_tokens_and_tokens_without_experts():
     E, C, F, k = 4, 256, 128, 2
     w_in = torch.randn((E, 2 * F, C), device=DEV).bfloat16().requires_grad_(True)
