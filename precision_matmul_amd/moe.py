@@ -384,7 +384,9 @@ class _Combine(torch.autograd.Function):
     def forward(ctx, rows, row_of_slot, weights):
         rows, row_of_slot = rows.contiguous(), row_of_slot.contiguous()
         weights = None if weights is None else weights.contiguous()
-        ctx.save_for_backward(rows, row_of_slot, weights)
+        # the rows are for the gradient of the weights alone
+        ctx.save_for_backward(rows if ctx.needs_input_grad[2] else None, row_of_slot, weights)
+        ctx.dtype = rows.dtype
         return moe_combine_forward(rows, row_of_slot, weights)
 
     @staticmethod
@@ -392,7 +394,7 @@ class _Combine(torch.autograd.Function):
     def backward(ctx, grad):
         rows, row_of_slot, weights = ctx.saved_tensors
         need = ctx.needs_input_grad
-        grad_rows, grad_weights = moe_combine_backward(grad.to(rows.dtype).contiguous(), rows, row_of_slot, weights,
+        grad_rows, grad_weights = moe_combine_backward(grad.to(ctx.dtype).contiguous(), rows, row_of_slot, weights,
                                                        need[0], need[2])
         return grad_rows, None, grad_weights
 
@@ -495,8 +497,9 @@ def _experts_mm(q, s, w_q, w_s, offsets, layout="NK"):
     return fp8_scaled_grouped_mm_v2(q, w_q, offsets, s, "1x128", w_s, "128x128", b_layout=layout, out=out)
 
 
-def _experts_forward(x, w_in, w_out, ids, weights, train):
-    """(y, what FP8MoE.backward needs: nothing without train)."""
+def _experts_forward(x, w_in, w_out, ids, weights, train, train_weights):
+    """(y, what FP8MoE.backward needs: nothing without train, no rows without
+    train_weights)."""
     for t, name in ((x, "x"), (w_in, "w_in"), (w_out, "w_out")):
         _need(t, torch.bfloat16, name)
     E = w_in.shape[0]
@@ -513,8 +516,10 @@ def _experts_forward(x, w_in, w_out, ids, weights, train):
     gate_up = _experts_mm(q, s, q_in, s_in, offsets)
     (hq, hs), checkpoint = fp8_swiglu_forward(gate_up, "fp8", train)
     rows = _experts_mm(hq, hs, q_out, s_out, offsets)
-    saved = (x, q_in, s_in, q_out, s_out, *checkpoint, rows, offsets, row_of_slot, weights) if train else ()
-    return moe_combine_forward(rows, row_of_slot, weights), saved
+    y = moe_combine_forward(rows, row_of_slot, weights)
+    if not train:
+        return y, ()
+    return y, (x, q_in, s_in, q_out, s_out, *checkpoint, rows if train_weights else None, offsets, row_of_slot, weights)
 
 
 class FP8MoE(torch.autograd.Function):
@@ -534,12 +539,13 @@ class FP8MoE(torch.autograd.Function):
                 first product's two gradients; dispatch's
 
     Kept for the backward: x once per token, the checkpoint (2 F bytes a row in
-    place of 4 F), the rows before combine (for the gradient of the weights) and
-    the weights' codes."""
+    place of 4 F), the weights' codes and, where `weights` needs its gradient, the
+    rows before combine."""
 
     @staticmethod
     def forward(ctx, x, w_in, w_out, ids, weights):
-        y, saved = _experts_forward(x, w_in, w_out, ids, weights, any(ctx.needs_input_grad))
+        y, saved = _experts_forward(x, w_in, w_out, ids, weights, any(ctx.needs_input_grad),
+                                    ctx.needs_input_grad[4])
         ctx.save_for_backward(*saved)
         return y
 
@@ -549,7 +555,7 @@ class FP8MoE(torch.autograd.Function):
         x, q_in, s_in, q_out, s_out, codes, scale, rows, offsets, row_of_slot, weights = ctx.saved_tensors
         need_x, need_in, need_out, _, need_w = ctx.needs_input_grad
         g = grad_out.to(torch.bfloat16).contiguous()
-        M = rows.shape[0]
+        M = row_of_slot.numel()
         grad_x = grad_in = grad_w_out = None
         grad_rows, grad_weights = moe_combine_backward(g, rows, row_of_slot, weights, need_x or need_in or need_out,
                                                        need_w)
@@ -581,4 +587,4 @@ def fp8_moe(x, w_in, w_out, ids, weights):
     or no input that needs one), its forward alone, without the 8-bit checkpoint."""
     if _differentiates(x, w_in, w_out, weights):
         return FP8MoE.apply(x, w_in, w_out, ids, weights)
-    return _experts_forward(x, w_in, w_out, ids, weights, False)[0]
+    return _experts_forward(x, w_in, w_out, ids, weights, False, False)[0]

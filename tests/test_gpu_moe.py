@@ -888,6 +888,30 @@ def test_no_checkpoint_where_no_gradient_can_follow(mode, monkeypatch):
     assert bool(w_in.grad.any()) and bool(w_out.grad.any())
 
 
+def test_rows_are_kept_for_the_gradient_of_the_weights_alone():
+    E, C, F, k, T = 4, 256, 128, 2, 40
+    torch.manual_seed(6)
+    w_in = torch.randn((E, 2 * F, C), device=DEV).bfloat16() / 16
+    w_out = torch.randn((E, C, F), device=DEV).bfloat16() / 11
+    ids, w = fp8mm.moe_route_forward(torch.randn((T, E), device=DEV), k)
+    slots = fp8mm.moe_plan(ids, E)[1]
+    x, rows = torch.randn((T, C), device=DEV).bfloat16(), torch.randn((T * k, C), device=DEV).bfloat16()
+    grads = []
+    for needs in (True, False):
+        weights = w.clone().requires_grad_(needs)
+        a, b = (t.clone().requires_grad_(True) for t in (x, rows))
+        y, z = fp8mm.fp8_moe(a, w_in, w_out, ids, weights), fp8mm.moe_combine(b, slots, weights)
+        for out in (y, z):
+            kept = [t for t in out.grad_fn.saved_tensors if t is not None and t.shape == rows.shape
+                    and t.dtype == rows.dtype]
+            assert len(kept) == needs
+            out.backward(torch.ones_like(out))
+        grads.append((a.grad, b.grad))
+        assert (weights.grad is not None) == needs
+    for with_weights, without in zip(*grads):
+        assert torch.equal(with_weights, without)
+
+
 def test_no_tokens_and_tokens_without_experts():
     E, C, F, k = 4, 256, 128, 2
     w_in = torch.randn((E, 2 * F, C), device=DEV).bfloat16().requires_grad_(True)
