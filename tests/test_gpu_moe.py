@@ -740,6 +740,48 @@ def test_swiglu(R, F):
     assert torch.equal(y.detach(), h) and torch.equal(leaf.grad, gx)
 
 
+@pytest.mark.parametrize("R,F", [(10007, 1408), (20003, 1408), (65000, 128)])
+def test_large_swiglu(R, F):
+    """Streaming stores (above 32 MiB) and loads (64 MiB) against calls on a few rows
+    each, which have neither: every output has the same bits."""
+    say(f"swiglu {R}x{F}")
+    torch.manual_seed(R)
+    x = (torch.randn((R, 2 * F), device=DEV) * torch.exp(torch.randn((R, 1), device=DEV))).bfloat16()
+    g = torch.randn((R, F), device=DEV).bfloat16()
+    parts = 16
+
+    def flat(out):
+        return [t for t in (out if isinstance(out, (tuple, list)) else (out,)) for t in
+                (flat(t) if isinstance(t, (tuple, list)) else [t]) if t is not None]
+
+    def check(whole, pieces):
+        whole, pieces = flat(whole), [flat(p) for p in pieces]
+        for i, t in enumerate(whole):
+            rows = 1 if t.dtype == torch.float32 else 0            # scales are [blocks, R]
+            assert torch.equal(t, torch.cat([p[i] for p in pieces], rows))
+
+    c, cs = fp8mm.fp8_quantize_blockwise(x, (1, 128))
+    for out in ("bf16", "fp8"):
+        for ckpt in (False, True):
+            check(fp8mm.fp8_swiglu_forward(x, out, ckpt),
+                  [fp8mm.fp8_swiglu_forward(p, out, ckpt) for p in x.chunk(parts)])
+    lib, st = fp8mm._lib.load(), torch.cuda.current_stream().cuda_stream
+    h, (q, s) = fp8mm.fp8_swiglu_forward(x)[0], fp8mm.fp8_swiglu_forward(x, "fp8")[0]
+    for ckpt in (False, True):                                     # both forms of h, from the C call
+        h2, q2, s2 = torch.empty_like(h), torch.empty_like(q), torch.empty_like(s)
+        c2, cs2 = torch.empty_like(c), torch.empty_like(cs)
+        assert lib.fp8_swiglu(x.data_ptr(), R, F, 2 * F, h2.data_ptr(), F, q2.data_ptr(), F, s2.data_ptr(),
+                              c2.data_ptr() if ckpt else None, 2 * F, cs2.data_ptr(), st) == 0
+        assert torch.equal(q2, q) and torch.equal(s2, s)
+        # bf16 of the float32 values that the codes come from, of the fast sigmoid alone: an ulp apart
+        assert bool(((h2.float() - h.float()).abs() <= 2 ** -7 * h.float().abs()).all())
+        assert not ckpt or torch.equal(c2, c) and torch.equal(cs2, cs)
+    for again in (False, True):
+        check(fp8mm.fp8_swiglu_backward(g, c, cs, recompute=again),
+              [fp8mm.fp8_swiglu_backward(a, b, d.contiguous(), recompute=again)
+               for a, b, d in zip(g.chunk(parts), c.chunk(parts), cs.chunk(parts, 1))])
+
+
 def test_swiglu_empty_and_extreme_values():
     x = torch.empty((0, 512), dtype=torch.bfloat16, device=DEV)
     h, (c, s) = fp8mm.fp8_swiglu_forward(x)
@@ -973,6 +1015,79 @@ def test_offsets_past_32_bits():
     gx, h = fp8mm.fp8_swiglu_backward(grad, c, cs, recompute=True)
     gx1, h1 = fp8mm.fp8_swiglu_backward(grad[:5].contiguous(), c1, cs1.contiguous(), recompute=True)
     assert torch.equal(gx[-5:], gx1) and torch.equal(h[-5:], h1)
+
+
+# Expert-order rows on both sides of 32 MiB (streaming stores) and 64 MiB (streaming
+# loads): rows of 16 lanes a slot and of a wave, whole and ending within a chunk.
+LARGE = [(C, k, mib) for C, k in ((339, 4), (220, 4), (256, 8), (2375, 4), (2048, 6), (1030, 3)) for mib in (30, 34, 62, 70)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("C,k,mib", LARGE)
+def test_large_dispatch_and_combine(C, k, mib, dtype):
+    T = mib * 2 ** 20 // (C * k * (2 if dtype == "bf16" else 4)) + 1
+    E = 64
+    say(f"dispatch/combine T={T} C={C} k={k} {dtype}: {mib} MiB")
+    torch.manual_seed(C + mib)
+    slots = fp8mm.moe_plan(torch.from_numpy(_ids(T, k, E, C)).to(DEV), E)[1]
+    used = slots >= 0
+    at = torch.where(used, slots, ~slots).long()
+    x = torch.randn((T, C), device=DEV).to(DT[dtype])
+    d = fp8mm.moe_dispatch_forward(x, slots)
+    want = torch.empty_like(d)
+    want[at.flatten()] = torch.where(used[..., None], x[:, None, :], torch.zeros_like(x[:, None, :])).flatten(0, 1)
+    assert torch.equal(d, want)
+    assert torch.equal(fp8mm.moe_dispatch_forward(_strided(x), slots), d)
+    del d, want
+    rows = torch.randn((T * k, C), device=DEV).to(DT[dtype])
+    w = torch.rand((T, k), device=DEV) + 0.1
+    rows[at[~used]] = float("nan")                    # rows and weights of empty slots are not read
+    w[~used] = float("nan")
+    wv = torch.where(used, w, torch.zeros_like(w)).double()
+    rv = torch.where(used[..., None], rows[at], torch.zeros_like(rows[at])).double()        # [T, k, C]
+    half = BF16 if dtype == "bf16" else U
+
+    def within(got, ref, tol, what):
+        off = (got.double() - ref).abs()
+        assert bool((off <= tol).all()), f"{what}: {int((~(off <= tol)).sum())} of {off.numel()} outside"
+
+    y = fp8mm.moe_combine_forward(rows, slots, w)
+    ref, tol = (wv[..., None] * rv).sum(1), (k + 1) * U * (wv[..., None] * rv.abs()).sum(1)
+    within(y, ref, tol + half * ref.abs() + half * tol + TINY, "combine")
+    assert torch.equal(fp8mm.moe_combine_forward(_strided(rows), slots, w), y)
+    g = torch.randn((T, C), device=DEV).to(DT[dtype])
+    gr, gw = fp8mm.moe_combine_backward(g, rows, slots, w)
+    gv = g.double()[:, None, :]
+    ref = wv[..., None] * gv
+    within(gr[at], ref, (half + 2 * U) * ref.abs() + TINY, "grad_rows")
+    depth = C / 16 + 6 + 14                           # of a slot's 16 or 64 lanes
+    within(gw, (gv * rv).sum(2), depth * U * (gv * rv).abs().sum(2) + TINY, "grad_weights")
+    grs, gws = fp8mm.moe_combine_backward(_strided(g), _strided(rows, 1, 1), slots, w)
+    assert torch.equal(grs, gr) and torch.equal(gws, gw)
+    assert torch.equal(fp8mm.moe_combine_backward(g, None, slots, w, need_weights=False)[0], gr)
+    assert torch.equal(fp8mm.moe_combine_backward(g, rows, slots, w, need_rows=False)[1], gw)
+
+
+@pytest.mark.parametrize("T,C,k", [(6000, 1152, 6), (35000, 128, 8), (5000, 2048, 3)])
+def test_large_fp8_dispatch(T, C, k):
+    say(f"fp8 dispatch T={T} C={C} k={k}")
+    slots = fp8mm.moe_plan(torch.from_numpy(_ids(T, k, 64, C)).to(DEV), 64)[1]
+    x = (torch.randn((T, C), device=DEV) * torch.exp(torch.randn((T, 1), device=DEV) * 4)).bfloat16()
+    q, s = fp8mm.fp8_moe_dispatch(x, slots)
+    rq, rs = fp8mm.fp8_quantize_blockwise(fp8mm.moe_dispatch_forward(x, slots), (1, 128))
+    assert torch.equal(q, rq) and torch.equal(s, rs)
+
+
+def test_gradients_of_weights_past_32_bits():
+    T, k, C, E = 270001, 4, 2048, 16
+    assert T * k * C > 2 ** 31
+    say("gradient of the weights of 1.1 million rows")
+    ids = (torch.arange(T * k, device=DEV, dtype=torch.int64) * 7919 % E).to(torch.int32).view(T, k)
+    slots = fp8mm.moe_plan(ids, E)[1]
+    x = torch.randn((T, C), device=DEV, dtype=torch.bfloat16)
+    gw = fp8mm.moe_combine_backward(x, fp8mm.moe_dispatch_forward(x, slots), slots, need_rows=False)[1]
+    dot = torch.cat([(part.double() ** 2).sum(1, keepdim=True) for part in x.split(30000)])
+    assert bool(((gw - dot).abs() <= (C / 64 + 6 + 10) * U * dot).all())
 
 
 def test_permutation_of_more_slots_than_waves():
