@@ -198,9 +198,11 @@ hipError_t run_swiglu(const SwigluProblem& p, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(workgroups(p))), dim3(256), 0, st, p, int(p.F / 128));
     return hipGetLastError();
   };
-  const int64_t bytes = p.R * p.F * (H ? 2 : 0) + p.R * p.F * (HQ ? 1 : 0) + p.R * p.F * (CKPT ? 2 : 0);
+  constexpr int kOut = (H ? 2 : 0) + (HQ ? 1 : 0) + (CKPT ? 2 : 0);      // bytes written for 4 read
   if (p.R * p.F * 4 > 2 * kL2Bytes) return run(swiglu_kernel<H, HQ, CKPT, true, true>);
-  if (bytes > kL2Bytes) return run(swiglu_kernel<H, HQ, CKPT, false, true>);
+  if constexpr (kOut > 2) {      // 2 or less are past the L2s only where the input is past twice them
+    if (p.R * p.F * kOut > kL2Bytes) return run(swiglu_kernel<H, HQ, CKPT, false, true>);
+  }
   return run(swiglu_kernel<H, HQ, CKPT, false, false>);
 }
 
