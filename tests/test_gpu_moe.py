@@ -930,6 +930,35 @@ def test_no_checkpoint_where_no_gradient_can_follow(mode, monkeypatch):
     assert bool(w_in.grad.any()) and bool(w_out.grad.any())
 
 
+def test_expert_layer_reads_no_row_without_an_expert(monkeypatch):
+    """The grouped products leave the rows of empty slots as they find them; whatever
+    is there, the layer's results and gradients have the same bits."""
+    E, C, F, k, T = 6, 256, 128, 3, 70
+    product = fp8mm.moe.fp8_scaled_grouped_mm_v2
+    r = np.random.default_rng(8)
+    ids = torch.from_numpy(_ids(T, k, E, 5, empty=0.4)).to(DEV)
+    assert int(((ids < 0) | (ids >= E)).sum()) > 40
+    torch.manual_seed(8)
+    inputs = (torch.randn((T, C), device=DEV).bfloat16(), torch.randn((E, 2 * F, C), device=DEV).bfloat16() / 16,
+              torch.randn((E, C, F), device=DEV).bfloat16() / 11, torch.rand((T, k), device=DEV))
+    g = torch.from_numpy(r.standard_normal((T, C))).to(torch.bfloat16).to(DEV)
+    results = []
+    for left in (0.0, float("nan"), float("inf"), -3e38):
+        def filled(*args, out, **kw):
+            return product(*args, out=out.fill_(left), **kw)
+
+        monkeypatch.setattr(fp8mm.moe, "fp8_scaled_grouped_mm_v2", filled)
+        for needs in ((True,) * 4, (True, False, False, False), (False, True, False, True), (False, False, True, False)):
+            leaves = [t.clone().requires_grad_(n) for t, n in zip(inputs, needs)]
+            y = fp8mm.fp8_moe(leaves[0], leaves[1], leaves[2], ids, leaves[3])
+            y.backward(g)
+            results.append([y.detach()] + [t.grad for t in leaves])
+    n = len(results) // 4
+    for i, got in enumerate(results):
+        for a, b in zip(got, results[i % n]):
+            assert (a is None) == (b is None) and (a is None or torch.equal(a, b) and bool(torch.isfinite(a).all()))
+
+
 def test_rows_are_kept_for_the_gradient_of_the_weights_alone():
     E, C, F, k, T = 4, 256, 128, 2, 40
     torch.manual_seed(6)
