@@ -58,13 +58,15 @@ __device__ __forceinline__ Chunk settle(const Chunk& v, int64_t c, int64_t C) {
 // in all of them, so it keeps its parameters in registers, and the next row is
 // loaded while this one is reduced and written.  Results larger than the L2s
 // are read and written by streaming accesses (NT).  16640 x 5120 bf16: 60 us,
-// 5.6 TB/s, more than a plain copy reaches (one row a workgroup, parameters
-// read again for each: 85 us; one wave a row: 102 us; plain accesses: 66 us).
-// Rows above 12 chunks of a wave (16 of fp32) take eight waves: 10000 x 8192 bf16 56
-// us (four waves 62), 4096 x 4764 fp32 30 (38), but 16640 x 5120 66.
-// PART where rows end within a chunk and, for results larger than the L2s, at
-// eight waves (6000 x 6144 fp32 50 against 54 us; four waves: 16000 x 5128 bf16 65
-// against 62; within the L2s 900 x 8192 fp32 16 against 14).
+// 5.6 TB/s, more than a plain copy reaches.  In us, the other choice in brackets:
+//   streaming: 16640 x 5120 60 (plain 66), but where the inputs come from the 256
+//   MiB cache of the memory it costs: 9830 x 5120 (96 MiB) 37 (35.5), 16384 x 2048
+//   (64 MiB) 32 (25), 8192 x 2048 (32 MiB) 19 (16)
+//   eight waves a row above 12 chunks of a wave (16 of fp32): 10000 x 8192 bf16 56
+//   (four: 62), 4096 x 4764 fp32 30 (38); 16640 x 5120 60 with four (66)
+//   PART where rows end within a chunk and, for results larger than the L2s, at
+//   eight waves: 6000 x 6144 fp32 50 (54); four waves 16000 x 5128 bf16 62 without
+//   (65); within the L2s 900 x 8192 fp32 14 without (16)
 // ---------------------------------------------------------------------------
 template <typename T, typename P, int WPR, int NIT, bool NT, bool PART>
 __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void norm_kernel(
@@ -188,18 +190,20 @@ __global__ __launch_bounds__(256) void norm_long_kernel(const T* __restrict__ x,
 // row of the workspace, [2][gridDim][C], which column_sum_kernel adds up in
 // workgroup order: no atomics, the same bits every time.  The partial rows are
 // traffic of their own (8 gridDim C bytes each way), so there are no more
-// workgroups than run at once: 256 of eight waves, with a row each or, above 8
-// chunks a lane, sharing one, and 512 of four waves that share a row in between
-// (256 below 2048 rows, where a partial row would stand for one or two rows).
-// 16384 x 2048 bf16: 43 us with the column sums, 4.7 TB/s of x, dy and dx; without
-// dw and db 37 us, what a sum of two such matrices takes (512 partial rows of
-// eight-wave workgroups 55 us; no row in flight ahead 55; the waves' shares added
-// one wave after the other 45).  16000 x 4096: 76 us (1024 partial rows 93).  Eight
-// waves a row: 16000 x 6144 101 us (four waves 106, 512 partial rows 107), 2841 x
-// 5127 27 (30, 33), 6000 x 6144 fp32 78 (103, 82).  PART wherever rows are shared
-// and stream or end within a chunk: 16000 x 3000 bf16 62 us (85 without), 16000 x
-// 2056 50 (75), 7534 x 3559 48 (84); within the L2s it costs: 1703 x 3000 fp32 25
-// against 22.5 (four waves).
+// workgroups than run at once: 256 of eight waves, with a row each (rows of at most
+// 4 chunks of a wave) or sharing one (above 8), and 512 of four waves that share a
+// row in between (256 below 2048 rows, where a partial row would stand for one or
+// two rows).  16384 x 2048 bf16: 41 us with the column sums, 4.9 TB/s of x, dy and
+// dx.  In us, the other choice in brackets:
+//   partial rows: 16384 x 2048 41 (512: 55), 16000 x 4096 77 (1024: 93)
+//   eight waves a row: 16000 x 6144 101 (four: 106), 2841 x 5127 27 (30), 6000 x
+//   6144 fp32 78 (103)
+//   PART, wherever rows are shared and stream or end within a chunk: 16000 x 3000
+//   62 (85), 16000 x 2056 49 (75), 7534 x 3559 48 (84); within the L2s it costs:
+//   1703 x 3000 fp32 22.5 (25 with it)
+// Streaming accesses pay above 32 MiB of rows that share waves (4096 x 5120 bf16, 40
+// MiB: 32 against 38; 16384 x 2048, 64 MiB: 42.5 against 41) and cost below (3276 x
+// 5120, 32 MiB: 28.4 against 27.9; 8192 x 2048 27.0 against 24.2).
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 

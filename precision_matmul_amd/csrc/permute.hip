@@ -157,7 +157,8 @@ __device__ __forceinline__ Slot slot_row(int32_t v) { return Slot{int64_t(v < 0 
 // ---------------------------------------------------------------------------
 // Dispatch: one wave an item of 64 chunks of one token, read once and written
 // to the token's k rows.  HBM-bound: (1 + k) rows a token.  16384 x 2048 x 6
-// bf16 with the plan: 87 us, 5.4 TB/s (plain stores 100 us).
+// bf16 with the plan: 87 us, 5.4 TB/s (plain stores 100 us); 40 MiB of rows 8.5 us
+// against 8.9, 24 MiB the same, but 96 MiB 20.1 against 18.6.
 // ---------------------------------------------------------------------------
 template <typename T, bool NT>
 __global__ __launch_bounds__(256) void dispatch_kernel(const PermuteProblem p, int strips) {
@@ -181,7 +182,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const PermuteProblem p, i
 // apart: with a contiguous range of tokens an XCD, neighbouring rows of an
 // expert meet in one L2 before they go out.  16384 x 2048 x 6: 41 us, 6.7 TB/s
 // of x, codes and scales (plain code stores 53, tokens in launch order 58 with
-// the streaming ones).
+// the streaming ones); 40 MiB of codes 10.7 us against 11.2, 24 MiB the same.
 template <bool NT>
 __global__ __launch_bounds__(256) void dispatch_fp8_kernel(const PermuteProblem p, int strips) {
   const int lane = threadIdx.x & 63;
@@ -244,11 +245,12 @@ __global__ __launch_bounds__(256) void combine_kernel(const PermuteProblem p, in
 // LANES lanes a slot (a wave, or 16 for rows of at most one chunk a lane of a wave),
 // U chunks a lane in flight: a token's k slots are neighbours and share its gradient
 // through the caches.  HBM-bound: (1 + 2 k) rows a token.  16384 x 2048, k = 6:
-// 154 us, 5.7 TB/s (plain stores 169; one wave a token, which reads the gradient
-// once, 4 us more, and 27 against 9 us for 64 tokens of 5120 columns).  Short rows
-// with a wave a slot and one chunk in flight: 16000 x 256, k = 4 19 us against 13,
-// 512 columns 25 against 24.  PART, a row's last chunk loaded whole and shifted:
-// 16000 x 339 24 us (30 without); long rows lose by it (4000 x 2048 38 against 34).
+// 154 us, 5.7 TB/s.  In us, the other choice in brackets:
+//   streaming stores 16384 x 2048 154 (plain 169)
+//   16 lanes a slot, rows of at most one chunk of a wave: 16000 x 256, k = 4 13 (a
+//   wave 19), 512 columns 24 (25)
+//   PART, a row's last chunk loaded whole and shifted: 16000 x 339 24 (30); long
+//   rows 34 without (4000 x 2048, 38 with it)
 template <typename T, bool LD, bool ST, int LANES, int U, bool PART>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const PermuteProblem p) {
   constexpr int V = kVec<T>;

@@ -20,8 +20,9 @@
 // k <= 16), and one wave a token.  16384 tokens in us, the calls of the other
 // form in brackets: 256 experts in 8 groups, sigmoid and bias, k = 8: 12.6 (17.8);
 // 256 experts, softmax and bias: 10.8 (15.3); 128 experts 7.7 (11.5); 64 experts,
-// k = 6: 7.6 (8.4), about what a call takes the host.  Backward of 64 experts: 4.3
-// in the kernel (7.3); of 256, softmax, k = 8: 10.9 (12.7).
+// k = 6: 7.6 (8.4), about what a call takes the host.  Backward, the kernel alone:
+// 64 experts 4.5 (9.2); 256 experts, k = 8, softmax 11.1 (14.3), renormalised 11.0
+// (13.4), sigmoid 10.1 (11.2).
 #include "moe_launch.hpp"
 #include "ops_common.hpp"
 
@@ -66,7 +67,8 @@ __device__ __forceinline__ void store_row_of(T* row, int e0, int E, const float 
 
 // exp(-a) for a >= 0, to an ulp or two: the hardware's exp2 with the rounding
 // error of a log2(e) put back (its part above 2^-24 and log2(e)'s own low part).
-// From a = 104 on the result is 0, as float32's would be.
+// The hardware's exp2 has no subnormal results: from a = 126 ln 2 = 87.3 on the
+// result is 0 (float32's own exp is 0 from 104 on).
 __device__ __forceinline__ float exp_neg(float a) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;
   a = fminf(a, 104.0f);
