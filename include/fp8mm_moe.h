@@ -63,7 +63,8 @@ fp8mm_status fp8mm_layer_norm_backward(const void* dy, int64_t ld_dy, const void
 
 /* ---------------------------------------------------------------------------
  * Routing of T tokens to k of E experts.
- *   s = softmax(logits) or sigmoid(logits) of a token's row, float32
+ *   s = softmax(logits) or sigmoid(logits) of a token's row, float32; scores
+ *     below 2^-126, where float32 has no normal numbers, count as 0
  *   key = s + bias (bias NULL: key = logit, which orders the same)
  *   groups > 1: the E experts are `groups` runs of E / groups; a group's score
  *     is its largest key, or (FP8MM_GROUP_TOP2) the sum of its two largest

@@ -5,6 +5,8 @@ ever enqueued (the fake non-null pointers are never dereferenced)."""
 
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 
@@ -228,3 +230,31 @@ def test_swiglu_refusals(lib, name, order, base, kw):
 def test_permutation_launch_limits(lib, name, order, base, kw, fits):
     assert _call(lib, name, order, base, kw) == _lib.EINVAL
     assert ("too large for one launch" in lib.fp8mm_last_error().decode()) != fits
+
+
+def test_header_compiles_as_c99_and_links(lib, tmp_path):
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("no gcc")
+    src = tmp_path / "moe.c"
+    src.write_text(r"""
+#include <stdio.h>
+#include <string.h>
+#include "fp8mm_moe.h"
+int main(void) {
+  if (fp8mm_layer_norm_backward_workspace(4, 64) != 0 || fp8mm_moe_plan_workspace(-1, 6, 64) != -1) return 1;
+  fp8mm_status st = fp8mm_moe_route(0, FP8MM_OUT_BF16, 4, 64, 64, 0, FP8MM_SCORE_SIGMOID, 65, 1, 1, FP8MM_GROUP_MAX, 1,
+                                    1.0f, 0, 0, 0);
+  if (st != FP8MM_EINVAL || strlen(fp8mm_last_error()) == 0) return 2;
+  if (fp8_swiglu(0, 0, 128, 256, 0, 0, 0, 0, 0, 0, 0, 0, 0) != FP8MM_OK) return 3;
+  printf("ok\n");
+  return 0;
+}
+""")
+    exe = tmp_path / "moe"
+    libdir = os.path.dirname(_lib.LIB_PATH)
+    cmd = [gcc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-D__HIP_PLATFORM_AMD__", f"-I{os.path.join(ROOT, 'include')}",
+           "-I/opt/rocm/include", str(src), f"-L{libdir}", "-lfp8mm", f"-Wl,-rpath,{libdir}", "-o", str(exe)]
+    subprocess.run(cmd, check=True, capture_output=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert run.returncode == 0 and run.stdout.strip() == "ok", (run.returncode, run.stdout, run.stderr)
