@@ -15,42 +15,12 @@
 // a (x - mean), which is 0 there; (x - mean) rstd alone can pass float32's range (a
 // row of one large value under a small eps), and 0 times that is NaN.
 #include "moe_launch.hpp"
-#include "ops_common.hpp"
+#include "norm_common.hpp"
 
 namespace fp8mm {
 namespace {
 
 using namespace ops;
-
-__device__ __forceinline__ Chunk pack4f(const float* f) {
-  return Chunk{{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])}};
-}
-
-// Sum of v over the WPR waves that share a row.  `slot` alternates between
-// calls, so that one barrier a call is enough.
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float (&part)[2][WPR], int slot) {
-  v = wave_sum(v);
-  if constexpr (WPR == 1) return v;
-  if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.0f;
-#pragma unroll
-  for (int w = 0; w < WPR; ++w) s += part[slot][w];
-  return s;
-}
-
-// The next row's chunks.  PART: without a path for a row's last elements, for
-// which the waves that share a row would all wait where they ask for them: the
-// last chunk is loaded whole and shifted, if it has to be, when its turn comes.
-template <typename T, bool NT, bool PART>
-__device__ __forceinline__ Chunk fetch(const T* row, int64_t c, int64_t C) {
-  return PART ? fetch_row<T, NT>(row, c, C) : load_row<T, NT>(row, c, C);
-}
-template <typename T, bool PART>
-__device__ __forceinline__ Chunk settle(const Chunk& v, int64_t c, int64_t C) {
-  return PART ? fetched<T>(v, c, C) : v;
-}
 
 // ---------------------------------------------------------------------------
 // Forward, row in registers: WPR waves a row, NIT chunks a lane.  A workgroup
