@@ -1,7 +1,7 @@
 """FP8 scaled matrix multiply for AMD MI355X (gfx950).
 
 Python binding over the C ABI of ``libfp8mm.so`` (include/fp8mm.h, and
-include/fp8mm_moe.h in moe.py).  The
+include/fp8mm_moe.h in moe.py, include/fp8mm_block.h in block.py).  The
 functions carry the C names; they only check and marshal arguments, allocate
 outputs with torch and pass device pointers plus the current HIP stream.
 Every step of the computation runs in the library's HIP kernels.
@@ -456,5 +456,7 @@ from .linear import (FP8BlockwiseLinear, FP8GroupedLinear, fp8_blockwise_linear,
                      fp8_grouped_linear)
 from .moe import *  # noqa: E402,F401,F403  (uses the functions above)
 from .moe import __all__ as _moe_all  # noqa: E402
+from .block import *  # noqa: E402,F401,F403  (uses the functions above)
+from .block import __all__ as _block_all  # noqa: E402
 
-__all__ += _moe_all
+__all__ += _moe_all + _block_all

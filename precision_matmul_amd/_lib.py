@@ -1,4 +1,5 @@
-"""ctypes declarations of the C ABI in include/fp8mm.h and include/fp8mm_moe.h.
+"""ctypes declarations of the C ABI in include/fp8mm.h, include/fp8mm_moe.h and
+include/fp8mm_block.h.
 
 Loading fails loudly when ``libfp8mm.so`` has not been built: there is no
 fallback implementation anywhere in this package.
@@ -56,6 +57,21 @@ SIGNATURES = {
     "fp8mm_moe_combine_backward": (_i, [_p, _i64, _p, _i64, _i, _i64, _i64, _p, _p, _i64, _p, _i64, _p, _p]),
     "fp8_swiglu": (_i, [_p, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _p]),
     "fp8_swiglu_backward": (_i, [_p, _i64, _p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _p]),
+    # include/fp8mm_block.h
+    "fp8mm_rms_norm": (_i, [_p, _i64, _p, _i64, _i, _i64, _i64, _p, _i, _f, _p, _i64, _p, _i64, _p, _i64, _p, _i, _p,
+                            _p]),
+    "fp8mm_rms_norm_backward_workspace": (_i64, [_i64, _i64]),
+    "fp8mm_rms_norm_backward": (_i, [_p, _i64, _p, _i64, _p, _i64, _i, _i64, _i64, _p, _i, _p, _p, _i64, _p, _p, _i64,
+                                     _p]),
+    "fp8mm_moe_balance_loss_workspace": (_i64, [_i64, _i64, _i64]),
+    "fp8mm_moe_balance_loss": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _i, _p, _i64, _f, _p, _p, _p, _p, _i64, _p]),
+    "fp8mm_moe_balance_loss_backward": (_i, [_p, _p, _i, _i64, _i64, _i64, _p, _p, _i64, _i, _p, _i64, _f, _p, _i64,
+                                             _p]),
+    "fp8mm_lora_splits": (_i64, [_i64, _i64, _i64, _i64]),
+    "fp8mm_lora": (_i, [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _p, _i64, _p, _i64, _p, _p]),
+    "fp8mm_lora_backward_workspace": (_i64, [_i64, _i64, _i64, _i64, _i64]),
+    "fp8mm_lora_backward": (_i, [_p, _i64, _p, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _p,
+                                 _p, _i, _p, _i64, _p]),
 }
 
 _lib = None

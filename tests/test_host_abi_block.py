@@ -1,0 +1,183 @@
+"""Host-side checks of the C ABI in include/fp8mm_block.h (no GPU): every symbol is
+exported and bound, queries answer, and bad arguments are refused before any launch.
+Every call below fails a check or has nothing to do, so nothing is ever enqueued (the
+fake non-null pointers are never dereferenced)."""
+
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+import precision_matmul_amd as fp8mm
+from precision_matmul_amd import _lib
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "fp8mm_block.h")
+FAKE = 0x1000
+NAN, INF = float("nan"), float("inf")
+EINVAL, ENOTIMPL, OK = _lib.EINVAL, _lib.ENOTIMPL, _lib.OK
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.fail("libfp8mm.so is not built (run __graft_entry__.build())")
+    return _lib.load()
+
+
+def test_every_declared_symbol_is_exported(lib):
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(fp8_\w+|fp8mm_\w+)\s*\(", text)))
+    assert len(names) == 10, names
+    for n in names:
+        assert hasattr(lib, n) and n in _lib.SIGNATURES, n
+
+
+CALLS = {
+    "fp8mm_rms_norm": dict(x=FAKE, ldx=256, res=FAKE, ldr=256, dt=0, R=4, C=256, w=FAKE, pd=0, eps=1e-6, h=FAKE,
+                           ldh=256, y=FAKE, ldy=256, q=FAKE, ldq=256, s=FAKE, recipe=2, rstd=FAKE, st=None),
+    "fp8mm_rms_norm_backward": dict(dy=FAKE, lddy=64, h=FAKE, ldh=64, gh=FAKE, ldg=64, dt=0, R=4, C=64, w=None, pd=0,
+                                    rstd=FAKE, dx=FAKE, lddx=64, dw=FAKE, ws=FAKE, wsb=1 << 20, st=None),
+    "fp8mm_moe_balance_loss": dict(l=FAKE, dt=0, T=16, E=64, ld=64, ids=FAKE, k=6, score=0, ends=FAKE, S=3, coeff=1.0,
+                                   loss=FAKE, counts=FAKE, tokens=FAKE, ws=FAKE, wsb=1 << 20, st=None),
+    "fp8mm_moe_balance_loss_backward": dict(g=FAKE, l=FAKE, dt=0, T=16, E=64, ld=64, counts=FAKE, tokens=FAKE, k=6,
+                                            score=0, ends=FAKE, S=3, coeff=1.0, out=FAKE, ldg=64, st=None),
+    "fp8mm_lora": dict(x=FAKE, ldx=64, T=8, K=64, down=FAKE, up=FAKE, n=4, r=16, N=96, ids=FAKE, scales=None,
+                       base=FAKE, ldb=96, out=FAKE + 64, ldo=96, v=FAKE, st=None),
+    "fp8mm_lora_backward": dict(dy=FAKE, lddy=96, x=FAKE, ldx=64, T=8, K=64, down=FAKE, up=FAKE, n=4, r=16, N=96,
+                                ids=FAKE, scales=None, v=FAKE, dx=FAKE, lddx=64, ddown=FAKE, dup=FAKE, gd=0, ws=FAKE,
+                                wsb=1 << 24, st=None),
+}
+
+
+def _call(lib, name, kw):
+    a = dict(CALLS[name])
+    assert set(kw) <= set(a), kw
+    a.update(kw)
+    return getattr(lib, name)(*a.values())
+
+
+@pytest.mark.parametrize("name,kw,code", [(n, kw, c) for n, cases in {
+    "fp8mm_rms_norm": [
+        (dict(dt=2), EINVAL), (dict(pd=7), EINVAL), (dict(R=-1), EINVAL), (dict(C=0), EINVAL), (dict(R=2 ** 31), EINVAL),
+        (dict(C=2 ** 22 + 128, ldx=2 ** 23, ldr=2 ** 23, ldh=2 ** 23, ldy=2 ** 23, ldq=2 ** 23), EINVAL),
+        (dict(ldx=255), EINVAL), (dict(ldr=255), EINVAL), (dict(ldh=255), EINVAL), (dict(ldy=255), EINVAL),
+        (dict(ldq=255), EINVAL), (dict(ldq=264), EINVAL), (dict(ldx=2 ** 40 + 1), EINVAL),
+        (dict(eps=-1.0), EINVAL), (dict(eps=NAN), EINVAL), (dict(eps=INF), EINVAL), (dict(x=None), EINVAL),
+        (dict(s=None), EINVAL), (dict(x=FAKE + 1), EINVAL), (dict(res=FAKE + 1), EINVAL), (dict(h=FAKE + 1), EINVAL),
+        (dict(y=FAKE + 1), EINVAL), (dict(q=FAKE + 8), EINVAL), (dict(s=FAKE + 2), EINVAL), (dict(rstd=FAKE + 2), EINVAL),
+        (dict(pd=1, w=FAKE + 2), EINVAL), (dict(C=192, recipe=2), EINVAL), (dict(C=200, recipe=1), EINVAL),
+        (dict(recipe=0), ENOTIMPL), (dict(recipe=3), ENOTIMPL), (dict(recipe=5), ENOTIMPL), (dict(recipe=9), EINVAL),
+        (dict(dt=1), ENOTIMPL), (dict(dt=1, q=None, x=FAKE + 2), EINVAL)],
+    "fp8mm_rms_norm_backward": [
+        (dict(lddy=10), EINVAL), (dict(ldh=10), EINVAL), (dict(ldg=10), EINVAL), (dict(lddx=10), EINVAL),
+        (dict(dy=None), EINVAL), (dict(h=None), EINVAL), (dict(rstd=None), EINVAL), (dict(R=9000, ws=None), EINVAL),
+        (dict(R=9000, wsb=64), EINVAL), (dict(R=9000, ws=FAKE + 4), EINVAL), (dict(dt=3), EINVAL), (dict(C=-1), EINVAL),
+        (dict(dw=FAKE + 1), EINVAL), (dict(dx=FAKE + 1), EINVAL), (dict(gh=FAKE + 1), EINVAL),
+        (dict(dx=FAKE, gh=FAKE, lddx=128), EINVAL)],
+    "fp8mm_moe_balance_loss": [
+        (dict(dt=2), EINVAL), (dict(score=2), EINVAL), (dict(T=-1), EINVAL), (dict(E=0), EINVAL), (dict(S=0), EINVAL),
+        (dict(S=2 ** 20 + 1), EINVAL), (dict(ends=None), EINVAL), (dict(k=0), EINVAL), (dict(T=2 ** 30), EINVAL),
+        (dict(coeff=NAN), EINVAL), (dict(coeff=INF), EINVAL), (dict(ld=63), EINVAL), (dict(l=None), EINVAL),
+        (dict(ids=None), EINVAL), (dict(loss=None), EINVAL), (dict(counts=None), EINVAL), (dict(tokens=None), EINVAL),
+        (dict(l=FAKE + 1), EINVAL), (dict(ws=None), EINVAL), (dict(wsb=100), EINVAL), (dict(ws=FAKE + 8), EINVAL),
+        (dict(E=1025, ld=1025), ENOTIMPL), (dict(k=65), ENOTIMPL), (dict(E=4096, ld=4096, S=2 ** 19), EINVAL)],
+    "fp8mm_moe_balance_loss_backward": [
+        (dict(g=None), EINVAL), (dict(l=None), EINVAL), (dict(counts=None), EINVAL), (dict(tokens=None), EINVAL),
+        (dict(out=None), EINVAL), (dict(ldg=63), EINVAL), (dict(ld=63), EINVAL), (dict(k=0), EINVAL),
+        (dict(score=-1), EINVAL), (dict(out=FAKE + 1), EINVAL), (dict(ends=None), EINVAL), (dict(coeff=NAN), EINVAL),
+        (dict(E=1025, ld=1025, ldg=1025), ENOTIMPL)],
+    "fp8mm_lora": [
+        (dict(T=-1), EINVAL), (dict(T=2 ** 31), EINVAL), (dict(n=0), EINVAL), (dict(n=2 ** 31), EINVAL),
+        (dict(r=0), EINVAL), (dict(r=257), ENOTIMPL), (dict(K=0), EINVAL), (dict(N=0), EINVAL),
+        (dict(K=2 ** 22 + 1, ldx=2 ** 23), EINVAL), (dict(N=2 ** 22 + 1, ldb=2 ** 23, ldo=2 ** 23), EINVAL),
+        (dict(ldx=63), EINVAL), (dict(ldb=95), EINVAL), (dict(ldo=95), EINVAL), (dict(x=None), EINVAL),
+        (dict(down=None), EINVAL), (dict(up=None), EINVAL), (dict(ids=None), EINVAL), (dict(out=None), EINVAL),
+        (dict(v=None), EINVAL), (dict(x=FAKE + 1), EINVAL), (dict(up=FAKE + 1), EINVAL), (dict(v=FAKE + 2), EINVAL),
+        (dict(scales=FAKE + 2), EINVAL), (dict(out=FAKE, ldb=128), EINVAL),
+        (dict(T=2 ** 30, N=2 ** 14, ldb=2 ** 14, ldo=2 ** 14), EINVAL)],
+    "fp8mm_lora_backward": [
+        (dict(gd=2), EINVAL), (dict(lddy=95), EINVAL), (dict(ldx=63), EINVAL), (dict(lddx=63), EINVAL),
+        (dict(dy=None), EINVAL), (dict(x=None), EINVAL), (dict(v=None), EINVAL), (dict(ids=None), EINVAL),
+        (dict(ws=None), EINVAL), (dict(wsb=64), EINVAL), (dict(ws=FAKE + 8), EINVAL), (dict(r=257), ENOTIMPL),
+        (dict(gd=1, dup=FAKE + 2), EINVAL), (dict(dx=FAKE + 1), EINVAL), (dict(n=2 ** 25), EINVAL)],
+}.items() for kw, c in cases])
+def test_refusals(lib, name, kw, code):
+    assert _call(lib, name, kw) == code
+    assert lib.fp8mm_last_error().decode()
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("fp8mm_rms_norm", dict(R=0, x=None, s=None)),
+    ("fp8mm_rms_norm", dict(res=None, y=None, q=None, rstd=None)),
+    ("fp8mm_rms_norm_backward", dict(dx=None, dw=None)),
+    ("fp8mm_rms_norm_backward", dict(R=0, dy=None, h=None, rstd=None, dw=None)),
+    ("fp8mm_moe_balance_loss_backward", dict(T=0, l=None)),
+    ("fp8mm_lora", dict(T=0, x=None, ids=None, v=None)),
+    ("fp8mm_lora_backward", dict(T=0, ddown=None, dup=None, ids=None, dy=None)),
+    ("fp8mm_lora_backward", dict(dx=None, ddown=None, dup=None)),
+])
+def test_calls_with_nothing_to_do(lib, name, kw):
+    assert _call(lib, name, kw) == OK
+
+
+def test_queries(lib):
+    assert lib.fp8mm_rms_norm_backward_workspace(4, 64) == 0            # one launch, nothing kept between
+    assert 0 < lib.fp8mm_rms_norm_backward_workspace(9000, 64) <= 1 << 20
+    assert lib.fp8mm_rms_norm_backward_workspace(-1, 64) == -1
+    assert 0 < lib.fp8mm_rms_norm_backward_workspace(2 ** 30, 64) <= 4096 * 64 * 4     # bounded in the rows
+    assert lib.fp8mm_moe_balance_loss_workspace(16384, 64, 1) > 0
+    assert 0 < lib.fp8mm_moe_balance_loss_workspace(0, 64, 1)
+    assert lib.fp8mm_moe_balance_loss_workspace(16, 64, 0) == -1
+    assert lib.fp8mm_moe_balance_loss_workspace(2 ** 31 - 1, 64, 1) < 1 << 20          # bounded in the tokens
+    for bad in ((-1, 64, 4, 16), (8, 0, 4, 16), (8, 64, 0, 16), (8, 64, 4, 0), (8, 64, 4, 257)):
+        assert lib.fp8mm_lora_splits(*bad) == -1
+    for T in (0, 1, 16, 300, 5000, 10 ** 6):
+        assert 1 <= lib.fp8mm_lora_splits(T, 5120, 8, 16) <= 16
+    assert lib.fp8mm_lora_splits(8, 64, 8, 16) == 1                     # nothing to split
+    assert lib.fp8mm_lora_backward_workspace(0, 64, 64, 4, 16) == 0
+    assert lib.fp8mm_lora_backward_workspace(8, 64, 64, 4, 16) >= 4 * 8 * 16
+    assert lib.fp8mm_lora_backward_workspace(8, 64, 0, 4, 16) == -1
+
+
+def test_binding_refuses_what_is_not_on_a_device():
+    x, ids = torch.zeros((4, 128), dtype=torch.bfloat16), torch.zeros((4, 2), dtype=torch.int32)
+    panels = torch.zeros((2, 16, 128), dtype=torch.bfloat16)
+    for call in (lambda: fp8mm.rms_norm_forward(x), lambda: fp8mm.fp8_rms_norm_forward(x),
+                 lambda: fp8mm.rms_norm_backward(x, x, None, x[:, 0].float()), lambda: fp8mm.rms_norm(x),
+                 lambda: fp8mm.moe_balance_loss_forward(x, ids), lambda: fp8mm.moe_balance_loss(x, ids),
+                 lambda: fp8mm.lora_forward(x, panels, panels, ids[:, 0].contiguous()),
+                 lambda: fp8mm.lora(x, panels, panels, ids[:, 0])):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_header_compiles_as_c99_and_links(lib, tmp_path):
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("no gcc")
+    src = tmp_path / "block.c"
+    src.write_text(r"""
+#include <stdio.h>
+#include <string.h>
+#include "fp8mm_block.h"
+int main(void) {
+  if (fp8mm_rms_norm_backward_workspace(4, 64) != 0 || fp8mm_lora_splits(-1, 6, 64, 1) != -1) return 1;
+  fp8mm_status st = fp8mm_moe_balance_loss(0, FP8MM_OUT_BF16, 4, 64, 64, 0, 65, FP8MM_SCORE_SIGMOID, 0, 1, 1.0f, 0, 0, 0,
+                                           0, 0, 0);
+  if (st != FP8MM_ENOTIMPL || strlen(fp8mm_last_error()) == 0) return 2;
+  if (fp8mm_lora(0, 64, 0, 64, 0, 0, 1, 8, 64, 0, 0, 0, 64, 0, 64, 0, 0) != FP8MM_OK) return 3;
+  printf("ok\n");
+  return 0;
+}
+""")
+    exe = tmp_path / "block"
+    libdir = os.path.dirname(_lib.LIB_PATH)
+    cmd = [gcc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-D__HIP_PLATFORM_AMD__", f"-I{os.path.join(ROOT, 'include')}",
+           "-I/opt/rocm/include", str(src), f"-L{libdir}", "-lfp8mm", f"-Wl,-rpath,{libdir}", "-o", str(exe)]
+    subprocess.run(cmd, check=True, capture_output=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert run.returncode == 0 and run.stdout.strip() == "ok", (run.returncode, run.stdout, run.stderr)
