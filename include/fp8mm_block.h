@@ -137,7 +137,8 @@ int64_t fp8mm_lora_backward_workspace(int64_t T, int64_t K, int64_t N, int64_t n
  * (base has dy itself for its gradient.)  dy: bf16 [T, N]; x, v: as in the forward;
  * dx: bf16 [T, K]; ddown [n, r, K], dup [n, r, N]: dense, of `grad_dtype`, zeros for
  * an adapter without tokens.  dx, ddown and dup may each be NULL; x is needed for
- * ddown only, v for dup only.  workspace: at least fp8mm_lora_backward_workspace bytes,
+ * ddown only, v for dup only.  ddown and dup are implemented for n <= 1024
+ * (FP8MM_ENOTIMPL).  workspace: at least fp8mm_lora_backward_workspace bytes,
  * 16-byte aligned. */
 fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t T, int64_t K,
                                  const void* down, const void* up, int64_t n, int64_t r, int64_t N,

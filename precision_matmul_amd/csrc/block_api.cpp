@@ -84,9 +84,13 @@ fp8mm_status check_lora(int64_t T, int64_t K, int64_t n, int64_t r, int64_t N, c
   return FP8MM_OK;
 }
 
-// Workgroups of a panel gradient; its launch takes at most 16 times as many.
-bool outer_fits(int64_t n, int64_t C, int64_t r) {
-  return n <= kMaxGroups / 16 / (((C + 127) / 128) * ((r + 63) / 64));
+// The parts of the backward's workspace.
+int64_t dv_bytes(int64_t T, int64_t N, int64_t n, int64_t r) {
+  return (4 * fp8mm::lora_splits(T, N, n, int(r)) * T * r + 15) / 16 * 16;
+}
+int64_t partial_bytes(int64_t T, int64_t K, int64_t N, int64_t n, int64_t r) {
+  const int64_t a = fp8mm::lora_outer_workspace(T, K, n, int(r)), b = fp8mm::lora_outer_workspace(T, N, n, int(r));
+  return ((a > b ? a : b) + 15) / 16 * 16;
 }
 
 }  // namespace
@@ -312,10 +316,8 @@ fp8mm_status fp8mm_lora(const void* x, int64_t ld_x, int64_t T, int64_t K, const
 
 int64_t fp8mm_lora_backward_workspace(int64_t T, int64_t K, int64_t N, int64_t n, int64_t r) {
   if (!lora_shape(T, n, r) || !lora_columns(K) || !lora_columns(N)) return -1;
-  if (T == 0) return 0;
-  const int64_t dv = (4 * fp8mm::lora_splits(T, N, n, int(r)) * T * r + 15) / 16 * 16;
-  const int64_t a = fp8mm::lora_outer_workspace(T, K, n, int(r)), b = fp8mm::lora_outer_workspace(T, N, n, int(r));
-  return dv + (a > b ? a : b);
+  if (n > fp8mm::kLoraMaxAdapters) return dv_bytes(T, N, n, r);
+  return dv_bytes(T, N, n, r) + partial_bytes(T, K, N, n, r) + fp8mm::lora_order_workspace(T, n);
 }
 
 fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t T, int64_t K,
@@ -329,8 +331,8 @@ fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, i
   if (st == FP8MM_OK && ddown) st = check_ld(ld_x, K, "ld_x");
   if (st == FP8MM_OK && dx) st = check_ld(ld_dx, K, "ld_dx");
   if (st != FP8MM_OK) return st;
-  if ((ddown && !outer_fits(n, K, r)) || (dup && !outer_fits(n, N, r)))
-    return fail(FP8MM_EINVAL, "the gradients of %lld adapters are too large for one launch", (long long)n);
+  if ((ddown || dup) && n > fp8mm::kLoraMaxAdapters)
+    return fail(FP8MM_ENOTIMPL, "gradients of more than %d adapters (%lld)", fp8mm::kLoraMaxAdapters, (long long)n);
   if (T > 0 && !dy) return fail(FP8MM_EINVAL, "dy must not be NULL");
   if (T > 0 && ((ddown && !x) || (dup && !v)))
     return fail(FP8MM_EINVAL, "ddown needs x and dup needs v");
@@ -351,9 +353,12 @@ fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, i
   p.ids = ids;
   p.scales = scales;
   p.grad_fp32 = grad_dtype == FP8MM_OUT_FP32;
-  p.partial = dv + (int64_t(dv_splits) * T * r + 3) / 4 * 4;
+  char* at = static_cast<char*>(workspace) + dv_bytes(T, N, n, r);
+  p.partial = reinterpret_cast<float*>(at);
+  fp8mm::LoraOrder order{};
   hipError_t e = hipSuccess;
-  if (dx || ddown) {
+  if (ddown || dup) e = fp8mm::launch_lora_order(p, at + partial_bytes(T, K, N, n, r), order, stream);
+  if (e == hipSuccess && (dx || ddown)) {
     fp8mm::LoraProblem q = p;
     q.C = N;
     q.panels = static_cast<const uint16_t*>(up);
@@ -371,7 +376,7 @@ fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, i
     q.v = const_cast<float*>(v);
     q.splits = fp8mm::lora_splits(T, K, n, int(r));
     q.grad = dup;
-    e = fp8mm::launch_lora_outer(q, stream);
+    e = fp8mm::launch_lora_outer(q, order, stream);
   }
   p.C = K;
   p.v = dv;
@@ -381,7 +386,7 @@ fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, i
     q.x = static_cast<const uint16_t*>(x);
     q.ld_x = ld_x;
     q.grad = ddown;
-    e = fp8mm::launch_lora_outer(q, stream);
+    e = fp8mm::launch_lora_outer(q, order, stream);
   }
   if (e == hipSuccess && dx) {
     p.panels = static_cast<const uint16_t*>(down);

@@ -83,15 +83,25 @@ struct LoraProblem {
   int64_t ld_out;
   void* grad;              // outer: [n, r, C]
   bool grad_fp32;
-  float* partial;          // outer: lora_outer_workspace floats
+  float* partial;          // outer: lora_outer_workspace bytes
+};
+
+// Tokens in adapter order: offsets [n], the adapters' cumulative end rows, and each
+// row's token.
+struct LoraOrder {
+  int32_t* offsets;
+  int32_t* order;
 };
 
 constexpr int kLoraMaxRank = 256;
+constexpr int kLoraMaxAdapters = 1024;   // of gradients: what a plan takes
 
 int lora_splits(int64_t T, int64_t C, int64_t n, int r);
 int64_t lora_outer_workspace(int64_t T, int64_t C, int64_t n, int r);   // bytes
 hipError_t launch_lora_shrink(const LoraProblem& p, hipStream_t st);
 hipError_t launch_lora_expand(const LoraProblem& p, hipStream_t st);
-hipError_t launch_lora_outer(const LoraProblem& p, hipStream_t st);
+int64_t lora_order_workspace(int64_t T, int64_t n);                     // bytes
+hipError_t launch_lora_order(const LoraProblem& p, void* workspace, LoraOrder& order, hipStream_t st);
+hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& order, hipStream_t st);
 
 }  // namespace fp8mm

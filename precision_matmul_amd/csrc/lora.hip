@@ -24,6 +24,7 @@
 // and the rest, in two instructions: the matrix work is not the bound, and v keeps 16
 // bits.
 #include "block_launch.hpp"
+#include "moe_launch.hpp"
 #include "ops_common.hpp"
 
 namespace fp8mm {
@@ -36,6 +37,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 64;          // tokens of a workgroup: one ballot
 constexpr int kRankBlock = 64;     // rows of a panel that a workgroup takes at once
+constexpr int kFewTokens = 512;    // batches of up to this many tokens are one tile
 
 __device__ __forceinline__ bf16x8 as_bf16(const Chunk& c) { return __builtin_bit_cast(bf16x8, c); }
 
@@ -43,60 +45,105 @@ __device__ __forceinline__ f32x4 mfma(const bf16x8& a, const bf16x8& b, const f3
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// The tokens of one adapter among a tile's 64: `rows` of them, lane i < rows holds the
-// i-th one's place in the tile.
+// At most 64 tokens of one adapter: `rows` of them, lane i < rows holds the i-th one.
 struct Members {
-  int rows, place;
+  int rows, token;
+  // Member i (the last one, past it).
+  __device__ __forceinline__ int at(int i) const { return __shfl(token, min(i, rows - 1), 64); }
 };
-__device__ __forceinline__ Members members(uint64_t same, int lane) {
-  const uint64_t below = (uint64_t(1) << lane) - 1;
-  const int rows = __popcll(same);
-  const bool in = same >> lane & 1;
-  // members to the front, the others behind them: a permutation of the lanes
-  const int to = in ? __popcll(same & below) : rows + __popcll(~same & below);
-  return Members{rows, __builtin_amdgcn_ds_permute(to * 4, lane)};
-}
-// The place of member i (of the last one, past it).
-__device__ __forceinline__ int place_of(const Members& m, int i) { return __shfl(m.place, min(i, m.rows - 1), 64); }
 
-// Adapter of each lane's token, -1 without one (or no token); runs body(a, members) for
-// each that occurs (a < 0 if NONE is true: those without).  With more than one
-// workgroup in y, workgroup y handles the adapter of token y, if y is its first.
+// The adapter of token t, -1 without one (or no token).
+__device__ __forceinline__ int adapter_of(const LoraProblem& p, int64_t t) {
+  const int id = t < p.T ? p.ids[t] : -1;
+  return id >= 0 && id < p.n ? id : -1;
+}
+
+// body(a, members) for each adapter among the 64 tokens from t0 on (NONE: and with a =
+// -1 for those without one).
 template <bool NONE, typename Body>
 __device__ __forceinline__ void each_adapter(const LoraProblem& p, int64_t t0, const Body& body) {
   const int lane = threadIdx.x & 63;
   const bool in = t0 + lane < p.T;
-  int id = in ? p.ids[t0 + lane] : -1;
-  if (id < 0 || id >= p.n) id = -1;
+  const int id = adapter_of(p, t0 + lane);
+  const uint64_t below = (uint64_t(1) << lane) - 1;
   uint64_t todo = __ballot(in && (NONE || id >= 0));
-  const bool one = gridDim.y > 1;
-  if (one) {
-    if (!(todo >> blockIdx.y & 1)) return;
-    todo &= ~((uint64_t(1) << blockIdx.y) - 1);
-  }
   while (todo) {
-    const int first = __builtin_ctzll(todo);
-    const int a = __builtin_amdgcn_readlane(id, first);
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
     const uint64_t same = __ballot(in && id == a);
-    if (one && __builtin_ctzll(same) != int(blockIdx.y)) return;
     todo &= ~same;
-    body(a, members(same, lane));
-    if (one) return;
+    // members to the front, the others behind them: a permutation of the lanes
+    const int rows = __popcll(same);
+    const int to = same >> lane & 1 ? __popcll(same & below) : rows + __popcll(~same & below);
+    body(a, Members{rows, int(t0) + __builtin_amdgcn_ds_permute(to * 4, lane)});
   }
+}
+
+// The same for a batch of few tokens as a whole, which may all have adapters of their
+// own: workgroup y handles the adapter of token y if y is its first token, up to 64 of
+// its tokens at a time.  `list` is the wave's own.
+template <bool NONE, typename Body>
+__device__ __forceinline__ void one_adapter(const LoraProblem& p, uint16_t* list, const Body& body) {
+  const int lane = threadIdx.x & 63;
+  const int a = adapter_of(p, blockIdx.y);
+  if (!NONE && a < 0) return;
+  int rows = 0, first = -1, id[kFewTokens / kTile];
+#pragma unroll
+  for (int i = 0; i < kFewTokens / kTile; ++i)
+    if (i * kTile < int(p.T)) id[i] = adapter_of(p, i * kTile + lane);
+#pragma unroll
+  for (int i = 0; i < kFewTokens / kTile; ++i)
+    if (i * kTile < int(p.T)) {
+      const bool in = i * kTile + lane < p.T && id[i] == a;
+      const uint64_t same = __ballot(in);
+      if (first < 0 && same) first = i * kTile + __builtin_ctzll(same);
+      if (in) list[rows + __popcll(same & ((uint64_t(1) << lane) - 1))] = uint16_t(i * kTile + lane);
+      rows += __popcll(same);
+    }
+  if (first != int(blockIdx.y)) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  for (int i = 0; i < rows; i += kTile) body(a, Members{min(kTile, rows - i), int(list[min(i + lane, rows - 1)])});
 }
 
 // -------------------------------------------------------------------- shrink
 
-// Partial v of one adapter's tokens over this wave's columns: chunks of 128 columns
-// first, first + 4, ... below last.
+// Rows of MF x 16 tokens and RF x 16 panel rows at ST steps of 32 columns from k on.
+template <int MF, int RF, int ST>
+struct Piece {
+  Chunk A[ST][MF], B[ST][RF];
+
+  __device__ __forceinline__ void load(const uint16_t* const (&xr)[MF], const uint16_t* const (&pr)[RF], int64_t k) {
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+#pragma unroll
+      for (int i = 0; i < MF; ++i) A[s][i] = load_chunk(xr[i] + k + 32 * s);
+#pragma unroll
+      for (int f = 0; f < RF; ++f) B[s][f] = load_chunk(pr[f] + k + 32 * s);
+    }
+  }
+  __device__ __forceinline__ void add(f32x4 (&acc)[MF][RF]) const {
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int f = 0; f < RF; ++f) acc[i][f] = mfma(as_bf16(A[s][i]), as_bf16(B[s][f]), acc[i][f]);
+  }
+};
+
+// Steps of a wave's turn: 64 columns, whole lines of memory; two turns are in registers,
+// one of them in flight.
+constexpr int kSteps = 2;
+
+// Partial v of up to MF x 16 tokens over pieces first, first + 4, ... below last.
 template <int MF, int RF>
-__device__ __forceinline__ void shrink_rows(const LoraProblem& p, int64_t t0, int a, const Members& m, int rank0,
-                                            int first, int last, f32x4 (&acc)[MF][RF]) {
+__device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const Members& m, int rank0, int first,
+                                            int last, f32x4 (&acc)[MF][RF]) {
+  constexpr int ST = kSteps;
   const int lane = threadIdx.x & 63, l15 = lane & 15, g8 = (lane >> 4) * 8;
   const uint16_t* xr[MF];
   const uint16_t* pr[RF];
 #pragma unroll
-  for (int i = 0; i < MF; ++i) xr[i] = p.x + (t0 + place_of(m, i * 16 + l15)) * p.ld_x;
+  for (int i = 0; i < MF; ++i) xr[i] = p.x + int64_t(m.at(i * 16 + l15)) * p.ld_x;
 #pragma unroll
   for (int f = 0; f < RF; ++f)
     pr[f] = p.panels + (int64_t(a) * p.r + min(rank0 + f * 16 + l15, p.r - 1)) * p.C;
@@ -104,45 +151,38 @@ __device__ __forceinline__ void shrink_rows(const LoraProblem& p, int64_t t0, in
   for (int i = 0; i < MF; ++i)
 #pragma unroll
     for (int f = 0; f < RF; ++f) acc[i][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int c = first; c < last; c += 4) {
-    const int64_t k0 = int64_t(c) * 128;
-    if (k0 + 128 <= p.C) {
+  const int whole = min(last, int(p.C / (32 * ST)));
+  int c = first;
+  Piece<MF, RF, ST> u, w;
+  if (c < whole) u.load(xr, pr, int64_t(c) * (32 * ST) + g8);
+  while (c < whole) {
+    if (c + 4 < whole) w.load(xr, pr, int64_t(c + 4) * (32 * ST) + g8);
+    u.add(acc);
+    c += 4;
+    if (c >= whole) break;
+    if (c + 4 < whole) u.load(xr, pr, int64_t(c + 4) * (32 * ST) + g8);
+    w.add(acc);
+    c += 4;
+  }
+  if (c < last) {                        // the row's last columns, zeros past them
+#pragma unroll 1
+    for (int64_t k = int64_t(c) * (32 * ST) + g8; k < p.C + g8; k += 32) {
+      Piece<MF, RF, 1> end;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int64_t k = k0 + 32 * s + g8;
-        Chunk A[MF], B[RF];
+      for (int i = 0; i < MF; ++i) end.A[0][i] = load_row(xr[i], k, p.C);
 #pragma unroll
-        for (int i = 0; i < MF; ++i) A[i] = load_chunk(xr[i] + k);
-#pragma unroll
-        for (int f = 0; f < RF; ++f) B[f] = load_chunk(pr[f] + k);
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-          for (int f = 0; f < RF; ++f) acc[i][f] = mfma(as_bf16(A[i]), as_bf16(B[f]), acc[i][f]);
-      }
-    } else {
-      for (int s = 0; s < 4; ++s) {
-        const int64_t k = k0 + 32 * s + g8;
-        Chunk A[MF], B[RF];
-#pragma unroll
-        for (int i = 0; i < MF; ++i) A[i] = load_row(xr[i], k, p.C);
-#pragma unroll
-        for (int f = 0; f < RF; ++f) B[f] = load_row(pr[f], k, p.C);
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-          for (int f = 0; f < RF; ++f) acc[i][f] = mfma(as_bf16(A[i]), as_bf16(B[f]), acc[i][f]);
-      }
+      for (int f = 0; f < RF; ++f) end.B[0][f] = load_row(pr[f], k, p.C);
+      end.add(acc);
     }
   }
 }
 
 template <int MF, int RF>
-__device__ __forceinline__ void shrink_tile(const LoraProblem& p, int64_t t0, int a, const Members& m, int split,
-                                            int rank0, int first, int last, float* red) {
+__device__ __forceinline__ void shrink_tile(const LoraProblem& p, int a, const Members& m, int split, int rank0,
+                                            int first, int last, float* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   f32x4 acc[MF][RF];
-  shrink_rows<MF, RF>(p, t0, a, m, rank0, first + wave, last, acc);
+  shrink_rows<MF, RF>(p, a, m, rank0, first + wave, last, acc);
   // the four waves' sums, added in wave order
 #pragma unroll
   for (int i = 0; i < MF; ++i)
@@ -158,29 +198,34 @@ __device__ __forceinline__ void shrink_tile(const LoraProblem& p, int64_t t0, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int at = q / RF * 16 + (lane >> 4) * 4 + i;
-      const int place = place_of(m, at);
-      if (at < m.rows && j < p.r) p.v[(int64_t(split) * p.T + t0 + place) * p.r + j] = s[i];
+      const int64_t t = m.at(at);
+      if (at < m.rows && j < p.r) p.v[(int64_t(split) * p.T + t) * p.r + j] = s[i];
     }
   }
   __syncthreads();
 }
 
-template <int RF>
+template <int RF, bool FEW>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraProblem p, int rank_blocks) {
   __shared__ __attribute__((aligned(16))) float red[4 * 4 * RF * 64 * 4];
+  __shared__ uint16_t list[4][FEW ? kFewTokens : 1];
   const int per = p.splits * rank_blocks;
-  const int64_t t0 = int64_t(blockIdx.x / per) * kTile;
   const int rest = blockIdx.x % per, split = rest % p.splits, rank0 = rest / p.splits * kRankBlock;
-  const int chunks = int((p.C + 127) / 128), each = (chunks + p.splits - 1) / p.splits;
-  const int first = split * each, last = min(chunks, first + each);
-  each_adapter<false>(p, t0, [&](int a, const Members& m) {
+  constexpr int COLS = 32 * kSteps;
+  const int pieces = int((p.C + COLS - 1) / COLS), each = (pieces + p.splits - 1) / p.splits;
+  const int first = split * each, last = min(pieces, first + each);
+  const auto body = [&](int a, const Members& m) {
     if (m.rows <= 16)
-      shrink_tile<1, RF>(p, t0, a, m, split, rank0, first, last, red);
+      shrink_tile<1, RF>(p, a, m, split, rank0, first, last, red);
     else if (m.rows <= 32)
-      shrink_tile<2, RF>(p, t0, a, m, split, rank0, first, last, red);
+      shrink_tile<2, RF>(p, a, m, split, rank0, first, last, red);
     else
-      shrink_tile<4, RF>(p, t0, a, m, split, rank0, first, last, red);
-  });
+      shrink_tile<4, RF>(p, a, m, split, rank0, first, last, red);
+  };
+  if constexpr (FEW)
+    one_adapter<false>(p, list[threadIdx.x >> 6], body);
+  else
+    each_adapter<false>(p, int64_t(blockIdx.x / per) * kTile, body);
 }
 
 // ------------------------------------------------- fragments of rows of columns
@@ -197,319 +242,422 @@ __device__ __forceinline__ void transpose8(const Chunk (&w)[8], bf16x8 (&b)[8]) 
   }
 }
 
-// 8 float32 values as bf16 and the rest of them as bf16 (0 where the value is past
-// bf16's range or not finite).
-__device__ __forceinline__ void split8(const float (&v)[8], bf16x8& hi, bf16x8& lo) {
-  Chunk h, l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    const float a = __uint_as_float(h.w[i] << 16), b = __uint_as_float(h.w[i] & 0xFFFF0000u);
-    const float ra = v[2 * i] - a, rb = v[2 * i + 1] - b;
-    l.w[i] = pack_bf16(fabsf(a) < __builtin_inff() ? ra : 0.0f, fabsf(b) < __builtin_inff() ? rb : 0.0f);
-  }
-  hi = as_bf16(h);
-  lo = as_bf16(l);
+// Two float32 values as packed bf16 and the rest of them as packed bf16 (0 where the
+// value is past bf16's range or not finite).
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(x, y);
+  const float a = __uint_as_float(hi << 16), b = __uint_as_float(hi & 0xFFFF0000u);
+  const float ra = x - a, rb = y - b;
+  lo = pack_bf16(fabsf(a) < __builtin_inff() ? ra : 0.0f, fabsf(b) < __builtin_inff() ? rb : 0.0f);
 }
 
 // -------------------------------------------------------------------- expand
 
-// v[j0 .. j0 + 8) of a token, its partial sums added, times s; 0 past the rank.
-__device__ __forceinline__ void load_v8(const LoraProblem& p, int64_t t, int j0, float s, float (&v)[8]) {
+// v of the members (zeros in the rows up to a multiple of 16 behind them and in the
+// columns up to ld - 8 behind the rank), its partial sums added, times s, as two bf16
+// numbers each: hi and lo [64][ld].
+template <int THREADS>
+__device__ __forceinline__ void stage_v(const LoraProblem& p, const Members& m, float s, int ld, uint16_t* hi,
+                                        uint16_t* lo) {
+  const int quads = (ld - 8) / 4, rows = (m.rows + 15) / 16 * 16;
+  for (int i0 = 0; i0 < rows * quads; i0 += THREADS) {     // every lane takes part in m.at
+    const int i = i0 + threadIdx.x;
+    const int row = min(i / quads, kTile - 1), j = i % quads * 4;
+    const int64_t t = m.at(row);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (row < m.rows && i < rows * quads) {
+      const float* at = p.v + t * p.r + j;
+      const int64_t next = p.T * p.r;
+      if (j + 4 <= p.r) {
+#pragma unroll 4
+        for (int k = 0; k < p.splits; ++k) {
+          float f[4];
+          unpack<float>(load_chunk(at + k * next), f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  for (int k = 0; k < p.splits; ++k) {
-    const float* at = p.v + (int64_t(k) * p.T + t) * p.r + j0;
-    if (j0 + 8 <= p.r) {
-      float a[4], b[4];
-      unpack<float>(load_chunk(at), a);
-      unpack<float>(load_chunk(at + 4), b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += a[i], v[4 + i] += b[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (j0 + i < p.r) v[i] += at[i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= s;
-}
-
-template <int MF>
-__device__ __forceinline__ void expand_rows(const LoraProblem& p, int64_t t0, int a, const Members& m, int64_t c) {
-  const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
-  const float s = p.scales ? p.scales[a] : 1.0f;
-  f32x4 acc[MF][8];
-  int64_t t[MF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    t[i] = t0 + place_of(m, i * 16 + l15);
-#pragma unroll
-    for (int f = 0; f < 8; ++f) acc[i][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  for (int j = 0; j < p.r; j += 32) {
-    Chunk w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = j + g * 8 + i;
-      w[i] = row < p.r ? load_row(p.panels + (int64_t(a) * p.r + row) * p.C, c, p.C) : Chunk{{0u, 0u, 0u, 0u}};
-    }
-    bf16x8 b[8];
-    transpose8(w, b);
-#pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      float v[8];
-      load_v8(p, t[i], j + g * 8, s, v);
-      bf16x8 hi, lo;
-      split8(v, hi, lo);
-#pragma unroll
-      for (int f = 0; f < 8; ++f) acc[i][f] = mfma(lo, b[f], acc[i][f]);
-#pragma unroll
-      for (int f = 0; f < 8; ++f) acc[i][f] = mfma(hi, b[f], acc[i][f]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int at = i * 16 + g * 4 + k;
-      const int64_t row = t0 + place_of(m, at);
-      if (at < m.rows) {
-        float f[8], y[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) y[q] = acc[i][q][k];
-        if (p.base) {
-          unpack<uint16_t>(load_row(p.base + row * p.ld_base, c, p.C), f);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) y[q] += f[q];
+          for (int e = 0; e < 4; ++e) v[e] += f[e];
         }
-        store_row(p.out + row * p.ld_out, c, p.C, pack<uint16_t>(y));
+      } else {
+        for (int k = 0; k < p.splits; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e < p.r) v[e] += at[k * next + e];
       }
     }
+    if (i < rows * quads) {
+      uint32_t h[2], l[2];
+      split2(v[0] * s, v[1] * s, h[0], l[0]);
+      split2(v[2] * s, v[3] * s, h[1], l[1]);
+      *reinterpret_cast<uint2*>(hi + row * ld + j) = make_uint2(h[0], h[1]);
+      *reinterpret_cast<uint2*>(lo + row * ld + j) = make_uint2(l[0], l[1]);
+    }
+  }
 }
 
+// The panel's rows j .. j + 32 at a lane's columns, as fragments.
+__device__ __forceinline__ void load_panel(const LoraProblem& p, int a, int j, int64_t c, bf16x8 (&b)[8]) {
+  Chunk w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = j + (threadIdx.x >> 4 & 3) * 8 + i;
+    w[i] = row < p.r ? load_row(p.panels + (int64_t(a) * p.r + row) * p.C, c, p.C) : Chunk{{0u, 0u, 0u, 0u}};
+  }
+  transpose8(w, b);
+}
+
+// Columns c .. c + 8 of the members' rows, 16 rows at a time with the next ones' base in
+// flight.  KS: steps of 32 rank rows whose fragments stay in registers (0: any number,
+// read again for each 16 rows).
+template <int KS, bool NT>
+__device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const Members& m, int64_t c, int ld,
+                                            const uint16_t* hi, const uint16_t* lo, bf16x8 (&b)[KS ? KS : 1][8]) {
+  const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
+  Chunk next[4];
+  const auto ask = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      next[k] = load_row<uint16_t, NT>(p.base + int64_t(m.at(i + g * 4 + k)) * p.ld_base, c, p.C);
+  };
+  if (p.base) ask(0);
+  for (int i = 0; i < m.rows; i += 16) {
+    Chunk base[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) base[k] = p.base ? next[k] : Chunk{{0u, 0u, 0u, 0u}};
+    if (p.base && i + 16 < m.rows) ask(i + 16);
+    f32x4 acc[8];
+#pragma unroll
+    for (int f = 0; f < 8; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const auto step = [&](int ks, const bf16x8 (&bf)[8]) {
+      const int at = (i + l15) * ld + ks * 32 + g * 8;
+      const bf16x8 l = *reinterpret_cast<const bf16x8*>(lo + at), h = *reinterpret_cast<const bf16x8*>(hi + at);
+#pragma unroll
+      for (int f = 0; f < 8; ++f) acc[f] = mfma(l, bf[f], acc[f]);
+#pragma unroll
+      for (int f = 0; f < 8; ++f) acc[f] = mfma(h, bf[f], acc[f]);
+    };
+    if constexpr (KS > 0) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) step(ks, b[ks]);
+    } else {
+      for (int ks = 0; ks * 32 < p.r; ++ks) {
+        load_panel(p, a, ks * 32, c, b[0]);
+        step(ks, b[0]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = i + g * 4 + k;
+      const int64_t row = m.at(at);
+      float f[8], y[8];
+      unpack<uint16_t>(base[k], f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) y[q] = acc[q][k] + f[q];
+      if (at < m.rows) store_row<uint16_t, NT>(p.out + row * p.ld_out, c, p.C, pack<uint16_t>(y));
+    }
+  }
+}
+
+template <int KS, bool FEW, bool NT>
 __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, int column_blocks) {
-  const int64_t t0 = int64_t(blockIdx.x / column_blocks) * kTile;
-  const int lane = threadIdx.x & 63;
+  constexpr int MAX = (KS ? KS * 32 : kLoraMaxRank) + 8;
+  __shared__ __attribute__((aligned(16))) uint16_t hi[kTile * MAX], lo[kTile * MAX];
+  __shared__ uint16_t list[4][FEW ? kFewTokens : 1];
+  const int lane = threadIdx.x & 63, ld = KS ? MAX : (p.r + 31) / 32 * 32 + 8;
   const int64_t first = int64_t(blockIdx.x % column_blocks) * 512 + (threadIdx.x >> 6) * 128;
-  if (first >= p.C) return;              // whole waves; nothing below waits for others
+  const bool idle = first >= p.C;        // whole waves, which still stage v
   const int64_t c = first + (lane & 15) * 8;
-  each_adapter<true>(p, t0, [&](int a, const Members& m) {
+  const auto body = [&](int a, const Members& m) {
     if (a < 0) {                         // no adapter: base alone
-      if (p.base == p.out) return;
+      if (p.base == p.out || idle) return;
       for (int i0 = 0; i0 < m.rows; i0 += 4) {
         const int i = i0 + (lane >> 4);
-        const int64_t row = t0 + place_of(m, i);
+        const int64_t row = m.at(i);
         if (i >= m.rows) continue;
         const Chunk v = p.base ? load_row(p.base + row * p.ld_base, c, p.C) : Chunk{{0u, 0u, 0u, 0u}};
         store_row(p.out + row * p.ld_out, c, p.C, v);
       }
-    } else if (m.rows <= 16) {
-      expand_rows<1>(p, t0, a, m, c);
-    } else if (m.rows <= 32) {
-      expand_rows<2>(p, t0, a, m, c);
-    } else {
-      expand_rows<4>(p, t0, a, m, c);
+      return;
     }
-  });
+    bf16x8 b[KS ? KS : 1][8];
+    if constexpr (KS > 0) {
+      if (!idle) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) load_panel(p, a, ks * 32, c, b[ks]);
+      }
+    }
+    stage_v<256>(p, m, p.scales ? p.scales[a] : 1.0f, ld, hi, lo);
+    __syncthreads();
+    if (!idle) expand_rows<KS, NT>(p, a, m, c, ld, hi, lo, b);
+    __syncthreads();
+  };
+  if constexpr (FEW)
+    one_adapter<true>(p, list[threadIdx.x >> 6], body);
+  else
+    each_adapter<true>(p, int64_t(blockIdx.x / column_blocks) * kTile, body);
 }
 
 // --------------------------------------------------------------------- outer
 
-// Gradient rows of one adapter's panel: 64 rows of the rank (or fewer) and 128 columns a
-// workgroup; its waves take the tokens 64 at a time in turns, skipping those of other
-// adapters, and their sums are added in wave order.  Z workgroups share the tokens of
-// long batches; their sums go to the workspace and lora_sum_kernel adds them.
+// order[row] = t, from each token's row in adapter order (negative: no adapter).
+__global__ __launch_bounds__(256) void lora_order_kernel(const int32_t* row_of_token, int64_t T, int32_t* order) {
+  const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (t < T && row_of_token[t] >= 0) order[row_of_token[t]] = int32_t(t);
+}
+
+constexpr int kOuterRows = 32;           // tokens of a turn: one matrix step
+
+// Panel gradients from tokens in adapter order.  A workgroup takes 512 columns (its
+// waves 128 each), 64 rows of the rank (or fewer) and a range z of the rows; for each
+// adapter in the range it adds up its rows, 32 at a time, and writes one partial
+// gradient.  As z and the adapter only grow from one to the next, z + a names it: no two
+// have the same, and lora_sum_kernel finds an adapter's by its rows.  The next turn's
+// rows of x and v are in flight while this one's are multiplied; v goes through LDS,
+// which turns its rows (ranks of one token) into columns (tokens of one rank).
 template <int RF>
-__global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, int rank_blocks, int column_blocks,
-                                                         int Z) {
-  __shared__ __attribute__((aligned(16))) float red[2 * RF * 8 * 64 * 4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l15 = lane & 15, g = lane >> 4;
-  unsigned at = blockIdx.x;
-  const int cb = at % column_blocks;
-  at /= column_blocks;
-  const int rank0 = at % rank_blocks * kRankBlock;
-  at /= rank_blocks;
-  const int z = at % Z, a = at / Z;
-  const int64_t c = int64_t(cb) * 128 + l15 * 8;
-  const int64_t tiles = (p.T + kTile - 1) / kTile, each = (tiles + Z - 1) / Z;
-  const int64_t last = min(tiles, (z + 1) * each);
-  f32x4 acc[RF][8];
+__global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, const int32_t* offsets,
+                                                         const int32_t* order, int rank_blocks, int column_blocks,
+                                                         int64_t per) {
+  constexpr int RANKS = RF * 16, LD = kOuterRows + 8;
+  __shared__ __attribute__((aligned(16))) uint16_t hi[2][RANKS * LD], lo[2][RANKS * LD];
+  const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
+  const int cb = blockIdx.x % column_blocks, rest = blockIdx.x / column_blocks;
+  const int rank0 = rest % rank_blocks * kRankBlock, z = rest / rank_blocks;
+  const int64_t first = int64_t(cb) * 512 + (threadIdx.x >> 6) * 128;
+  const bool idle = first >= p.C;
+  const int64_t c = first + l15 * 8;
+  const int used = offsets[p.n - 1];     // rows that have an adapter
+  const int z0 = int(min(int64_t(used), z * per)), z1 = int(min(int64_t(used), (z + 1) * per));
+  if (z0 >= z1) return;
+  // a thread's share of v: 8 tokens of one rank
+  static_assert(RANKS * (kOuterRows / 8) <= 256, "a share for each thread");
+  const int share = threadIdx.x / RANKS, rank = threadIdx.x % RANKS;
+  const bool mine = share < kOuterRows / 8 && rank0 + rank < p.r;
+  int a;
+  {
+    int low = 0, high = p.n - 1;         // the adapter of row z0: the first that ends past it
+    while (low < high) {
+      const int mid = (low + high) >> 1;
+      if (offsets[mid] > z0)
+        high = mid;
+      else
+        low = mid + 1;
+    }
+    a = low;
+  }
+  for (int begin = z0; begin < z1; ++a) {
+    const int end = min(offsets[a], z1);
+    if (end <= begin) continue;
+    f32x4 acc[RF][8];
 #pragma unroll
-  for (int f = 0; f < RF; ++f)
+    for (int f = 0; f < RF; ++f)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc[f][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t tile = z * each + wave; tile < last; tile += 4) {
-    const int64_t t0 = tile * kTile;
-    const uint64_t same = __ballot(t0 + lane < p.T && p.ids[min(t0 + lane, p.T - 1)] == a);
-    if (!same) continue;
-    const Members m = members(same, lane);
-    for (int i0 = 0; i0 < m.rows; i0 += 32) {
-      Chunk w[8];
-      float v[RF][8];
+      for (int q = 0; q < 8; ++q) acc[f][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    Chunk w[8];
+    float v[8];
+    int tx[8], tv[8];                    // the tokens of the next turn's rows of x and v
+    const auto find = [&](int row0) {    // reads up to 31 rows past the end, which nothing uses
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int i1 = i0 + g * 8 + i;
-        const int64_t t = t0 + place_of(m, i1);
-        const bool in = i1 < m.rows;
-        w[i] = in ? load_row(p.x + t * p.ld_x, c, p.C) : Chunk{{0u, 0u, 0u, 0u}};
+        tx[i] = order[row0 + g * 8 + i];
+        tv[i] = order[row0 + min(share, kOuterRows / 8 - 1) * 8 + i];
+      }
+    };
+    const auto ask = [&](int row0) {
 #pragma unroll
-        for (int f = 0; f < RF; ++f) {
-          const int j = rank0 + f * 16 + l15;
-          v[f][i] = 0.0f;
-          if (in && j < p.r)
-            for (int k = 0; k < p.splits; ++k) v[f][i] += p.v[(int64_t(k) * p.T + t) * p.r + j];
+      for (int i = 0; i < 8; ++i)
+        w[i] = row0 + g * 8 + i < end && !idle ? load_row(p.x + int64_t(tx[i]) * p.ld_x, c, p.C)
+                                               : Chunk{{0u, 0u, 0u, 0u}};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = 0.0f;
+        if (mine && row0 + share * 8 + i < end) {
+          const float* at = p.v + int64_t(tv[i]) * p.r + rank0 + rank;
+          v[i] = at[0];
+          for (int k = 1; k < p.splits; ++k) v[i] += at[k * p.T * p.r];
         }
+      }
+    };
+    find(begin);
+    ask(begin);
+    if (begin + kOuterRows < end) find(begin + kOuterRows);
+    int buffer = 0;
+    for (int row0 = begin; row0 < end; row0 += kOuterRows, buffer ^= 1) {
+      if (share < kOuterRows / 8) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
+        *reinterpret_cast<uint4*>(hi[buffer] + rank * LD + share * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(lo[buffer] + rank * LD + share * 8) = make_uint4(l[0], l[1], l[2], l[3]);
       }
       bf16x8 b[8];
       transpose8(w, b);
+      __syncthreads();                   // one a turn: the other buffer is read until the next one
+      if (row0 + kOuterRows < end) ask(row0 + kOuterRows);
+      if (row0 + 2 * kOuterRows < end) find(row0 + 2 * kOuterRows);
 #pragma unroll
       for (int f = 0; f < RF; ++f) {
-        bf16x8 hi, lo;
-        split8(v[f], hi, lo);
+        const int at = (f * 16 + l15) * LD + g * 8;
+        const bf16x8 h = *reinterpret_cast<const bf16x8*>(hi[buffer] + at);
+        const bf16x8 l = *reinterpret_cast<const bf16x8*>(lo[buffer] + at);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(lo, b[q], acc[f][q]);
+        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(l, b[q], acc[f][q]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(hi, b[q], acc[f][q]);
+        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(h, b[q], acc[f][q]);
       }
     }
-  }
-  // the waves' sums, halved twice
-#pragma unroll
-  for (int half = 2; half >= 1; half >>= 1) {
-    if (wave >= half && wave < 2 * half) {
+    __syncthreads();                     // the next adapter starts with buffer 0
+    if (!idle) {
+      float* out = p.partial + int64_t(z + a) * p.r * p.C;
 #pragma unroll
       for (int f = 0; f < RF; ++f)
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<f32x4*>(red + (((wave - half) * RF * 8 + f * 8 + q) * 64 + lane) * 4) = acc[f][q];
-    }
-    __syncthreads();
-    if (wave < half) {
+        for (int k = 0; k < 4; ++k) {
+          const int j = rank0 + f * 16 + g * 4 + k;
+          if (j >= p.r) continue;
 #pragma unroll
-      for (int f = 0; f < RF; ++f)
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          acc[f][q] += *reinterpret_cast<const f32x4*>(red + ((wave * RF * 8 + f * 8 + q) * 64 + lane) * 4);
+          for (int q = 0; q < 8; q += 4)
+            store_row(out + int64_t(j) * p.C, c + q, p.C,
+                      Chunk{{__float_as_uint(acc[f][q][k]), __float_as_uint(acc[f][q + 1][k]),
+                             __float_as_uint(acc[f][q + 2][k]), __float_as_uint(acc[f][q + 3][k])}});
+        }
     }
-    __syncthreads();
+    begin = end;
   }
-  if (wave != 0) return;
-  const float s = p.scales ? p.scales[a] : 1.0f;
-#pragma unroll
-  for (int f = 0; f < RF; ++f)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = rank0 + f * 16 + g * 4 + k;
-      if (j >= p.r) continue;
-      float y[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) y[q] = acc[f][q][k] * s;
-      const int64_t row = (int64_t(a) * p.r + j) * p.C;
-      if (Z > 1 || p.grad_fp32) {
-        float* out = Z > 1 ? p.partial + int64_t(z) * p.n * p.r * p.C + row : static_cast<float*>(p.grad) + row;
-        store_row(out, c, p.C, Chunk{{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
-                                      __float_as_uint(y[3])}});
-        store_row(out, c + 4, p.C, Chunk{{__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]),
-                                          __float_as_uint(y[7])}});
-      } else {
-        store_row(static_cast<uint16_t*>(p.grad) + row, c, p.C, pack<uint16_t>(y));
-      }
-    }
 }
 
-// Adds the Z partial gradients in order: four values a thread.
-__global__ __launch_bounds__(256) void lora_sum_kernel(const float* partial, int Z, int64_t count, void* grad,
-                                                       bool fp32) {
-  for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < count; i += int64_t(gridDim.x) * 1024) {
+// Adds an adapter's partial gradients in order, times its scale: four values a thread.
+__global__ __launch_bounds__(256) void lora_sum_kernel(const LoraProblem p, const int32_t* offsets, int64_t per,
+                                                       unsigned blocks) {
+  const int a = blockIdx.x / blocks;
+  const int64_t count = int64_t(p.r) * p.C;
+  const int begin = a ? offsets[a - 1] : 0, end = offsets[a];
+  const int64_t z0 = begin / per + a, z1 = end > begin ? (end - 1) / per + a + 1 : z0;
+  const float scale = p.scales ? p.scales[a] : 1.0f;
+  for (int64_t i = (int64_t(blockIdx.x % blocks) * 256 + threadIdx.x) * 4; i < count; i += int64_t(blocks) * 1024) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int z = 0; z < Z; ++z) {
+#pragma unroll 4
+    for (int64_t z = z0; z < z1; ++z) {
       float f[4];
-      unpack<float>(load_row(partial + z * count, i, count), f);
+      unpack<float>(load_row(p.partial + z * count, i, count), f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[k] += f[k];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + k < count) {
-        if (fp32)
-          static_cast<float*>(grad)[i + k] = s[k];
-        else
-          static_cast<uint16_t*>(grad)[i + k] = to_bf16(s[k]);
-      }
+    for (int k = 0; k < 4; ++k) s[k] *= scale;
+    const Chunk v = Chunk{{__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), __float_as_uint(s[3])}};
+    if (p.grad_fp32) {
+      store_row(static_cast<float*>(p.grad) + a * count, i, count, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k < count) static_cast<uint16_t*>(p.grad)[a * count + i + k] = to_bf16(s[k]);
+    }
   }
 }
 
-int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
+int64_t tiles_of(int64_t T) { return T <= kFewTokens ? 1 : (T + kTile - 1) / kTile; }
 int rank_blocks_of(int r) { return (r + kRankBlock - 1) / kRankBlock; }
 
-// Workgroups of a tile in y: one for each of its tokens where there are few tokens
-// (each may have an adapter of its own), else one that takes its adapters in turn.
-constexpr int64_t kFewTokens = 256;
-unsigned tile_groups(int64_t T) { return unsigned(T <= kFewTokens ? (T < kTile ? T : kTile) : 1); }
+// Workgroups in y: one for each token of a small batch.
+unsigned tokens_y(int64_t T) { return unsigned(T <= kFewTokens ? T : 1); }
 
-// Workgroups that share the tokens of a panel's gradient.
-int outer_shares(int64_t T, int64_t C, int64_t n, int r) {
-  const int64_t blocks = n * ((C + 127) / 128) * rank_blocks_of(r);
+// Ranges of rows that share a panel's gradient.
+int64_t outer_ranges(int64_t T, int64_t C, int r) {
+  const int64_t blocks = ((C + 511) / 512) * rank_blocks_of(r);
   int64_t z = (512 + blocks - 1) / blocks;
-  const int64_t most = T / (16 * n * r);      // partial sums: at most a quarter of x
-  if (z > most) z = most;
-  return int(z < 1 ? 1 : z > 16 ? 16 : z);
+  const int64_t most = T / (16 * r);          // partial gradients: at most a quarter of x's bytes
+  z = z < most ? z : most;
+  const int64_t turns = (T + 2 * kOuterRows - 1) / (2 * kOuterRows);
+  z = z < turns ? z : turns;
+  return z < 1 ? 1 : z;
 }
 
 }  // namespace
 
 int lora_splits(int64_t T, int64_t C, int64_t n, int r) {
   if (T <= 0) return 1;
-  const int64_t adapters = T <= kFewTokens ? (n < kTile ? n : kTile) : 1;
-  const int64_t tokens = T < kTile ? T : kTile;
-  const int64_t blocks = tiles_of(T) * (adapters < tokens ? adapters : tokens) * rank_blocks_of(r);
-  const int64_t quads = (C + 511) / 512;      // a chunk of 128 columns for each wave
+  const int64_t adapters = T <= kFewTokens ? (n < T ? n : T) : 1;
+  const int64_t blocks = tiles_of(T) * adapters * rank_blocks_of(r);
+  const int64_t turns = (C + 511) / 512;      // a turn or two for each wave
   int64_t s = (512 + blocks - 1) / blocks;
-  if (s > quads) s = quads;
+  if (s > turns) s = turns;
   return int(s > 16 ? 16 : s);
 }
 
 int64_t lora_outer_workspace(int64_t T, int64_t C, int64_t n, int r) {
-  const int z = outer_shares(T, C, n, r);
-  return z > 1 ? 4 * z * n * r * C : 0;
+  return 4 * (outer_ranges(T, C, r) + n) * r * C;
+}
+
+int64_t lora_order_workspace(int64_t T, int64_t n) {
+  return ((2 * T + kOuterRows + n) * 4 + 15) / 16 * 16 + plan_workspace(T, n);
+}
+
+hipError_t launch_lora_order(const LoraProblem& p, void* workspace, LoraOrder& order, hipStream_t st) {
+  int32_t* at = static_cast<int32_t*>(workspace);
+  int32_t* row_of_token = at;
+  order.order = at + p.T;
+  order.offsets = at + 2 * p.T + kOuterRows;     // the rows past the last are read, but not used
+  char* rest = static_cast<char*>(workspace) + ((2 * p.T + kOuterRows + p.n) * 4 + 15) / 16 * 16;
+  const hipError_t e =
+      launch_plan(p.ids, p.T, p.n, order.offsets, row_of_token, reinterpret_cast<int32_t*>(rest), st);
+  if (e != hipSuccess || p.T == 0) return e;
+  hipLaunchKernelGGL(lora_order_kernel, dim3(unsigned((p.T + 255) / 256)), dim3(256), 0, st, row_of_token, p.T,
+                     order.order);
+  return hipGetLastError();
+}
+
+template <bool FEW>
+hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
+  const int rb = rank_blocks_of(p.r);
+  const dim3 grid(unsigned(tiles_of(p.T) * p.splits * rb), tokens_y(p.T));
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, rb);
+    return hipGetLastError();
+  };
+  if (p.r <= 16) return run(lora_shrink_kernel<1, FEW>);
+  return p.r <= 32 ? run(lora_shrink_kernel<2, FEW>) : run(lora_shrink_kernel<4, FEW>);
+}
+
+template <bool FEW, bool NT>
+hipError_t run_expand(const LoraProblem& p, hipStream_t st) {
+  const int cb = int((p.C + 511) / 512);
+  const dim3 grid(unsigned(tiles_of(p.T) * cb), tokens_y(p.T));
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, cb);
+    return hipGetLastError();
+  };
+  if (p.r <= 32) return run(lora_expand_kernel<1, FEW, NT>);
+  return p.r <= 64 ? run(lora_expand_kernel<2, FEW, NT>) : run(lora_expand_kernel<0, FEW, NT>);
 }
 
 hipError_t launch_lora_shrink(const LoraProblem& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  const int rb = rank_blocks_of(p.r);
-  const dim3 grid(unsigned(tiles_of(p.T) * p.splits * rb), tile_groups(p.T));
-  if (p.r <= 16)
-    hipLaunchKernelGGL((lora_shrink_kernel<1>), grid, dim3(256), 0, st, p, rb);
-  else if (p.r <= 32)
-    hipLaunchKernelGGL((lora_shrink_kernel<2>), grid, dim3(256), 0, st, p, rb);
-  else
-    hipLaunchKernelGGL((lora_shrink_kernel<4>), grid, dim3(256), 0, st, p, rb);
-  return hipGetLastError();
+  return p.T <= kFewTokens ? run_shrink<true>(p, st) : run_shrink<false>(p, st);
 }
 
 hipError_t launch_lora_expand(const LoraProblem& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  const int cb = int((p.C + 511) / 512);
-  hipLaunchKernelGGL(lora_expand_kernel, dim3(unsigned(tiles_of(p.T) * cb), tile_groups(p.T)), dim3(256), 0, st, p, cb);
-  return hipGetLastError();
+  if (p.T <= kFewTokens) return run_expand<true, false>(p, st);
+  return p.T * p.C * 2 > kL2Bytes ? run_expand<false, true>(p, st) : run_expand<false, false>(p, st);
 }
 
-hipError_t launch_lora_outer(const LoraProblem& p, hipStream_t st) {
-  const int rb = rank_blocks_of(p.r), cb = int((p.C + 127) / 128), Z = outer_shares(p.T, p.C, p.n, p.r);
-  const dim3 grid(unsigned(int64_t(p.n) * cb * rb * Z));
-  if (p.r <= 16)
-    hipLaunchKernelGGL((lora_outer_kernel<1>), grid, dim3(256), 0, st, p, rb, cb, Z);
-  else if (p.r <= 32)
-    hipLaunchKernelGGL((lora_outer_kernel<2>), grid, dim3(256), 0, st, p, rb, cb, Z);
-  else
-    hipLaunchKernelGGL((lora_outer_kernel<4>), grid, dim3(256), 0, st, p, rb, cb, Z);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || Z == 1) return e;
-  const int64_t count = int64_t(p.n) * p.r * p.C, blocks = (count + 1023) / 1024;
-  hipLaunchKernelGGL(lora_sum_kernel, dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, p.partial, Z,
-                     count, p.grad, p.grad_fp32);
+hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& order, hipStream_t st) {
+  const int rb = rank_blocks_of(p.r), cb = int((p.C + 511) / 512);
+  const int64_t Z = outer_ranges(p.T, p.C, p.r);
+  const int64_t per = ((p.T + Z - 1) / Z + kOuterRows - 1) / kOuterRows * kOuterRows;
+  hipError_t e = hipSuccess;
+  if (p.T > 0) {
+    const dim3 grid(unsigned(Z * cb * rb));
+    const auto run = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, order.offsets, order.order, rb, cb, per);
+      return hipGetLastError();
+    };
+    e = p.r <= 16 ? run(lora_outer_kernel<1>) : p.r <= 32 ? run(lora_outer_kernel<2>) : run(lora_outer_kernel<4>);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t blocks = (int64_t(p.r) * p.C + 1023) / 1024;
+  const unsigned each = unsigned(blocks < 1024 ? blocks : 1024);
+  hipLaunchKernelGGL(lora_sum_kernel, dim3(unsigned(p.n) * each), dim3(256), 0, st, p, order.offsets, per > 0 ? per : 1,
+                     each);
   return hipGetLastError();
 }
 
