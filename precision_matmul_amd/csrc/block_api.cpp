@@ -317,7 +317,7 @@ fp8mm_status fp8mm_lora(const void* x, int64_t ld_x, int64_t T, int64_t K, const
 int64_t fp8mm_lora_backward_workspace(int64_t T, int64_t K, int64_t N, int64_t n, int64_t r) {
   if (!lora_shape(T, n, r) || !lora_columns(K) || !lora_columns(N)) return -1;
   if (n > fp8mm::kLoraMaxAdapters) return dv_bytes(T, N, n, r);
-  return dv_bytes(T, N, n, r) + partial_bytes(T, K, N, n, r) + fp8mm::lora_order_workspace(T, n);
+  return dv_bytes(T, N, n, r) + partial_bytes(T, K, N, n, r) + fp8mm::lora_order_workspace(T, n, int(r));
 }
 
 fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t T, int64_t K,
@@ -355,10 +355,8 @@ fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, i
   p.grad_fp32 = grad_dtype == FP8MM_OUT_FP32;
   char* at = static_cast<char*>(workspace) + dv_bytes(T, N, n, r);
   p.partial = reinterpret_cast<float*>(at);
-  fp8mm::LoraOrder order{};
   hipError_t e = hipSuccess;
-  if (ddown || dup) e = fp8mm::launch_lora_order(p, at + partial_bytes(T, K, N, n, r), order, stream);
-  if (e == hipSuccess && (dx || ddown)) {
+  if (dx || ddown) {
     fp8mm::LoraProblem q = p;
     q.C = N;
     q.panels = static_cast<const uint16_t*>(up);
@@ -368,27 +366,32 @@ fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, i
     q.splits = dv_splits;
     e = fp8mm::launch_lora_shrink(q, stream);
   }
+  fp8mm::LoraOrder o{};
+  o.v[0] = dup ? v : nullptr;
+  o.splits[0] = fp8mm::lora_splits(T, K, n, int(r));
+  o.v[1] = ddown ? dv : nullptr;
+  o.splits[1] = dv_splits;
+  if (e == hipSuccess && (ddown || dup))
+    e = fp8mm::launch_lora_order(p, at + partial_bytes(T, K, N, n, r), o, stream);
   if (e == hipSuccess && dup) {
     fp8mm::LoraProblem q = p;
     q.C = N;
     q.x = static_cast<const uint16_t*>(dy);
     q.ld_x = ld_dy;
-    q.v = const_cast<float*>(v);
-    q.splits = fp8mm::lora_splits(T, K, n, int(r));
     q.grad = dup;
-    e = fp8mm::launch_lora_outer(q, order, stream);
+    e = fp8mm::launch_lora_outer(q, o, 0, stream);
   }
   p.C = K;
-  p.v = dv;
-  p.splits = dv_splits;
   if (e == hipSuccess && ddown) {
     fp8mm::LoraProblem q = p;
     q.x = static_cast<const uint16_t*>(x);
     q.ld_x = ld_x;
     q.grad = ddown;
-    e = fp8mm::launch_lora_outer(q, order, stream);
+    e = fp8mm::launch_lora_outer(q, o, 1, stream);
   }
   if (e == hipSuccess && dx) {
+    p.v = dv;
+    p.splits = dv_splits;
     p.panels = static_cast<const uint16_t*>(down);
     p.out = static_cast<uint16_t*>(dx);
     p.ld_out = ld_dx;

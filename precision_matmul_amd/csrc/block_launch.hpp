@@ -86,11 +86,15 @@ struct LoraProblem {
   float* partial;          // outer: lora_outer_workspace bytes
 };
 
-// Tokens in adapter order: offsets [n], the adapters' cumulative end rows, and each
-// row's token.
+// Tokens in adapter order, for the gradients: offsets [n], the adapters' cumulative end
+// rows, each row's token, and v of both products in that order.
 struct LoraOrder {
+  const float* v[2];       // as the forward and the backward wrote them, or null
+  int splits[2];
   int32_t* offsets;
   int32_t* order;
+  uint16_t* sorted[2];
+  int64_t ld;
 };
 
 constexpr int kLoraMaxRank = 256;
@@ -100,8 +104,10 @@ int lora_splits(int64_t T, int64_t C, int64_t n, int r);
 int64_t lora_outer_workspace(int64_t T, int64_t C, int64_t n, int r);   // bytes
 hipError_t launch_lora_shrink(const LoraProblem& p, hipStream_t st);
 hipError_t launch_lora_expand(const LoraProblem& p, hipStream_t st);
-int64_t lora_order_workspace(int64_t T, int64_t n);                     // bytes
-hipError_t launch_lora_order(const LoraProblem& p, void* workspace, LoraOrder& order, hipStream_t st);
-hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& order, hipStream_t st);
+int64_t lora_order_workspace(int64_t T, int64_t n, int r);              // bytes
+// o.v and o.splits are the caller's, the rest is filled in
+hipError_t launch_lora_order(const LoraProblem& p, void* workspace, LoraOrder& o, hipStream_t st);
+// with the `which`-th v of o
+hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, int which, hipStream_t st);
 
 }  // namespace fp8mm

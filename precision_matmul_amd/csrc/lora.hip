@@ -52,6 +52,13 @@ struct Members {
   __device__ __forceinline__ int at(int i) const { return __shfl(token, min(i, rows - 1), 64); }
 };
 
+// Batches that are one tile: as many adapters as make its tokens few for each.
+__host__ __device__ inline bool few_tokens(int64_t T, int64_t n) {
+  return T <= kTile || (T <= kFewTokens && n > T / 16);
+}
+// Workgroups of such a batch stand for its tokens, else for the adapters.
+__host__ __device__ inline bool by_tokens(const LoraProblem& p) { return p.T < p.n; }
+
 // The adapter of token t, -1 without one (or no token).
 __device__ __forceinline__ int adapter_of(const LoraProblem& p, int64_t t) {
   const int id = t < p.T ? p.ids[t] : -1;
@@ -79,12 +86,14 @@ __device__ __forceinline__ void each_adapter(const LoraProblem& p, int64_t t0, c
 }
 
 // The same for a batch of few tokens as a whole, which may all have adapters of their
-// own: workgroup y handles the adapter of token y if y is its first token, up to 64 of
-// its tokens at a time.  `list` is the wave's own.
-template <bool NONE, typename Body>
+// own: workgroup y handles adapter y (the one past the last: the tokens without), or,
+// where there are more adapters than tokens, that of token y if y is its first token;
+// MOST of its tokens at a time.  `list` is the wave's own.
+template <bool NONE, int MOST, typename Body>
 __device__ __forceinline__ void one_adapter(const LoraProblem& p, uint16_t* list, const Body& body) {
   const int lane = threadIdx.x & 63;
-  const int a = adapter_of(p, blockIdx.y);
+  const bool by_token = by_tokens(p);
+  const int a = by_token ? adapter_of(p, blockIdx.y) : int(blockIdx.y) < p.n ? int(blockIdx.y) : -1;
   if (!NONE && a < 0) return;
   int rows = 0, first = -1, id[kFewTokens / kTile];
 #pragma unroll
@@ -99,9 +108,9 @@ __device__ __forceinline__ void one_adapter(const LoraProblem& p, uint16_t* list
       if (in) list[rows + __popcll(same & ((uint64_t(1) << lane) - 1))] = uint16_t(i * kTile + lane);
       rows += __popcll(same);
     }
-  if (first != int(blockIdx.y)) return;
+  if (by_token && first != int(blockIdx.y)) return;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  for (int i = 0; i < rows; i += kTile) body(a, Members{min(kTile, rows - i), int(list[min(i + lane, rows - 1)])});
+  for (int i = 0; i < rows; i += MOST) body(a, Members{min(MOST, rows - i), int(list[min(i + lane, rows - 1)])});
 }
 
 // -------------------------------------------------------------------- shrink
@@ -134,16 +143,16 @@ struct Piece {
 // one of them in flight.
 constexpr int kSteps = 2;
 
-// Partial v of up to MF x 16 tokens over pieces first, first + 4, ... below last.
-template <int MF, int RF>
-__device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const Members& m, int rank0, int first,
+// Partial v of MF x 16 members from `row` on over turns first, first + BY, ... below last.
+template <int MF, int RF, int BY>
+__device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const Members& m, int row, int rank0, int first,
                                             int last, f32x4 (&acc)[MF][RF]) {
   constexpr int ST = kSteps;
   const int lane = threadIdx.x & 63, l15 = lane & 15, g8 = (lane >> 4) * 8;
   const uint16_t* xr[MF];
   const uint16_t* pr[RF];
 #pragma unroll
-  for (int i = 0; i < MF; ++i) xr[i] = p.x + int64_t(m.at(i * 16 + l15)) * p.ld_x;
+  for (int i = 0; i < MF; ++i) xr[i] = p.x + int64_t(m.at(row + i * 16 + l15)) * p.ld_x;
 #pragma unroll
   for (int f = 0; f < RF; ++f)
     pr[f] = p.panels + (int64_t(a) * p.r + min(rank0 + f * 16 + l15, p.r - 1)) * p.C;
@@ -156,13 +165,13 @@ __device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const M
   Piece<MF, RF, ST> u, w;
   if (c < whole) u.load(xr, pr, int64_t(c) * (32 * ST) + g8);
   while (c < whole) {
-    if (c + 4 < whole) w.load(xr, pr, int64_t(c + 4) * (32 * ST) + g8);
+    if (c + BY < whole) w.load(xr, pr, int64_t(c + BY) * (32 * ST) + g8);
     u.add(acc);
-    c += 4;
+    c += BY;
     if (c >= whole) break;
-    if (c + 4 < whole) u.load(xr, pr, int64_t(c + 4) * (32 * ST) + g8);
+    if (c + BY < whole) u.load(xr, pr, int64_t(c + BY) * (32 * ST) + g8);
     w.add(acc);
-    c += 4;
+    c += BY;
   }
   if (c < last) {                        // the row's last columns, zeros past them
 #pragma unroll 1
@@ -177,23 +186,26 @@ __device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const M
   }
 }
 
-template <int MF, int RF>
+// v of up to MF x 16 members: the waves share the columns, or (HALVES = 2) two of them
+// the columns of each half of the members, which keeps fewer sums in a wave.
+template <int MF, int RF, int HALVES>
 __device__ __forceinline__ void shrink_tile(const LoraProblem& p, int a, const Members& m, int split, int rank0,
                                             int first, int last, float* red) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  f32x4 acc[MF][RF];
-  shrink_rows<MF, RF>(p, a, m, rank0, first + wave, last, acc);
-  // the four waves' sums, added in wave order
+  constexpr int BY = 4 / HALVES, MW = MF / HALVES;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = wave / BY, part = wave % BY;
+  f32x4 acc[MW][RF];
+  shrink_rows<MW, RF, BY>(p, a, m, half * MW * 16, rank0, first + part, last, acc);
+  // the waves' sums, added in wave order
 #pragma unroll
-  for (int i = 0; i < MF; ++i)
+  for (int i = 0; i < MW; ++i)
 #pragma unroll
     for (int f = 0; f < RF; ++f)
-      *reinterpret_cast<f32x4*>(red + ((wave * MF * RF + i * RF + f) * 64 + lane) * 4) = acc[i][f];
+      *reinterpret_cast<f32x4*>(red + ((part * MF * RF + (half * MW + i) * RF + f) * 64 + lane) * 4) = acc[i][f];
   __syncthreads();
   for (int q = wave; q < MF * RF; q += 4) {
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) s += *reinterpret_cast<const f32x4*>(red + ((w * MF * RF + q) * 64 + lane) * 4);
+    for (int w = 0; w < BY; ++w) s += *reinterpret_cast<const f32x4*>(red + ((w * MF * RF + q) * 64 + lane) * 4);
     const int j = rank0 + q % RF * 16 + (lane & 15);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -207,7 +219,9 @@ __device__ __forceinline__ void shrink_tile(const LoraProblem& p, int a, const M
 
 template <int RF, bool FEW>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraProblem p, int rank_blocks) {
-  __shared__ __attribute__((aligned(16))) float red[4 * 4 * RF * 64 * 4];
+  // sums of 32 members of all waves, or of 64 members of two or four
+  constexpr int SUMS = FEW ? 4 * 2 : (RF == 4 ? 2 * 4 : 4 * 4);
+  __shared__ __attribute__((aligned(16))) float red[SUMS * RF * 64 * 4];
   __shared__ uint16_t list[4][FEW ? kFewTokens : 1];
   const int per = p.splits * rank_blocks;
   const int rest = blockIdx.x % per, split = rest % p.splits, rank0 = rest / p.splits * kRankBlock;
@@ -216,14 +230,14 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraProblem p, i
   const int first = split * each, last = min(pieces, first + each);
   const auto body = [&](int a, const Members& m) {
     if (m.rows <= 16)
-      shrink_tile<1, RF>(p, a, m, split, rank0, first, last, red);
+      shrink_tile<1, RF, 1>(p, a, m, split, rank0, first, last, red);
     else if (m.rows <= 32)
-      shrink_tile<2, RF>(p, a, m, split, rank0, first, last, red);
-    else
-      shrink_tile<4, RF>(p, a, m, split, rank0, first, last, red);
+      shrink_tile<2, RF, 1>(p, a, m, split, rank0, first, last, red);
+    else if constexpr (!FEW)
+      shrink_tile<4, RF, RF == 4 ? 2 : 1>(p, a, m, split, rank0, first, last, red);
   };
   if constexpr (FEW)
-    one_adapter<false>(p, list[threadIdx.x >> 6], body);
+    one_adapter<false, 32>(p, list[threadIdx.x >> 6], body);
   else
     each_adapter<false>(p, int64_t(blockIdx.x / per) * kTile, body);
 }
@@ -390,136 +404,147 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, i
     __syncthreads();
   };
   if constexpr (FEW)
-    one_adapter<true>(p, list[threadIdx.x >> 6], body);
+    one_adapter<true, kTile>(p, list[threadIdx.x >> 6], body);
   else
     each_adapter<true>(p, int64_t(blockIdx.x / column_blocks) * kTile, body);
 }
 
 // --------------------------------------------------------------------- outer
 
-// order[row] = t, from each token's row in adapter order (negative: no adapter).
-__global__ __launch_bounds__(256) void lora_order_kernel(const int32_t* row_of_token, int64_t T, int32_t* order) {
+// Tokens and their v in adapter order: order[row] = t, and for each of the two (v of the
+// forward, dv) its partial sums added, as two bf16 numbers each in hi and lo [r][ld], a
+// rank's tokens next to each other.  A thread takes four ranks of a token.
+__global__ __launch_bounds__(256) void lora_sort_kernel(const LoraProblem p, const int32_t* row_of_token, LoraOrder o) {
   const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (t < T && row_of_token[t] >= 0) order[row_of_token[t]] = int32_t(t);
+  if (t >= p.T) return;
+  const int64_t row = row_of_token[t];
+  if (row < 0) return;                   // no adapter
+  if (blockIdx.y == 0) o.order[row] = int32_t(t);
+  const int j = blockIdx.y * 4;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const float* v = o.v[which];
+    if (!v) continue;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < o.splits[which]; ++k) {
+      const float* at = v + (k * p.T + t) * p.r;
+      float f[4];
+      unpack<float>(load_row(at, j, p.r), f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += f[e];
+    }
+    uint16_t* hi = o.sorted[which] + j * o.ld + row;
+    uint16_t* lo = hi + p.r * o.ld;
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      uint32_t h, l;
+      split2(s[e], s[e + 1], h, l);
+      if (j + e < p.r) hi[e * o.ld] = uint16_t(h), lo[e * o.ld] = uint16_t(l);
+      if (j + e + 1 < p.r) hi[(e + 1) * o.ld] = uint16_t(h >> 16), lo[(e + 1) * o.ld] = uint16_t(l >> 16);
+    }
+  }
 }
 
 constexpr int kOuterRows = 32;           // tokens of a turn: one matrix step
+
+// The first n of a lane's 8 values, zeros after them.
+__device__ __forceinline__ Chunk first_of(const Chunk& v, int n) {
+  Chunk c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c.w[i] = 2 * i + 1 < n ? v.w[i] : 2 * i < n ? v.w[i] & 0xFFFFu : 0u;
+  return c;
+}
 
 // Panel gradients from tokens in adapter order.  A workgroup takes 512 columns (its
 // waves 128 each), 64 rows of the rank (or fewer) and a range z of the rows; for each
 // adapter in the range it adds up its rows, 32 at a time, and writes one partial
 // gradient.  As z and the adapter only grow from one to the next, z + a names it: no two
 // have the same, and lora_sum_kernel finds an adapter's by its rows.  The next turn's
-// rows of x and v are in flight while this one's are multiplied; v goes through LDS,
-// which turns its rows (ranks of one token) into columns (tokens of one rank).
+// rows are in flight while this one's are multiplied.
 template <int RF>
-__global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, const int32_t* offsets,
-                                                         const int32_t* order, int rank_blocks, int column_blocks,
-                                                         int64_t per) {
-  constexpr int RANKS = RF * 16, LD = kOuterRows + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t hi[2][RANKS * LD], lo[2][RANKS * LD];
-  const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
+__global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, const LoraOrder o, int which,
+                                                         int rank_blocks, int column_blocks, int64_t per) {
+  const int lane = threadIdx.x & 63, l15 = lane & 15, g8 = (lane >> 4) * 8;
   const int cb = blockIdx.x % column_blocks, rest = blockIdx.x / column_blocks;
   const int rank0 = rest % rank_blocks * kRankBlock, z = rest / rank_blocks;
   const int64_t first = int64_t(cb) * 512 + (threadIdx.x >> 6) * 128;
-  const bool idle = first >= p.C;
+  if (first >= p.C) return;              // whole waves, which wait for no others
   const int64_t c = first + l15 * 8;
-  const int used = offsets[p.n - 1];     // rows that have an adapter
+  const int used = o.offsets[p.n - 1];   // rows that have an adapter
   const int z0 = int(min(int64_t(used), z * per)), z1 = int(min(int64_t(used), (z + 1) * per));
   if (z0 >= z1) return;
-  // a thread's share of v: 8 tokens of one rank
-  static_assert(RANKS * (kOuterRows / 8) <= 256, "a share for each thread");
-  const int share = threadIdx.x / RANKS, rank = threadIdx.x % RANKS;
-  const bool mine = share < kOuterRows / 8 && rank0 + rank < p.r;
   int a;
   {
     int low = 0, high = p.n - 1;         // the adapter of row z0: the first that ends past it
     while (low < high) {
       const int mid = (low + high) >> 1;
-      if (offsets[mid] > z0)
+      if (o.offsets[mid] > z0)
         high = mid;
       else
         low = mid + 1;
     }
     a = low;
   }
+  const uint16_t* vr[RF];
+#pragma unroll
+  for (int f = 0; f < RF; ++f) vr[f] = o.sorted[which] + min(rank0 + f * 16 + l15, p.r - 1) * o.ld + g8;
+  const int64_t to_lo = p.r * o.ld;
   for (int begin = z0; begin < z1; ++a) {
-    const int end = min(offsets[a], z1);
+    const int end = min(o.offsets[a], z1);
     if (end <= begin) continue;
     f32x4 acc[RF][8];
 #pragma unroll
     for (int f = 0; f < RF; ++f)
 #pragma unroll
       for (int q = 0; q < 8; ++q) acc[f][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    Chunk w[8];
-    float v[8];
-    int tx[8], tv[8];                    // the tokens of the next turn's rows of x and v
+    Chunk w[8], hi[RF], lo[RF];
+    int token[8];                        // of the next turn
     const auto find = [&](int row0) {    // reads up to 31 rows past the end, which nothing uses
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        tx[i] = order[row0 + g * 8 + i];
-        tv[i] = order[row0 + min(share, kOuterRows / 8 - 1) * 8 + i];
-      }
+      for (int i = 0; i < 8; ++i) token[i] = o.order[row0 + g8 + i];
     };
     const auto ask = [&](int row0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        w[i] = row0 + g * 8 + i < end && !idle ? load_row(p.x + int64_t(tx[i]) * p.ld_x, c, p.C)
-                                               : Chunk{{0u, 0u, 0u, 0u}};
+        w[i] = row0 + g8 + i < end ? load_row(p.x + int64_t(token[i]) * p.ld_x, c, p.C) : Chunk{{0u, 0u, 0u, 0u}};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = 0.0f;
-        if (mine && row0 + share * 8 + i < end) {
-          const float* at = p.v + int64_t(tv[i]) * p.r + rank0 + rank;
-          v[i] = at[0];
-          for (int k = 1; k < p.splits; ++k) v[i] += at[k * p.T * p.r];
-        }
-      }
+      for (int f = 0; f < RF; ++f) hi[f] = load_chunk(vr[f] + row0), lo[f] = load_chunk(vr[f] + row0 + to_lo);
     };
     find(begin);
     ask(begin);
     if (begin + kOuterRows < end) find(begin + kOuterRows);
-    int buffer = 0;
-    for (int row0 = begin; row0 < end; row0 += kOuterRows, buffer ^= 1) {
-      if (share < kOuterRows / 8) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
-        *reinterpret_cast<uint4*>(hi[buffer] + rank * LD + share * 8) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo[buffer] + rank * LD + share * 8) = make_uint4(l[0], l[1], l[2], l[3]);
-      }
-      bf16x8 b[8];
+    for (int row0 = begin; row0 < end; row0 += kOuterRows) {
+      bf16x8 b[8], h[RF], l[RF];
       transpose8(w, b);
-      __syncthreads();                   // one a turn: the other buffer is read until the next one
+#pragma unroll
+      for (int f = 0; f < RF; ++f) {
+        const int left = end - row0 - g8;          // the next adapter's v are not this one's
+        h[f] = as_bf16(left < 8 ? first_of(hi[f], left) : hi[f]);
+        l[f] = as_bf16(left < 8 ? first_of(lo[f], left) : lo[f]);
+      }
       if (row0 + kOuterRows < end) ask(row0 + kOuterRows);
       if (row0 + 2 * kOuterRows < end) find(row0 + 2 * kOuterRows);
 #pragma unroll
       for (int f = 0; f < RF; ++f) {
-        const int at = (f * 16 + l15) * LD + g * 8;
-        const bf16x8 h = *reinterpret_cast<const bf16x8*>(hi[buffer] + at);
-        const bf16x8 l = *reinterpret_cast<const bf16x8*>(lo[buffer] + at);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(l, b[q], acc[f][q]);
+        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(l[f], b[q], acc[f][q]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(h, b[q], acc[f][q]);
+        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(h[f], b[q], acc[f][q]);
       }
     }
-    __syncthreads();                     // the next adapter starts with buffer 0
-    if (!idle) {
-      float* out = p.partial + int64_t(z + a) * p.r * p.C;
+    float* out = p.partial + int64_t(z + a) * p.r * p.C;
 #pragma unroll
-      for (int f = 0; f < RF; ++f)
+    for (int f = 0; f < RF; ++f)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int j = rank0 + f * 16 + g * 4 + k;
-          if (j >= p.r) continue;
+      for (int k = 0; k < 4; ++k) {
+        const int j = rank0 + f * 16 + (lane >> 4) * 4 + k;
+        if (j >= p.r) continue;
 #pragma unroll
-          for (int q = 0; q < 8; q += 4)
-            store_row(out + int64_t(j) * p.C, c + q, p.C,
-                      Chunk{{__float_as_uint(acc[f][q][k]), __float_as_uint(acc[f][q + 1][k]),
-                             __float_as_uint(acc[f][q + 2][k]), __float_as_uint(acc[f][q + 3][k])}});
-        }
-    }
+        for (int q = 0; q < 8; q += 4)
+          store_row(out + int64_t(j) * p.C, c + q, p.C,
+                    Chunk{{__float_as_uint(acc[f][q][k]), __float_as_uint(acc[f][q + 1][k]),
+                           __float_as_uint(acc[f][q + 2][k]), __float_as_uint(acc[f][q + 3][k])}});
+      }
     begin = end;
   }
 }
@@ -554,11 +579,8 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraProblem p, cons
   }
 }
 
-int64_t tiles_of(int64_t T) { return T <= kFewTokens ? 1 : (T + kTile - 1) / kTile; }
+int64_t tiles_of(int64_t T, int64_t n) { return few_tokens(T, n) ? 1 : (T + kTile - 1) / kTile; }
 int rank_blocks_of(int r) { return (r + kRankBlock - 1) / kRankBlock; }
-
-// Workgroups in y: one for each token of a small batch.
-unsigned tokens_y(int64_t T) { return unsigned(T <= kFewTokens ? T : 1); }
 
 // Ranges of rows that share a panel's gradient.
 int64_t outer_ranges(int64_t T, int64_t C, int r) {
@@ -575,8 +597,8 @@ int64_t outer_ranges(int64_t T, int64_t C, int r) {
 
 int lora_splits(int64_t T, int64_t C, int64_t n, int r) {
   if (T <= 0) return 1;
-  const int64_t adapters = T <= kFewTokens ? (n < T ? n : T) : 1;
-  const int64_t blocks = tiles_of(T) * adapters * rank_blocks_of(r);
+  const int64_t adapters = few_tokens(T, n) ? (n < T ? n : T) : 1;
+  const int64_t blocks = tiles_of(T, n) * adapters * rank_blocks_of(r);
   const int64_t turns = (C + 511) / 512;      // a turn or two for each wave
   int64_t s = (512 + blocks - 1) / blocks;
   if (s > turns) s = turns;
@@ -587,28 +609,48 @@ int64_t lora_outer_workspace(int64_t T, int64_t C, int64_t n, int r) {
   return 4 * (outer_ranges(T, C, r) + n) * r * C;
 }
 
-int64_t lora_order_workspace(int64_t T, int64_t n) {
-  return ((2 * T + kOuterRows + n) * 4 + 15) / 16 * 16 + plan_workspace(T, n);
+// Parts of the order's workspace: rows of tokens, tokens of rows (up to 31 past the last
+// are read, but not used), offsets, both v in order, the plan's own.
+namespace {
+struct OrderBytes {
+  int64_t ld, rows, order, offsets, sorted, all;
+};
+OrderBytes order_bytes(int64_t T, int64_t n, int r) {
+  const auto whole = [](int64_t bytes) { return (bytes + 15) / 16 * 16; };
+  OrderBytes b;
+  b.ld = (T + kOuterRows + 7) / 8 * 8;
+  b.rows = whole(4 * T);
+  b.order = 4 * b.ld;
+  b.offsets = whole(4 * n);
+  b.sorted = 2 * 2 * r * b.ld;
+  b.all = b.rows + b.order + b.offsets + 2 * b.sorted + plan_workspace(T, n);
+  return b;
 }
+}  // namespace
 
-hipError_t launch_lora_order(const LoraProblem& p, void* workspace, LoraOrder& order, hipStream_t st) {
-  int32_t* at = static_cast<int32_t*>(workspace);
-  int32_t* row_of_token = at;
-  order.order = at + p.T;
-  order.offsets = at + 2 * p.T + kOuterRows;     // the rows past the last are read, but not used
-  char* rest = static_cast<char*>(workspace) + ((2 * p.T + kOuterRows + p.n) * 4 + 15) / 16 * 16;
+int64_t lora_order_workspace(int64_t T, int64_t n, int r) { return order_bytes(T, n, r).all; }
+
+hipError_t launch_lora_order(const LoraProblem& p, void* workspace, LoraOrder& o, hipStream_t st) {
+  const OrderBytes b = order_bytes(p.T, p.n, p.r);
+  char* at = static_cast<char*>(workspace);
+  int32_t* row_of_token = reinterpret_cast<int32_t*>(at);
+  o.ld = b.ld;
+  o.order = reinterpret_cast<int32_t*>(at += b.rows);
+  o.offsets = reinterpret_cast<int32_t*>(at += b.order);
+  o.sorted[0] = reinterpret_cast<uint16_t*>(at += b.offsets);
+  o.sorted[1] = reinterpret_cast<uint16_t*>(at += b.sorted);
   const hipError_t e =
-      launch_plan(p.ids, p.T, p.n, order.offsets, row_of_token, reinterpret_cast<int32_t*>(rest), st);
+      launch_plan(p.ids, p.T, p.n, o.offsets, row_of_token, reinterpret_cast<int32_t*>(at += b.sorted), st);
   if (e != hipSuccess || p.T == 0) return e;
-  hipLaunchKernelGGL(lora_order_kernel, dim3(unsigned((p.T + 255) / 256)), dim3(256), 0, st, row_of_token, p.T,
-                     order.order);
+  hipLaunchKernelGGL(lora_sort_kernel, dim3(unsigned((p.T + 255) / 256), unsigned((p.r + 3) / 4)), dim3(256), 0, st, p,
+                     row_of_token, o);
   return hipGetLastError();
 }
 
 template <bool FEW>
 hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
   const int rb = rank_blocks_of(p.r);
-  const dim3 grid(unsigned(tiles_of(p.T) * p.splits * rb), tokens_y(p.T));
+  const dim3 grid(unsigned(tiles_of(p.T, p.n) * p.splits * rb), unsigned(FEW ? (by_tokens(p) ? p.T : p.n) : 1));
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, rb);
     return hipGetLastError();
@@ -620,7 +662,7 @@ hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
 template <bool FEW, bool NT>
 hipError_t run_expand(const LoraProblem& p, hipStream_t st) {
   const int cb = int((p.C + 511) / 512);
-  const dim3 grid(unsigned(tiles_of(p.T) * cb), tokens_y(p.T));
+  const dim3 grid(unsigned(tiles_of(p.T, p.n) * cb), unsigned(FEW ? (by_tokens(p) ? p.T : p.n + 1) : 1));
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, cb);
     return hipGetLastError();
@@ -631,16 +673,16 @@ hipError_t run_expand(const LoraProblem& p, hipStream_t st) {
 
 hipError_t launch_lora_shrink(const LoraProblem& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  return p.T <= kFewTokens ? run_shrink<true>(p, st) : run_shrink<false>(p, st);
+  return few_tokens(p.T, p.n) ? run_shrink<true>(p, st) : run_shrink<false>(p, st);
 }
 
 hipError_t launch_lora_expand(const LoraProblem& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  if (p.T <= kFewTokens) return run_expand<true, false>(p, st);
+  if (few_tokens(p.T, p.n)) return run_expand<true, false>(p, st);
   return p.T * p.C * 2 > kL2Bytes ? run_expand<false, true>(p, st) : run_expand<false, false>(p, st);
 }
 
-hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& order, hipStream_t st) {
+hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, int which, hipStream_t st) {
   const int rb = rank_blocks_of(p.r), cb = int((p.C + 511) / 512);
   const int64_t Z = outer_ranges(p.T, p.C, p.r);
   const int64_t per = ((p.T + Z - 1) / Z + kOuterRows - 1) / kOuterRows * kOuterRows;
@@ -648,7 +690,7 @@ hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& order, hipSt
   if (p.T > 0) {
     const dim3 grid(unsigned(Z * cb * rb));
     const auto run = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, order.offsets, order.order, rb, cb, per);
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, o, which, rb, cb, per);
       return hipGetLastError();
     };
     e = p.r <= 16 ? run(lora_outer_kernel<1>) : p.r <= 32 ? run(lora_outer_kernel<2>) : run(lora_outer_kernel<4>);
@@ -656,7 +698,7 @@ hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& order, hipSt
   }
   const int64_t blocks = (int64_t(p.r) * p.C + 1023) / 1024;
   const unsigned each = unsigned(blocks < 1024 ? blocks : 1024);
-  hipLaunchKernelGGL(lora_sum_kernel, dim3(unsigned(p.n) * each), dim3(256), 0, st, p, order.offsets, per > 0 ? per : 1,
+  hipLaunchKernelGGL(lora_sum_kernel, dim3(unsigned(p.n) * each), dim3(256), 0, st, p, o.offsets, per > 0 ? per : 1,
                      each);
   return hipGetLastError();
 }
