@@ -84,7 +84,7 @@ fp8mm_status fp8mm_rms_norm_backward(const void* dy, int64_t ld_dy, const void* 
  * counted row (or +inf under softmax) makes the loss NaN.
  * E <= 1024 and k <= 64, else FP8MM_ENOTIMPL; T k < 2^31, S E < 2^31, S <= 2^20.
  * workspace: at least fp8mm_moe_balance_loss_workspace(T, E, S) bytes, 16-byte
- * aligned.
+ * aligned (NULL if that is 0, as for one sequence of a few tokens).
  * ------------------------------------------------------------------------- */
 int64_t fp8mm_moe_balance_loss_workspace(int64_t T, int64_t E, int64_t S);
 

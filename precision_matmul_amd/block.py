@@ -23,16 +23,21 @@ __all__ = [
 ]
 
 
+# The current device's number, without the checks around torch.cuda.current_device (0.14
+# against 0.26 us).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _call(name, t, *args):
     """The library's call on the current stream of t's device."""
-    fn = getattr(_lib.load(), name)
-    device = t.get_device()
-    if device == torch.cuda.current_device():
+    fn = getattr(_lib._lib or _lib.load(), name)
+    if t.get_device() == _current_device():
         st = fn(*args, _stream(t))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(t.get_device()):
             st = fn(*args, _stream(t))
-    _lib.check(st, name)
+    if st != _lib.OK:
+        _lib.check(st, name)
 
 
 def _need_like(t, x, name):
@@ -195,10 +200,10 @@ def moe_balance_loss_forward(logits, ids, score="softmax", coeff=1.0, ends=None)
     loss = logits.new_empty((), dtype=torch.float32)
     counts = logits.new_empty((S, E), dtype=torch.int32)
     tokens = logits.new_empty((S,), dtype=torch.int32)
-    workspace = logits.new_empty((max(size, 0),), dtype=torch.uint8)
+    workspace = logits.new_empty((size,), dtype=torch.uint8) if size > 0 else None
     _call("fp8mm_moe_balance_loss", logits, logits.data_ptr(), dtype, T, E, ld, ids.data_ptr(), ids.shape[1],
           _code(_lib.SCORES, score, "score"), _ptr(ends), S, coeff, loss.data_ptr(), counts.data_ptr(),
-          tokens.data_ptr(), workspace.data_ptr(), max(size, 0))
+          tokens.data_ptr(), _ptr(workspace), max(size, 0))
     return loss, counts, tokens
 
 

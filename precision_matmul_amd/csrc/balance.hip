@@ -27,13 +27,20 @@ namespace {
 
 using namespace ops;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 1024;           // of the forward: four waves a SIMD hide each other's chains
+constexpr int kBackThreads = 256;
 
 // exp(x) for x <= 0: exp2 corrected by the rounding of its argument; 0 below 2^-150.
 __device__ __forceinline__ float exp_down(float x) {
   const float t = x * 1.44269504f, e = __builtin_amdgcn_exp2f(t);
   const float rest = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;
   return x < -104.0f ? 0.0f : fmaf(e, rest * 0.693147182f, e);
+}
+
+// 1 / d of a normal d, within an ulp (d in [1, 2] here): the hardware's and one Newton step.
+__device__ __forceinline__ float reciprocal(float d) {
+  const float r = __builtin_amdgcn_rcpf(d);
+  return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
 // Four logits at column c of E; -inf past the end.
@@ -81,6 +88,14 @@ __device__ __forceinline__ float max_of(float v) {
   return fmaxf(v, __uint_as_float(row_ror<1>(__float_as_uint(v))));
 }
 
+// v + v of the lane 16 (32) away.
+__device__ __forceinline__ float add_rows(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // Probabilities from logits, in place; false for a row of -inf alone (padding),
 // whose probabilities are 0.  A NaN logit (+inf under softmax) makes all NaN.
 template <int L, int NQ, bool SIGMOID>
@@ -94,15 +109,20 @@ __device__ __forceinline__ bool probabilities(float (&f)[NQ][4]) {
   const bool used = m > -__builtin_inff();
   if (SIGMOID || !used) m = used ? fminf(m, 0.0f) : 0.0f;
   float total = 0.0f;
+  // where no row's factor exp(-m) is needed, the sigmoid has one exponential
+  const bool plain = SIGMOID && !__any(m < 0.0f);
 #pragma unroll
   for (int q = 0; q < NQ; ++q)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x = f[q][i];
-      if constexpr (SIGMOID)
-        f[q][i] = exp_down(x > 0.0f ? 0.0f : x - m) / (1.0f + exp_down(-fabsf(x)));
-      else
+      if constexpr (SIGMOID) {
+        const float e = exp_down(-fabsf(x));
+        const float top = x > 0.0f ? 1.0f : plain ? e : exp_down(x - m);
+        f[q][i] = top * reciprocal(1.0f + e);
+      } else {
         f[q][i] = exp_down(x - m);
+      }
       total += f[q][i];
     }
   total = sum_of<L>(total);
@@ -114,32 +134,25 @@ __device__ __forceinline__ bool probabilities(float (&f)[NQ][4]) {
   return used;
 }
 
-// The runs that chunk [r0, r1) of the tokens shares with the sequences: body(s, begin,
-// end) for each, in order; the first row behind the last of them comes back.
-template <typename Body>
-__device__ __forceinline__ int64_t each_run(const int32_t* ends, int S, int64_t T, int64_t r0, int64_t r1,
-                                            const Body& body) {
-  if (!ends) {
-    body(0, r0, r1);
-    return r1;
-  }
-  int lo = 0, hi = S;                    // the first sequence that ends past r0
+// The first sequence that ends past row r0, by every wave for itself; S if there is none.
+// `end` is the wave's lanes' end of the first 64 sequences: one load for few sequences,
+// in place of a chain of them.
+__device__ __forceinline__ int lane_end(const BalanceProblem& p) {
+  const int lane = threadIdx.x & 63;
+  return p.ends && lane < p.S ? p.ends[lane] : 0x7FFFFFFF;
+}
+__device__ __forceinline__ int sequence_of(const BalanceProblem& p, int end, int64_t r0) {
+  if (!p.ends) return 0;
+  if (p.S <= 64) return __popcll(__ballot(end <= r0));
+  int lo = 0, hi = p.S;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (ends[mid] > r0)
+    if (p.ends[mid] > r0)
       hi = mid;
     else
       lo = mid + 1;
   }
-  int64_t begin = r0;
-  for (int s = lo; s < S && begin < r1; ++s) {
-    const int64_t end = min(int64_t(ends[s]), r1);
-    if (end > begin) {
-      body(s, begin, end);
-      begin = end;
-    }
-  }
-  return begin;
+  return lo;
 }
 
 // Partial sums of a run: P [runs][E4] (sums of probabilities), C [runs][E4] (slots),
@@ -153,59 +166,6 @@ struct Partials {
   int64_t rows;                          // tokens of a chunk
 };
 
-template <typename T, int L, int NQ, bool SIGMOID>
-__global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem p, const Partials part) {
-  constexpr int SLOTS = kThreads / L;    // tokens at once
-  constexpr int COLS = NQ * 4 * L;
-  __shared__ float sums[SLOTS][COLS];
-  __shared__ int32_t counts[COLS], tokens;
-  const int lane = threadIdx.x % L, slot = threadIdx.x / L;
-  const int64_t b = blockIdx.x, r0 = b * part.rows, r1 = min(p.T, r0 + part.rows);
-  each_run(p.ends, p.S, p.T, r0, r1, [&](int s, int64_t begin, int64_t end) {
-    for (int c = threadIdx.x; c < COLS; c += kThreads) counts[c] = 0;
-    if (threadIdx.x == 0) tokens = 0;
-    __syncthreads();
-    float acc[NQ][4];
-    int mine = 0;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
-    for (int64_t row = begin + slot; row < end; row += SLOTS) {
-      const T* x = static_cast<const T*>(p.logits) + row * p.ld;
-      float f[NQ][4];
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) load4(x, (q * L + lane) * 4, p.E, f[q]);
-      if (!probabilities<L, NQ, SIGMOID>(f)) continue;
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[q][i] += f[q][i];
-      ++mine;
-      for (int j = lane; j < p.k; j += L) {
-        const int id = p.ids[row * p.k + j];
-        if (id >= 0 && id < p.E) atomicAdd(&counts[id], 1);       // whole numbers: any order
-      }
-    }
-    if (lane == 0 && mine) atomicAdd(&tokens, mine);
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sums[slot][(q * L + lane) * 4 + i] = acc[q][i];
-    __syncthreads();
-    const int64_t run = b + s;
-    for (int c = threadIdx.x; c < part.E4; c += kThreads) {
-      float v = 0.0f;
-#pragma unroll
-      for (int i = 0; i < SLOTS; ++i) v += sums[i][c];
-      part.P[run * part.E4 + c] = v;
-      part.C[run * part.E4 + c] = counts[c];
-    }
-    if (threadIdx.x == 0) part.n[run] = tokens;
-    __syncthreads();
-  });
-}
-
 // Sum over a workgroup of 1024 threads, in every thread, in a fixed order.
 __device__ __forceinline__ float block_sum(float v, float (&part)[16]) {
   v = wave_sum(v);
@@ -218,63 +178,209 @@ __device__ __forceinline__ float block_sum(float v, float (&part)[16]) {
   return v;
 }
 
-// A sequence's counts and loss from its runs' partial sums: four columns a thread, the
-// runs shared by 1024 / quads slices.
+// A sequence's loss from the sum over its experts of counts times sums.
+__device__ __forceinline__ float loss_of(const BalanceProblem& p, float term, int tokens) {
+  const float inv = 1.0f / float(max(tokens, 1));
+  return tokens ? term * inv * (p.coeff * float(p.E) / float(p.k)) * inv : 0.0f;
+}
+
+// The tokens in runs: their probabilities summed over the tokens of each run, their slots
+// counted.  L lanes hold a token; a token is loaded before it is known which run it is in.
+// ONE: the batch is one sequence of few tokens and one workgroup, which then gives the
+// loss itself.
+template <typename T, int L, int NQ, bool SIGMOID, bool ONE>
+__global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem p, const Partials part) {
+  constexpr int SLOTS = kThreads / L;    // tokens of a turn
+  constexpr int COLS = NQ * 4 * L, WAVES = kThreads / 64;
+  __shared__ float sums[WAVES][COLS];
+  __shared__ int32_t counts[COLS], tokens;
+  __shared__ float loss_part[16];
+  const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+  const int64_t b = blockIdx.x, r0 = b * part.rows, r1 = ONE ? p.T : min(p.T, r0 + part.rows);
+  float acc[NQ][4];
+  int mine = 0;
+  const auto clear = [&] {
+    for (int c = threadIdx.x; c < COLS; c += kThreads) counts[c] = 0;
+    if (threadIdx.x == 0) tokens = 0;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[q][i] = 0.0f;
+    mine = 0;
+    __syncthreads();
+  };
+  // a run's sums: partial row b + s, or (ONE) the loss
+  const auto finish = [&](int64_t run) {
+    if (lane == 0 && mine) atomicAdd(&tokens, mine);
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v = acc[q][i];
+        if constexpr (L == 16) v = add_rows(v);          // the wave's four tokens
+        if (L == 64 || (threadIdx.x & 48) == 0) sums[threadIdx.x >> 6][(q * L + lane) * 4 + i] = v;
+      }
+    __syncthreads();
+    float term = 0.0f;
+    if (threadIdx.x < part.E4) {         // at most 1024 columns
+      const int c = threadIdx.x;
+      float v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) v += sums[i][c];
+      if constexpr (ONE) {
+        if (c < p.E) {
+          p.counts[c] = counts[c];
+          term = float(counts[c]) * v;
+        }
+      } else {
+        part.P[run * part.E4 + c] = v;
+        part.C[run * part.E4 + c] = counts[c];
+      }
+    }
+    if constexpr (ONE) term = block_sum(term, loss_part);
+    if (threadIdx.x == 0) {
+      if constexpr (ONE) {
+        p.tokens[0] = tokens;
+        *p.loss = loss_of(p, term, tokens);
+      } else {
+        part.n[run] = tokens;
+      }
+    }
+    __syncthreads();
+  };
+  const auto end_of = [&](int s) { return p.ends ? min(int64_t(p.ends[s]), r1) : r1; };
+  float raw[NQ][4];                      // the next turn's logits and first ids
+  int raw_id = -1;
+  const auto ask = [&](int64_t row) {
+    raw_id = -1;
+    if (row < r1) {
+      const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) load4(x, (q * L + lane) * 4, p.E, raw[q]);
+      if (lane < p.k) raw_id = p.ids[row * p.k + lane];
+    } else {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[q][i] = -__builtin_inff();
+    }
+  };
+  const int my_end = lane_end(p);
+  ask(r0 + slot);
+  clear();
+  int s = ONE ? 0 : sequence_of(p, my_end, r0);
+  int64_t begin = r0, end = s < p.S ? end_of(s) : r0;    // the rest of this run
+  for (int64_t turn = r0; turn < r1; turn += SLOTS) {
+    const int64_t row = turn + slot, next = min(turn + SLOTS, r1);
+    float f[NQ][4];
+    const int id0 = raw_id;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[q][i] = raw[q][i];
+    if (next < r1) ask(next + slot);
+    const bool used = probabilities<L, NQ, SIGMOID>(f);
+    while (s < p.S) {
+      if (used && row >= begin && row < end) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[q][i] += f[q][i];
+        ++mine;
+        if (id0 >= 0 && id0 < p.E) atomicAdd(&counts[id0], 1);        // whole numbers: any order
+        for (int j = lane + L; j < p.k; j += L) {
+          const int id = p.ids[row * p.k + j];
+          if (id >= 0 && id < p.E) atomicAdd(&counts[id], 1);
+        }
+      }
+      if (ONE || end > next) break;      // goes on in the next turn
+      finish(b + s);
+      begin = end;
+      do {
+        ++s;
+        end = s < p.S ? end_of(s) : r1;
+      } while (s < p.S && end <= begin);
+      if (s < p.S) clear();
+      if (begin >= next) break;          // the next run starts with the next turn
+    }
+    if (s >= p.S) return;                // rows behind the last sequence
+  }
+  if constexpr (ONE) finish(0);
+}
+
+// A sequence's counts and loss from its runs' partial sums.  A wave's lanes hold four
+// columns each (QL = 1: up to 256 columns, several runs at once where there are fewer;
+// else four times four), the 16 waves take the runs in turns.
+template <int QL>
 __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceProblem p, const Partials part, int quads) {
-  __shared__ float4 sums[1024];
-  __shared__ int4 slots[1024];
-  __shared__ float sum_part[16];
-  const int s = blockIdx.x;
+  __shared__ float4 sums[16][QL * 64];
+  __shared__ int4 slots[16][QL * 64];
+  __shared__ int32_t tokens[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, s = blockIdx.x;
+  const int groups = 64 / quads, q = lane % quads, group = lane / quads;
+  float4 v[QL];
+  int4 c[QL];
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < QL; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c[i] = make_int4(0, 0, 0, 0);
   int64_t begin = s && p.ends ? p.ends[s - 1] : 0, end = p.ends ? p.ends[s] : p.T;
   begin = max(begin, int64_t(0));
   end = min(end, p.T);
   // runs [first, last) of the partial rows
-  const int64_t first = begin / part.rows + s, last = end > begin ? (end - 1) / part.rows + s + 1 : first;
-  const int q = threadIdx.x % quads, slice = threadIdx.x / quads, slices = 1024 / quads;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  int4 c = make_int4(0, 0, 0, 0);
-  if (q * 4 < part.E4) {
+  const int first = int(begin / part.rows) + s, last = end > begin ? int((end - 1) / part.rows) + s + 1 : first;
 #pragma unroll 4
-    for (int64_t run = first + slice; run < last; run += slices) {
-      const float4 a = *reinterpret_cast<const float4*>(part.P + run * part.E4 + q * 4);
-      const int4 d = *reinterpret_cast<const int4*>(part.C + run * part.E4 + q * 4);
-      v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
-      c.x += d.x, c.y += d.y, c.z += d.z, c.w += d.w;
+  for (int run = first + wave * groups + group; run < last; run += 16 * groups) {
+#pragma unroll
+    for (int i = 0; i < QL; ++i) {
+      const int at = (i * 64 + q) * 4;
+      if (at >= part.E4) continue;
+      const float4 a = *reinterpret_cast<const float4*>(part.P + int64_t(run) * part.E4 + at);
+      const int4 d = *reinterpret_cast<const int4*>(part.C + int64_t(run) * part.E4 + at);
+      v[i].x += a.x, v[i].y += a.y, v[i].z += a.z, v[i].w += a.w;
+      c[i].x += d.x, c[i].y += d.y, c[i].z += d.z, c[i].w += d.w;
     }
+    if (q == 0) n += part.n[run];
   }
-  sums[threadIdx.x] = v;
-  slots[threadIdx.x] = c;
-  int n = 0;
-  for (int64_t run = first + threadIdx.x; run < last; run += 1024) n += part.n[run];
+  for (int off = quads; off < 64; off <<= 1) {   // the lanes' groups (QL = 1)
+    v[0].x += __shfl_xor(v[0].x, off, 64), v[0].y += __shfl_xor(v[0].y, off, 64);
+    v[0].z += __shfl_xor(v[0].z, off, 64), v[0].w += __shfl_xor(v[0].w, off, 64);
+    c[0].x += __shfl_xor(c[0].x, off, 64), c[0].y += __shfl_xor(c[0].y, off, 64);
+    c[0].z += __shfl_xor(c[0].z, off, 64), c[0].w += __shfl_xor(c[0].w, off, 64);
+    n += __shfl_xor(n, off, 64);
+  }
+#pragma unroll
+  for (int i = 0; i < QL; ++i) sums[wave][i * 64 + lane] = v[i], slots[wave][i * 64 + lane] = c[i];
+  if (lane == 0) tokens[wave] = n;
   __syncthreads();
+  if (wave != 0) return;
   float term = 0.0f;
-  if (threadIdx.x < part.E4) {
-    const int at = threadIdx.x / 4, i = threadIdx.x % 4;
-    float P = 0.0f;
-    int C = 0;
-    for (int k = 0; k < slices; ++k) {
-      P += reinterpret_cast<const float*>(&sums[k * quads + at])[i];
-      C += reinterpret_cast<const int*>(&slots[k * quads + at])[i];
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) n += tokens[w];
+#pragma unroll
+  for (int i = 0; i < QL; ++i) {
+    const int at = (i * 64 + q) * 4;
+    if (group != 0 || at >= p.E) continue;
+    float P[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int C[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      const float4 a = sums[w][i * 64 + lane];
+      const int4 d = slots[w][i * 64 + lane];
+      P[0] += a.x, P[1] += a.y, P[2] += a.z, P[3] += a.w;
+      C[0] += d.x, C[1] += d.y, C[2] += d.z, C[3] += d.w;
     }
-    if (threadIdx.x < unsigned(p.E)) {
-      p.counts[int64_t(s) * p.E + threadIdx.x] = C;
-      term = float(C) * P;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (at + e >= p.E) continue;
+      p.counts[int64_t(s) * p.E + at + e] = C[e];
+      term = fmaf(float(C[e]), P[e], term);
     }
   }
-  term = block_sum(term, sum_part);
-  __shared__ int32_t total;
-  if (threadIdx.x == 0) total = 0;
-  __syncthreads();
-  if (n) atomicAdd(&total, n);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    p.tokens[s] = total;
-    const float inv = 1.0f / float(max(total, 1));
-    const float loss = total ? term * inv * (p.coeff * float(p.E) / float(p.k)) * inv : 0.0f;
-    if (p.S == 1)
-      *p.loss = loss;
-    else
-      part.losses[s] = loss;
+  term = wave_sum(term);
+  if (lane == 0) {
+    p.tokens[s] = n;
+    *(p.S == 1 ? p.loss : part.losses + s) = loss_of(p, term, n);
   }
 }
 
@@ -296,17 +402,21 @@ __global__ __launch_bounds__(1024) void balance_mean_kernel(const BalanceProblem
 }
 
 template <typename T, int L, int NQ, bool SIGMOID>
-__global__ __launch_bounds__(kThreads) void balance_backward_kernel(const BalanceProblem p, int64_t rows) {
-  constexpr int SLOTS = kThreads / L;
+__global__ __launch_bounds__(kBackThreads) void balance_backward_kernel(const BalanceProblem p, int64_t rows) {
+  constexpr int SLOTS = kBackThreads / L;
   const int lane = threadIdx.x % L, slot = threadIdx.x / L;
   const int64_t r0 = int64_t(blockIdx.x) * rows, r1 = min(p.T, r0 + rows);
+  const int my_end = lane_end(p);
   int alive = 0;                         // sequences with tokens, counted by every wave for itself
   for (int s = 0; s < p.S; s += 64) {
     const int at = s + int(threadIdx.x & 63);
     alive += __popcll(__ballot(at < p.S && p.tokens[min(at, p.S - 1)] > 0));
   }
   const float whole = *p.grad_loss * p.coeff * float(p.E) / (float(p.k) * float(max(alive, 1)));
-  const int64_t done = each_run(p.ends, p.S, p.T, r0, r1, [&](int s, int64_t begin, int64_t end) {
+  int64_t begin = r0;
+  for (int s = sequence_of(p, my_end, r0); s < p.S && begin < r1; ++s) {
+    const int64_t end = p.ends ? min(int64_t(p.ends[s]), r1) : r1;
+    if (end <= begin) continue;
     int c[NQ][4];
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
@@ -326,7 +436,10 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Balanc
         if constexpr (SIGMOID) {         // 1 - sigmoid(x)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            u[q][i] = exp_down(fminf(-f[q][i], 0.0f)) / (1.0f + exp_down(-fabsf(f[q][i])));
+            {
+            const float e = exp_down(-fabsf(f[q][i]));
+            u[q][i] = (f[q][i] > 0.0f ? e : 1.0f) * reciprocal(1.0f + e);
+          }
         }
       }
       const bool used = probabilities<L, NQ, SIGMOID>(f);
@@ -360,9 +473,10 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Balanc
         store4(static_cast<T*>(p.grad_logits) + row * p.ld_grad, (q * L + lane) * 4, p.E, g);
       }
     }
-  });
+    begin = end;
+  }
   const float zeros[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t row = done + slot; row < r1; row += SLOTS)
+  for (int64_t row = begin + slot; row < r1; row += SLOTS)   // rows behind the last sequence
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
       store4(static_cast<T*>(p.grad_logits) + row * p.ld_grad, (q * L + lane) * 4, p.E, zeros);
@@ -371,9 +485,11 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Balanc
 // Tokens of a chunk of the forward: at most 256 chunks, each a few turns.
 int64_t chunk_rows(int64_t T) { return T > 256 * 64 ? (T + 255) / 256 : 64; }
 int64_t chunks(int64_t T) { return T ? (T + chunk_rows(T) - 1) / chunk_rows(T) : 0; }
+// One sequence of so few tokens that one workgroup does it all, without a workspace.
+bool one_group(int64_t T, int64_t S) { return S == 1 && T > 0 && T <= 256; }
 int padded(int64_t E) { return int((E + 3) / 4 * 4); }
 
-constexpr int64_t kBackwardRows = 64;    // tokens of a workgroup of the backward at least
+constexpr int64_t kBackwardRows = 32;    // tokens of a workgroup of the backward at least
 
 template <typename Run>
 hipError_t by_experts(int E, const Run& run) {
@@ -387,8 +503,12 @@ hipError_t by_experts(int E, const Run& run) {
 template <typename T, bool SIGMOID>
 hipError_t forward_typed(const BalanceProblem& p, const Partials& part, hipStream_t st) {
   return by_experts(p.E, [&](auto L, auto NQ) {
-    hipLaunchKernelGGL((balance_kernel<T, decltype(L)::value, decltype(NQ)::value, SIGMOID>),
-                       dim3(unsigned(chunks(p.T))), dim3(kThreads), 0, st, p, part);
+    constexpr int l = decltype(L)::value, nq = decltype(NQ)::value;
+    if (one_group(p.T, p.S))
+      hipLaunchKernelGGL((balance_kernel<T, l, nq, SIGMOID, true>), dim3(1), dim3(kThreads), 0, st, p, part);
+    else
+      hipLaunchKernelGGL((balance_kernel<T, l, nq, SIGMOID, false>), dim3(unsigned(chunks(p.T))), dim3(kThreads), 0, st,
+                         p, part);
     return hipGetLastError();
   });
 }
@@ -398,7 +518,7 @@ hipError_t backward_typed(const BalanceProblem& p, hipStream_t st) {
   const int64_t rows = p.T > kBackwardRows << 20 ? (p.T + (1 << 20) - 1) >> 20 : kBackwardRows;
   return by_experts(p.E, [&](auto L, auto NQ) {
     hipLaunchKernelGGL((balance_backward_kernel<T, decltype(L)::value, decltype(NQ)::value, SIGMOID>),
-                       dim3(unsigned((p.T + rows - 1) / rows)), dim3(kThreads), 0, st, p, rows);
+                       dim3(unsigned((p.T + rows - 1) / rows)), dim3(kBackThreads), 0, st, p, rows);
     return hipGetLastError();
   });
 }
@@ -418,6 +538,7 @@ Partials layout(const BalanceProblem& p) {
 }  // namespace
 
 int64_t balance_workspace(int64_t T, int64_t E, int64_t S) {
+  if (one_group(T, S)) return 0;
   const int64_t runs = chunks(T) + S;
   return 4 * (2 * runs * padded(E) + runs + S);
 }
@@ -430,11 +551,14 @@ hipError_t launch_balance(const BalanceProblem& p, hipStream_t st) {
       e = p.sigmoid ? forward_typed<float, true>(p, part, st) : forward_typed<float, false>(p, part, st);
     else
       e = p.sigmoid ? forward_typed<uint16_t, true>(p, part, st) : forward_typed<uint16_t, false>(p, part, st);
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || one_group(p.T, p.S)) return e;
   }
   int quads = 1;
-  while (quads * 4 < part.E4) quads *= 2;
-  hipLaunchKernelGGL(balance_sum_kernel, dim3(unsigned(p.S)), dim3(1024), 0, st, p, part, quads);
+  while (quads < 64 && quads * 4 < part.E4) quads *= 2;
+  if (p.E <= 256)
+    hipLaunchKernelGGL((balance_sum_kernel<1>), dim3(unsigned(p.S)), dim3(1024), 0, st, p, part, quads);
+  else
+    hipLaunchKernelGGL((balance_sum_kernel<4>), dim3(unsigned(p.S)), dim3(1024), 0, st, p, part, quads);
   e = hipGetLastError();
   if (e != hipSuccess || p.S == 1) return e;
   hipLaunchKernelGGL(balance_mean_kernel, dim3(1), dim3(1024), 0, st, p, part.losses);

@@ -333,13 +333,15 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
   };
   if (p.base) ask(0);
   for (int i = 0; i < m.rows; i += 16) {
-    Chunk base[4];
+    f32x4 acc[8];                        // sums start from base
 #pragma unroll
-    for (int k = 0; k < 4; ++k) base[k] = p.base ? next[k] : Chunk{{0u, 0u, 0u, 0u}};
+    for (int k = 0; k < 4; ++k) {
+      float f[8];
+      unpack<uint16_t>(p.base ? next[k] : Chunk{{0u, 0u, 0u, 0u}}, f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q][k] = f[q];
+    }
     if (p.base && i + 16 < m.rows) ask(i + 16);
-    f32x4 acc[8];
-#pragma unroll
-    for (int f = 0; f < 8; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const auto step = [&](int ks, const bf16x8 (&bf)[8]) {
       const int at = (i + l15) * ld + ks * 32 + g * 8;
       const bf16x8 l = *reinterpret_cast<const bf16x8*>(lo + at), h = *reinterpret_cast<const bf16x8*>(hi + at);
@@ -361,10 +363,9 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
     for (int k = 0; k < 4; ++k) {
       const int at = i + g * 4 + k;
       const int64_t row = m.at(at);
-      float f[8], y[8];
-      unpack<uint16_t>(base[k], f);
+      float y[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) y[q] = acc[q][k] + f[q];
+      for (int q = 0; q < 8; ++q) y[q] = acc[q][k];
       if (at < m.rows) store_row<uint16_t, NT>(p.out + row * p.ld_out, c, p.C, pack<uint16_t>(y));
     }
   }

@@ -130,6 +130,8 @@ def test_queries(lib):
     assert lib.fp8mm_rms_norm_backward_workspace(-1, 64) == -1
     assert 0 < lib.fp8mm_rms_norm_backward_workspace(2 ** 30, 64) <= 4096 * 64 * 4     # bounded in the rows
     assert lib.fp8mm_moe_balance_loss_workspace(16384, 64, 1) > 0
+    assert lib.fp8mm_moe_balance_loss_workspace(16, 64, 1) == 0         # one workgroup
+    assert 0 < lib.fp8mm_moe_balance_loss_workspace(16, 64, 2)
     assert 0 < lib.fp8mm_moe_balance_loss_workspace(0, 64, 1)
     assert lib.fp8mm_moe_balance_loss_workspace(16, 64, 0) == -1
     assert lib.fp8mm_moe_balance_loss_workspace(2 ** 31 - 1, 64, 1) < 1 << 20          # bounded in the tokens
