@@ -40,6 +40,36 @@ def _call(name, t, *args):
         _lib.check(st, name)
 
 
+# The checks below first ask whether all is well, in a few attribute reads, and look for
+# what is wrong only if not: the calls for a few tokens take the host longer than the
+# GPU, and 2 to 3 of their 10 to 13 us were checks.
+
+def _dense(t, dtype, shape, device, name):
+    """t is a dense tensor of this type, shape and device number."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need_dense(t, dtype, shape, device, name)
+
+
+_CODES = {torch.bfloat16: _lib.OUT_BF16, torch.float32: _lib.OUT_FP32}
+
+
+def _matrix(t, name):
+    """(type code, row stride, device number) of a bf16 or float32 matrix."""
+    try:
+        device, code = t.get_device(), _CODES[t.dtype]
+        R, C = t.shape
+        row, column = t.stride()
+        if device >= 0 and (column == 1 or C <= 1):
+            return code, (row if R > 1 else C), device
+    except (AttributeError, KeyError, ValueError):
+        pass
+    return _need_float(t, name), _rows(t, name), t.get_device()
+
+
 def _need_like(t, x, name):
     """Row stride of a matrix of x's type, shape and device."""
     if not isinstance(t, torch.Tensor) or t.dtype != x.dtype or t.shape != x.shape or t.get_device() != x.get_device():
@@ -53,6 +83,11 @@ def _weight(x, weight):
     """Type code of the weight vector."""
     if weight is None:
         return _lib.OUT_FP32
+    try:
+        if weight.shape == x.shape[1:] and weight.get_device() == x.get_device() and weight.is_contiguous():
+            return _CODES[weight.dtype]
+    except (AttributeError, KeyError):
+        pass
     code = _need_float(weight, "weight")
     if weight.shape != x.shape[1:] or not weight.is_contiguous() or weight.get_device() != x.get_device():
         raise ValueError(f"weight must be a contiguous [{x.shape[1]}] tensor on {x.device}, got {list(weight.shape)}")
@@ -60,8 +95,7 @@ def _weight(x, weight):
 
 
 def _rms(x, weight, residual, eps, recipe, want_y):
-    dtype = _need_float(x, "x")
-    ld = _rows(x, "x")
+    dtype, ld, _ = _matrix(x, "x")
     params = _weight(x, weight)
     R, C = x.shape
     h, ld_res = x, 0
@@ -106,12 +140,12 @@ def rms_norm_backward(dy, h, weight, rstd, grad_h=None, need_dx=True, need_weigh
     gradient of x and of the residual; grad_h, the gradient that arrives at h from
     behind, is added to it.  dweight has the weight's type (param_dtype, or float32,
     where there is no weight); None where not needed."""
-    dtype = _need_float(h, "h")
-    ld_h, ld_dy = _rows(h, "h"), _need_like(dy, h, "dy")
+    dtype, ld_h, device = _matrix(h, "h")
+    ld_dy = _need_like(dy, h, "dy")
     ld_gh = 0 if grad_h is None else _need_like(grad_h, h, "grad_h")
     R, C = h.shape
     params = _weight(h, weight)
-    _need_dense(rstd, torch.float32, (R,), h.get_device(), "rstd")
+    _dense(rstd, torch.float32, (R,), device, "rstd")
     if weight is None:
         param_dtype = torch.float32 if param_dtype is None else param_dtype
         params = _out_code(param_dtype)
@@ -189,17 +223,16 @@ def moe_balance_loss_forward(logits, ids, score="softmax", coeff=1.0, ends=None)
     count.  With p = softmax(logits), or the sigmoids divided by their sum, and n the
     tokens of a sequence, its loss is coeff sum_e (E counts_e / (k n)) (sum_t p_te /
     n); loss is the mean over the sequences that have tokens."""
-    dtype = _need_float(logits, "logits")
-    ld = _rows(logits, "logits")
+    dtype, ld, device = _matrix(logits, "logits")
     T, E = logits.shape
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError(f"ids must be an int32 [{T}, k] tensor")
-    _need_dense(ids, torch.int32, (T, ids.shape[1]), logits.get_device(), "ids")
+    _dense(ids, torch.int32, (T, ids.shape[1]), device, "ids")
     S = _sequences(ends, logits)
     size = _lib.load().fp8mm_moe_balance_loss_workspace(T, E, S)
     loss = logits.new_empty((), dtype=torch.float32)
-    counts = logits.new_empty((S, E), dtype=torch.int32)
-    tokens = logits.new_empty((S,), dtype=torch.int32)
+    counts = ids.new_empty((S, E))
+    tokens = ids.new_empty((S,))
     workspace = logits.new_empty((size,), dtype=torch.uint8) if size > 0 else None
     _call("fp8mm_moe_balance_loss", logits, logits.data_ptr(), dtype, T, E, ld, ids.data_ptr(), ids.shape[1],
           _code(_lib.SCORES, score, "score"), _ptr(ends), S, coeff, loss.data_ptr(), counts.data_ptr(),
@@ -211,16 +244,14 @@ def moe_balance_loss_backward(grad_loss, logits, counts, tokens, k, score="softm
     """Gradient of the logits (their type and shape) from the gradient of
     moe_balance_loss_forward's loss (float32 []), its counts and tokens; k: slots of a
     token.  Zeros in rows of no sequence and in padding."""
-    dtype = _need_float(logits, "logits")
-    ld = _rows(logits, "logits")
+    dtype, ld, device = _matrix(logits, "logits")
     T, E = logits.shape
     S = _sequences(ends, logits)
-    device = logits.get_device()
     _need(grad_loss, torch.float32, "grad_loss")
     if grad_loss.numel() != 1 or grad_loss.get_device() != device:
         raise ValueError("grad_loss must be one float32 number on the logits' device")
-    _need_dense(counts, torch.int32, (S, E), device, "counts")
-    _need_dense(tokens, torch.int32, (S,), device, "tokens")
+    _dense(counts, torch.int32, (S, E), device, "counts")
+    _dense(tokens, torch.int32, (S,), device, "tokens")
     grad = _like(logits)
     _call("fp8mm_moe_balance_loss_backward", logits, grad_loss.data_ptr(), logits.data_ptr(), dtype, T, E, ld,
           counts.data_ptr(), tokens.data_ptr(), k, _code(_lib.SCORES, score, "score"), _ptr(ends), S, coeff,
@@ -255,23 +286,27 @@ def moe_balance_loss(logits, ids, score="softmax", coeff=1.0, ends=None):
 
 # -------------------------------------------------------------------- adapters
 
-def _need_panels(x, down, up, ids, scales):
-    """(T, K, n, r, N) of an adapter call; x is a row matrix of T rows (K is taken
-    from the panels)."""
-    device = x.get_device()
-    for t, name in ((down, "down"), (up, "up")):
-        _need(t, torch.bfloat16, name)
-        if t.dim() != 3 or not t.is_contiguous() or t.get_device() != device:
-            raise ValueError(f"{name} must be a contiguous [adapters, rank, columns] tensor on {x.device}")
-    if down.shape[:2] != up.shape[:2]:
-        raise ValueError(f"down and up must have the same adapters and rank, got {list(down.shape)} and "
-                         f"{list(up.shape)}")
-    n, r, K = down.shape
-    T = x.shape[0]
-    _need_dense(ids, torch.int32, (T,), device, "ids")
+def _panels(down, up, T, ids, scales, device):
+    """(K, n, r, N) of an adapter call for T tokens on a device."""
+    try:
+        n, r, K = down.shape
+        N = up.shape[2]
+    except (AttributeError, ValueError, IndexError):
+        raise ValueError("down and up must be [adapters, rank, columns] tensors") from None
+    _dense(down, torch.bfloat16, (n, r, K), device, "down")
+    _dense(up, torch.bfloat16, (n, r, N), device, "up")
+    _dense(ids, torch.int32, (T,), device, "ids")
     if scales is not None:
-        _need_dense(scales, torch.float32, (n,), device, "scales")
-    return T, K, n, r, up.shape[2]
+        _dense(scales, torch.float32, (n,), device, "scales")
+    return K, n, r, N
+
+
+def _bf16_matrix(t, T, C, device, name):
+    """Row stride of a bf16 matrix [T, C]."""
+    code, ld, own = _matrix(t, name)
+    if code != _lib.OUT_BF16 or t.shape != (T, C) or own != device:
+        raise ValueError(f"{name} must be a bf16 [{T}, {C}] tensor on device {device}, got {t.dtype} {list(t.shape)}")
+    return ld
 
 
 def lora_forward(x, down, up, ids, scales=None, base=None, out=None):
@@ -280,24 +315,15 @@ def lora_forward(x, down, up, ids, scales=None, base=None, out=None):
     = ids[t], and base[t] where ids[t] is outside [0, n).  scales: float32 [n], 1
     without; base: bf16 [T, N], 0 without; out may be base itself.  v: float32
     [splits, T, r], the inner products in partial sums, which lora_backward takes."""
-    _need(x, torch.bfloat16, "x")
-    ld = _rows(x, "x")
-    T, K, n, r, N = _need_panels(x, down, up, ids, scales)
-    if x.shape[1] != K:
-        raise ValueError(f"x has {x.shape[1]} columns, down {K}")
-    ld_base = 0
-    if base is not None:
-        _need(base, torch.bfloat16, "base")
-        if base.shape != (T, N) or base.get_device() != x.get_device():
-            raise ValueError(f"base must be a [{T}, {N}] tensor on {x.device}")
-        ld_base = _rows(base, "base")
+    device = _matrix(x, "x")[2]
+    T = x.shape[0]
+    K, n, r, N = _panels(down, up, T, ids, scales, device)
+    ld = _bf16_matrix(x, T, K, device, "x")
+    ld_base = 0 if base is None else _bf16_matrix(base, T, N, device, "base")
     if out is None:
         out, ld_out = x.new_empty((T, N)), N
     else:
-        _need(out, torch.bfloat16, "out")
-        if out.shape != (T, N) or out.get_device() != x.get_device():
-            raise ValueError(f"out must be a [{T}, {N}] tensor on {x.device}")
-        ld_out = _rows(out, "out")
+        ld_out = _bf16_matrix(out, T, N, device, "out")
     v = x.new_empty((max(_lib.load().fp8mm_lora_splits(T, K, n, r), 1), T, r), dtype=torch.float32)
     _call("fp8mm_lora", x, x.data_ptr(), ld, T, K, down.data_ptr(), up.data_ptr(), n, r, N, ids.data_ptr(),
           _ptr(scales), _ptr(base), ld_base, out.data_ptr(), ld_out, v.data_ptr())
@@ -309,23 +335,19 @@ def lora_backward(dy, x, v, down, up, ids, scales=None, need_dx=True, need_down=
     needed.  dx: bf16 [T, K] (base's gradient is dy itself); ddown [n, r, K] and dup
     [n, r, N] have the panels' type, or out_dtype (bf16 or float32).  x may be None
     without need_down, v without need_up."""
-    _need(dy, torch.bfloat16, "dy")
-    ld_dy = _rows(dy, "dy")
-    T, K, n, r, N = _need_panels(dy, down, up, ids, scales)
-    if dy.shape[1] != N:
-        raise ValueError(f"dy has {dy.shape[1]} columns, up {N}")
+    device = _matrix(dy, "dy")[2]
+    T = dy.shape[0]
+    K, n, r, N = _panels(down, up, T, ids, scales, device)
+    ld_dy = _bf16_matrix(dy, T, N, device, "dy")
     lib = _lib.load()
     ld = 0
     if x is not None:
-        _need(x, torch.bfloat16, "x")
-        if x.shape != (T, K) or x.get_device() != dy.get_device():
-            raise ValueError(f"x must be a [{T}, {K}] tensor on {dy.device}")
-        ld = _rows(x, "x")
+        ld = _bf16_matrix(x, T, K, device, "x")
     elif need_down:
         raise ValueError("x is needed for the gradient of down")
     if v is not None:
         splits = max(lib.fp8mm_lora_splits(T, K, n, r), 1)
-        _need_dense(v, torch.float32, (splits, T, r), dy.get_device(), "v")
+        _dense(v, torch.float32, (splits, T, r), device, "v")
     elif need_up:
         raise ValueError("v is needed for the gradient of up")
     out_dtype = down.dtype if out_dtype is None else out_dtype
