@@ -88,9 +88,8 @@ fp8mm_status check_lora(int64_t T, int64_t K, int64_t n, int64_t r, int64_t N, c
 int64_t dv_bytes(int64_t T, int64_t N, int64_t n, int64_t r) {
   return (4 * fp8mm::lora_splits(T, N, n, int(r)) * T * r + 15) / 16 * 16;
 }
-int64_t partial_bytes(int64_t T, int64_t K, int64_t N, int64_t n, int64_t r) {
-  const int64_t a = fp8mm::lora_outer_workspace(T, K, n, int(r)), b = fp8mm::lora_outer_workspace(T, N, n, int(r));
-  return ((a > b ? a : b) + 15) / 16 * 16;
+int64_t partial_bytes(int64_t T, int64_t C, int64_t n, int64_t r) {
+  return (fp8mm::lora_outer_workspace(T, C, n, int(r)) + 15) / 16 * 16;
 }
 
 }  // namespace
@@ -317,7 +316,8 @@ fp8mm_status fp8mm_lora(const void* x, int64_t ld_x, int64_t T, int64_t K, const
 int64_t fp8mm_lora_backward_workspace(int64_t T, int64_t K, int64_t N, int64_t n, int64_t r) {
   if (!lora_shape(T, n, r) || !lora_columns(K) || !lora_columns(N)) return -1;
   if (n > fp8mm::kLoraMaxAdapters) return dv_bytes(T, N, n, r);
-  return dv_bytes(T, N, n, r) + partial_bytes(T, K, N, n, r) + fp8mm::lora_order_workspace(T, n, int(r));
+  return dv_bytes(T, N, n, r) + partial_bytes(T, N, n, r) + partial_bytes(T, K, n, r) +
+         fp8mm::lora_order_workspace(T, n, int(r));
 }
 
 fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t T, int64_t K,
@@ -354,7 +354,10 @@ fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, i
   p.scales = scales;
   p.grad_fp32 = grad_dtype == FP8MM_OUT_FP32;
   char* at = static_cast<char*>(workspace) + dv_bytes(T, N, n, r);
-  p.partial = reinterpret_cast<float*>(at);
+  const fp8mm::LoraSide sides[2] = {
+      {static_cast<const uint16_t*>(dy), ld_dy, N, dup, reinterpret_cast<float*>(at)},
+      {static_cast<const uint16_t*>(x), ld_x, K, ddown, reinterpret_cast<float*>(at + partial_bytes(T, N, n, r))}};
+  at += partial_bytes(T, N, n, r) + partial_bytes(T, K, n, r);
   hipError_t e = hipSuccess;
   if (dx || ddown) {
     fp8mm::LoraProblem q = p;
@@ -371,25 +374,12 @@ fp8mm_status fp8mm_lora_backward(const void* dy, int64_t ld_dy, const void* x, i
   o.splits[0] = fp8mm::lora_splits(T, K, n, int(r));
   o.v[1] = ddown ? dv : nullptr;
   o.splits[1] = dv_splits;
-  if (e == hipSuccess && (ddown || dup))
-    e = fp8mm::launch_lora_order(p, at + partial_bytes(T, K, N, n, r), o, stream);
-  if (e == hipSuccess && dup) {
-    fp8mm::LoraProblem q = p;
-    q.C = N;
-    q.x = static_cast<const uint16_t*>(dy);
-    q.ld_x = ld_dy;
-    q.grad = dup;
-    e = fp8mm::launch_lora_outer(q, o, 0, stream);
-  }
-  p.C = K;
-  if (e == hipSuccess && ddown) {
-    fp8mm::LoraProblem q = p;
-    q.x = static_cast<const uint16_t*>(x);
-    q.ld_x = ld_x;
-    q.grad = ddown;
-    e = fp8mm::launch_lora_outer(q, o, 1, stream);
+  if (e == hipSuccess && (ddown || dup)) {
+    e = fp8mm::launch_lora_order(p, at, o, stream);
+    if (e == hipSuccess) e = fp8mm::launch_lora_outer(p, o, sides, stream);
   }
   if (e == hipSuccess && dx) {
+    p.C = K;
     p.v = dv;
     p.splits = dv_splits;
     p.panels = static_cast<const uint16_t*>(down);

@@ -81,9 +81,15 @@ struct LoraProblem {
   int64_t ld_base;
   uint16_t* out;           // expand: [T, C]
   int64_t ld_out;
-  void* grad;              // outer: [n, r, C]
-  bool grad_fp32;
-  float* partial;          // outer: lora_outer_workspace bytes
+  bool grad_fp32;          // outer
+};
+
+// One panel's gradient.
+struct LoraSide {
+  const uint16_t* x;       // [T, C], row stride ld_x
+  int64_t ld_x, C;
+  void* grad;              // [n, r, C], or null: not wanted
+  float* partial;          // lora_outer_workspace bytes
 };
 
 // Tokens in adapter order, for the gradients: offsets [n], the adapters' cumulative end
@@ -107,7 +113,7 @@ hipError_t launch_lora_expand(const LoraProblem& p, hipStream_t st);
 int64_t lora_order_workspace(int64_t T, int64_t n, int r);              // bytes
 // o.v and o.splits are the caller's, the rest is filled in
 hipError_t launch_lora_order(const LoraProblem& p, void* workspace, LoraOrder& o, hipStream_t st);
-// with the `which`-th v of o
-hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, int which, hipStream_t st);
+// side i with the i-th v of o
+hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, const LoraSide (&side)[2], hipStream_t st);
 
 }  // namespace fp8mm

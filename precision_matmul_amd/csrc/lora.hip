@@ -220,7 +220,7 @@ __device__ __forceinline__ void shrink_tile(const LoraProblem& p, int a, const M
 template <int RF, bool FEW>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraProblem p, int rank_blocks) {
   // sums of 32 members of all waves, or of 64 members of two or four
-  constexpr int SUMS = FEW ? 4 * 2 : (RF == 4 ? 2 * 4 : 4 * 4);
+  constexpr int SUMS = FEW ? 4 * 2 : RF == 4 ? 2 * 4 : 4 * 4;
   __shared__ __attribute__((aligned(16))) float red[SUMS * RF * 64 * 4];
   __shared__ uint16_t list[4][FEW ? kFewTokens : 1];
   const int per = p.splits * rank_blocks;
@@ -462,14 +462,27 @@ __device__ __forceinline__ Chunk first_of(const Chunk& v, int n) {
 // gradient.  As z and the adapter only grow from one to the next, z + a names it: no two
 // have the same, and lora_sum_kernel finds an adapter's by its rows.  The next turn's
 // rows are in flight while this one's are multiplied.
+// Both panels' gradients are one launch, the first `blocks` workgroups side 0's.
+struct Sides {
+  LoraSide side[2];
+  int column_blocks[2];
+  int64_t per[2];                        // rows of a range
+  unsigned blocks;
+};
+
 template <int RF>
-__global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, const LoraOrder o, int which,
-                                                         int rank_blocks, int column_blocks, int64_t per) {
+__global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, const LoraOrder o, const Sides sides,
+                                                         int rank_blocks) {
   const int lane = threadIdx.x & 63, l15 = lane & 15, g8 = (lane >> 4) * 8;
-  const int cb = blockIdx.x % column_blocks, rest = blockIdx.x / column_blocks;
+  const int which = blockIdx.x >= sides.blocks;
+  const unsigned block = blockIdx.x - (which ? sides.blocks : 0);
+  const LoraSide& side = sides.side[which];
+  const int column_blocks = sides.column_blocks[which];
+  const int64_t per = sides.per[which], C = side.C;
+  const int cb = block % column_blocks, rest = block / column_blocks;
   const int rank0 = rest % rank_blocks * kRankBlock, z = rest / rank_blocks;
   const int64_t first = int64_t(cb) * 512 + (threadIdx.x >> 6) * 128;
-  if (first >= p.C) return;              // whole waves, which wait for no others
+  if (first >= C) return;              // whole waves, which wait for no others
   const int64_t c = first + l15 * 8;
   const int used = o.offsets[p.n - 1];   // rows that have an adapter
   const int z0 = int(min(int64_t(used), z * per)), z1 = int(min(int64_t(used), (z + 1) * per));
@@ -507,7 +520,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
     const auto ask = [&](int row0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        w[i] = row0 + g8 + i < end ? load_row(p.x + int64_t(token[i]) * p.ld_x, c, p.C) : Chunk{{0u, 0u, 0u, 0u}};
+        w[i] = row0 + g8 + i < end ? load_row(side.x + int64_t(token[i]) * side.ld_x, c, C) : Chunk{{0u, 0u, 0u, 0u}};
 #pragma unroll
       for (int f = 0; f < RF; ++f) hi[f] = load_chunk(vr[f] + row0), lo[f] = load_chunk(vr[f] + row0 + to_lo);
     };
@@ -533,7 +546,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
         for (int q = 0; q < 8; ++q) acc[f][q] = mfma(h[f], b[q], acc[f][q]);
       }
     }
-    float* out = p.partial + int64_t(z + a) * p.r * p.C;
+    float* out = side.partial + int64_t(z + a) * p.r * C;
 #pragma unroll
     for (int f = 0; f < RF; ++f)
 #pragma unroll
@@ -542,7 +555,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
         if (j >= p.r) continue;
 #pragma unroll
         for (int q = 0; q < 8; q += 4)
-          store_row(out + int64_t(j) * p.C, c + q, p.C,
+          store_row(out + int64_t(j) * C, c + q, C,
                     Chunk{{__float_as_uint(acc[f][q][k]), __float_as_uint(acc[f][q + 1][k]),
                            __float_as_uint(acc[f][q + 2][k]), __float_as_uint(acc[f][q + 3][k])}});
       }
@@ -551,19 +564,25 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
 }
 
 // Adds an adapter's partial gradients in order, times its scale: four values a thread.
-__global__ __launch_bounds__(256) void lora_sum_kernel(const LoraProblem p, const int32_t* offsets, int64_t per,
-                                                       unsigned blocks) {
+// The first `split` of an adapter's workgroups take side 0.
+__global__ __launch_bounds__(256) void lora_sum_kernel(const LoraProblem p, const LoraOrder o, const Sides sides,
+                                                       unsigned split, unsigned blocks) {
   const int a = blockIdx.x / blocks;
-  const int64_t count = int64_t(p.r) * p.C;
-  const int begin = a ? offsets[a - 1] : 0, end = offsets[a];
+  const unsigned block = blockIdx.x % blocks;
+  const int which = block >= split;
+  const LoraSide& side = sides.side[which];
+  const int64_t count = int64_t(p.r) * side.C, per = sides.per[which];
+  const int64_t first = int64_t(which ? block - split : block) * 256 + threadIdx.x;
+  const int64_t step = int64_t(which ? blocks - split : split) * 1024;
+  const int begin = a ? o.offsets[a - 1] : 0, end = o.offsets[a];
   const int64_t z0 = begin / per + a, z1 = end > begin ? (end - 1) / per + a + 1 : z0;
   const float scale = p.scales ? p.scales[a] : 1.0f;
-  for (int64_t i = (int64_t(blockIdx.x % blocks) * 256 + threadIdx.x) * 4; i < count; i += int64_t(blocks) * 1024) {
+  for (int64_t i = first * 4; i < count; i += step) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
     for (int64_t z = z0; z < z1; ++z) {
       float f[4];
-      unpack<float>(load_row(p.partial + z * count, i, count), f);
+      unpack<float>(load_row(side.partial + z * count, i, count), f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[k] += f[k];
     }
@@ -571,11 +590,11 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraProblem p, cons
     for (int k = 0; k < 4; ++k) s[k] *= scale;
     const Chunk v = Chunk{{__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), __float_as_uint(s[3])}};
     if (p.grad_fp32) {
-      store_row(static_cast<float*>(p.grad) + a * count, i, count, v);
+      store_row(static_cast<float*>(side.grad) + a * count, i, count, v);
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (i + k < count) static_cast<uint16_t*>(p.grad)[a * count + i + k] = to_bf16(s[k]);
+        if (i + k < count) static_cast<uint16_t*>(side.grad)[a * count + i + k] = to_bf16(s[k]);
     }
   }
 }
@@ -586,7 +605,7 @@ int rank_blocks_of(int r) { return (r + kRankBlock - 1) / kRankBlock; }
 // Ranges of rows that share a panel's gradient.
 int64_t outer_ranges(int64_t T, int64_t C, int r) {
   const int64_t blocks = ((C + 511) / 512) * rank_blocks_of(r);
-  int64_t z = (512 + blocks - 1) / blocks;
+  int64_t z = 512 / blocks;                   // what runs at once: no last round of a few
   const int64_t most = T / (16 * r);          // partial gradients: at most a quarter of x's bytes
   z = z < most ? z : most;
   const int64_t turns = (T + 2 * kOuterRows - 1) / (2 * kOuterRows);
@@ -683,24 +702,32 @@ hipError_t launch_lora_expand(const LoraProblem& p, hipStream_t st) {
   return p.T * p.C * 2 > kL2Bytes ? run_expand<false, true>(p, st) : run_expand<false, false>(p, st);
 }
 
-hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, int which, hipStream_t st) {
-  const int rb = rank_blocks_of(p.r), cb = int((p.C + 511) / 512);
-  const int64_t Z = outer_ranges(p.T, p.C, p.r);
-  const int64_t per = ((p.T + Z - 1) / Z + kOuterRows - 1) / kOuterRows * kOuterRows;
-  hipError_t e = hipSuccess;
+hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, const LoraSide (&side)[2], hipStream_t st) {
+  const int rb = rank_blocks_of(p.r);
+  Sides sides;
+  unsigned blocks[2], sums[2];
+  for (int i = 0; i < 2; ++i) {
+    sides.side[i] = side[i];
+    const int64_t C = side[i].C > 0 ? side[i].C : 1;
+    const int64_t Z = outer_ranges(p.T, C, p.r), per = (p.T + Z - 1) / Z;
+    sides.column_blocks[i] = int((C + 511) / 512);
+    sides.per[i] = per > 0 ? (per + kOuterRows - 1) / kOuterRows * kOuterRows : kOuterRows;
+    blocks[i] = side[i].grad ? unsigned(Z * sides.column_blocks[i] * rb) : 0;
+    const int64_t fours = (int64_t(p.r) * C + 1023) / 1024;
+    sums[i] = side[i].grad ? unsigned(fours < 1024 ? fours : 1024) : 0;
+  }
+  sides.blocks = blocks[0];
   if (p.T > 0) {
-    const dim3 grid(unsigned(Z * cb * rb));
     const auto run = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, o, which, rb, cb, per);
+      hipLaunchKernelGGL(kernel, dim3(blocks[0] + blocks[1]), dim3(256), 0, st, p, o, sides, rb);
       return hipGetLastError();
     };
-    e = p.r <= 16 ? run(lora_outer_kernel<1>) : p.r <= 32 ? run(lora_outer_kernel<2>) : run(lora_outer_kernel<4>);
+    const hipError_t e =
+        p.r <= 16 ? run(lora_outer_kernel<1>) : p.r <= 32 ? run(lora_outer_kernel<2>) : run(lora_outer_kernel<4>);
     if (e != hipSuccess) return e;
   }
-  const int64_t blocks = (int64_t(p.r) * p.C + 1023) / 1024;
-  const unsigned each = unsigned(blocks < 1024 ? blocks : 1024);
-  hipLaunchKernelGGL(lora_sum_kernel, dim3(unsigned(p.n) * each), dim3(256), 0, st, p, o.offsets, per > 0 ? per : 1,
-                     each);
+  hipLaunchKernelGGL(lora_sum_kernel, dim3(unsigned(p.n) * (sums[0] + sums[1])), dim3(256), 0, st, p, o, sides, sums[0],
+                     sums[0] + sums[1]);
   return hipGetLastError();
 }
 
