@@ -328,18 +328,19 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceProblem 
   end = min(end, p.T);
   // runs [first, last) of the partial rows
   const int first = int(begin / part.rows) + s, last = end > begin ? int((end - 1) / part.rows) + s + 1 : first;
+  // no branch in the loop, so that its loads are in flight together: lanes past the columns
+  // read the last ones, and all lanes of a run its tokens
 #pragma unroll 4
   for (int run = first + wave * groups + group; run < last; run += 16 * groups) {
 #pragma unroll
     for (int i = 0; i < QL; ++i) {
-      const int at = (i * 64 + q) * 4;
-      if (at >= part.E4) continue;
-      const float4 a = *reinterpret_cast<const float4*>(part.P + int64_t(run) * part.E4 + at);
-      const int4 d = *reinterpret_cast<const int4*>(part.C + int64_t(run) * part.E4 + at);
+      const int64_t at = int64_t(run) * part.E4 + min((i * 64 + q) * 4, part.E4 - 4);
+      const float4 a = *reinterpret_cast<const float4*>(part.P + at);
+      const int4 d = *reinterpret_cast<const int4*>(part.C + at);
       v[i].x += a.x, v[i].y += a.y, v[i].z += a.z, v[i].w += a.w;
       c[i].x += d.x, c[i].y += d.y, c[i].z += d.z, c[i].w += d.w;
     }
-    if (q == 0) n += part.n[run];
+    n += part.n[run];
   }
   for (int off = quads; off < 64; off <<= 1) {   // the lanes' groups (QL = 1)
     v[0].x += __shfl_xor(v[0].x, off, 64), v[0].y += __shfl_xor(v[0].y, off, 64);
