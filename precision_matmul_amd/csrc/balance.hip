@@ -43,13 +43,18 @@ __device__ __forceinline__ float reciprocal(float d) {
   return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
-// Four logits at column c of E; -inf past the end.
+// Four logits at column c of E; -inf past the end.  Where E is a multiple of four, without
+// a branch of the lanes, so that loads of several pieces are in flight together.
 template <typename T>
 __device__ __forceinline__ void load4(const T* row, int c, int E, float (&f)[4]) {
-  if (c + 4 <= E) {
-    struct __attribute__((packed, aligned(sizeof(T)))) At {
-      T v[4];
-    };
+  struct __attribute__((packed, aligned(sizeof(T)))) At {
+    T v[4];
+  };
+  if (E % 4 == 0) {
+    const At a = *reinterpret_cast<const At*>(row + min(c, E - 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = c < E ? to_float(a.v[i]) : -__builtin_inff();
+  } else if (c + 4 <= E) {
     const At a = *reinterpret_cast<const At*>(row + c);
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = to_float(a.v[i]);
@@ -250,20 +255,13 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem 
   };
   const auto end_of = [&](int s) { return p.ends ? min(int64_t(p.ends[s]), r1) : r1; };
   float raw[NQ][4];                      // the next turn's logits and first ids
-  int raw_id = -1;
-  const auto ask = [&](int64_t row) {
-    raw_id = -1;
-    if (row < r1) {
-      const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+  int raw_id;
+  const auto ask = [&](int64_t row) {    // past the chunk: its last row, which is not used
+    const int64_t at = min(row, r1 - 1);
+    const T* x = static_cast<const T*>(p.logits) + at * p.ld;
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) load4(x, (q * L + lane) * 4, p.E, raw[q]);
-      if (lane < p.k) raw_id = p.ids[row * p.k + lane];
-    } else {
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) raw[q][i] = -__builtin_inff();
-    }
+    for (int q = 0; q < NQ; ++q) load4(x, (q * L + lane) * 4, p.E, raw[q]);
+    raw_id = p.ids[at * p.k + min(lane, p.k - 1)];
   };
   const int my_end = lane_end(p);
   ask(r0 + slot);
@@ -273,13 +271,13 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem 
   for (int64_t turn = r0; turn < r1; turn += SLOTS) {
     const int64_t row = turn + slot, next = min(turn + SLOTS, r1);
     float f[NQ][4];
-    const int id0 = raw_id;
+    const int id0 = lane < p.k ? raw_id : -1;
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[q][i] = raw[q][i];
     if (next < r1) ask(next + slot);
-    const bool used = probabilities<L, NQ, SIGMOID>(f);
+    const bool used = probabilities<L, NQ, SIGMOID>(f) && row < r1;
     while (s < p.S) {
       if (used && row >= begin && row < end) {
 #pragma unroll
