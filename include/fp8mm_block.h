@@ -113,9 +113,10 @@ fp8mm_status fp8mm_moe_balance_loss_backward(const float* grad_loss, const void*
  * x: bf16 [T, K]; down: bf16 [n, r, K], up: bf16 [n, r, N], both dense; ids: int32
  * [T], in any order (tokens of one adapter next to each other are the fast case);
  * scales: float32 [n] or NULL (1); base, out: bf16 [T, N].  out may be base itself.
- * v: float32 [splits, T, r] with splits = fp8mm_lora_splits(T, K, n, r): each
- * token's products as that many partial sums over K (their sum is v), which the
- * backward takes; rows of tokens without an adapter are not written.
+ * v: float32 [splits, T, r rounded up to a multiple of 4] with splits =
+ * fp8mm_lora_splits(T, K, n, r): each token's products as that many partial sums over
+ * K (their sum is v; zeros behind the rank), which the backward takes; rows of tokens
+ * without an adapter are not written.
  * Sums are float32.  v enters the second product as two bf16 numbers, its
  * rounding and the rest, so that it keeps 16 bits.
  * r <= 256, else FP8MM_ENOTIMPL; 0 <= T < 2^31; 1 <= n < 2^31; 1 <= K, N <= 2^22.

@@ -314,7 +314,8 @@ def lora_forward(x, down, up, ids, scales=None, base=None, out=None):
     -> (out bf16 [T, N], v): out[t] = base[t] + scales[a] up[a]^T (down[a] x[t]) with a
     = ids[t], and base[t] where ids[t] is outside [0, n).  scales: float32 [n], 1
     without; base: bf16 [T, N], 0 without; out may be base itself.  v: float32
-    [splits, T, r], the inner products in partial sums, which lora_backward takes."""
+    [splits, T, r rounded up to 4], the inner products in partial sums, which
+    lora_backward takes."""
     device = _matrix(x, "x")[2]
     T = x.shape[0]
     K, n, r, N = _panels(down, up, T, ids, scales, device)
@@ -324,7 +325,7 @@ def lora_forward(x, down, up, ids, scales=None, base=None, out=None):
         out, ld_out = x.new_empty((T, N)), N
     else:
         ld_out = _bf16_matrix(out, T, N, device, "out")
-    v = x.new_empty((max(_lib.load().fp8mm_lora_splits(T, K, n, r), 1), T, r), dtype=torch.float32)
+    v = x.new_empty((max(_lib.load().fp8mm_lora_splits(T, K, n, r), 1), T, (r + 3) // 4 * 4), dtype=torch.float32)
     _call("fp8mm_lora", x, x.data_ptr(), ld, T, K, down.data_ptr(), up.data_ptr(), n, r, N, ids.data_ptr(),
           _ptr(scales), _ptr(base), ld_base, out.data_ptr(), ld_out, v.data_ptr())
     return out, v
@@ -347,7 +348,7 @@ def lora_backward(dy, x, v, down, up, ids, scales=None, need_dx=True, need_down=
         raise ValueError("x is needed for the gradient of down")
     if v is not None:
         splits = max(lib.fp8mm_lora_splits(T, K, n, r), 1)
-        _dense(v, torch.float32, (splits, T, r), device, "v")
+        _dense(v, torch.float32, (splits, T, (r + 3) // 4 * 4), device, "v")
     elif need_up:
         raise ValueError("v is needed for the gradient of up")
     out_dtype = down.dtype if out_dtype is None else out_dtype

@@ -86,7 +86,7 @@ fp8mm_status check_lora(int64_t T, int64_t K, int64_t n, int64_t r, int64_t N, c
 
 // The parts of the backward's workspace.
 int64_t dv_bytes(int64_t T, int64_t N, int64_t n, int64_t r) {
-  return (4 * fp8mm::lora_splits(T, N, n, int(r)) * T * r + 15) / 16 * 16;
+  return 16 * fp8mm::lora_splits(T, N, n, int(r)) * T * ((r + 3) / 4);
 }
 int64_t partial_bytes(int64_t T, int64_t C, int64_t n, int64_t r) {
   return (fp8mm::lora_outer_workspace(T, C, n, int(r)) + 15) / 16 * 16;

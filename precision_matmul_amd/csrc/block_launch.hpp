@@ -75,7 +75,7 @@ struct LoraProblem {
   const uint16_t* panels;  // [n, r, C]
   const uint16_t* x;       // shrink, outer: [T, C], row stride ld_x
   int64_t ld_x;
-  float* v;                // [splits, T, r]
+  float* v;                // [splits, T, r rounded up to 4]
   int splits;
   const uint16_t* base;    // expand: [T, C] or null (0)
   int64_t ld_base;

@@ -45,6 +45,50 @@ __device__ __forceinline__ f32x4 mfma(const bf16x8& a, const bf16x8& b, const f3
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// A lane's 8 columns from c on, of rows of C.  Where they reach past the end, the lane
+// works on the row's last 8 in place of them, so that no load needs a path for a row's
+// last elements, for which the wave would wait one by one; it stores only those that are
+// its own.  Lanes past the end work on the last 8 too, and store none.
+struct Columns {
+  int64_t at;                      // first column that is loaded
+  int skip;                        // leading ones that are other lanes'
+  bool tiny;                       // rows of less than 8 columns
+  __device__ __forceinline__ Columns(int64_t c, int64_t C) {
+    tiny = C < 8;
+    at = tiny ? c : min(c, C - 8);
+    skip = int(min(c - at, int64_t(8)));
+  }
+  template <bool NT = false>
+  __device__ __forceinline__ Chunk load(const uint16_t* row, int64_t C) const {
+    if (tiny) return load_row(row, at, C);
+    return NT ? load_chunk_nt(row + at) : load_chunk(row + at);
+  }
+  template <bool NT = false>
+  __device__ __forceinline__ void store(uint16_t* row, int64_t C, const Chunk& v) const {
+    if (tiny) {
+      store_row(row, at, C, v);
+    } else if (skip == 0) {
+      NT ? store_chunk_nt(row + at, v) : store_chunk(row + at, v);
+    } else {
+#pragma unroll
+      for (int i = 1; i < 8; ++i)
+        if (i >= skip) row[at + i] = uint16_t(v.w[i / 2] >> (i % 2 * 16));
+    }
+  }
+  __device__ __forceinline__ void store(float* row, int64_t C, const float (&f)[8]) const {
+    if (!tiny && skip == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        store_chunk(row + at + i, Chunk{{__float_as_uint(f[i]), __float_as_uint(f[i + 1]), __float_as_uint(f[i + 2]),
+                                         __float_as_uint(f[i + 3])}});
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= skip && at + i < C) row[at + i] = f[i];
+    }
+  }
+};
+
 // At most 64 tokens of one adapter: `rows` of them, lane i < rows holds the i-th one.
 struct Members {
   int rows, token;
@@ -52,9 +96,10 @@ struct Members {
   __device__ __forceinline__ int at(int i) const { return __shfl(token, min(i, rows - 1), 64); }
 };
 
-// Batches that are one tile: as many adapters as make its tokens few for each.
+// Batches of more than one tile that are taken adapter by adapter: as many adapters as
+// make the tokens few for each, so that a panel is read once and not for each tile.
 __host__ __device__ inline bool few_tokens(int64_t T, int64_t n) {
-  return T <= kTile || (T <= kFewTokens && n > T / 16);
+  return T > kTile && T <= kFewTokens && n > T / 16;
 }
 // Workgroups of such a batch stand for its tokens, else for the adapters.
 __host__ __device__ inline bool by_tokens(const LoraProblem& p) { return p.T < p.n; }
@@ -66,7 +111,7 @@ __device__ __forceinline__ int adapter_of(const LoraProblem& p, int64_t t) {
 }
 
 // body(a, members) for each adapter among the 64 tokens from t0 on (NONE: and with a =
-// -1 for those without one).
+// -1 for those without one); workgroup y of a tile takes every gridDim.y-th of them.
 template <bool NONE, typename Body>
 __device__ __forceinline__ void each_adapter(const LoraProblem& p, int64_t t0, const Body& body) {
   const int lane = threadIdx.x & 63;
@@ -74,10 +119,11 @@ __device__ __forceinline__ void each_adapter(const LoraProblem& p, int64_t t0, c
   const int id = adapter_of(p, t0 + lane);
   const uint64_t below = (uint64_t(1) << lane) - 1;
   uint64_t todo = __ballot(in && (NONE || id >= 0));
-  while (todo) {
+  for (unsigned turn = 0; todo; ++turn) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
     const uint64_t same = __ballot(in && id == a);
     todo &= ~same;
+    if (turn % gridDim.y != blockIdx.y) continue;
     // members to the front, the others behind them: a permutation of the lanes
     const int rows = __popcll(same);
     const int to = same >> lane & 1 ? __popcll(same & below) : rows + __popcll(~same & below);
@@ -85,8 +131,7 @@ __device__ __forceinline__ void each_adapter(const LoraProblem& p, int64_t t0, c
   }
 }
 
-// The same for a batch of few tokens as a whole, which may all have adapters of their
-// own: workgroup y handles adapter y (the one past the last: the tokens without), or,
+// The same for a batch of few tokens as a whole: workgroup y handles adapter y (the one past the last: the tokens without), or,
 // where there are more adapters than tokens, that of token y if y is its first token;
 // MOST of its tokens at a time.  `list` is the wave's own.
 template <bool NONE, int MOST, typename Body>
@@ -112,6 +157,9 @@ __device__ __forceinline__ void one_adapter(const LoraProblem& p, uint16_t* list
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   for (int i = 0; i < rows; i += MOST) body(a, Members{min(MOST, rows - i), int(list[min(i + lane, rows - 1)])});
 }
+
+// Row stride of v: whole 16 bytes, zeros behind the rank.
+__host__ __device__ inline int v_columns(int r) { return (r + 3) / 4 * 4; }
 
 // -------------------------------------------------------------------- shrink
 
@@ -173,14 +221,23 @@ __device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const M
     w.add(acc);
     c += BY;
   }
-  if (c < last) {                        // the row's last columns, zeros past them
+  if (c < last) {                        // the row's last columns: zeros past them
 #pragma unroll 1
     for (int64_t k = int64_t(c) * (32 * ST) + g8; k < p.C + g8; k += 32) {
+      const Columns cols(k, p.C);
+      const auto own = [&](Chunk v) {    // without the columns of the lane before
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (2 * i + 1 < cols.skip) v.w[i] = 0;
+          if (2 * i + 1 == cols.skip) v.w[i] &= 0xFFFF0000u;
+        }
+        return v;
+      };
       Piece<MF, RF, 1> end;
 #pragma unroll
-      for (int i = 0; i < MF; ++i) end.A[0][i] = load_row(xr[i], k, p.C);
+      for (int i = 0; i < MF; ++i) end.A[0][i] = own(cols.load(xr[i], p.C));
 #pragma unroll
-      for (int f = 0; f < RF; ++f) end.B[0][f] = load_row(pr[f], k, p.C);
+      for (int f = 0; f < RF; ++f) end.B[0][f] = own(cols.load(pr[f], p.C));
       end.add(acc);
     }
   }
@@ -211,7 +268,7 @@ __device__ __forceinline__ void shrink_tile(const LoraProblem& p, int a, const M
     for (int i = 0; i < 4; ++i) {
       const int at = q / RF * 16 + (lane >> 4) * 4 + i;
       const int64_t t = m.at(at);
-      if (at < m.rows && j < p.r) p.v[(int64_t(split) * p.T + t) * p.r + j] = s[i];
+      if (at < m.rows && j < v_columns(p.r)) p.v[(int64_t(split) * p.T + t) * v_columns(p.r) + j] = j < p.r ? s[i] : 0.0f;
     }
   }
   __syncthreads();
@@ -279,22 +336,15 @@ __device__ __forceinline__ void stage_v(const LoraProblem& p, const Members& m, 
     const int row = min(i / quads, kTile - 1), j = i % quads * 4;
     const int64_t t = m.at(row);
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (row < m.rows && i < rows * quads) {
-      const float* at = p.v + t * p.r + j;
-      const int64_t next = p.T * p.r;
-      if (j + 4 <= p.r) {
+    if (row < m.rows && i < rows * quads && j < p.r) {
+      const float* at = p.v + t * v_columns(p.r) + j;
+      const int64_t next = p.T * v_columns(p.r);
 #pragma unroll 4
-        for (int k = 0; k < p.splits; ++k) {
-          float f[4];
-          unpack<float>(load_chunk(at + k * next), f);
+      for (int k = 0; k < p.splits; ++k) {
+        float f[4];
+        unpack<float>(load_chunk(at + k * next), f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] += f[e];
-        }
-      } else {
-        for (int k = 0; k < p.splits; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j + e < p.r) v[e] += at[k * next + e];
+        for (int e = 0; e < 4; ++e) v[e] += f[e];
       }
     }
     if (i < rows * quads) {
@@ -308,12 +358,13 @@ __device__ __forceinline__ void stage_v(const LoraProblem& p, const Members& m, 
 }
 
 // The panel's rows j .. j + 32 at a lane's columns, as fragments.
-__device__ __forceinline__ void load_panel(const LoraProblem& p, int a, int j, int64_t c, bf16x8 (&b)[8]) {
+__device__ __forceinline__ void load_panel(const LoraProblem& p, int a, int j, const Columns& c, bf16x8 (&b)[8]) {
   Chunk w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = j + (threadIdx.x >> 4 & 3) * 8 + i;
-    w[i] = row < p.r ? load_row(p.panels + (int64_t(a) * p.r + row) * p.C, c, p.C) : Chunk{{0u, 0u, 0u, 0u}};
+    w[i] = c.load(p.panels + (int64_t(a) * p.r + min(row, p.r - 1)) * p.C, p.C);
+    if (row >= p.r) w[i] = Chunk{{0u, 0u, 0u, 0u}};
   }
   transpose8(w, b);
 }
@@ -322,14 +373,14 @@ __device__ __forceinline__ void load_panel(const LoraProblem& p, int a, int j, i
 // flight.  KS: steps of 32 rank rows whose fragments stay in registers (0: any number,
 // read again for each 16 rows).
 template <int KS, bool NT>
-__device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const Members& m, int64_t c, int ld,
+__device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const Members& m, const Columns& c, int ld,
                                             const uint16_t* hi, const uint16_t* lo, bf16x8 (&b)[KS ? KS : 1][8]) {
   const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   Chunk next[4];
   const auto ask = [&](int i) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      next[k] = load_row<uint16_t, NT>(p.base + int64_t(m.at(i + g * 4 + k)) * p.ld_base, c, p.C);
+      next[k] = c.load<NT>(p.base + int64_t(m.at(i + g * 4 + k)) * p.ld_base, p.C);
   };
   if (p.base) ask(0);
   for (int i = 0; i < m.rows; i += 16) {
@@ -366,7 +417,7 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
       float y[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) y[q] = acc[q][k];
-      if (at < m.rows) store_row<uint16_t, NT>(p.out + row * p.ld_out, c, p.C, pack<uint16_t>(y));
+      if (at < m.rows) c.store<NT>(p.out + row * p.ld_out, p.C, pack<uint16_t>(y));
     }
   }
 }
@@ -379,7 +430,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, i
   const int lane = threadIdx.x & 63, ld = KS ? MAX : (p.r + 31) / 32 * 32 + 8;
   const int64_t first = int64_t(blockIdx.x % column_blocks) * 512 + (threadIdx.x >> 6) * 128;
   const bool idle = first >= p.C;        // whole waves, which still stage v
-  const int64_t c = first + (lane & 15) * 8;
+  const Columns c(first + (lane & 15) * 8, p.C);
   const auto body = [&](int a, const Members& m) {
     if (a < 0) {                         // no adapter: base alone
       if (p.base == p.out || idle) return;
@@ -387,8 +438,8 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, i
         const int i = i0 + (lane >> 4);
         const int64_t row = m.at(i);
         if (i >= m.rows) continue;
-        const Chunk v = p.base ? load_row(p.base + row * p.ld_base, c, p.C) : Chunk{{0u, 0u, 0u, 0u}};
-        store_row(p.out + row * p.ld_out, c, p.C, v);
+        const Chunk v = p.base ? c.load(p.base + row * p.ld_base, p.C) : Chunk{{0u, 0u, 0u, 0u}};
+        c.store(p.out + row * p.ld_out, p.C, v);
       }
       return;
     }
@@ -428,9 +479,8 @@ __global__ __launch_bounds__(256) void lora_sort_kernel(const LoraProblem p, con
     if (!v) continue;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int k = 0; k < o.splits[which]; ++k) {
-      const float* at = v + (k * p.T + t) * p.r;
       float f[4];
-      unpack<float>(load_row(at, j, p.r), f);
+      unpack<float>(load_chunk(v + (k * p.T + t) * v_columns(p.r) + j), f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[e] += f[e];
     }
@@ -483,7 +533,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
   const int rank0 = rest % rank_blocks * kRankBlock, z = rest / rank_blocks;
   const int64_t first = int64_t(cb) * 512 + (threadIdx.x >> 6) * 128;
   if (first >= C) return;              // whole waves, which wait for no others
-  const int64_t c = first + l15 * 8;
+  const Columns c(first + l15 * 8, C);
   const int used = o.offsets[p.n - 1];   // rows that have an adapter
   const int z0 = int(min(int64_t(used), z * per)), z1 = int(min(int64_t(used), (z + 1) * per));
   if (z0 >= z1) return;
@@ -520,7 +570,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
     const auto ask = [&](int row0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        w[i] = row0 + g8 + i < end ? load_row(side.x + int64_t(token[i]) * side.ld_x, c, C) : Chunk{{0u, 0u, 0u, 0u}};
+        w[i] = row0 + g8 + i < end ? c.load(side.x + int64_t(token[i]) * side.ld_x, C) : Chunk{{0u, 0u, 0u, 0u}};
 #pragma unroll
       for (int f = 0; f < RF; ++f) hi[f] = load_chunk(vr[f] + row0), lo[f] = load_chunk(vr[f] + row0 + to_lo);
     };
@@ -553,11 +603,10 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
       for (int k = 0; k < 4; ++k) {
         const int j = rank0 + f * 16 + (lane >> 4) * 4 + k;
         if (j >= p.r) continue;
+        float y[8];
 #pragma unroll
-        for (int q = 0; q < 8; q += 4)
-          store_row(out + int64_t(j) * C, c + q, C,
-                    Chunk{{__float_as_uint(acc[f][q][k]), __float_as_uint(acc[f][q + 1][k]),
-                           __float_as_uint(acc[f][q + 2][k]), __float_as_uint(acc[f][q + 3][k])}});
+        for (int q = 0; q < 8; ++q) y[q] = acc[f][q][k];
+        c.store(out + int64_t(j) * C, C, y);
       }
     begin = end;
   }
@@ -602,12 +651,19 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraProblem p, cons
 int64_t tiles_of(int64_t T, int64_t n) { return few_tokens(T, n) ? 1 : (T + kTile - 1) / kTile; }
 int rank_blocks_of(int r) { return (r + kRankBlock - 1) / kRankBlock; }
 
+// Workgroups that share a tile's adapters: where there are few tiles.
+unsigned tile_groups(const LoraProblem& p) {
+  const int64_t most = p.T <= kTile ? p.T : p.T <= 512 ? 8 : p.T <= 1024 ? 4 : p.T <= 2048 ? 2 : 1;
+  return unsigned(p.n + 1 < most ? p.n + 1 : most);
+}
+
 // Ranges of rows that share a panel's gradient.
 int64_t outer_ranges(int64_t T, int64_t C, int r) {
   const int64_t blocks = ((C + 511) / 512) * rank_blocks_of(r);
   int64_t z = 512 / blocks;                   // what runs at once: no last round of a few
-  const int64_t most = T / (16 * r);          // partial gradients: at most a quarter of x's bytes
-  z = z < most ? z : most;
+  // partial gradients: at most a quarter of x's bytes, or 4 MiB
+  const int64_t most = T / (16 * r), least = (int64_t(1) << 20) / (r * C);
+  z = z < most || z < least ? z : most > least ? most : least;
   const int64_t turns = (T + 2 * kOuterRows - 1) / (2 * kOuterRows);
   z = z < turns ? z : turns;
   return z < 1 ? 1 : z;
@@ -617,7 +673,7 @@ int64_t outer_ranges(int64_t T, int64_t C, int r) {
 
 int lora_splits(int64_t T, int64_t C, int64_t n, int r) {
   if (T <= 0) return 1;
-  const int64_t adapters = few_tokens(T, n) ? (n < T ? n : T) : 1;
+  const int64_t adapters = few_tokens(T, n) || T <= kTile ? (n < T ? n : T) : 1;
   const int64_t blocks = tiles_of(T, n) * adapters * rank_blocks_of(r);
   const int64_t turns = (C + 511) / 512;      // a turn or two for each wave
   int64_t s = (512 + blocks - 1) / blocks;
@@ -670,7 +726,7 @@ hipError_t launch_lora_order(const LoraProblem& p, void* workspace, LoraOrder& o
 template <bool FEW>
 hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
   const int rb = rank_blocks_of(p.r);
-  const dim3 grid(unsigned(tiles_of(p.T, p.n) * p.splits * rb), unsigned(FEW ? (by_tokens(p) ? p.T : p.n) : 1));
+  const dim3 grid(unsigned(tiles_of(p.T, p.n) * p.splits * rb), FEW ? unsigned(by_tokens(p) ? p.T : p.n) : tile_groups(p));
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, rb);
     return hipGetLastError();
@@ -682,7 +738,7 @@ hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
 template <bool FEW, bool NT>
 hipError_t run_expand(const LoraProblem& p, hipStream_t st) {
   const int cb = int((p.C + 511) / 512);
-  const dim3 grid(unsigned(tiles_of(p.T, p.n) * cb), unsigned(FEW ? (by_tokens(p) ? p.T : p.n + 1) : 1));
+  const dim3 grid(unsigned(tiles_of(p.T, p.n) * cb), FEW ? unsigned(by_tokens(p) ? p.T : p.n + 1) : tile_groups(p));
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, cb);
     return hipGetLastError();

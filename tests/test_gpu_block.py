@@ -511,7 +511,7 @@ def _check_lora(dev, val, scaled=True, based=True):
     out, v = fp8mm.lora_forward(x, down, up, ids, scales, base)
     ref, vref = block.lora(xv, downv, upv, idv, sv, basev)
     tol = np.zeros_like(ref)
-    got_v = _f64(v).sum(0)
+    got_v = _f64(v).sum(0)[:, :r]
     for a, at, s in _gather(idv, downv, sv):
         ev = (K + 24) * U * (np.abs(xv[at]) @ np.abs(downv[a]).T)
         _within(got_v[at], vref[at], ev, "v")
