@@ -48,24 +48,24 @@ __device__ __forceinline__ f32x4 mfma(const bf16x8& a, const bf16x8& b, const f3
 // A lane's 8 columns from c on, of rows of C.  Where they reach past the end, the lane
 // works on the row's last 8 in place of them, so that no load needs a path for a row's
 // last elements, for which the wave would wait one by one; it stores only those that are
-// its own.  Lanes past the end work on the last 8 too, and store none.
+// its own.  Lanes past the end work on the last 8 too, and store none.  TINY: rows of less
+// than 8 columns, which do need that path (in kernels of their own).
+template <bool TINY>
 struct Columns {
   int64_t at;                      // first column that is loaded
   int skip;                        // leading ones that are other lanes'
-  bool tiny;                       // rows of less than 8 columns
   __device__ __forceinline__ Columns(int64_t c, int64_t C) {
-    tiny = C < 8;
-    at = tiny ? c : min(c, C - 8);
+    at = TINY ? c : min(c, C - 8);
     skip = int(min(c - at, int64_t(8)));
   }
   template <bool NT = false>
   __device__ __forceinline__ Chunk load(const uint16_t* row, int64_t C) const {
-    if (tiny) return load_row(row, at, C);
+    if constexpr (TINY) return load_row(row, at, C);
     return NT ? load_chunk_nt(row + at) : load_chunk(row + at);
   }
   template <bool NT = false>
   __device__ __forceinline__ void store(uint16_t* row, int64_t C, const Chunk& v) const {
-    if (tiny) {
+    if constexpr (TINY) {
       store_row(row, at, C, v);
     } else if (skip == 0) {
       NT ? store_chunk_nt(row + at, v) : store_chunk(row + at, v);
@@ -76,7 +76,7 @@ struct Columns {
     }
   }
   __device__ __forceinline__ void store(float* row, int64_t C, const float (&f)[8]) const {
-    if (!tiny && skip == 0) {
+    if (!TINY && skip == 0) {
 #pragma unroll
       for (int i = 0; i < 8; i += 4)
         store_chunk(row + at + i, Chunk{{__float_as_uint(f[i]), __float_as_uint(f[i + 1]), __float_as_uint(f[i + 2]),
@@ -133,7 +133,8 @@ __device__ __forceinline__ void each_adapter(const LoraProblem& p, int64_t t0, c
 
 // The same for a batch of few tokens as a whole: workgroup y handles adapter y (the one past the last: the tokens without), or,
 // where there are more adapters than tokens, that of token y if y is its first token;
-// MOST of its tokens at a time.  `list` is the wave's own.
+// MOST of its tokens at a time, in turns with the gridDim.z - 1 others of the adapter (if
+// most tokens have the same one after all).  `list` is the wave's own.
 template <bool NONE, int MOST, typename Body>
 __device__ __forceinline__ void one_adapter(const LoraProblem& p, uint16_t* list, const Body& body) {
   const int lane = threadIdx.x & 63;
@@ -155,7 +156,8 @@ __device__ __forceinline__ void one_adapter(const LoraProblem& p, uint16_t* list
     }
   if (by_token && first != int(blockIdx.y)) return;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  for (int i = 0; i < rows; i += MOST) body(a, Members{min(MOST, rows - i), int(list[min(i + lane, rows - 1)])});
+  for (int i = blockIdx.z * MOST; i < rows; i += gridDim.z * MOST)
+    body(a, Members{min(MOST, rows - i), int(list[min(i + lane, rows - 1)])});
 }
 
 // Row stride of v: whole 16 bytes, zeros behind the rank.
@@ -192,7 +194,7 @@ struct Piece {
 constexpr int kSteps = 2;
 
 // Partial v of MF x 16 members from `row` on over turns first, first + BY, ... below last.
-template <int MF, int RF, int BY>
+template <int MF, int RF, int BY, bool TINY>
 __device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const Members& m, int row, int rank0, int first,
                                             int last, f32x4 (&acc)[MF][RF]) {
   constexpr int ST = kSteps;
@@ -224,7 +226,7 @@ __device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const M
   if (c < last) {                        // the row's last columns: zeros past them
 #pragma unroll 1
     for (int64_t k = int64_t(c) * (32 * ST) + g8; k < p.C + g8; k += 32) {
-      const Columns cols(k, p.C);
+      const Columns<TINY> cols(k, p.C);
       const auto own = [&](Chunk v) {    // without the columns of the lane before
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -245,13 +247,13 @@ __device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const M
 
 // v of up to MF x 16 members: the waves share the columns, or (HALVES = 2) two of them
 // the columns of each half of the members, which keeps fewer sums in a wave.
-template <int MF, int RF, int HALVES>
+template <int MF, int RF, int HALVES, bool TINY>
 __device__ __forceinline__ void shrink_tile(const LoraProblem& p, int a, const Members& m, int split, int rank0,
                                             int first, int last, float* red) {
   constexpr int BY = 4 / HALVES, MW = MF / HALVES;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = wave / BY, part = wave % BY;
   f32x4 acc[MW][RF];
-  shrink_rows<MW, RF, BY>(p, a, m, half * MW * 16, rank0, first + part, last, acc);
+  shrink_rows<MW, RF, BY, TINY>(p, a, m, half * MW * 16, rank0, first + part, last, acc);
   // the waves' sums, added in wave order
 #pragma unroll
   for (int i = 0; i < MW; ++i)
@@ -274,7 +276,7 @@ __device__ __forceinline__ void shrink_tile(const LoraProblem& p, int a, const M
   __syncthreads();
 }
 
-template <int RF, bool FEW>
+template <int RF, bool FEW, bool TINY = false>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraProblem p, int rank_blocks) {
   // sums of 32 members of all waves, or of 64 members of two or four
   constexpr int SUMS = FEW ? 4 * 2 : RF == 4 ? 2 * 4 : 4 * 4;
@@ -287,11 +289,11 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraProblem p, i
   const int first = split * each, last = min(pieces, first + each);
   const auto body = [&](int a, const Members& m) {
     if (m.rows <= 16)
-      shrink_tile<1, RF, 1>(p, a, m, split, rank0, first, last, red);
+      shrink_tile<1, RF, 1, TINY>(p, a, m, split, rank0, first, last, red);
     else if (m.rows <= 32)
-      shrink_tile<2, RF, 1>(p, a, m, split, rank0, first, last, red);
+      shrink_tile<2, RF, 1, TINY>(p, a, m, split, rank0, first, last, red);
     else if constexpr (!FEW)
-      shrink_tile<4, RF, RF == 4 ? 2 : 1>(p, a, m, split, rank0, first, last, red);
+      shrink_tile<4, RF, RF == 4 ? 2 : 1, TINY>(p, a, m, split, rank0, first, last, red);
   };
   if constexpr (FEW)
     one_adapter<false, 32>(p, list[threadIdx.x >> 6], body);
@@ -324,65 +326,72 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 
 // -------------------------------------------------------------------- expand
 
-// v of the members (zeros in the rows up to a multiple of 16 behind them and in the
-// columns up to ld - 8 behind the rank), its partial sums added, times s, as two bf16
-// numbers each: hi and lo [64][ld].
-template <int THREADS>
-__device__ __forceinline__ void stage_v(const LoraProblem& p, const Members& m, float s, int ld, uint16_t* hi,
+// v of the members (zeros in the rows behind them and in the columns up to ld - 8 behind
+// the rank), its partial sums added, times s, as two bf16 numbers each: hi and lo [64][ld].
+// QUADS: 4 columns each of a row.  The loads of all rows are in flight together.
+template <int QUADS>
+__device__ __forceinline__ void stage_v(const LoraProblem& p, const Members& m, float s, int j0, int ld, uint16_t* hi,
                                         uint16_t* lo) {
-  const int quads = (ld - 8) / 4, rows = (m.rows + 15) / 16 * 16;
-  for (int i0 = 0; i0 < rows * quads; i0 += THREADS) {     // every lane takes part in m.at
-    const int i = i0 + threadIdx.x;
-    const int row = min(i / quads, kTile - 1), j = i % quads * 4;
-    const int64_t t = m.at(row);
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (row < m.rows && i < rows * quads && j < p.r) {
-      const float* at = p.v + t * v_columns(p.r) + j;
-      const int64_t next = p.T * v_columns(p.r);
-#pragma unroll 4
-      for (int k = 0; k < p.splits; ++k) {
-        float f[4];
-        unpack<float>(load_chunk(at + k * next), f);
+  constexpr int ITEMS = kTile * QUADS / 256;
+  float v[ITEMS][4];
+  const float* at[ITEMS];
+  bool in[ITEMS];
+  const int64_t next = p.T * v_columns(p.r);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += f[e];
-      }
+  for (int e = 0; e < ITEMS; ++e) {
+    const int i = e * 256 + threadIdx.x, row = i / QUADS, j = j0 + i % QUADS * 4;
+    in[e] = row < m.rows && j < p.r;
+    at[e] = p.v + int64_t(m.at(row)) * v_columns(p.r) + (j < p.r ? j : 0);
+    unpack<float>(load_chunk(at[e]), v[e]);
+  }
+#pragma unroll 4
+  for (int k = 1; k < p.splits; ++k)
+#pragma unroll
+    for (int e = 0; e < ITEMS; ++e) {
+      float f[4];
+      unpack<float>(load_chunk(at[e] + k * next), f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[e][i] += f[i];
     }
-    if (i < rows * quads) {
-      uint32_t h[2], l[2];
-      split2(v[0] * s, v[1] * s, h[0], l[0]);
-      split2(v[2] * s, v[3] * s, h[1], l[1]);
-      *reinterpret_cast<uint2*>(hi + row * ld + j) = make_uint2(h[0], h[1]);
-      *reinterpret_cast<uint2*>(lo + row * ld + j) = make_uint2(l[0], l[1]);
-    }
+#pragma unroll
+  for (int e = 0; e < ITEMS; ++e) {
+    const int i = e * 256 + threadIdx.x, to = i / QUADS * ld + j0 + i % QUADS * 4;
+    uint32_t h[2], l[2];
+    split2(in[e] ? v[e][0] * s : 0.0f, in[e] ? v[e][1] * s : 0.0f, h[0], l[0]);
+    split2(in[e] ? v[e][2] * s : 0.0f, in[e] ? v[e][3] * s : 0.0f, h[1], l[1]);
+    *reinterpret_cast<uint2*>(hi + to) = make_uint2(h[0], h[1]);
+    *reinterpret_cast<uint2*>(lo + to) = make_uint2(l[0], l[1]);
   }
 }
 
-// The panel's rows j .. j + 32 at a lane's columns, as fragments.
-__device__ __forceinline__ void load_panel(const LoraProblem& p, int a, int j, const Columns& c, bf16x8 (&b)[8]) {
-  Chunk w[8];
+// The panel's rows j .. j + 32 at a lane's columns.
+template <bool TINY>
+__device__ __forceinline__ void load_panel(const LoraProblem& p, int a, int j, const Columns<TINY>& c, Chunk (&w)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = j + (threadIdx.x >> 4 & 3) * 8 + i;
     w[i] = c.load(p.panels + (int64_t(a) * p.r + min(row, p.r - 1)) * p.C, p.C);
     if (row >= p.r) w[i] = Chunk{{0u, 0u, 0u, 0u}};
   }
-  transpose8(w, b);
+}
+
+// Base of 4 of the members from `row` on.
+template <bool NT, bool TINY>
+__device__ __forceinline__ void load_base(const LoraProblem& p, const Members& m, int row, const Columns<TINY>& c,
+                                          Chunk (&to)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    to[k] = c.template load<NT>(p.base + int64_t(m.at(row + (threadIdx.x >> 4 & 3) * 4 + k)) * p.ld_base, p.C);
 }
 
 // Columns c .. c + 8 of the members' rows, 16 rows at a time with the next ones' base in
-// flight.  KS: steps of 32 rank rows whose fragments stay in registers (0: any number,
-// read again for each 16 rows).
-template <int KS, bool NT>
-__device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const Members& m, const Columns& c, int ld,
-                                            const uint16_t* hi, const uint16_t* lo, bf16x8 (&b)[KS ? KS : 1][8]) {
+// flight (`next` holds the first ones').  KS: steps of 32 rank rows whose fragments stay
+// in registers (0: any number, read again for each 16 rows).
+template <int KS, bool NT, bool TINY>
+__device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const Members& m, const Columns<TINY>& c, int ld,
+                                            const uint16_t* hi, const uint16_t* lo, bf16x8 (&b)[KS ? KS : 1][8],
+                                            Chunk (&next)[4]) {
   const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
-  Chunk next[4];
-  const auto ask = [&](int i) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      next[k] = c.load<NT>(p.base + int64_t(m.at(i + g * 4 + k)) * p.ld_base, p.C);
-  };
-  if (p.base) ask(0);
   for (int i = 0; i < m.rows; i += 16) {
     f32x4 acc[8];                        // sums start from base
 #pragma unroll
@@ -392,7 +401,7 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
 #pragma unroll
       for (int q = 0; q < 8; ++q) acc[q][k] = f[q];
     }
-    if (p.base && i + 16 < m.rows) ask(i + 16);
+    if (p.base && i + 16 < m.rows) load_base<NT>(p, m, i + 16, c, next);
     const auto step = [&](int ks, const bf16x8 (&bf)[8]) {
       const int at = (i + l15) * ld + ks * 32 + g * 8;
       const bf16x8 l = *reinterpret_cast<const bf16x8*>(lo + at), h = *reinterpret_cast<const bf16x8*>(hi + at);
@@ -406,7 +415,9 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
       for (int ks = 0; ks < KS; ++ks) step(ks, b[ks]);
     } else {
       for (int ks = 0; ks * 32 < p.r; ++ks) {
-        load_panel(p, a, ks * 32, c, b[0]);
+        Chunk w[8];
+        load_panel(p, a, ks * 32, c, w);
+        transpose8(w, b[0]);
         step(ks, b[0]);
       }
     }
@@ -417,12 +428,12 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
       float y[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) y[q] = acc[q][k];
-      if (at < m.rows) c.store<NT>(p.out + row * p.ld_out, p.C, pack<uint16_t>(y));
+      if (at < m.rows) c.template store<NT>(p.out + row * p.ld_out, p.C, pack<uint16_t>(y));
     }
   }
 }
 
-template <int KS, bool FEW, bool NT>
+template <int KS, bool FEW, bool NT, bool TINY = false>
 __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, int column_blocks) {
   constexpr int MAX = (KS ? KS * 32 : kLoraMaxRank) + 8;
   __shared__ __attribute__((aligned(16))) uint16_t hi[kTile * MAX], lo[kTile * MAX];
@@ -430,7 +441,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, i
   const int lane = threadIdx.x & 63, ld = KS ? MAX : (p.r + 31) / 32 * 32 + 8;
   const int64_t first = int64_t(blockIdx.x % column_blocks) * 512 + (threadIdx.x >> 6) * 128;
   const bool idle = first >= p.C;        // whole waves, which still stage v
-  const Columns c(first + (lane & 15) * 8, p.C);
+  const Columns<TINY> c(first + (lane & 15) * 8, p.C);
   const auto body = [&](int a, const Members& m) {
     if (a < 0) {                         // no adapter: base alone
       if (p.base == p.out || idle) return;
@@ -443,16 +454,28 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, i
       }
       return;
     }
+    // all loads first: the panel's, the first base's, v's (two steps of a panel are turned
+    // at once, for the registers)
     bf16x8 b[KS ? KS : 1][8];
-    if constexpr (KS > 0) {
-      if (!idle) {
+    Chunk w[8], next[4];
+    if (!idle) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) load_panel(p, a, ks * 32, c, b[ks]);
+      for (int ks = 0; ks < KS; ++ks) {
+        load_panel(p, a, ks * 32, c, w);
+        if (KS > 1) transpose8(w, b[ks]);
       }
+      if (p.base) load_base<NT>(p, m, 0, c, next);
     }
-    stage_v<256>(p, m, p.scales ? p.scales[a] : 1.0f, ld, hi, lo);
+    const float s = p.scales ? p.scales[a] : 1.0f;
+    if constexpr (KS > 0)
+      stage_v<KS * 8>(p, m, s, 0, ld, hi, lo);
+    else
+      for (int j = 0; j < p.r; j += 32) stage_v<8>(p, m, s, j, ld, hi, lo);
     __syncthreads();
-    if (!idle) expand_rows<KS, NT>(p, a, m, c, ld, hi, lo, b);
+    if (!idle) {
+      if (KS == 1) transpose8(w, b[0]);
+      expand_rows<KS, NT>(p, a, m, c, ld, hi, lo, b, next);
+    }
     __syncthreads();
   };
   if constexpr (FEW)
@@ -497,6 +520,7 @@ __global__ __launch_bounds__(256) void lora_sort_kernel(const LoraProblem p, con
 }
 
 constexpr int kOuterRows = 32;           // tokens of a turn: one matrix step
+__host__ __device__ inline int64_t partial_size(int r, int64_t C) { return (r * C + 3) / 4 * 4; }
 
 // The first n of a lane's 8 values, zeros after them.
 __device__ __forceinline__ Chunk first_of(const Chunk& v, int n) {
@@ -520,7 +544,7 @@ struct Sides {
   unsigned blocks;
 };
 
-template <int RF>
+template <int RF, bool TINY = false>
 __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, const LoraOrder o, const Sides sides,
                                                          int rank_blocks) {
   const int lane = threadIdx.x & 63, l15 = lane & 15, g8 = (lane >> 4) * 8;
@@ -533,7 +557,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
   const int rank0 = rest % rank_blocks * kRankBlock, z = rest / rank_blocks;
   const int64_t first = int64_t(cb) * 512 + (threadIdx.x >> 6) * 128;
   if (first >= C) return;              // whole waves, which wait for no others
-  const Columns c(first + l15 * 8, C);
+  const Columns<TINY> c(first + l15 * 8, C);
   const int used = o.offsets[p.n - 1];   // rows that have an adapter
   const int z0 = int(min(int64_t(used), z * per)), z1 = int(min(int64_t(used), (z + 1) * per));
   if (z0 >= z1) return;
@@ -596,7 +620,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
         for (int q = 0; q < 8; ++q) acc[f][q] = mfma(h[f], b[q], acc[f][q]);
       }
     }
-    float* out = side.partial + int64_t(z + a) * p.r * C;
+    float* out = side.partial + (z + a) * partial_size(p.r, C);
 #pragma unroll
     for (int f = 0; f < RF; ++f)
 #pragma unroll
@@ -613,6 +637,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
 }
 
 // Adds an adapter's partial gradients in order, times its scale: four values a thread.
+// (Partial gradients start at whole 16 bytes.)
 // The first `split` of an adapter's workgroups take side 0.
 __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraProblem p, const LoraOrder o, const Sides sides,
                                                        unsigned split, unsigned blocks) {
@@ -628,10 +653,10 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraProblem p, cons
   const float scale = p.scales ? p.scales[a] : 1.0f;
   for (int64_t i = first * 4; i < count; i += step) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t z = z0; z < z1; ++z) {
       float f[4];
-      unpack<float>(load_row(side.partial + z * count, i, count), f);
+      unpack<float>(load_chunk(side.partial + z * partial_size(p.r, side.C) + i), f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[k] += f[k];
     }
@@ -653,7 +678,7 @@ int rank_blocks_of(int r) { return (r + kRankBlock - 1) / kRankBlock; }
 
 // Workgroups that share a tile's adapters: where there are few tiles.
 unsigned tile_groups(const LoraProblem& p) {
-  const int64_t most = p.T <= kTile ? p.T : p.T <= 512 ? 8 : p.T <= 1024 ? 4 : p.T <= 2048 ? 2 : 1;
+  const int64_t most = p.T <= kTile ? p.T : p.T <= 512 ? 16 : p.T <= 1024 ? 4 : p.T <= 2048 ? 2 : 1;
   return unsigned(p.n + 1 < most ? p.n + 1 : most);
 }
 
@@ -682,7 +707,7 @@ int lora_splits(int64_t T, int64_t C, int64_t n, int r) {
 }
 
 int64_t lora_outer_workspace(int64_t T, int64_t C, int64_t n, int r) {
-  return 4 * (outer_ranges(T, C, r) + n) * r * C;
+  return 4 * (outer_ranges(T, C, r) + n) * partial_size(r, C);
 }
 
 // Parts of the order's workspace: rows of tokens, tokens of rows (up to 31 past the last
@@ -723,14 +748,22 @@ hipError_t launch_lora_order(const LoraProblem& p, void* workspace, LoraOrder& o
   return hipGetLastError();
 }
 
+// Whether a launch goes adapter by adapter.  (Rows of less than 8 columns always go by
+// tiles: one kernel for them.)
+bool few(const LoraProblem& p) { return few_tokens(p.T, p.n) && p.C >= 8; }
+int64_t tiles_of(const LoraProblem& p) { return few(p) ? 1 : (p.T + kTile - 1) / kTile; }
+
 template <bool FEW>
 hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
   const int rb = rank_blocks_of(p.r);
-  const dim3 grid(unsigned(tiles_of(p.T, p.n) * p.splits * rb), FEW ? unsigned(by_tokens(p) ? p.T : p.n) : tile_groups(p));
+  const dim3 grid(unsigned(tiles_of(p) * p.splits * rb), FEW ? unsigned(by_tokens(p) ? p.T : p.n) : tile_groups(p),
+                  FEW ? 2 : 1);
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, rb);
     return hipGetLastError();
   };
+  if constexpr (!FEW)
+    if (p.C < 8) return run(lora_shrink_kernel<4, false, true>);
   if (p.r <= 16) return run(lora_shrink_kernel<1, FEW>);
   return p.r <= 32 ? run(lora_shrink_kernel<2, FEW>) : run(lora_shrink_kernel<4, FEW>);
 }
@@ -738,24 +771,27 @@ hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
 template <bool FEW, bool NT>
 hipError_t run_expand(const LoraProblem& p, hipStream_t st) {
   const int cb = int((p.C + 511) / 512);
-  const dim3 grid(unsigned(tiles_of(p.T, p.n) * cb), FEW ? unsigned(by_tokens(p) ? p.T : p.n + 1) : tile_groups(p));
+  const dim3 grid(unsigned(tiles_of(p) * cb), FEW ? unsigned(by_tokens(p) ? p.T : p.n + 1) : tile_groups(p),
+                  FEW ? 2 : 1);
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, cb);
     return hipGetLastError();
   };
+  if constexpr (!FEW && !NT)
+    if (p.C < 8) return run(lora_expand_kernel<0, false, false, true>);
   if (p.r <= 32) return run(lora_expand_kernel<1, FEW, NT>);
   return p.r <= 64 ? run(lora_expand_kernel<2, FEW, NT>) : run(lora_expand_kernel<0, FEW, NT>);
 }
 
 hipError_t launch_lora_shrink(const LoraProblem& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  return few_tokens(p.T, p.n) ? run_shrink<true>(p, st) : run_shrink<false>(p, st);
+  return few(p) ? run_shrink<true>(p, st) : run_shrink<false>(p, st);
 }
 
 hipError_t launch_lora_expand(const LoraProblem& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  if (few_tokens(p.T, p.n)) return run_expand<true, false>(p, st);
-  return p.T * p.C * 2 > kL2Bytes ? run_expand<false, true>(p, st) : run_expand<false, false>(p, st);
+  if (few(p)) return run_expand<true, false>(p, st);
+  return p.C >= 8 && p.T * p.C * 2 > kL2Bytes ? run_expand<false, true>(p, st) : run_expand<false, false>(p, st);
 }
 
 hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, const LoraSide (&side)[2], hipStream_t st) {
@@ -778,8 +814,11 @@ hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, const Lor
       hipLaunchKernelGGL(kernel, dim3(blocks[0] + blocks[1]), dim3(256), 0, st, p, o, sides, rb);
       return hipGetLastError();
     };
-    const hipError_t e =
-        p.r <= 16 ? run(lora_outer_kernel<1>) : p.r <= 32 ? run(lora_outer_kernel<2>) : run(lora_outer_kernel<4>);
+    const bool tiny = (side[0].grad && side[0].C < 8) || (side[1].grad && side[1].C < 8);
+    const hipError_t e = tiny        ? run(lora_outer_kernel<4, true>)
+                         : p.r <= 16 ? run(lora_outer_kernel<1>)
+                         : p.r <= 32 ? run(lora_outer_kernel<2>)
+                                     : run(lora_outer_kernel<4>);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(lora_sum_kernel, dim3(unsigned(p.n) * (sums[0] + sums[1])), dim3(256), 0, st, p, o, sides, sums[0],

@@ -549,7 +549,8 @@ def _check_lora_backward(dev, val, v, dy, dyv, scaled=True, grad="bf16"):
 LORA_SHAPES = [(1, 1, 1, 1, 1), (1, 64, 128, 3, 8), (3, 7, 130, 2, 5), (16, 513, 64, 70, 16), (63, 128, 1000, 3, 17),
                (64, 640, 513, 1, 32), (65, 130, 520, 4, 33), (200, 1000, 129, 70, 40), (256, 512, 512, 9, 64),
                (257, 260, 1030, 3, 65), (300, 2048, 1408, 5, 16), (130, 384, 640, 2, 130), (70, 256, 300, 2, 256),
-               (1000, 333, 257, 6, 16), (5, 5120, 1024, 2, 24)]
+               (1000, 333, 257, 6, 16), (5, 5120, 1024, 2, 24), (70, 3, 7, 2, 20), (90, 7, 64, 9, 64), (600, 8, 5, 3, 8),
+               (500, 264, 136, 40, 16), (300, 130, 70, 400, 9), (513, 72, 1090, 2, 128)]
 
 
 @pytest.mark.parametrize("T,K,N,n,r", LORA_SHAPES)
