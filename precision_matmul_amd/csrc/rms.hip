@@ -26,6 +26,51 @@ constexpr float kRowwiseEps = 1e-12f;   // the rowwise recipe's, as its quantize
 
 enum Form { ROWS = 0, BLOCKS = 1, WHOLE = 2 };   // codes: none, a scale per 128 columns, a scale per row
 
+// A lane's chunk at column c of a row of C >= kVec<T> elements, in two steps: the load, and,
+// when it is used, what of it is the lane's own, zeros behind that.  Only a lane's last
+// chunk (LAST) can reach past the row; the load is then of the row's last whole chunk, so
+// that no branch of the lanes stands between a row's loads, for which they would wait for
+// each other.  `first` is the column of the wave's first lane: waves past the end load
+// nothing (8000 x 5120 bf16 backward, 10 of 16 waves' chunks in use: 76 us, 85 if they do).
+template <typename T, bool NT, bool LAST>
+__device__ __forceinline__ Chunk ask_chunk(const T* row, int64_t first, int64_t c, int64_t C) {
+  if (LAST && first >= C) return Chunk{{0u, 0u, 0u, 0u}};
+  const T* p = row + (LAST ? min(c, C - kVec<T>) : c);
+  return NT ? load_chunk_nt(p) : load_chunk(p);
+}
+template <typename T, bool LAST>
+__device__ __forceinline__ Chunk own_chunk(const Chunk& v, int64_t c, int64_t C) {
+  if (!LAST) return v;
+  if (C % kVec<T> == 0) return c < C ? v : Chunk{{0u, 0u, 0u, 0u}};
+  const int n = int(min(max(c + kVec<T> - C, int64_t(0)), int64_t(kVec<T>))) * int(sizeof(T)) * 8;   // bits to drop
+  const uint64_t lo = uint64_t(v.w[1]) << 32 | v.w[0], hi = uint64_t(v.w[3]) << 32 | v.w[2];
+  const uint64_t a = n == 0 ? lo : n < 64 ? lo >> n | hi << (64 - n) : n < 128 ? hi >> (n - 64) : 0;
+  const uint64_t b = n < 64 ? hi >> n : 0;
+  return Chunk{{uint32_t(a), uint32_t(a >> 32), uint32_t(b), uint32_t(b >> 32)}};
+}
+
+// NIT chunks of a row, STEP columns apart; all but the last are within the row.
+template <typename T, bool NT, int NIT>
+__device__ __forceinline__ void ask_row(const T* row, int64_t first, int64_t c, int64_t step, int64_t C,
+                                        Chunk (&v)[NIT]) {
+#pragma unroll
+  for (int it = 0; it < NIT; ++it)
+    v[it] = it + 1 < NIT ? ask_chunk<T, NT, false>(row, 0, c + it * step, C)
+                         : ask_chunk<T, NT, true>(row, first + it * step, c + it * step, C);
+}
+template <typename T, int NIT>
+__device__ __forceinline__ void own_row(const Chunk (&v)[NIT], int64_t c, int64_t step, int64_t C, Chunk (&out)[NIT]) {
+#pragma unroll
+  for (int it = 0; it < NIT; ++it)
+    out[it] = it + 1 < NIT ? v[it] : own_chunk<T, true>(v[it], c + it * step, C);
+}
+
+// Column of the wave's first lane in its row, a scalar.
+template <int WPR>
+__device__ __forceinline__ int64_t wave_column(int vec) {
+  return WPR == 1 ? 0 : int64_t(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 64 * vec;
+}
+
 // N parameters at column c of C as float32; `none` without a vector, 0 past its end.
 template <int N>
 __device__ __forceinline__ void load_weight(const void* weight, bool fp32, int64_t c, int64_t C, float (&w)[N]) {
@@ -109,7 +154,7 @@ __device__ __forceinline__ Turns my_rows(int64_t R, int rpb, int wave) {
 // are the same in all rows that a workgroup takes, so it keeps its weights in
 // registers, and the next row is loaded while this one is reduced and written.
 // ---------------------------------------------------------------------------
-template <typename T, int FORM, int WPR, int NIT, bool NT, bool PART>
+template <typename T, int FORM, int WPR, int NIT, bool NT>
 __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void rms_kernel(const RmsProblem p) {
   constexpr int V = kVec<T>;
   constexpr int RPB = WPR == 1 ? 4 : 1;           // rows of a workgroup
@@ -117,7 +162,7 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void rms_kernel(const RmsProb
   __shared__ float part[2][WPR];
   __shared__ uint32_t top[2][WPR];
   const int in_row = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t c0 = int64_t(in_row) * V, C = p.C;
+  const int64_t c0 = int64_t(in_row) * V, C = p.C, w0 = wave_column<WPR>(V);
   const T* x = static_cast<const T*>(p.x);
   const T* res = static_cast<const T*>(p.residual);
   float w[NIT][V];
@@ -126,21 +171,20 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void rms_kernel(const RmsProb
   Turns t = my_rows(p.R, RPB, WPR == 1 ? threadIdx.x >> 6 : 0);
   Chunk nx[NIT], nr[NIT];
   const auto ask = [&](int64_t row) {
-#pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-      nx[it] = fetch<T, NT, PART>(x + row * p.ld_x, c0 + it * STEP, C);
-      if (res) nr[it] = fetch<T, NT, PART>(res + row * p.ld_res, c0 + it * STEP, C);
-    }
+    ask_row<T, NT>(x + row * p.ld_x, w0, c0, STEP, C, nx);
+    if (res) ask_row<T, NT>(res + row * p.ld_res, w0, c0, STEP, C, nr);
   };
   if (t.row < t.end) ask(t.row);
   int slot = 0;
   for (; t.row < t.end; t.row += t.stride, slot ^= 1) {   // all waves of a row take the same turns
     const int64_t row = t.row;
     Chunk v[NIT];
+    own_row<T>(nx, c0, STEP, C, v);
+    if (res) {
+      Chunk r[NIT];
+      own_row<T>(nr, c0, STEP, C, r);
 #pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-      v[it] = settle<T, PART>(nx[it], c0 + it * STEP, C);
-      if (res) v[it] = add_chunks<T>(v[it], settle<T, PART>(nr[it], c0 + it * STEP, C));
+      for (int it = 0; it < NIT; ++it) v[it] = add_chunks<T>(v[it], r[it]);
     }
     if (row + t.stride < t.end) ask(row + t.stride);
     float ss = 0.0f;
@@ -266,7 +310,7 @@ __global__ __launch_bounds__(256) void rms_long_kernel(const RmsProblem p) {
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 
-template <typename T, int WPR, int NIT, bool NT, bool PART>
+template <typename T, int WPR, int NIT, bool NT>
 __global__ __launch_bounds__(64 * (WPR == 1 ? kRowWaves : WPR)) void rms_backward_kernel(const RmsProblem p,
                                                                                          float* partial) {
   constexpr int V = kVec<T>;
@@ -276,7 +320,7 @@ __global__ __launch_bounds__(64 * (WPR == 1 ? kRowWaves : WPR)) void rms_backwar
   constexpr int Q = NIT * V / 4;                  // a lane's sums, in fours
   __shared__ float4 acc[WPR == 1 ? kRowWaves / 2 * Q * 64 : 1];
   const int wave = threadIdx.x >> 6;
-  const int64_t c0 = int64_t(WPR == 1 ? threadIdx.x & 63 : threadIdx.x) * V, C = p.C;
+  const int64_t c0 = int64_t(WPR == 1 ? threadIdx.x & 63 : threadIdx.x) * V, C = p.C, w0 = wave_column<WPR>(V);
   const T* hs = static_cast<const T*>(p.h_in);
   const T* dys = static_cast<const T*>(p.dy);
   const T* ghs = static_cast<const T*>(p.grad_h);
@@ -293,23 +337,17 @@ __global__ __launch_bounds__(64 * (WPR == 1 ? kRowWaves : WPR)) void rms_backwar
   Chunk nh[NIT], ng[NIT], ns[NIT];
   float nrstd = 0.0f;
   const auto ask = [&](int64_t at) {
-#pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-      nh[it] = fetch<T, NT, PART>(hs + at * p.ld_h, c0 + it * STEP, C);
-      ng[it] = fetch<T, NT, PART>(dys + at * p.ld_dy, c0 + it * STEP, C);
-      if (ghs) ns[it] = fetch<T, NT, PART>(ghs + at * p.ld_gh, c0 + it * STEP, C);
-    }
+    ask_row<T, NT>(hs + at * p.ld_h, w0, c0, STEP, C, nh);
+    ask_row<T, NT>(dys + at * p.ld_dy, w0, c0, STEP, C, ng);
+    if (ghs) ask_row<T, NT>(ghs + at * p.ld_gh, w0, c0, STEP, C, ns);
     nrstd = p.rstd[at];
   };
   if (row < p.R) ask(row);
   for (int slot = 0; row < p.R; row += stride, slot ^= 1) {
     Chunk vh[NIT], vg[NIT], vs[NIT];
-#pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-      vh[it] = settle<T, PART>(nh[it], c0 + it * STEP, C);
-      vg[it] = settle<T, PART>(ng[it], c0 + it * STEP, C);
-      if (ghs) vs[it] = settle<T, PART>(ns[it], c0 + it * STEP, C);
-    }
+    own_row<T>(nh, c0, STEP, C, vh);
+    own_row<T>(ng, c0, STEP, C, vg);
+    if (ghs) own_row<T>(ns, c0, STEP, C, vs);
     const float rstd = nrstd;
     if (row + stride < p.R) ask(row + stride);
     float sah = 0.0f;
@@ -400,17 +438,20 @@ __global__ __launch_bounds__(256) void rms_backward_few_kernel(const RmsProblem 
     constexpr int64_t STEP = int64_t(WPR) * 64 * V;
     const int64_t row = WPR == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
     if (row >= p.R) return;                     // WPR = 1: waves of their own; else never
-    const int64_t c0 = int64_t(WPR == 1 ? threadIdx.x & 63 : threadIdx.x) * V;
-    Chunk vh[NIT], vg[NIT], vs[NIT];
+    const int64_t c0 = int64_t(WPR == 1 ? threadIdx.x & 63 : threadIdx.x) * V, w0 = wave_column<WPR>(V);
+    Chunk nh[NIT], ng[NIT], ns[NIT], vh[NIT], vg[NIT], vs[NIT];
     float w[NIT][V];
+    ask_row<T, false>(hs + row * p.ld_h, w0, c0, STEP, C, nh);
+    ask_row<T, false>(dys + row * p.ld_dy, w0, c0, STEP, C, ng);
+    if (p.grad_h) ask_row<T, false>(static_cast<const T*>(p.grad_h) + row * p.ld_gh, w0, c0, STEP, C, ns);
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
-      vh[it] = load_row(hs + row * p.ld_h, c0 + it * STEP, C);
-      vg[it] = load_row(dys + row * p.ld_dy, c0 + it * STEP, C);
-      vs[it] = p.grad_h ? load_row(static_cast<const T*>(p.grad_h) + row * p.ld_gh, c0 + it * STEP, C)
-                        : Chunk{{0u, 0u, 0u, 0u}};
+      vs[it] = Chunk{{0u, 0u, 0u, 0u}};
       load_weight(p.weight, p.param_fp32, c0 + it * STEP, C, w[it]);
     }
+    own_row<T>(nh, c0, STEP, C, vh);
+    own_row<T>(ng, c0, STEP, C, vg);
+    if (p.grad_h) own_row<T>(ns, c0, STEP, C, vs);
     const float rstd = p.rstd[row];
     float sah = 0.0f;
 #pragma unroll
@@ -443,8 +484,8 @@ __global__ __launch_bounds__(256) void rms_backward_few_kernel(const RmsProblem 
 #pragma unroll 4
   for (int64_t row = slice; row < p.R; row += SLICES) {
     float f[V], g[V];
-    unpack<T>(load_row(hs + row * p.ld_h, c, C), f);
-    unpack<T>(load_row(dys + row * p.ld_dy, c, C), g);
+    unpack<T>(own_chunk<T, true>(ask_chunk<T, false, true>(hs + row * p.ld_h, 0, c, C), c, C), f);
+    unpack<T>(own_chunk<T, true>(ask_chunk<T, false, true>(dys + row * p.ld_dy, 0, c, C), c, C), g);
     const float rstd = p.rstd[row];
 #pragma unroll
     for (int i = 0; i < V; ++i) dw[i] = fmaf(g[i], f[i] * rstd, dw[i]);
@@ -552,7 +593,9 @@ constexpr int kBackwardGrid = 512;      // partial rows at most
 constexpr int64_t kRegisterCols = 8192; // longest row kept in registers
 constexpr int64_t kFewRows = 512;       // rows at most of the backward in one launch
 
-bool few_rows(int64_t R, int64_t C) { return R <= kFewRows && C <= kRegisterCols; }
+// Rows that the long rows' kernels take: those, and rows of less than a chunk.
+bool long_rows(int64_t C) { return C < 8 || C > kRegisterCols; }
+bool few_rows(int64_t R, int64_t C) { return R <= kFewRows && !long_rows(C); }
 
 // Workgroups of the long rows' kernels, which take further rows in turns past this.
 dim3 row_grid(int64_t rows) { return dim3(unsigned(rows < (1 << 20) ? rows : (1 << 20))); }
@@ -577,73 +620,88 @@ hipError_t run_rms(const RmsProblem& p, hipStream_t st) {
     hipLaunchKernelGGL(kernel, grid, dim3(WPR == 8 ? 512 : 256), 0, st, p);
     return hipGetLastError();
   };
-  // rows that end within a chunk (no row of codes does)
-  if (FORM == ROWS && WPR > 1 && p.C % kVec<T> != 0)
-    return streams(p, sizeof(T)) ? run(rms_kernel<T, FORM, WPR, NIT, true, FORM == ROWS && (WPR > 1)>)
-                                 : run(rms_kernel<T, FORM, WPR, NIT, false, FORM == ROWS && (WPR > 1)>);
-  return streams(p, sizeof(T)) ? run(rms_kernel<T, FORM, WPR, NIT, true, false>)
-                               : run(rms_kernel<T, FORM, WPR, NIT, false, false>);
+  return streams(p, sizeof(T)) ? run(rms_kernel<T, FORM, WPR, NIT, true>) : run(rms_kernel<T, FORM, WPR, NIT, false>);
 }
 
 template <typename T, int FORM>
 hipError_t rms_typed(const RmsProblem& p, hipStream_t st) {
   constexpr int64_t S = 64 * kVec<T>;   // columns of one wave chunk
+  if (long_rows(p.C)) {
+    hipLaunchKernelGGL((rms_long_kernel<T, FORM>), row_grid(p.R), dim3(256), 0, st, p);
+    return hipGetLastError();
+  }
   if (p.C <= S) return run_rms<T, FORM, 1, 1>(p, st);
   if (p.C <= 2 * S) return run_rms<T, FORM, 1, 2>(p, st);
-  if (p.C <= 4 * S) return run_rms<T, FORM, 1, 4>(p, st);
+  // bf16: four waves a row (16384 x 2048 49.5 us, by single waves 52.5; with codes 16000 x
+  // 1920 50 against 55); fp32: a wave a row (16384 x 700 18 us, by four 29)
+  if constexpr (sizeof(T) == 2) {
+    if (p.C <= 4 * S) return run_rms<T, FORM, 4, 1>(p, st);
+  } else {
+    if (p.C <= 3 * S) return run_rms<T, FORM, 1, 3>(p, st);
+    if (p.C <= 4 * S) return run_rms<T, FORM, 1, 4>(p, st);
+  }
   if (p.C <= 8 * S) return run_rms<T, FORM, 4, 2>(p, st);
   if (p.C <= 12 * S) return run_rms<T, FORM, 4, 3>(p, st);
   if constexpr (sizeof(T) == 2) {   // 16 S is 8192 columns of bf16, 4096 of fp32
-    if (p.C <= 16 * S) return run_rms<T, FORM, 8, 2>(p, st);
+    return run_rms<T, FORM, 8, 2>(p, st);
   } else {
     if (p.C <= 16 * S) return run_rms<T, FORM, 4, 4>(p, st);
     if (p.C <= 24 * S) return run_rms<T, FORM, 8, 3>(p, st);
-    if (p.C <= 32 * S) return run_rms<T, FORM, 8, 4>(p, st);
+    return run_rms<T, FORM, 8, 4>(p, st);
   }
-  hipLaunchKernelGGL((rms_long_kernel<T, FORM>), row_grid(p.R), dim3(256), 0, st, p);
+}
+
+template <typename T, int WPR, int NIT>
+hipError_t run_few(const RmsProblem& p, hipStream_t st) {
+  const int64_t rows = p.dx ? (WPR == 1 ? (p.R + 3) / 4 : p.R) : 0;
+  constexpr int STRIP = kStripChunks<WPR> * kVec<T>;
+  const int64_t strips = p.dweight ? (p.C + STRIP - 1) / STRIP : 0;
+  hipLaunchKernelGGL((rms_backward_few_kernel<T, WPR, NIT>), dim3(unsigned(rows + strips)), dim3(256), 0, st, p,
+                     unsigned(rows));
   return hipGetLastError();
+}
+
+// All chunks of a lane but the last are within the row: as many as it takes, no more.
+template <typename T>
+hipError_t few_typed(const RmsProblem& p, hipStream_t st) {
+  constexpr int64_t S = 64 * kVec<T>;
+  switch (p.C <= 4 * S ? (p.C + S - 1) / S : 10 + (p.C + 4 * S - 1) / (4 * S)) {
+    case 1: return run_few<T, 1, 1>(p, st);
+    case 2: return run_few<T, 1, 2>(p, st);
+    case 3: return run_few<T, 1, 3>(p, st);
+    case 4: return run_few<T, 1, 4>(p, st);
+    case 12: return run_few<T, 4, 2>(p, st);
+    case 13: return run_few<T, 4, 3>(p, st);
+    case 14: return run_few<T, 4, 4>(p, st);
+  }
+  if constexpr (sizeof(T) == 4) {        // up to 8192 columns
+    switch ((p.C + 4 * S - 1) / (4 * S)) {
+      case 5: return run_few<T, 4, 5>(p, st);
+      case 6: return run_few<T, 4, 6>(p, st);
+      case 7: return run_few<T, 4, 7>(p, st);
+      case 8: return run_few<T, 4, 8>(p, st);
+    }
+  }
+  return hipErrorInvalidValue;           // no row of kRegisterCols columns or fewer comes here
 }
 
 template <typename T, int WPR, int NIT>
 hipError_t run_backward(const RmsProblem& p, int grid, float* partial, hipStream_t st) {
-  if (few_rows(p.R, p.C)) {
-    const int64_t rows = p.dx ? (WPR == 1 ? (p.R + 3) / 4 : p.R) : 0;
-    constexpr int W = WPR == 1 ? 1 : 4, STRIP = kStripChunks<W> * kVec<T>;
-    const int64_t strips = p.dweight ? (p.C + STRIP - 1) / STRIP : 0;
-    hipLaunchKernelGGL((rms_backward_few_kernel<T, W, NIT * WPR / W>), dim3(unsigned(rows + strips)), dim3(256), 0, st,
-                       p, unsigned(rows));
-    return hipGetLastError();
-  }
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * (WPR == 1 ? kRowWaves : WPR)), 0, st, p, partial);
     return hipGetLastError();
   };
-  constexpr bool MANY = WPR > 1;
-  if (streams(p, sizeof(T))) return run(rms_backward_kernel<T, WPR, NIT, true, MANY>);
-  return MANY && p.C % kVec<T> != 0 ? run(rms_backward_kernel<T, WPR, NIT, false, MANY>)
-                                    : run(rms_backward_kernel<T, WPR, NIT, false, false>);
+  return streams(p, sizeof(T)) ? run(rms_backward_kernel<T, WPR, NIT, true>) : run(rms_backward_kernel<T, WPR, NIT, false>);
 }
 
 template <typename T>
 hipError_t backward_typed(const RmsProblem& p, hipStream_t st) {
   constexpr int64_t S = 64 * kVec<T>;
+  if (few_rows(p.R, p.C)) return few_typed<T>(p, st);
   const int grid = backward_grid(p.R, p.C, kVec<T>);
-  float* partial = p.dweight && !few_rows(p.R, p.C) ? p.workspace : nullptr;
+  float* partial = p.dweight ? p.workspace : nullptr;
   hipError_t e = hipSuccess;
-  if (p.C <= S) {
-    e = run_backward<T, 1, 1>(p, grid, partial, st);
-  } else if (p.C <= 2 * S) {
-    e = run_backward<T, 1, 2>(p, grid, partial, st);
-  } else if (p.C <= 4 * S) {
-    e = run_backward<T, 1, 4>(p, grid, partial, st);
-  } else if (p.C <= 8 * S) {
-    e = run_backward<T, 4, 2>(p, grid, partial, st);
-  } else if (p.C <= 16 * S) {
-    e = run_backward<T, 8, 2>(p, grid, partial, st);
-  } else if (sizeof(T) == 4 && p.C <= kRegisterCols) {
-    if constexpr (sizeof(T) == 4)
-      e = p.C <= 24 * S ? run_backward<T, 8, 3>(p, grid, partial, st) : run_backward<T, 8, 4>(p, grid, partial, st);
-  } else {
+  if (long_rows(p.C)) {
     if (p.dx) {
       hipLaunchKernelGGL((rms_backward_long_kernel<T>), row_grid(p.R), dim3(256), 0, st, p);
       e = hipGetLastError();
@@ -653,6 +711,20 @@ hipError_t backward_typed(const RmsProblem& p, hipStream_t st) {
                          partial);
       e = hipGetLastError();
     }
+  } else if (p.C <= S) {
+    e = run_backward<T, 1, 1>(p, grid, partial, st);
+  } else if (p.C <= 2 * S) {
+    e = run_backward<T, 1, 2>(p, grid, partial, st);
+  } else if (p.C <= 3 * S) {
+    e = run_backward<T, 1, 3>(p, grid, partial, st);
+  } else if (p.C <= 4 * S) {
+    e = run_backward<T, 1, 4>(p, grid, partial, st);
+  } else if (p.C <= 8 * S) {
+    e = run_backward<T, 4, 2>(p, grid, partial, st);
+  } else if (p.C <= 16 * S) {
+    e = run_backward<T, 8, 2>(p, grid, partial, st);
+  } else if constexpr (sizeof(T) == 4) {
+    e = p.C <= 24 * S ? run_backward<T, 8, 3>(p, grid, partial, st) : run_backward<T, 8, 4>(p, grid, partial, st);
   }
   if (e != hipSuccess || !partial) return e;
   hipLaunchKernelGGL(rms_column_sum_kernel, dim3(unsigned((p.C + 63) / 64)), dim3(1024), 0, st, partial, grid, p.C,
