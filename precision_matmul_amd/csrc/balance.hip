@@ -43,25 +43,28 @@ __device__ __forceinline__ float reciprocal(float d) {
   return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
-// Four logits at column c of E; -inf past the end.  Where E is a multiple of four, without
-// a branch of the lanes, so that loads of several pieces are in flight together.
+// Four logits at column c of E; -inf past the end.  Without a branch of the lanes (the
+// last four columns in place of what reaches past them, moved up), so that loads of
+// several pieces are in flight together.
 template <typename T>
 __device__ __forceinline__ void load4(const T* row, int c, int E, float (&f)[4]) {
   struct __attribute__((packed, aligned(sizeof(T)))) At {
     T v[4];
   };
-  if (E % 4 == 0) {
-    const At a = *reinterpret_cast<const At*>(row + min(c, E - 4));
+  const float none = -__builtin_inff();
+  if (E < 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = c < E ? to_float(a.v[i]) : -__builtin_inff();
-  } else if (c + 4 <= E) {
-    const At a = *reinterpret_cast<const At*>(row + c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = to_float(a.v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = c + i < E ? to_float(row[c + i]) : -__builtin_inff();
+    for (int i = 0; i < 4; ++i) f[i] = c + i < E ? to_float(row[c + i]) : none;
+    return;
   }
+  const int at = min(c, E - 4), n = c - at;
+  const At a = *reinterpret_cast<const At*>(row + at);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = n < 4 ? to_float(a.v[i]) : none;
+  if (E % 4 == 0) return;
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (n > k && n < 4) f[0] = f[1], f[1] = f[2], f[2] = f[3], f[3] = none;
 }
 
 template <typename T>
@@ -422,7 +425,8 @@ __global__ __launch_bounds__(kBackThreads) void balance_backward_kernel(const Ba
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int e = (q * L + lane) * 4 + i;
-        c[q][i] = e < p.E ? p.counts[int64_t(s) * p.E + e] : 0;
+        const int count = p.counts[int64_t(s) * p.E + min(e, p.E - 1)];
+        c[q][i] = e < p.E ? count : 0;
       }
     const float inv = 1.0f / float(max(p.tokens[s], 1));
     const float d = whole * inv * inv;

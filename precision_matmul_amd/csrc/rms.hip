@@ -615,7 +615,10 @@ template <typename T, int FORM, int WPR, int NIT>
 hipError_t run_rms(const RmsProblem& p, hipStream_t st) {
   constexpr int RPB = WPR == 1 ? 4 : 1;
   const int64_t blocks = (p.R + RPB - 1) / RPB;
-  const dim3 grid(xcd_grid(blocks < kForwardGrid ? blocks : kForwardGrid));
+  // six workgroups a compute unit where a lane has one chunk (16384 x 2048 without a
+  // residual 25.5 us, with four 29)
+  constexpr int64_t MOST = WPR == 4 && NIT == 1 ? 1536 : kForwardGrid;
+  const dim3 grid(xcd_grid(blocks < MOST ? blocks : MOST));
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(WPR == 8 ? 512 : 256), 0, st, p);
     return hipGetLastError();
@@ -632,14 +635,10 @@ hipError_t rms_typed(const RmsProblem& p, hipStream_t st) {
   }
   if (p.C <= S) return run_rms<T, FORM, 1, 1>(p, st);
   if (p.C <= 2 * S) return run_rms<T, FORM, 1, 2>(p, st);
-  // bf16: four waves a row (16384 x 2048 49.5 us, by single waves 52.5; with codes 16000 x
-  // 1920 50 against 55); fp32: a wave a row (16384 x 700 18 us, by four 29)
-  if constexpr (sizeof(T) == 2) {
-    if (p.C <= 4 * S) return run_rms<T, FORM, 4, 1>(p, st);
-  } else {
-    if (p.C <= 3 * S) return run_rms<T, FORM, 1, 3>(p, st);
-    if (p.C <= 4 * S) return run_rms<T, FORM, 1, 4>(p, st);
-  }
+  if (p.C <= 3 * S) return run_rms<T, FORM, 1, 3>(p, st);
+  // bf16: four waves a row (16384 x 2048 46.5 us, by single waves 50; 4000 x 2048 with codes
+  // 12.5 and 15); fp32: a wave a row
+  if (p.C <= 4 * S) return run_rms<T, FORM, sizeof(T) == 2 ? 4 : 1, sizeof(T) == 2 ? 1 : 4>(p, st);
   if (p.C <= 8 * S) return run_rms<T, FORM, 4, 2>(p, st);
   if (p.C <= 12 * S) return run_rms<T, FORM, 4, 3>(p, st);
   if constexpr (sizeof(T) == 2) {   // 16 S is 8192 columns of bf16, 4096 of fp32
