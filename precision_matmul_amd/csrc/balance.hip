@@ -194,8 +194,7 @@ __device__ __forceinline__ float loss_of(const BalanceProblem& p, float term, in
 
 // The tokens in runs: their probabilities summed over the tokens of each run, their slots
 // counted.  L lanes hold a token; a token is loaded before it is known which run it is in.
-// ONE: the batch is one sequence of few tokens and one workgroup, which then gives the
-// loss itself.
+// ONE: few tokens, a workgroup for each sequence, which then gives its loss itself.
 template <typename T, int L, int NQ, bool SIGMOID, bool ONE>
 __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem p, const Partials part) {
   constexpr int SLOTS = kThreads / L;    // tokens of a turn
@@ -204,7 +203,9 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem 
   __shared__ int32_t counts[COLS], tokens;
   __shared__ float loss_part[16];
   const int lane = threadIdx.x % L, slot = threadIdx.x / L;
-  const int64_t b = blockIdx.x, r0 = b * part.rows, r1 = ONE ? p.T : min(p.T, r0 + part.rows);
+  const int64_t b = ONE ? 0 : blockIdx.x;
+  const int64_t r0 = !ONE ? b * part.rows : p.ends && blockIdx.x ? max(p.ends[blockIdx.x - 1], 0) : 0;
+  const int64_t r1 = !ONE ? min(p.T, r0 + part.rows) : p.ends ? min(int64_t(p.ends[blockIdx.x]), p.T) : p.T;
   float acc[NQ][4];
   int mine = 0;
   const auto clear = [&] {
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem 
       for (int i = 0; i < WAVES; ++i) v += sums[i][c];
       if constexpr (ONE) {
         if (c < p.E) {
-          p.counts[c] = counts[c];
+          p.counts[int64_t(blockIdx.x) * p.E + c] = counts[c];
           term = float(counts[c]) * v;
         }
       } else {
@@ -248,8 +249,8 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem 
     if constexpr (ONE) term = block_sum(term, loss_part);
     if (threadIdx.x == 0) {
       if constexpr (ONE) {
-        p.tokens[0] = tokens;
-        *p.loss = loss_of(p, term, tokens);
+        p.tokens[blockIdx.x] = tokens;
+        *(p.S == 1 ? p.loss : part.losses + blockIdx.x) = loss_of(p, term, tokens);
       } else {
         part.n[run] = tokens;
       }
@@ -266,11 +267,11 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem 
     for (int q = 0; q < NQ; ++q) load4(x, (q * L + lane) * 4, p.E, raw[q]);
     raw_id = p.ids[at * p.k + min(lane, p.k - 1)];
   };
-  const int my_end = lane_end(p);
-  ask(r0 + slot);
+  const int my_end = ONE ? 0 : lane_end(p);
+  if (r0 < r1) ask(r0 + slot);
   clear();
   int s = ONE ? 0 : sequence_of(p, my_end, r0);
-  int64_t begin = r0, end = s < p.S ? end_of(s) : r0;    // the rest of this run
+  int64_t begin = r0, end = ONE ? r1 : s < p.S ? end_of(s) : r0;    // the rest of this run
   for (int64_t turn = r0; turn < r1; turn += SLOTS) {
     const int64_t row = turn + slot, next = min(turn + SLOTS, r1);
     float f[NQ][4];
@@ -403,93 +404,117 @@ __global__ __launch_bounds__(1024) void balance_mean_kernel(const BalanceProblem
   if (threadIdx.x == 0) *p.loss = alive ? v / float(alive) : 0.0f;
 }
 
+// Gradient: L lanes hold a token, loaded a turn ahead; its sequence's counts are loaded
+// when they are not those of the lanes' token before.
 template <typename T, int L, int NQ, bool SIGMOID>
 __global__ __launch_bounds__(kBackThreads) void balance_backward_kernel(const BalanceProblem p, int64_t rows) {
   constexpr int SLOTS = kBackThreads / L;
-  const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+  const int lane = threadIdx.x % L, slot = threadIdx.x / L, wave_lane = threadIdx.x & 63;
   const int64_t r0 = int64_t(blockIdx.x) * rows, r1 = min(p.T, r0 + rows);
   const int my_end = lane_end(p);
-  int alive = 0;                         // sequences with tokens, counted by every wave for itself
-  for (int s = 0; s < p.S; s += 64) {
-    const int at = s + int(threadIdx.x & 63);
+  const int my_tokens = wave_lane < p.S ? p.tokens[wave_lane] : 0;
+  float raw[NQ][4];
+  const auto ask = [&](int64_t row) {    // past the chunk: its last row, which is not used
+    const T* x = static_cast<const T*>(p.logits) + min(row, r1 - 1) * p.ld;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) load4(x, (q * L + lane) * 4, p.E, raw[q]);
+  };
+  ask(r0 + slot);
+  int alive = __popcll(__ballot(my_tokens > 0));         // sequences with tokens
+  for (int s = 64; s < p.S; s += 64) {
+    const int at = s + wave_lane;
     alive += __popcll(__ballot(at < p.S && p.tokens[min(at, p.S - 1)] > 0));
   }
   const float whole = *p.grad_loss * p.coeff * float(p.E) / (float(p.k) * float(max(alive, 1)));
-  int64_t begin = r0;
-  for (int s = sequence_of(p, my_end, r0); s < p.S && begin < r1; ++s) {
-    const int64_t end = p.ends ? min(int64_t(p.ends[s]), r1) : r1;
-    if (end <= begin) continue;
-    int c[NQ][4];
+  int c[NQ][4], of = -1;                 // counts of the sequence `of`
+  float d = 0.0f;
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[q][i] = 0;
+  for (int64_t turn = r0; turn < r1; turn += SLOTS) {
+    const int64_t row = turn + slot;
+    float f[NQ][4], u[NQ][4];
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = (q * L + lane) * 4 + i;
-        const int count = p.counts[int64_t(s) * p.E + min(e, p.E - 1)];
-        c[q][i] = e < p.E ? count : 0;
+      for (int i = 0; i < 4; ++i) f[q][i] = raw[q][i];
+    if (turn + SLOTS < r1) ask(row + SLOTS);
+    int s = 0;                           // the token's sequence; S behind the last
+    if (p.ends && p.S <= 64) {
+#pragma unroll
+      for (int k = 0; k < 64 / L; ++k) { // the wave's tokens
+        const int64_t other = row - slot + (threadIdx.x >> 6) * (64 / L) + k;
+        const int before = __popcll(__ballot(my_end <= other));
+        s = wave_lane / L == k ? before : s;
       }
-    const float inv = 1.0f / float(max(p.tokens[s], 1));
-    const float d = whole * inv * inv;
-    for (int64_t row = begin + slot; row < end; row += SLOTS) {
-      const T* x = static_cast<const T*>(p.logits) + row * p.ld;
-      float f[NQ][4], u[NQ][4];
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        load4(x, (q * L + lane) * 4, p.E, f[q]);
-        if constexpr (SIGMOID) {         // 1 - sigmoid(x)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            {
-            const float e = exp_down(-fabsf(f[q][i]));
-            u[q][i] = (f[q][i] > 0.0f ? e : 1.0f) * reciprocal(1.0f + e);
-          }
-        }
-      }
-      const bool used = probabilities<L, NQ, SIGMOID>(f);
-      float top = 0.0f;
+    } else if (p.ends) {
+      s = sequence_of(p, my_end, row);
+    }
+    if (__any(s != of)) {
+      const int at = min(s, p.S - 1);
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, f[q][i]);
-      top = max_of<L>(top);
-      int ref = -1;                      // the most probable expert's count (the largest, of equals)
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ref = f[q][i] == top ? max(ref, c[q][i]) : ref;
-      ref = int(L == 64 ? wave_max_u(uint32_t(ref + 1)) : row_max_u(uint32_t(ref + 1))) - 1;
-      float mean = 0.0f;
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mean = fmaf(f[q][i], float(c[q][i] - ref), mean);
-      mean = sum_of<L>(mean);
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        float g[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          g[i] = f[q][i] * (float(c[q][i] - ref) - mean) * d;
-          if constexpr (SIGMOID) g[i] *= u[q][i];
-          if (!used) g[i] = 0.0f;
+          const int e = (q * L + lane) * 4 + i;
+          const int count = p.counts[int64_t(at) * p.E + min(e, p.E - 1)];
+          c[q][i] = e < p.E ? count : 0;
         }
-        store4(static_cast<T*>(p.grad_logits) + row * p.ld_grad, (q * L + lane) * 4, p.E, g);
-      }
+      const int n = p.S <= 64 ? __shfl(my_tokens, at, 64) : p.tokens[at];
+      const float inv = 1.0f / float(max(n, 1));
+      d = whole * inv * inv;
+      of = s;
     }
-    begin = end;
-  }
-  const float zeros[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t row = begin + slot; row < r1; row += SLOTS)   // rows behind the last sequence
+    if constexpr (SIGMOID) {             // 1 - sigmoid(x)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = exp_down(-fabsf(f[q][i]));
+          u[q][i] = (f[q][i] > 0.0f ? e : 1.0f) * reciprocal(1.0f + e);
+        }
+    }
+    const bool used = probabilities<L, NQ, SIGMOID>(f) && s < p.S;
+    float top = 0.0f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
-      store4(static_cast<T*>(p.grad_logits) + row * p.ld_grad, (q * L + lane) * 4, p.E, zeros);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, f[q][i]);
+    top = max_of<L>(top);
+    int ref = -1;                        // the most probable expert's count (the largest, of equals)
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ref = f[q][i] == top ? max(ref, c[q][i]) : ref;
+    ref = int(L == 64 ? wave_max_u(uint32_t(ref + 1)) : row_max_u(uint32_t(ref + 1))) - 1;
+    float mean = 0.0f;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mean = fmaf(f[q][i], float(c[q][i] - ref), mean);
+    mean = sum_of<L>(mean);
+    if (row >= r1) continue;             // (the wave's other tokens may be there)
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float g[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        g[i] = f[q][i] * (float(c[q][i] - ref) - mean) * d;
+        if constexpr (SIGMOID) g[i] *= u[q][i];
+        if (!used) g[i] = 0.0f;          // padding, and rows behind the last sequence
+      }
+      store4(static_cast<T*>(p.grad_logits) + row * p.ld_grad, (q * L + lane) * 4, p.E, g);
+    }
+  }
 }
 
 // Tokens of a chunk of the forward: at most 256 chunks, each a few turns.
 int64_t chunk_rows(int64_t T) { return T > 256 * 64 ? (T + 255) / 256 : 64; }
 int64_t chunks(int64_t T) { return T ? (T + chunk_rows(T) - 1) / chunk_rows(T) : 0; }
-// One sequence of so few tokens that one workgroup does it all, without a workspace.
-bool one_group(int64_t T, int64_t S) { return S == 1 && T > 0 && T <= 256; }
+// So few tokens that a workgroup takes a sequence, whatever their lengths: without partial
+// sums (one sequence: without a workspace).
+bool one_group(int64_t T, int64_t S) { return T <= (S == 1 ? 256 : 1024); }
 int padded(int64_t E) { return int((E + 3) / 4 * 4); }
 
 constexpr int64_t kBackwardRows = 32;    // tokens of a workgroup of the backward at least
@@ -508,7 +533,7 @@ hipError_t forward_typed(const BalanceProblem& p, const Partials& part, hipStrea
   return by_experts(p.E, [&](auto L, auto NQ) {
     constexpr int l = decltype(L)::value, nq = decltype(NQ)::value;
     if (one_group(p.T, p.S))
-      hipLaunchKernelGGL((balance_kernel<T, l, nq, SIGMOID, true>), dim3(1), dim3(kThreads), 0, st, p, part);
+      hipLaunchKernelGGL((balance_kernel<T, l, nq, SIGMOID, true>), dim3(unsigned(p.S)), dim3(kThreads), 0, st, p, part);
     else
       hipLaunchKernelGGL((balance_kernel<T, l, nq, SIGMOID, false>), dim3(unsigned(chunks(p.T))), dim3(kThreads), 0, st,
                          p, part);
@@ -527,7 +552,7 @@ hipError_t backward_typed(const BalanceProblem& p, hipStream_t st) {
 }
 
 Partials layout(const BalanceProblem& p) {
-  const int64_t runs = chunks(p.T) + p.S;
+  const int64_t runs = one_group(p.T, p.S) ? 0 : chunks(p.T) + p.S;
   Partials part;
   part.E4 = padded(p.E);
   part.rows = chunk_rows(p.T);
@@ -541,29 +566,30 @@ Partials layout(const BalanceProblem& p) {
 }  // namespace
 
 int64_t balance_workspace(int64_t T, int64_t E, int64_t S) {
-  if (one_group(T, S)) return 0;
+  if (one_group(T, S)) return S == 1 ? 0 : (4 * S + 15) / 16 * 16;
   const int64_t runs = chunks(T) + S;
   return 4 * (2 * runs * padded(E) + runs + S);
 }
 
 hipError_t launch_balance(const BalanceProblem& p, hipStream_t st) {
   const Partials part = layout(p);
-  hipError_t e = hipSuccess;
-  if (p.T > 0) {
-    if (p.fp32)
-      e = p.sigmoid ? forward_typed<float, true>(p, part, st) : forward_typed<float, false>(p, part, st);
-    else
-      e = p.sigmoid ? forward_typed<uint16_t, true>(p, part, st) : forward_typed<uint16_t, false>(p, part, st);
-    if (e != hipSuccess || one_group(p.T, p.S)) return e;
-  }
-  int quads = 1;
-  while (quads < 64 && quads * 4 < part.E4) quads *= 2;
-  if (p.E <= 256)
-    hipLaunchKernelGGL((balance_sum_kernel<1>), dim3(unsigned(p.S)), dim3(1024), 0, st, p, part, quads);
+  hipError_t e;
+  if (p.fp32)
+    e = p.sigmoid ? forward_typed<float, true>(p, part, st) : forward_typed<float, false>(p, part, st);
   else
-    hipLaunchKernelGGL((balance_sum_kernel<4>), dim3(unsigned(p.S)), dim3(1024), 0, st, p, part, quads);
-  e = hipGetLastError();
-  if (e != hipSuccess || p.S == 1) return e;
+    e = p.sigmoid ? forward_typed<uint16_t, true>(p, part, st) : forward_typed<uint16_t, false>(p, part, st);
+  if (e != hipSuccess) return e;
+  if (!one_group(p.T, p.S)) {
+    int quads = 1;
+    while (quads < 64 && quads * 4 < part.E4) quads *= 2;
+    if (p.E <= 256)
+      hipLaunchKernelGGL((balance_sum_kernel<1>), dim3(unsigned(p.S)), dim3(1024), 0, st, p, part, quads);
+    else
+      hipLaunchKernelGGL((balance_sum_kernel<4>), dim3(unsigned(p.S)), dim3(1024), 0, st, p, part, quads);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (p.S == 1) return e;
   hipLaunchKernelGGL(balance_mean_kernel, dim3(1), dim3(1024), 0, st, p, part.losses);
   return hipGetLastError();
 }

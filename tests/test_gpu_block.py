@@ -376,7 +376,8 @@ def _check_balance(x, xv, ids, idv, score, coeff, ends, endv, g=1.7, strided=Tru
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 3), (5, 63, 6), (64, 64, 6), (65, 65, 1), (300, 128, 8),
                                    (129, 129, 2), (1000, 256, 8), (77, 257, 40), (140, 512, 17), (90, 1023, 64),
-                                   (33, 1024, 5), (20000, 24, 2)])
+                                   (33, 1024, 5), (20000, 24, 2), (256, 1022, 3), (257, 1021, 9), (700, 600, 3),
+                                   (16500, 260, 4)])
 def test_balance_loss(T, E, k, score, dtype):
     say(f"balance loss {T}x{E} k {k} {score} {dtype}")
     _, x, xv, ids, idv = _router(T, E, min(k, E), dtype, T + E)
@@ -386,7 +387,10 @@ def test_balance_loss(T, E, k, score, dtype):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T,E,endv", [(10, 16, [3, 3, 7]), (200, 64, [0, 0, 63, 64, 65, 128, 200]), (130, 70, [130]),
                                       (130, 70, [1]), (64, 300, [64, 64]), (9, 16, [0]), (500, 33, list(range(0, 500))),
-                                      (3000, 128, [64, 700, 701, 2111, 2990]), (40, 600, [5, 39])])
+                                      (3000, 128, [64, 700, 701, 2111, 2990]), (40, 600, [5, 39]),
+                                      (1024, 40, [1024, 1024]), (1025, 40, [1, 1025]),
+                                      (2100, 301, list(range(0, 2080, 32))), (1500, 1023, [700, 702, 1400]),
+                                      (1200, 18, sorted(i * 7919 % 1201 for i in range(200)))])
 def test_balance_loss_of_sequences(T, E, endv, score):
     """Ends inside, on and around chunks; empty sequences; rows behind the last."""
     say(f"balance loss {T}x{E} ends {endv[:8]} {score}")

@@ -83,7 +83,7 @@ def _call(lib, name, kw):
         (dict(S=2 ** 20 + 1), EINVAL), (dict(ends=None), EINVAL), (dict(k=0), EINVAL), (dict(T=2 ** 30), EINVAL),
         (dict(coeff=NAN), EINVAL), (dict(coeff=INF), EINVAL), (dict(ld=63), EINVAL), (dict(l=None), EINVAL),
         (dict(ids=None), EINVAL), (dict(loss=None), EINVAL), (dict(counts=None), EINVAL), (dict(tokens=None), EINVAL),
-        (dict(l=FAKE + 1), EINVAL), (dict(ws=None), EINVAL), (dict(wsb=100), EINVAL), (dict(ws=FAKE + 8), EINVAL),
+        (dict(l=FAKE + 1), EINVAL), (dict(ws=None), EINVAL), (dict(wsb=8), EINVAL), (dict(T=2000, wsb=100), EINVAL), (dict(ws=FAKE + 8), EINVAL),
         (dict(E=1025, ld=1025), ENOTIMPL), (dict(k=65), ENOTIMPL), (dict(E=4096, ld=4096, S=2 ** 19), EINVAL)],
     "fp8mm_moe_balance_loss_backward": [
         (dict(g=None), EINVAL), (dict(l=None), EINVAL), (dict(counts=None), EINVAL), (dict(tokens=None), EINVAL),
@@ -132,7 +132,7 @@ def test_queries(lib):
     assert lib.fp8mm_moe_balance_loss_workspace(16384, 64, 1) > 0
     assert lib.fp8mm_moe_balance_loss_workspace(16, 64, 1) == 0         # one workgroup
     assert 0 < lib.fp8mm_moe_balance_loss_workspace(16, 64, 2)
-    assert 0 < lib.fp8mm_moe_balance_loss_workspace(0, 64, 1)
+    assert lib.fp8mm_moe_balance_loss_workspace(0, 64, 1) == 0
     assert lib.fp8mm_moe_balance_loss_workspace(16, 64, 0) == -1
     assert lib.fp8mm_moe_balance_loss_workspace(2 ** 31 - 1, 64, 1) < 1 << 20          # bounded in the tokens
     for bad in ((-1, 64, 4, 16), (8, 0, 4, 16), (8, 64, 0, 16), (8, 64, 4, 0), (8, 64, 4, 257)):
