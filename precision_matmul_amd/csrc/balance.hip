@@ -43,28 +43,36 @@ __device__ __forceinline__ float reciprocal(float d) {
   return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
-// Four logits at column c of E; -inf past the end.  Without a branch of the lanes (the
-// last four columns in place of what reaches past them, moved up), so that loads of
-// several pieces are in flight together.
+// Logits of a token as they come from memory, four at column c of E each: past the row's
+// end its last four (columns, of less than four: its last) in their place.  No branch of
+// the lanes and nothing done with them before the turn that uses them, so that all loads
+// of a turn are in flight together, beside the turn before.
 template <typename T>
-__device__ __forceinline__ void load4(const T* row, int c, int E, float (&f)[4]) {
-  struct __attribute__((packed, aligned(sizeof(T)))) At {
-    T v[4];
-  };
+struct __attribute__((packed, aligned(sizeof(T)))) Four {
+  T v[4];
+};
+template <int NQ, typename T>
+__device__ __forceinline__ Four<T> ask4(const T* row, int c, int E) {
+  if (NQ > 1 || E >= 4) return *reinterpret_cast<const Four<T>*>(row + min(c, E - 4));
+  return Four<T>{{row[0], row[min(1, E - 1)], row[E - 1], row[E - 1]}};
+}
+// Their values; -inf past the end.
+template <int NQ, typename T>
+__device__ __forceinline__ void settle4(const Four<T>& a, int c, int E, float (&f)[4]) {
   const float none = -__builtin_inff();
-  if (E < 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = c + i < E ? to_float(row[c + i]) : none;
+  for (int i = 0; i < 4; ++i) f[i] = to_float(a.v[i]);
+  if (E % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = c < E ? f[i] : none;
     return;
   }
-  const int at = min(c, E - 4), n = c - at;
-  const At a = *reinterpret_cast<const At*>(row + at);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = n < 4 ? to_float(a.v[i]) : none;
-  if (E % 4 == 0) return;
+  const int n = NQ > 1 || E >= 4 ? c - min(c, E - 4) : 0;          // columns that are other lanes'
 #pragma unroll
   for (int k = 0; k < 3; ++k)
-    if (n > k && n < 4) f[0] = f[1], f[1] = f[2], f[2] = f[3], f[3] = none;
+    if (n > k) f[0] = f[1], f[1] = f[2], f[2] = f[3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = c + i < E ? f[i] : none;
 }
 
 template <typename T>
@@ -258,17 +266,17 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem 
     __syncthreads();
   };
   const auto end_of = [&](int s) { return p.ends ? min(int64_t(p.ends[s]), r1) : r1; };
-  float raw[NQ][4];                      // the next turn's logits and first ids
+  Four<T> raw[NQ];                       // the next turn's logits and first ids
   int raw_id;
   const auto ask = [&](int64_t row) {    // past the chunk: its last row, which is not used
     const int64_t at = min(row, r1 - 1);
     const T* x = static_cast<const T*>(p.logits) + at * p.ld;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) load4(x, (q * L + lane) * 4, p.E, raw[q]);
+    for (int q = 0; q < NQ; ++q) raw[q] = ask4<NQ>(x, (q * L + lane) * 4, p.E);
     raw_id = p.ids[at * p.k + min(lane, p.k - 1)];
   };
-  const int my_end = ONE ? 0 : lane_end(p);
   if (r0 < r1) ask(r0 + slot);
+  const int my_end = ONE ? 0 : lane_end(p);
   clear();
   int s = ONE ? 0 : sequence_of(p, my_end, r0);
   int64_t begin = r0, end = ONE ? r1 : s < p.S ? end_of(s) : r0;    // the rest of this run
@@ -277,9 +285,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceProblem 
     float f[NQ][4];
     const int id0 = lane < p.k ? raw_id : -1;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[q][i] = raw[q][i];
+    for (int q = 0; q < NQ; ++q) settle4<NQ>(raw[q], (q * L + lane) * 4, p.E, f[q]);
     if (next < r1) ask(next + slot);
     const bool used = probabilities<L, NQ, SIGMOID>(f) && row < r1;
     while (s < p.S) {
@@ -332,7 +338,7 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceProblem 
   const int first = int(begin / part.rows) + s, last = end > begin ? int((end - 1) / part.rows) + s + 1 : first;
   // no branch in the loop, so that its loads are in flight together: lanes past the columns
   // read the last ones, and all lanes of a run its tokens
-#pragma unroll 4
+#pragma unroll QL == 1 ? 4 : 2
   for (int run = first + wave * groups + group; run < last; run += 16 * groups) {
 #pragma unroll
     for (int i = 0; i < QL; ++i) {
@@ -366,7 +372,7 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const BalanceProblem 
     if (group != 0 || at >= p.E) continue;
     float P[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int C[4] = {0, 0, 0, 0};
-#pragma unroll
+#pragma unroll 4
     for (int w = 0; w < 16; ++w) {
       const float4 a = sums[w][i * 64 + lane];
       const int4 d = slots[w][i * 64 + lane];
@@ -411,21 +417,22 @@ __global__ __launch_bounds__(kBackThreads) void balance_backward_kernel(const Ba
   constexpr int SLOTS = kBackThreads / L;
   const int lane = threadIdx.x % L, slot = threadIdx.x / L, wave_lane = threadIdx.x & 63;
   const int64_t r0 = int64_t(blockIdx.x) * rows, r1 = min(p.T, r0 + rows);
-  const int my_end = lane_end(p);
-  const int my_tokens = wave_lane < p.S ? p.tokens[wave_lane] : 0;
-  float raw[NQ][4];
+  Four<T> raw[NQ];
   const auto ask = [&](int64_t row) {    // past the chunk: its last row, which is not used
     const T* x = static_cast<const T*>(p.logits) + min(row, r1 - 1) * p.ld;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) load4(x, (q * L + lane) * 4, p.E, raw[q]);
+    for (int q = 0; q < NQ; ++q) raw[q] = ask4<NQ>(x, (q * L + lane) * 4, p.E);
   };
   ask(r0 + slot);
+  const float grad = *p.grad_loss;
+  const int my_tokens = wave_lane < p.S ? p.tokens[wave_lane] : 0;
+  const int my_end = lane_end(p);
   int alive = __popcll(__ballot(my_tokens > 0));         // sequences with tokens
   for (int s = 64; s < p.S; s += 64) {
     const int at = s + wave_lane;
     alive += __popcll(__ballot(at < p.S && p.tokens[min(at, p.S - 1)] > 0));
   }
-  const float whole = *p.grad_loss * p.coeff * float(p.E) / (float(p.k) * float(max(alive, 1)));
+  const float whole = grad * p.coeff * float(p.E) / (float(p.k) * float(max(alive, 1)));
   int c[NQ][4], of = -1;                 // counts of the sequence `of`
   float d = 0.0f;
 #pragma unroll
@@ -436,9 +443,7 @@ __global__ __launch_bounds__(kBackThreads) void balance_backward_kernel(const Ba
     const int64_t row = turn + slot;
     float f[NQ][4], u[NQ][4];
 #pragma unroll
-    for (int q = 0; q < NQ; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[q][i] = raw[q][i];
+    for (int q = 0; q < NQ; ++q) settle4<NQ>(raw[q], (q * L + lane) * 4, p.E, f[q]);
     if (turn + SLOTS < r1) ask(row + SLOTS);
     int s = 0;                           // the token's sequence; S behind the last
     if (p.ends && p.S <= 64) {
