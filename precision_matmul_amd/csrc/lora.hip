@@ -347,16 +347,31 @@ __device__ __forceinline__ void stage_v(const LoraProblem& p, const Members& m, 
     at[e] = p.v + int64_t(m.at(row)) * v_columns(p.r) + (j < p.r ? j : 0);
     unpack<float>(load_chunk(at[e]), v[e]);
   }
-#pragma unroll 4
-  for (int k = 1; k < p.splits; ++k)
+  // several partial sums' loads together, in arrays: from one value a sum the compiler makes
+  // a chain of loads that wait for each other
+  const auto add = [&](int k, auto count) {
+    constexpr int N = decltype(count)::value;
+    Chunk c[N][ITEMS];
 #pragma unroll
-    for (int e = 0; e < ITEMS; ++e) {
-      if (FEW && e * (256 / QUADS) >= m.rows) continue;
-      float f[4];
-      unpack<float>(load_chunk(at[e] + k * next), f);
+    for (int u = 0; u < N; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[e][i] += f[i];
-    }
+      for (int e = 0; e < ITEMS; ++e)
+        if (!FEW || e * (256 / QUADS) < m.rows) c[u][e] = load_chunk(at[e] + (k + u) * next);
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int e = 0; e < ITEMS; ++e) {
+        if (FEW && e * (256 / QUADS) >= m.rows) continue;
+        float f[4];
+        unpack<float>(c[u][e], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[e][i] += f[i];
+      }
+  };
+  constexpr int MANY = 8 / ITEMS;
+  int k = 1;
+  for (; k + MANY <= p.splits; k += MANY) add(k, std::integral_constant<int, MANY>{});
+  for (; k < p.splits; ++k) add(k, std::integral_constant<int, 1>{});
 #pragma unroll
   for (int e = 0; e < ITEMS; ++e) {
     if (FEW && e * (256 / QUADS) >= m.rows) continue;
@@ -372,11 +387,20 @@ __device__ __forceinline__ void stage_v(const LoraProblem& p, const Members& m, 
 // The panel's rows j .. j + 32 at a lane's columns.
 template <bool TINY>
 __device__ __forceinline__ void load_panel(const LoraProblem& p, int a, int j, const Columns<TINY>& c, Chunk (&w)[8]) {
+  const int row = j + (threadIdx.x >> 4 & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = c.load(p.panels + (int64_t(a) * p.r + min(row + i, p.r - 1)) * p.C, p.C);
+}
+
+// Zeros in the place of rows from the rank on, which repeat the last one.  (Of 0 and v's
+// zeros there, but not of an infinity and a zero, the product would be 0.)
+__device__ __forceinline__ void clear_rows(const LoraProblem& p, int j, Chunk (&w)[8]) {
+  const int rows = p.r - j - int(threadIdx.x >> 4 & 3) * 8;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int row = j + (threadIdx.x >> 4 & 3) * 8 + i;
-    w[i] = c.load(p.panels + (int64_t(a) * p.r + min(row, p.r - 1)) * p.C, p.C);
-    if (row >= p.r) w[i] = Chunk{{0u, 0u, 0u, 0u}};
+    const uint32_t keep = i < rows ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[i].w[k] &= keep;
   }
 }
 
@@ -389,15 +413,15 @@ __device__ __forceinline__ void load_base(const LoraProblem& p, const Members& m
     to[k] = c.template load<NT>(p.base + int64_t(m.at(row + (threadIdx.x >> 4 & 3) * 4 + k)) * p.ld_base, p.C);
 }
 
-// Columns c .. c + 8 of the members' rows, 16 rows at a time with the next ones' base in
-// flight (`next` holds the first ones').  KS: steps of 32 rank rows whose fragments stay
+// Columns c .. c + 8 of every (step / 16)-th 16 of the members' rows from `row` on, with the
+// next ones' base in flight (`next` holds the first ones').  KS: steps of 32 rank rows whose fragments stay
 // in registers (0: any number, read again for each 16 rows).
 template <int KS, bool NT, bool TINY>
 __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const Members& m, const Columns<TINY>& c, int ld,
                                             const uint16_t* hi, const uint16_t* lo, bf16x8 (&b)[KS ? KS : 1][8],
-                                            Chunk (&next)[4]) {
+                                            Chunk (&next)[4], int row, int by) {
   const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
-  for (int i = 0; i < m.rows; i += 16) {
+  for (int i = row; i < m.rows; i += by) {
     f32x4 acc[8];                        // sums start from base
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -406,7 +430,7 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
 #pragma unroll
       for (int q = 0; q < 8; ++q) acc[q][k] = f[q];
     }
-    if (p.base && i + 16 < m.rows) load_base<NT>(p, m, i + 16, c, next);
+    if (p.base && i + by < m.rows) load_base<NT>(p, m, i + by, c, next);
     const auto step = [&](int ks, const bf16x8 (&bf)[8]) {
       const int at = (i + l15) * ld + ks * 32 + g * 8;
       const bf16x8 l = *reinterpret_cast<const bf16x8*>(lo + at), h = *reinterpret_cast<const bf16x8*>(hi + at);
@@ -422,6 +446,7 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
       for (int ks = 0; ks * 32 < p.r; ++ks) {
         Chunk w[8];
         load_panel(p, a, ks * 32, c, w);
+        clear_rows(p, ks * 32, w);
         transpose8(w, b[0]);
         step(ks, b[0]);
       }
@@ -439,18 +464,20 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
 }
 
 template <int KS, bool FEW, bool NT, bool TINY = false>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, int column_blocks) {
+__global__ __launch_bounds__(256, KS == 1 ? 3 : 2) void lora_expand_kernel(const LoraProblem p, int column_blocks,
+                                                          int column_waves) {
   constexpr int MAX = (KS ? KS * 32 : kLoraMaxRank) + 8;
   __shared__ __attribute__((aligned(16))) uint16_t hi[kTile * MAX], lo[kTile * MAX];
   __shared__ uint16_t list[4][FEW ? kFewTokens : 1];
   const int lane = threadIdx.x & 63, ld = KS ? MAX : (p.r + 31) / 32 * 32 + 8;
-  const int64_t first = int64_t(blockIdx.x % column_blocks) * 512 + (threadIdx.x >> 6) * 128;
-  const bool idle = first >= p.C;        // whole waves, which still stage v
+  const int wave = threadIdx.x >> 6, row = wave / column_waves * 16, by = 64 / column_waves;
+  const int64_t first = (int64_t(blockIdx.x % column_blocks) * column_waves + wave % column_waves) * 128;
   const Columns<TINY> c(first + (lane & 15) * 8, p.C);
   const auto body = [&](int a, const Members& m) {
+    const bool idle = first >= p.C || row >= m.rows;     // whole waves, which still stage v
     if (a < 0) {                         // no adapter: base alone
-      if (p.base == p.out || idle) return;
-      for (int i0 = 0; i0 < m.rows; i0 += 4) {
+      if (p.base == p.out || first >= p.C) return;
+      for (int i0 = row / 4; i0 < m.rows; i0 += by / 4) {
         const int i = i0 + (lane >> 4);
         const int64_t row = m.at(i);
         if (i >= m.rows) continue;
@@ -459,17 +486,13 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, i
       }
       return;
     }
-    // all loads first: the panel's, the first base's, v's (two steps of a panel are turned
-    // at once, for the registers)
+    // all loads first: the panel's, the first base's, v's
     bf16x8 b[KS ? KS : 1][8];
-    Chunk w[8], next[4];
+    Chunk w[KS ? KS : 1][8], next[4];
     if (!idle) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        load_panel(p, a, ks * 32, c, w);
-        if (KS > 1) transpose8(w, b[ks]);
-      }
-      if (p.base) load_base<NT>(p, m, 0, c, next);
+      for (int ks = 0; ks < KS; ++ks) load_panel(p, a, ks * 32, c, w[ks]);
+      if (p.base) load_base<NT>(p, m, row, c, next);
     }
     const float s = p.scales ? p.scales[a] : 1.0f;
     if constexpr (KS > 0)
@@ -478,8 +501,12 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraProblem p, i
       for (int j = 0; j < p.r; j += 32) stage_v<8, FEW>(p, m, s, j, ld, hi, lo);
     __syncthreads();
     if (!idle) {
-      if (KS == 1) transpose8(w, b[0]);
-      expand_rows<KS, NT>(p, a, m, c, ld, hi, lo, b, next);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        clear_rows(p, ks * 32, w[ks]);
+        transpose8(w[ks], b[ks]);
+      }
+      expand_rows<KS, NT>(p, a, m, c, ld, hi, lo, b, next, row, by);
     }
     __syncthreads();
   };
@@ -506,11 +533,18 @@ __global__ __launch_bounds__(256) void lora_sort_kernel(const LoraProblem p, con
     const float* v = o.v[which];
     if (!v) continue;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < o.splits[which]; ++k) {
-      float f[4];
-      unpack<float>(load_chunk(v + (k * p.T + t) * v_columns(p.r) + j), f);
+    for (int k = 0; k < o.splits[which]; k += 4) {       // four loads together
+      Chunk c[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] += f[e];
+      for (int u = 0; u < 4; ++u)
+        c[u] = load_chunk(v + (min(k + u, o.splits[which] - 1) * p.T + t) * v_columns(p.r) + j);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float f[4];
+        unpack<float>(c[u], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += k + u < o.splits[which] ? f[e] : 0.0f;
+      }
     }
     uint16_t* hi = o.sorted[which] + j * o.ld + row;
     uint16_t* lo = hi + p.r * o.ld;
@@ -592,14 +626,13 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
       for (int q = 0; q < 8; ++q) acc[f][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     Chunk w[8], hi[RF], lo[RF];
     int token[8];                        // of the next turn
-    const auto find = [&](int row0) {    // reads up to 31 rows past the end, which nothing uses
+    const auto find = [&](int row0) {    // the last row again, past the end
 #pragma unroll
-      for (int i = 0; i < 8; ++i) token[i] = o.order[row0 + g8 + i];
+      for (int i = 0; i < 8; ++i) token[i] = o.order[min(row0 + g8 + i, end - 1)];
     };
-    const auto ask = [&](int row0) {
+    const auto ask = [&](int row0) {     // v: up to 31 rows past the end
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = row0 + g8 + i < end ? c.load(side.x + int64_t(token[i]) * side.ld_x, C) : Chunk{{0u, 0u, 0u, 0u}};
+      for (int i = 0; i < 8; ++i) w[i] = c.load(side.x + int64_t(token[i]) * side.ld_x, C);
 #pragma unroll
       for (int f = 0; f < RF; ++f) hi[f] = load_chunk(vr[f] + row0), lo[f] = load_chunk(vr[f] + row0 + to_lo);
     };
@@ -608,6 +641,12 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
     if (begin + kOuterRows < end) find(begin + kOuterRows);
     for (int row0 = begin; row0 < end; row0 += kOuterRows) {
       bf16x8 b[8], h[RF], l[RF];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {      // zeros past the end
+        const uint32_t keep = row0 + g8 + i < end ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[i].w[k] &= keep;
+      }
       transpose8(w, b);
 #pragma unroll
       for (int f = 0; f < RF; ++f) {
@@ -691,8 +730,8 @@ unsigned tile_groups(const LoraProblem& p) {
 int64_t outer_ranges(int64_t T, int64_t C, int r) {
   const int64_t blocks = ((C + 511) / 512) * rank_blocks_of(r);
   int64_t z = 512 / blocks;                   // what runs at once: no last round of a few
-  // partial gradients: at most a quarter of x's bytes, or 4 MiB
-  const int64_t most = T / (16 * r), least = (int64_t(1) << 20) / (r * C);
+  // partial gradients: at most a quarter of x's bytes, or 16 MiB (4096 x 1408 x 2048 ...)
+  const int64_t most = T / (16 * r), least = (int64_t(4) << 20) / (r * C);
   z = z < most || z < least ? z : most > least ? most : least;
   const int64_t turns = (T + 2 * kOuterRows - 1) / (2 * kOuterRows);
   z = z < turns ? z : turns;
@@ -775,11 +814,14 @@ hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
 
 template <bool FEW, bool NT>
 hipError_t run_expand(const LoraProblem& p, hipStream_t st) {
-  const int cb = int((p.C + 511) / 512);
+  int cw = 4;
+  if (!FEW)
+    while (cw > 1 && (p.C <= 64 * cw || tiles_of(p) * ((p.C + 128 * cw - 1) / (128 * cw)) < 128)) cw /= 2;
+  const int cb = int((p.C + 128 * cw - 1) / (128 * cw));
   const dim3 grid(unsigned(tiles_of(p) * cb), FEW ? unsigned(by_tokens(p) ? p.T : p.n + 1) : tile_groups(p),
                   FEW ? 2 : 1);
   const auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, cb);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, p, cb, cw);
     return hipGetLastError();
   };
   if constexpr (!FEW && !NT)
@@ -793,10 +835,19 @@ hipError_t launch_lora_shrink(const LoraProblem& p, hipStream_t st) {
   return few(p) ? run_shrink<true>(p, st) : run_shrink<false>(p, st);
 }
 
+// Whether expand reads base and writes its result past the caches.  Of 128 MiB on, where
+// little of either would be found there again (16640 x 8192 93 us against 96; 16384 x 5120
+// 69 against 65, but the training step it belongs to 204 against 216, whose other kernels
+// find their operands; 7730 x 4864 31 against 26), and of whole lines (16640 x 8200, lines
+// in parts, 123 against 108).
+bool streams(const LoraProblem& p) {
+  return p.C >= 8 && p.T * p.C * 2 > 4 * kL2Bytes && p.ld_out % 64 == 0 && reinterpret_cast<uintptr_t>(p.out) % 128 == 0;
+}
+
 hipError_t launch_lora_expand(const LoraProblem& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
   if (few(p)) return run_expand<true, false>(p, st);
-  return p.C >= 8 && p.T * p.C * 2 > kL2Bytes ? run_expand<false, true>(p, st) : run_expand<false, false>(p, st);
+  return streams(p) ? run_expand<false, true>(p, st) : run_expand<false, false>(p, st);
 }
 
 hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, const LoraSide (&side)[2], hipStream_t st) {
