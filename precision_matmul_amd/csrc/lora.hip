@@ -165,44 +165,82 @@ __host__ __device__ inline int v_columns(int r) { return (r + 3) / 4 * 4; }
 
 // -------------------------------------------------------------------- shrink
 
+// 8 values from p on.  ODD: p may lie between two words, for which a 16-byte load takes
+// several times as long: the words that hold them, moved into place at their use.
+template <bool ODD>
+struct Eight {
+  Chunk v;
+  uint32_t end[ODD ? 1 : 0];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    if constexpr (ODD) {
+      struct __attribute__((packed, aligned(4))) Words {
+        Chunk c;
+      };
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      v = reinterpret_cast<const Words*>(at & ~uintptr_t(3))->c;
+      end[0] = *reinterpret_cast<const uint32_t*>((at + 14) & ~uintptr_t(3));
+    } else {
+      v = load_chunk(p);
+    }
+  }
+  // `p`: of the load, or that many bytes from it that their last two bits are the same
+  __device__ __forceinline__ bf16x8 get(const uint16_t* p) const {
+    if constexpr (!ODD) return as_bf16(v);
+    const uint32_t by = (reinterpret_cast<uintptr_t>(p) & 2) * 8;
+    Chunk c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.w[i] = __builtin_amdgcn_alignbit(i < 3 ? v.w[i + 1] : end[0], v.w[i], by);
+    return as_bf16(c);
+  }
+};
+
 // Rows of MF x 16 tokens and RF x 16 panel rows at ST steps of 32 columns from k on.
-template <int MF, int RF, int ST>
+template <int MF, int RF, int ST, bool ODD>
 struct Piece {
-  Chunk A[ST][MF], B[ST][RF];
+  Eight<ODD> A[ST][MF], B[ST][RF];
 
   __device__ __forceinline__ void load(const uint16_t* const (&xr)[MF], const uint16_t* const (&pr)[RF], int64_t k) {
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
 #pragma unroll
-      for (int i = 0; i < MF; ++i) A[s][i] = load_chunk(xr[i] + k + 32 * s);
+      for (int i = 0; i < MF; ++i) A[s][i].load(xr[i] + k + 32 * s);
 #pragma unroll
-      for (int f = 0; f < RF; ++f) B[s][f] = load_chunk(pr[f] + k + 32 * s);
+      for (int f = 0; f < RF; ++f) B[s][f].load(pr[f] + k + 32 * s);
     }
   }
-  __device__ __forceinline__ void add(f32x4 (&acc)[MF][RF]) const {
+  __device__ __forceinline__ void add(const uint16_t* const (&xr)[MF], const uint16_t* const (&pr)[RF],
+                                      f32x4 (&acc)[MF][RF]) const {
 #pragma unroll
-    for (int s = 0; s < ST; ++s)
+    for (int s = 0; s < ST; ++s) {
+      bf16x8 b[RF];
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
+      for (int f = 0; f < RF; ++f) b[f] = B[s][f].get(pr[f]);
 #pragma unroll
-        for (int f = 0; f < RF; ++f) acc[i][f] = mfma(as_bf16(A[s][i]), as_bf16(B[s][f]), acc[i][f]);
+      for (int i = 0; i < MF; ++i) {
+        const bf16x8 a = A[s][i].get(xr[i]);
+#pragma unroll
+        for (int f = 0; f < RF; ++f) acc[i][f] = mfma(a, b[f], acc[i][f]);
+      }
+    }
   }
 };
 
-// Steps of a wave's turn: 64 columns, whole lines of memory; two turns are in registers,
-// one of them in flight.
-constexpr int kSteps = 2;
+// Steps of 32 columns of a wave's turn; two turns are in registers, one of them in flight.
+// 64 columns are whole lines of memory, but with 64 tokens by 64 panel rows the registers
+// are for one step (4099 x 5120 of rank 64: 15.2 us, with two steps of 32 tokens, whose
+// two halves each read the panel, 19.0).
+template <int RF, bool FEW>
+constexpr int steps_of = RF == 4 && !FEW ? 1 : 2;
 
-// Partial v of MF x 16 members from `row` on over turns first, first + BY, ... below last.
-template <int MF, int RF, int BY, bool TINY>
-__device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const Members& m, int row, int rank0, int first,
-                                            int last, f32x4 (&acc)[MF][RF]) {
-  constexpr int ST = kSteps;
+// Partial v of MF x 16 members over the wave's turns first, first + 4, ... below last.
+template <int MF, int RF, int ST, bool TINY, bool ODD>
+__device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const Members& m, int rank0, int first, int last,
+                                            f32x4 (&acc)[MF][RF]) {
   const int lane = threadIdx.x & 63, l15 = lane & 15, g8 = (lane >> 4) * 8;
   const uint16_t* xr[MF];
   const uint16_t* pr[RF];
 #pragma unroll
-  for (int i = 0; i < MF; ++i) xr[i] = p.x + int64_t(m.at(row + i * 16 + l15)) * p.ld_x;
+  for (int i = 0; i < MF; ++i) xr[i] = p.x + int64_t(m.at(i * 16 + l15)) * p.ld_x;
 #pragma unroll
   for (int f = 0; f < RF; ++f)
     pr[f] = p.panels + (int64_t(a) * p.r + min(rank0 + f * 16 + l15, p.r - 1)) * p.C;
@@ -212,16 +250,16 @@ __device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const M
     for (int f = 0; f < RF; ++f) acc[i][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int whole = min(last, int(p.C / (32 * ST)));
   int c = first;
-  Piece<MF, RF, ST> u, w;
+  Piece<MF, RF, ST, ODD> u, w;
   if (c < whole) u.load(xr, pr, int64_t(c) * (32 * ST) + g8);
   while (c < whole) {
-    if (c + BY < whole) w.load(xr, pr, int64_t(c + BY) * (32 * ST) + g8);
-    u.add(acc);
-    c += BY;
+    if (c + 4 < whole) w.load(xr, pr, int64_t(c + 4) * (32 * ST) + g8);
+    u.add(xr, pr, acc);
+    c += 4;
     if (c >= whole) break;
-    if (c + BY < whole) u.load(xr, pr, int64_t(c + BY) * (32 * ST) + g8);
-    w.add(acc);
-    c += BY;
+    if (c + 4 < whole) u.load(xr, pr, int64_t(c + 4) * (32 * ST) + g8);
+    w.add(xr, pr, acc);
+    c += 4;
   }
   if (c < last) {                        // the row's last columns: zeros past them
 #pragma unroll 1
@@ -235,36 +273,34 @@ __device__ __forceinline__ void shrink_rows(const LoraProblem& p, int a, const M
         }
         return v;
       };
-      Piece<MF, RF, 1> end;
+      Piece<MF, RF, 1, false> end;
 #pragma unroll
-      for (int i = 0; i < MF; ++i) end.A[0][i] = own(cols.load(xr[i], p.C));
+      for (int i = 0; i < MF; ++i) end.A[0][i].v = own(cols.load(xr[i], p.C));
 #pragma unroll
-      for (int f = 0; f < RF; ++f) end.B[0][f] = own(cols.load(pr[f], p.C));
-      end.add(acc);
+      for (int f = 0; f < RF; ++f) end.B[0][f].v = own(cols.load(pr[f], p.C));
+      end.add(xr, pr, acc);
     }
   }
 }
 
-// v of up to MF x 16 members: the waves share the columns, or (HALVES = 2) two of them
-// the columns of each half of the members, which keeps fewer sums in a wave.
-template <int MF, int RF, int HALVES, bool TINY>
+// v of up to MF x 16 members; the waves share the columns.
+template <int MF, int RF, int ST, bool TINY, bool ODD>
 __device__ __forceinline__ void shrink_tile(const LoraProblem& p, int a, const Members& m, int split, int rank0,
                                             int first, int last, float* red) {
-  constexpr int BY = 4 / HALVES, MW = MF / HALVES;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = wave / BY, part = wave % BY;
-  f32x4 acc[MW][RF];
-  shrink_rows<MW, RF, BY, TINY>(p, a, m, half * MW * 16, rank0, first + part, last, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  f32x4 acc[MF][RF];
+  shrink_rows<MF, RF, ST, TINY, ODD>(p, a, m, rank0, first + wave, last, acc);
   // the waves' sums, added in wave order
 #pragma unroll
-  for (int i = 0; i < MW; ++i)
+  for (int i = 0; i < MF; ++i)
 #pragma unroll
     for (int f = 0; f < RF; ++f)
-      *reinterpret_cast<f32x4*>(red + ((part * MF * RF + (half * MW + i) * RF + f) * 64 + lane) * 4) = acc[i][f];
+      *reinterpret_cast<f32x4*>(red + ((wave * MF * RF + i * RF + f) * 64 + lane) * 4) = acc[i][f];
   __syncthreads();
   for (int q = wave; q < MF * RF; q += 4) {
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < BY; ++w) s += *reinterpret_cast<const f32x4*>(red + ((w * MF * RF + q) * 64 + lane) * 4);
+    for (int w = 0; w < 4; ++w) s += *reinterpret_cast<const f32x4*>(red + ((w * MF * RF + q) * 64 + lane) * 4);
     const int j = rank0 + q % RF * 16 + (lane & 15);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -276,24 +312,23 @@ __device__ __forceinline__ void shrink_tile(const LoraProblem& p, int a, const M
   __syncthreads();
 }
 
-template <int RF, bool FEW, bool TINY = false>
+template <int RF, bool FEW, bool ODD, bool TINY = false>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraProblem p, int rank_blocks) {
-  // sums of 32 members of all waves, or of 64 members of two or four
-  constexpr int SUMS = FEW ? 4 * 2 : RF == 4 ? 2 * 4 : 4 * 4;
+  constexpr int ST = steps_of<RF, FEW>, SUMS = 4 * (FEW ? 2 : 4);      // 32 or 64 members' of four waves
   __shared__ __attribute__((aligned(16))) float red[SUMS * RF * 64 * 4];
   __shared__ uint16_t list[4][FEW ? kFewTokens : 1];
   const int per = p.splits * rank_blocks;
   const int rest = blockIdx.x % per, split = rest % p.splits, rank0 = rest / p.splits * kRankBlock;
-  constexpr int COLS = 32 * kSteps;
+  constexpr int COLS = 32 * ST;
   const int pieces = int((p.C + COLS - 1) / COLS), each = (pieces + p.splits - 1) / p.splits;
   const int first = split * each, last = min(pieces, first + each);
   const auto body = [&](int a, const Members& m) {
     if (m.rows <= 16)
-      shrink_tile<1, RF, 1, TINY>(p, a, m, split, rank0, first, last, red);
+      shrink_tile<1, RF, ST, TINY, ODD>(p, a, m, split, rank0, first, last, red);
     else if (m.rows <= 32)
-      shrink_tile<2, RF, 1, TINY>(p, a, m, split, rank0, first, last, red);
+      shrink_tile<2, RF, ST, TINY, ODD>(p, a, m, split, rank0, first, last, red);
     else if constexpr (!FEW)
-      shrink_tile<4, RF, RF == 4 ? 2 : 1, TINY>(p, a, m, split, rank0, first, last, red);
+      shrink_tile<4, RF, ST, TINY, ODD>(p, a, m, split, rank0, first, last, red);
   };
   if constexpr (FEW)
     one_adapter<false, 32>(p, list[threadIdx.x >> 6], body);
@@ -807,9 +842,14 @@ hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
     return hipGetLastError();
   };
   if constexpr (!FEW)
-    if (p.C < 8) return run(lora_shrink_kernel<4, false, true>);
-  if (p.r <= 16) return run(lora_shrink_kernel<1, FEW>);
-  return p.r <= 32 ? run(lora_shrink_kernel<2, FEW>) : run(lora_shrink_kernel<4, FEW>);
+    if (p.C < 8) return run(lora_shrink_kernel<4, false, false, true>);
+  const auto words = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 4 == 0; };
+  if (words(p.x) && words(p.panels) && p.ld_x % 2 == 0 && p.C % 2 == 0) {
+    if (p.r <= 16) return run(lora_shrink_kernel<1, FEW, false>);
+    return p.r <= 32 ? run(lora_shrink_kernel<2, FEW, false>) : run(lora_shrink_kernel<4, FEW, false>);
+  }
+  if (p.r <= 16) return run(lora_shrink_kernel<1, FEW, true>);
+  return p.r <= 32 ? run(lora_shrink_kernel<2, FEW, true>) : run(lora_shrink_kernel<4, FEW, true>);
 }
 
 template <bool FEW, bool NT>
