@@ -517,12 +517,16 @@ __global__ __launch_bounds__(kBackThreads) void balance_backward_kernel(const Ba
 // Tokens of a chunk of the forward: at most 256 chunks, each a few turns.
 int64_t chunk_rows(int64_t T) { return T > 256 * 64 ? (T + 255) / 256 : 64; }
 int64_t chunks(int64_t T) { return T ? (T + chunk_rows(T) - 1) / chunk_rows(T) : 0; }
-// So few tokens that a workgroup takes a sequence, whatever their lengths: without partial
-// sums (one sequence: without a workspace).
-bool one_group(int64_t T, int64_t S) { return T <= (S == 1 ? 256 : 1024); }
+// Whether a workgroup takes a whole sequence, without partial sums: four turns of tokens (200
+// x 64 7.4 us, by chunks 4.8 + 3.3 and a launch), or sequences of few, on average (4000
+// tokens in 64 sequences 11 us, by chunks 16 + 5).  Not more: 1000 x 256 in two sequences
+// would take 37 us in place of 15, and as much if one sequence has nearly all of the tokens.
+bool one_group(int64_t T, int64_t E, int64_t S) { return T <= (E <= 256 ? 256 : 64) || (T <= 1024 && T <= 16 * S); }
 int padded(int64_t E) { return int((E + 3) / 4 * 4); }
 
-constexpr int64_t kBackwardRows = 32;    // tokens of a workgroup of the backward at least
+// Tokens of a workgroup of the backward at least, for 16 or 64 lanes a token: one turn, or
+// two (4000 x 256 7.2 us, two turns 9.8; 200 x 800 7.8, four turns 12.6).
+constexpr int64_t kBackwardRows[2] = {16, 8};
 
 template <typename Run>
 hipError_t by_experts(int E, const Run& run) {
@@ -537,7 +541,7 @@ template <typename T, bool SIGMOID>
 hipError_t forward_typed(const BalanceProblem& p, const Partials& part, hipStream_t st) {
   return by_experts(p.E, [&](auto L, auto NQ) {
     constexpr int l = decltype(L)::value, nq = decltype(NQ)::value;
-    if (one_group(p.T, p.S))
+    if (one_group(p.T, p.E, p.S))
       hipLaunchKernelGGL((balance_kernel<T, l, nq, SIGMOID, true>), dim3(unsigned(p.S)), dim3(kThreads), 0, st, p, part);
     else
       hipLaunchKernelGGL((balance_kernel<T, l, nq, SIGMOID, false>), dim3(unsigned(chunks(p.T))), dim3(kThreads), 0, st,
@@ -548,7 +552,7 @@ hipError_t forward_typed(const BalanceProblem& p, const Partials& part, hipStrea
 
 template <typename T, bool SIGMOID>
 hipError_t backward_typed(const BalanceProblem& p, hipStream_t st) {
-  const int64_t rows = p.T > kBackwardRows << 20 ? (p.T + (1 << 20) - 1) >> 20 : kBackwardRows;
+  const int64_t least = kBackwardRows[p.E > 256], rows = p.T > least << 20 ? (p.T + (1 << 20) - 1) >> 20 : least;
   return by_experts(p.E, [&](auto L, auto NQ) {
     hipLaunchKernelGGL((balance_backward_kernel<T, decltype(L)::value, decltype(NQ)::value, SIGMOID>),
                        dim3(unsigned((p.T + rows - 1) / rows)), dim3(kBackThreads), 0, st, p, rows);
@@ -557,7 +561,7 @@ hipError_t backward_typed(const BalanceProblem& p, hipStream_t st) {
 }
 
 Partials layout(const BalanceProblem& p) {
-  const int64_t runs = one_group(p.T, p.S) ? 0 : chunks(p.T) + p.S;
+  const int64_t runs = one_group(p.T, p.E, p.S) ? 0 : chunks(p.T) + p.S;
   Partials part;
   part.E4 = padded(p.E);
   part.rows = chunk_rows(p.T);
@@ -571,7 +575,7 @@ Partials layout(const BalanceProblem& p) {
 }  // namespace
 
 int64_t balance_workspace(int64_t T, int64_t E, int64_t S) {
-  if (one_group(T, S)) return S == 1 ? 0 : (4 * S + 15) / 16 * 16;
+  if (one_group(T, E, S)) return S == 1 ? 0 : (4 * S + 15) / 16 * 16;
   const int64_t runs = chunks(T) + S;
   return 4 * (2 * runs * padded(E) + runs + S);
 }
@@ -584,7 +588,7 @@ hipError_t launch_balance(const BalanceProblem& p, hipStream_t st) {
   else
     e = p.sigmoid ? forward_typed<uint16_t, true>(p, part, st) : forward_typed<uint16_t, false>(p, part, st);
   if (e != hipSuccess) return e;
-  if (!one_group(p.T, p.S)) {
+  if (!one_group(p.T, p.E, p.S)) {
     int quads = 1;
     while (quads < 64 && quads * 4 < part.E4) quads *= 2;
     if (p.E <= 256)

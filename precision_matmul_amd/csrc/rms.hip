@@ -591,11 +591,13 @@ __global__ __launch_bounds__(1024) void rms_column_sum_kernel(const float* parti
 constexpr int64_t kForwardGrid = 1024;  // four workgroups a compute unit; whole XCDs
 constexpr int kBackwardGrid = 512;      // partial rows at most
 constexpr int64_t kRegisterCols = 8192; // longest row kept in registers
-constexpr int64_t kFewRows = 512;       // rows at most of the backward in one launch
 
 // Rows that the long rows' kernels take: those, and rows of less than a chunk.
 bool long_rows(int64_t C) { return C < 8 || C > kRegisterCols; }
-bool few_rows(int64_t R, int64_t C) { return R <= kFewRows && !long_rows(C); }
+// Backward in one launch: while its columns' sums over all rows, without partial rows, do not
+// take longer than the second launch (bf16 512 x 2048 5.7 us, in two launches 7.3 + 3.4; 256 x
+// 5120 8.0 and 8.1 + 3.1, but 512 x 5120 21 and 10.4 + 3.9).
+bool few_rows(int64_t R, int64_t C) { return R <= (C <= 2048 ? 512 : 256) && !long_rows(C); }
 
 // Workgroups of the long rows' kernels, which take further rows in turns past this.
 dim3 row_grid(int64_t rows) { return dim3(unsigned(rows < (1 << 20) ? rows : (1 << 20))); }
