@@ -7,7 +7,10 @@
 // Three products make all of them, because both panels have the rank first: shrink
 // (v = panel x), expand (out = base + s panel^T v) and outer (sum_t s v x^T).  The
 // rank is small, so all three are HBM-bound: x, base and out pass once, and the panels
-// of the adapters in use.
+// of the adapters in use.  Of rank 16, 16640 x 5120 x 8192 takes 31 us of shrink (5.5
+// TB/s) and 92 of expand (5.9), both panels' gradients of 16384 x 2048 x 5120 40 us (5.9);
+// of rank 64, 4099 x 5120 takes 15 us (2.8: each tile reads as many bytes of panel).  Short
+// batches are bound by the latency of a few dependent loads.
 //
 // Tokens come in any order.  A workgroup takes 64 neighbouring ones and handles each
 // adapter that occurs among them in turn, its tokens gathered into the rows of 16-row
@@ -97,7 +100,9 @@ struct Members {
 };
 
 // Batches of more than one tile that are taken adapter by adapter: as many adapters as
-// make the tokens few for each, so that a panel is read once and not for each tile.
+// make the tokens few for each, so that a panel is read once and not for each tile (256 x
+// 5120 x 8192 of 64 adapters, rank 32: 8.4 + 16 us against 18 + 35 by tiles; 512 tokens of
+// 33 adapters 10 + 14 against 17 + 23).
 __host__ __device__ inline bool few_tokens(int64_t T, int64_t n) {
   return T > kTile && T <= kFewTokens && n > T / 16;
 }
@@ -131,10 +136,11 @@ __device__ __forceinline__ void each_adapter(const LoraProblem& p, int64_t t0, c
   }
 }
 
-// The same for a batch of few tokens as a whole: workgroup y handles adapter y (the one past the last: the tokens without), or,
-// where there are more adapters than tokens, that of token y if y is its first token;
-// MOST of its tokens at a time, in turns with the gridDim.z - 1 others of the adapter (if
-// most tokens have the same one after all).  `list` is the wave's own.
+// The same for a batch of few tokens as a whole: workgroup y handles adapter y (the one
+// past the last: the tokens without), or, where there are more adapters than tokens, that
+// of token y if y is its first token; MOST of its tokens at a time, in turns with the
+// gridDim.z - 1 others of the adapter (if most tokens have the same one after all).  `list`
+// is the wave's own.
 template <bool NONE, int MOST, typename Body>
 __device__ __forceinline__ void one_adapter(const LoraProblem& p, uint16_t* list, const Body& body) {
   const int lane = threadIdx.x & 63;
@@ -449,8 +455,9 @@ __device__ __forceinline__ void load_base(const LoraProblem& p, const Members& m
 }
 
 // Columns c .. c + 8 of every (step / 16)-th 16 of the members' rows from `row` on, with the
-// next ones' base in flight (`next` holds the first ones').  KS: steps of 32 rank rows whose fragments stay
-// in registers (0: any number, read again for each 16 rows).
+// next ones' base in flight (`next` holds the first ones').  KS: steps of 32 rank rows whose
+// fragments stay in registers (0: any number, read again for each 16 rows: 4099 x 8192 of
+// rank 64 41 us, with two steps kept 33).
 template <int KS, bool NT, bool TINY>
 __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const Members& m, const Columns<TINY>& c, int ld,
                                             const uint16_t* hi, const uint16_t* lo, bf16x8 (&b)[KS ? KS : 1][8],
@@ -756,20 +763,22 @@ int64_t tiles_of(int64_t T, int64_t n) { return few_tokens(T, n) ? 1 : (T + kTil
 int rank_blocks_of(int r) { return (r + kRankBlock - 1) / kRankBlock; }
 
 // Workgroups that share a tile's adapters.  Those that find none for them cost little where
-// there are few tiles (1453 x 2048 x 2048, rank 16, in 5 runs 6.8 us of expand for any number;
-// 3000 x 5120 x 8192 29), and tiles of many adapters gain (1453 tokens each of another of 20
-// adapters than the one before: 61 -> 29 us by one and four workgroups, 3000 86 -> 52).
+// there are few tiles (1453 x 2048 x 2048 of rank 16, in 5 runs, 6.3 us of expand by one
+// and by four; 6000 x 2048 x 2048 in 5 runs 25 by two, 27 by one), and tiles of many
+// adapters gain (1453 tokens of 20 adapters in any order: expand 54 us by one, 18 by four).
 unsigned tile_groups(const LoraProblem& p) {
   const int64_t most = p.T <= kTile ? p.T : p.T <= 512 ? 16 : p.T <= 1024 ? 8 : p.T <= 2048 ? 4 : p.T <= 8192 ? 2 : 1;
   const int64_t all = int64_t(p.n) + 1;       // adapters, and the tokens without one
   return unsigned(all < most ? all : most);
 }
 
-// Ranges of rows that share a panel's gradient.
+// Ranges of rows that share a panel's gradient: a workgroup a compute unit (two: a training
+// step of 16384 x 2048 x 5120 210 us against 203).  More of them for short batches pay up to
+// some 16 MiB of partial gradients (both of 1453 x 2688 x 128, rank 64: 13 us, with 4 MiB 22).
 int64_t outer_ranges(int64_t T, int64_t C, int r) {
   const int64_t blocks = ((C + 511) / 512) * rank_blocks_of(r);
-  int64_t z = 512 / blocks;                   // what runs at once: no last round of a few
-  // partial gradients: at most a quarter of x's bytes, or 16 MiB (4096 x 1408 x 2048 ...)
+  int64_t z = 256 / blocks;
+  // partial gradients: at most a quarter of x's bytes, or 16 MiB
   const int64_t most = T / (16 * r), least = (int64_t(4) << 20) / (r * C);
   z = z < most || z < least ? z : most > least ? most : least;
   const int64_t turns = (T + 2 * kOuterRows - 1) / (2 * kOuterRows);
@@ -779,6 +788,8 @@ int64_t outer_ranges(int64_t T, int64_t C, int r) {
 
 }  // namespace
 
+// Workgroups that share a tile's columns: as many as run at once, two a compute unit
+// (16640 x 5120 of rank 16 31 us with two, 50 with one).
 int lora_splits(int64_t T, int64_t C, int64_t n, int r) {
   if (T <= 0) return 1;
   const int64_t adapters = few_tokens(T, n) || T <= kTile ? (n < T ? n : T) : 1;
@@ -858,6 +869,9 @@ hipError_t run_shrink(const LoraProblem& p, hipStream_t st) {
 
 template <bool FEW, bool NT>
 hipError_t run_expand(const LoraProblem& p, hipStream_t st) {
+  // Waves side by side, of 128 columns each; the others take every second or fourth 16 rows.
+  // Four, for whole stretches of memory (4099 x 8192 34 us, by two waves 50), but fewer where
+  // columns are few or workgroups would be (2475 x 384 6.3 us, by four 9.2).
   int cw = 4;
   if (!FEW)
     while (cw > 1 && (p.C <= 64 * cw || tiles_of(p) * ((p.C + 128 * cw - 1) / (128 * cw)) < 128)) cw /= 2;
@@ -879,13 +893,14 @@ hipError_t launch_lora_shrink(const LoraProblem& p, hipStream_t st) {
   return few(p) ? run_shrink<true>(p, st) : run_shrink<false>(p, st);
 }
 
-// Whether expand reads base and writes its result past the caches.  Of 128 MiB on, where
-// little of either would be found there again (16640 x 8192 93 us against 96; 16384 x 5120
-// 69 against 65, but the training step it belongs to 204 against 216, whose other kernels
-// find their operands; 7730 x 4864 31 against 26), and of whole lines (16640 x 8200, lines
-// in parts, 123 against 108).
+// Whether expand reads base and writes its result past the caches: where the result is larger
+// than the L2s together and of whole lines.  Calls with several sets of operands in turn, so
+// that nothing is in the caches from the call before: 4099 x 5120 x 8192 53 us against 57,
+// 16640 x 8192 138 and 150, a training step of 16384 x 2048 x 5120 209 and 217; but 7730 x
+// 4856, whose rows share lines, 46 against 43.  (The same operands again and again: 7730 x
+// 4864 31 against 26.)
 bool streams(const LoraProblem& p) {
-  return p.C >= 8 && p.T * p.C * 2 > 4 * kL2Bytes && p.ld_out % 64 == 0 && reinterpret_cast<uintptr_t>(p.out) % 128 == 0;
+  return p.C >= 8 && p.T * p.C * 2 > kL2Bytes && p.ld_out % 64 == 0 && reinterpret_cast<uintptr_t>(p.out) % 128 == 0;
 }
 
 hipError_t launch_lora_expand(const LoraProblem& p, hipStream_t st) {

@@ -7,7 +7,9 @@
 //   dx = rstd (a - hr sum(a hr) / C) + grad_h,   dw = sum over rows of dy hr
 //
 // HBM-bound: x and residual (dy, h and grad_h) are read once, h, y and the codes
-// (dx) written once.  A row stays in registers between its sum and its output.  The
+// (dx) written once: 16640 x 5120 bf16 with residual and 1x128 codes 113 us (5.3 TB/s),
+// backward of 16384 x 2048 43 + 4.8 us (6.3 TB/s in the first kernel), 8000 x 5120 59 +
+// 4.7.  A row stays in registers between its sum and its output.  The
 // norm is that of the rounded h, which is what the residual stream holds and what
 // the backward pass reads.  All sums are float32; codes come from float32 values of
 // y with no rounding to bf16 in between.
@@ -306,7 +308,7 @@ __global__ __launch_bounds__(256) void rms_long_kernel(const RmsProblem p) {
 // flight while this one is worked on, and keeps its share of dw in registers over
 // all of them; it then writes one partial row of the workspace, [gridDim][C], which
 // rms_column_sum_kernel adds up in workgroup order: no atomics, the same bits every
-// time.
+// time.  A row by as few waves as hold it in four chunks a lane: sums across waves wait.
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 
@@ -602,12 +604,16 @@ bool few_rows(int64_t R, int64_t C) { return R <= (C <= 2048 ? 512 : 256) && !lo
 // Workgroups of the long rows' kernels, which take further rows in turns past this.
 dim3 row_grid(int64_t rows) { return dim3(unsigned(rows < (1 << 20) ? rows : (1 << 20))); }
 
-// Whether rows go past the caches: those of more than 64 MiB (fp32 16384 x 1100, 69 MiB, 56
-// us against 62, 16384 x 2048 94 against 104; but bf16 16384 x 2048, 64 MiB, with codes 42
-// against 37, its backward 45.8 against 44.3, 16384 x 1101 32.5 against 29).
-bool streams(const RmsProblem& p, size_t size) { return p.R * p.C * int64_t(size) > 2 * kL2Bytes; }
+// Whether rows go past the caches: those larger than the L2s together.  Calls with several
+// sets of operands in turn: backward of bf16 16384 x 2048 49.6 us against 53.6, 16384 x 1536
+// 39 and 44, fp32 16384 x 1024 51 and 59, codes of 16384 x 2048 43 and 48; about even at the
+// border (codes of 16384 x 1152 29 and 27).  The same operands again and again, half of them
+// in the memory's cache, gain less, or lose (16384 x 2048 with codes 42 and 37).
+bool streams(const RmsProblem& p, size_t size) { return p.R * p.C * int64_t(size) > kL2Bytes; }
 
-// Workgroups of the backward (one partial row each): as many as run at once.
+// Workgroups of the backward (one partial row each): two a compute unit for rows by four
+// waves (bf16 4000 x 2500 20.6 us against 25.5, fp32 16384 x 1280 64 and 73), else one (bf16
+// 16384 x 2048 49.8 against 52.9).
 int backward_grid(int64_t R, int64_t C, int vec) {
   const int64_t one_wave = 256 * vec;         // rows of up to this many columns: a wave each
   const int64_t rows = C <= one_wave ? kRowWaves : 1;
