@@ -763,9 +763,10 @@ int64_t tiles_of(int64_t T, int64_t n) { return few_tokens(T, n) ? 1 : (T + kTil
 int rank_blocks_of(int r) { return (r + kRankBlock - 1) / kRankBlock; }
 
 // Workgroups that share a tile's adapters.  Those that find none for them cost little where
-// there are few tiles (1453 x 2048 x 2048 of rank 16, in 5 runs, 6.3 us of expand by one
-// and by four; 6000 x 2048 x 2048 in 5 runs 25 by two, 27 by one), and tiles of many
-// adapters gain (1453 tokens of 20 adapters in any order: expand 54 us by one, 18 by four).
+// there are few tiles (1453 x 2048 x 2048 of rank 16, in 5 runs, 6.4 us of expand by four
+// and 6.8 by two; a call of 6000 x 2048 x 2048 in 5 runs 25 by two and 27 by one), and tiles
+// of many adapters gain (20 adapters in any order: 1453 tokens 18 us of expand by four and 29
+// by two, 3000 33 by two and 54 by one).
 unsigned tile_groups(const LoraProblem& p) {
   const int64_t most = p.T <= kTile ? p.T : p.T <= 512 ? 16 : p.T <= 1024 ? 8 : p.T <= 2048 ? 4 : p.T <= 8192 ? 2 : 1;
   const int64_t all = int64_t(p.n) + 1;       // adapters, and the tokens without one

@@ -389,6 +389,7 @@ def test_balance_loss(T, E, k, score, dtype):
                                       (130, 70, [1]), (64, 300, [64, 64]), (9, 16, [0]), (500, 33, list(range(0, 500))),
                                       (3000, 128, [64, 700, 701, 2111, 2990]), (40, 600, [5, 39]),
                                       (1024, 40, [1024, 1024]), (1025, 40, [1, 1025]),
+                                      (800, 40, list(range(0, 800, 10))), (900, 300, sorted(i * 613 % 901 for i in range(70))),
                                       (2100, 301, list(range(0, 2080, 32))), (1500, 1023, [700, 702, 1400]),
                                       (1200, 18, sorted(i * 7919 % 1201 for i in range(200)))])
 def test_balance_loss_of_sequences(T, E, endv, score):
@@ -577,7 +578,8 @@ def test_lora(T, K, N, n, r):
 
 @pytest.mark.parametrize("T,K,N,n,r,segments", [(300, 512, 640, 4, 16, 1), (1025, 520, 777, 3, 64, 5),
                                                 (2000, 1024, 384, 40, 8, 30), (4099, 256, 512, 2, 32, 3),
-                                                (700, 2048, 5120, 2, 100, 4)])
+                                                (700, 2048, 5120, 2, 100, 4), (2100, 64, 2100, 2, 64, 3),
+                                                (8300, 64, 2048, 2, 16, 3)])
 def test_lora_of_packed_prompts(T, K, N, n, r, segments):
     say(f"lora {T}x{K}x{N} adapters {n} rank {r} segments {segments}")
     rng, dev, val = _adapters(T, K, N, n, r, T + r, segments, without=0.0 if T % 2 else 0.02)
