@@ -9,7 +9,7 @@
 //
 // HBM-bound in principle (the logits read once, their gradient written once), in
 // practice a few launches of dependent loads: 16384 x 64 float32 logits are 4 MiB, and
-// take 5.1 + 4.1 us forward and 5.7 backward; 16384 x 256 sigmoid scores in 7 sequences 14
+// take 4.8 + 4.1 us forward and 5.1 backward; 16384 x 256 sigmoid scores in 7 sequences 14
 // + 5 + 2 and 14 us, of which the probabilities' vector instructions are most.  The forward needs
 // sums over all tokens of a sequence, so it is a pass over the tokens that leaves
 // partial sums and a sum over those.  Chunk b of the tokens and sequence s meet in at
