@@ -157,7 +157,7 @@ __device__ __forceinline__ Turns my_rows(int64_t R, int rpb, int wave) {
 // registers, and the next row is loaded while this one is reduced and written.
 // ---------------------------------------------------------------------------
 template <typename T, int FORM, int WPR, int NIT, bool NT>
-__global__ __launch_bounds__(WPR == 8 ? 512 : 256) void rms_kernel(const RmsProblem p) {
+__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rms_kernel(const RmsProblem p) {
   constexpr int V = kVec<T>;
   constexpr int RPB = WPR == 1 ? 4 : 1;           // rows of a workgroup
   constexpr int64_t STEP = int64_t(WPR) * 64 * V;
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(64 * (WPR == 1 ? kRowWaves : WPR)) void rms_backwar
   const auto ask = [&](int64_t at) {
     ask_row<T, NT>(hs + at * p.ld_h, w0, c0, STEP, C, nh);
     ask_row<T, NT>(dys + at * p.ld_dy, w0, c0, STEP, C, ng);
-    if (ghs) ask_row<T, NT>(ghs + at * p.ld_gh, w0, c0, STEP, C, ns);
+    if (ghs && WPR < 16) ask_row<T, NT>(ghs + at * p.ld_gh, w0, c0, STEP, C, ns);
     nrstd = p.rstd[at];
   };
   if (row < p.R) ask(row);
@@ -349,7 +349,8 @@ __global__ __launch_bounds__(64 * (WPR == 1 ? kRowWaves : WPR)) void rms_backwar
     Chunk vh[NIT], vg[NIT], vs[NIT];
     own_row<T>(nh, c0, STEP, C, vh);
     own_row<T>(ng, c0, STEP, C, vg);
-    if (ghs) own_row<T>(ns, c0, STEP, C, vs);
+    if (ghs && WPR < 16) own_row<T>(ns, c0, STEP, C, vs);
+    if (ghs && WPR == 16) ask_row<T, NT>(ghs + row * p.ld_gh, w0, c0, STEP, C, vs);   // for the registers
     const float rstd = nrstd;
     if (row + stride < p.R) ask(row + stride);
     float sah = 0.0f;
@@ -375,7 +376,7 @@ __global__ __launch_bounds__(64 * (WPR == 1 ? kRowWaves : WPR)) void rms_backwar
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = rstd * (g[i] * w[it][i] - f[i] * rstd * sah);
         if (ghs) {
-          unpack<T>(vs[it], g);
+          unpack<T>(WPR == 16 && it + 1 == NIT ? own_chunk<T, true>(vs[it], c0 + it * STEP, C) : vs[it], g);
 #pragma unroll
           for (int i = 0; i < V; ++i) f[i] += g[i];
         }
@@ -592,7 +593,7 @@ __global__ __launch_bounds__(1024) void rms_column_sum_kernel(const float* parti
 
 constexpr int64_t kForwardGrid = 1024;  // four workgroups a compute unit; whole XCDs
 constexpr int kBackwardGrid = 512;      // partial rows at most
-constexpr int64_t kRegisterCols = 8192; // longest row kept in registers
+constexpr int64_t kRegisterCols = 8192; // longest row kept in registers (bf16: twice that)
 
 // Rows that the long rows' kernels take: those, and rows of less than a chunk.
 bool long_rows(int64_t C) { return C < 8 || C > kRegisterCols; }
@@ -600,6 +601,11 @@ bool long_rows(int64_t C) { return C < 8 || C > kRegisterCols; }
 // take longer than the second launch (bf16 512 x 2048 5.7 us, in two launches 7.3 + 3.4; 256 x
 // 5120 8.0 and 8.1 + 3.1, but 512 x 5120 21 and 10.4 + 3.9).
 bool few_rows(int64_t R, int64_t C) { return R <= (C <= 2048 ? 512 : 256) && !long_rows(C); }
+
+// Long bf16 rows that 16 waves still keep in registers (4096 x 12288 70 us forward and 97
+// backward, read twice 93 and 139; the backward with grad_h a row ahead too 109).
+template <typename T>
+bool by_sixteen(int64_t C) { return sizeof(T) == 2 && C > kRegisterCols && C <= 2 * kRegisterCols; }
 
 // Workgroups of the long rows' kernels, which take further rows in turns past this.
 dim3 row_grid(int64_t rows) { return dim3(unsigned(rows < (1 << 20) ? rows : (1 << 20))); }
@@ -631,7 +637,7 @@ hipError_t run_rms(const RmsProblem& p, hipStream_t st) {
   constexpr int64_t MOST = WPR == 4 && NIT == 1 ? 1536 : kForwardGrid;
   const dim3 grid(xcd_grid(blocks < MOST ? blocks : MOST));
   const auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(WPR == 8 ? 512 : 256), 0, st, p);
+    hipLaunchKernelGGL(kernel, grid, dim3(WPR > 4 ? 64 * WPR : 256), 0, st, p);
     return hipGetLastError();
   };
   return streams(p, sizeof(T)) ? run(rms_kernel<T, FORM, WPR, NIT, true>) : run(rms_kernel<T, FORM, WPR, NIT, false>);
@@ -640,6 +646,8 @@ hipError_t run_rms(const RmsProblem& p, hipStream_t st) {
 template <typename T, int FORM>
 hipError_t rms_typed(const RmsProblem& p, hipStream_t st) {
   constexpr int64_t S = 64 * kVec<T>;   // columns of one wave chunk
+  if constexpr (sizeof(T) == 2)
+    if (by_sixteen<T>(p.C)) return run_rms<T, FORM, 16, 2>(p, st);
   if (long_rows(p.C)) {
     hipLaunchKernelGGL((rms_long_kernel<T, FORM>), row_grid(p.R), dim3(256), 0, st, p);
     return hipGetLastError();
@@ -711,7 +719,9 @@ hipError_t backward_typed(const RmsProblem& p, hipStream_t st) {
   const int grid = backward_grid(p.R, p.C, kVec<T>);
   float* partial = p.dweight ? p.workspace : nullptr;
   hipError_t e = hipSuccess;
-  if (long_rows(p.C)) {
+  if (by_sixteen<T>(p.C)) {
+    if constexpr (sizeof(T) == 2) e = run_backward<T, 16, 2>(p, grid, partial, st);
+  } else if (long_rows(p.C)) {
     if (p.dx) {
       hipLaunchKernelGGL((rms_backward_long_kernel<T>), row_grid(p.R), dim3(256), 0, st, p);
       e = hipGetLastError();

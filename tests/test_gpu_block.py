@@ -147,7 +147,8 @@ def test_rms_norm(R, C, dtype, params):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("R,C", [(512, 100), (513, 100), (600, 513), (530, 1024), (521, 2047), (519, 2049), (520, 3560),
-                                 (515, 4104), (514, 6200), (516, 8190), (2100, 1001), (4500, 3557), (700, 8200)])
+                                 (515, 4104), (514, 6200), (516, 8190), (2100, 1001), (4500, 3557), (700, 8200),
+                                 (520, 16384), (300, 12289), (260, 16385)])
 def test_rms_norm_of_many_rows(R, C, dtype):
     """Both sides of the step from one launch of the backward to partial sums, more
     rows than workgroups, every width."""
@@ -163,7 +164,7 @@ def test_rms_norm_of_many_rows(R, C, dtype):
 
 @pytest.mark.parametrize("R,C,dtype", [(9000, 2048, "bf16"), (8200, 2056, "bf16"), (4000, 5120, "bf16"),
                                        (2400, 7177, "bf16"), (3000, 4097, "fp32"), (1500, 6148, "fp32"),
-                                       (1100, 8192, "fp32")])
+                                       (1100, 8192, "fp32"), (2100, 8201, "bf16")])
 def test_rms_norm_past_the_caches(R, C, dtype):
     """More than 32 MiB of rows: streaming accesses."""
     test_rms_norm_of_many_rows(R, C, dtype)
