@@ -388,7 +388,7 @@ class _Lora(torch.autograd.Function):
 
 def lora(x, down, up, ids, scales=None, base=None):
     """lora_forward's result, differentiable in x, down, up and base (not in scales)."""
-    if _differentiates(x, down, up, base):
+    if _differentiates(x, down, up, scales, base):
         return _Lora.apply(x, down, up, ids, scales, base)
     return lora_forward(x.contiguous(), down.contiguous(), up.contiguous(), ids.contiguous(),
                         None if scales is None else scales.contiguous(), base)[0]

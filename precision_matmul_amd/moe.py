@@ -13,6 +13,7 @@ RuntimeError.
 """
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import (_ld, _lib, _need, _out_code, _ptr, fp8_grouped_linear_grad_weight, fp8_quantize_blockwise,
@@ -80,10 +81,15 @@ def _code(table, value, name):
 
 
 def _differentiates(*tensors):
-    """Whether a gradient of one of the inputs can be asked for later.  (Inside an
-    autograd function it is too late to ask: grad mode is off there, and its
+    """Whether a derivative of one of the inputs is asked for: a gradient, later, or a
+    forward-mode tangent, now (which the autograd functions refuse, in no_grad too).
+    (Inside an autograd function it is too late to ask: grad mode is off there, and its
     needs_input_grad is true of a parameter under no_grad too.)"""
-    return torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in tensors)
+    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in tensors):
+        return True
+    # outside of all dual levels there is no tangent: 0.1 us, and not one look at each input
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(
+        isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 # ------------------------------------------------------------------ layer norm

@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import precision_matmul_amd as fp8mm
-from precision_matmul_amd import _lib
+from precision_matmul_amd import _lib, block, moe
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "fp8mm_block.h")
@@ -182,3 +182,39 @@ int main(void) {
     subprocess.run(cmd, check=True, capture_output=True)
     run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert run.returncode == 0 and run.stdout.strip() == "ok", (run.returncode, run.stdout, run.stderr)
+
+
+def _on_the_host(monkeypatch):
+    """The library's calls behind lora, fp8_swiglu and fp8_moe replaced by ones that check
+    nothing and compute zeros, so that their Python paths run on CPU tensors."""
+    monkeypatch.setattr(block, "lora_forward", lambda x, down, up, ids, scales=None, base=None: (
+        x.new_zeros((x.shape[0], up.shape[2])), torch.zeros(1, x.shape[0], down.shape[1])))
+    monkeypatch.setattr(moe, "fp8_swiglu_forward", lambda x, recipe, checkpoint: (
+        x.new_zeros((x.shape[0], x.shape[1] // 2)), (x, x) if checkpoint else None))
+    monkeypatch.setattr(moe, "_experts_forward", lambda x, *rest: (torch.zeros_like(x), ()))
+
+
+def _lora_inputs():
+    return (torch.zeros((4, 16), dtype=torch.bfloat16), torch.zeros((2, 8, 16), dtype=torch.bfloat16),
+            torch.zeros((2, 8, 32), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32), torch.ones(2),
+            torch.zeros((4, 32), dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_forward_mode_derivatives_are_refused_not_dropped(monkeypatch, grad):
+    """A dual tensor has no requires_grad: its tangent must not vanish on the way."""
+    _on_the_host(monkeypatch)
+    ad = torch.autograd.forward_ad
+    rows, panel = torch.zeros((4, 256), dtype=torch.bfloat16), torch.zeros((2, 256, 256), dtype=torch.bfloat16)
+    ids, weights = torch.zeros((4, 1), dtype=torch.int32), torch.ones((4, 1))
+    calls = [(fp8mm.lora, _lora_inputs(), (0, 1, 2, 4, 5)), (fp8mm.fp8_swiglu, (rows,), (0,)),
+             (fp8mm.fp8_moe, (rows, panel, panel, ids, weights), (0, 1, 2, 4))]
+    with torch.set_grad_enabled(grad):
+        for fn, args, moved in calls:
+            fn(*args)                    # without a tangent: runs, inside a dual level too
+            for i in moved:
+                with ad.dual_level():
+                    fn(*args)
+                    duals = [ad.make_dual(t, torch.ones_like(t)) if j == i else t for j, t in enumerate(args)]
+                    with pytest.raises(NotImplementedError):
+                        fn(*duals)
