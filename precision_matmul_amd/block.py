@@ -366,6 +366,8 @@ def lora_backward(dy, x, v, down, up, ids, scales=None, need_dx=True, need_down=
 class _Lora(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, down, up, ids, scales, base):
+        if ctx.needs_input_grad[4]:
+            raise NotImplementedError("there is no gradient of the adapters' scales: pass scales.detach()")
         x, down, up, ids = x.contiguous(), down.contiguous(), up.contiguous(), ids.contiguous()
         scales = None if scales is None else scales.contiguous()
         base = None if base is None else base.contiguous()
@@ -387,7 +389,8 @@ class _Lora(torch.autograd.Function):
 
 
 def lora(x, down, up, ids, scales=None, base=None):
-    """lora_forward's result, differentiable in x, down, up and base (not in scales)."""
+    """lora_forward's result, differentiable in x, down, up and base.  scales has no
+    gradient: one that needs it is refused (NotImplementedError)."""
     if _differentiates(x, down, up, scales, base):
         return _Lora.apply(x, down, up, ids, scales, base)
     return lora_forward(x.contiguous(), down.contiguous(), up.contiguous(), ids.contiguous(),

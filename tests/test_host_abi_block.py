@@ -218,3 +218,16 @@ def test_forward_mode_derivatives_are_refused_not_dropped(monkeypatch, grad):
                     duals = [ad.make_dual(t, torch.ones_like(t)) if j == i else t for j, t in enumerate(args)]
                     with pytest.raises(NotImplementedError):
                         fn(*duals)
+
+
+def test_a_gradient_of_the_scales_is_refused(monkeypatch):
+    """There is none: asked for, it must not be missing without a word."""
+    _on_the_host(monkeypatch)
+    x, down, up, ids, scales, base = _lora_inputs()
+    needs = scales.clone().requires_grad_()
+    for leaf in (x, x.clone().requires_grad_()):
+        with pytest.raises(NotImplementedError):
+            fp8mm.lora(leaf, down, up, ids, needs, base)
+        assert fp8mm.lora(leaf, down, up, ids, needs.detach(), base).requires_grad == leaf.requires_grad
+    with torch.no_grad():
+        assert not fp8mm.lora(x.clone().requires_grad_(), down, up, ids, needs, base).requires_grad
