@@ -394,4 +394,4 @@ def lora(x, down, up, ids, scales=None, base=None):
     if _differentiates(x, down, up, scales, base):
         return _Lora.apply(x, down, up, ids, scales, base)
     return lora_forward(x.contiguous(), down.contiguous(), up.contiguous(), ids.contiguous(),
-                        None if scales is None else scales.contiguous(), base)[0]
+                        None if scales is None else scales.contiguous(), None if base is None else base.contiguous())[0]

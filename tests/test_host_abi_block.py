@@ -231,3 +231,23 @@ def test_a_gradient_of_the_scales_is_refused(monkeypatch):
         assert fp8mm.lora(leaf, down, up, ids, needs.detach(), base).requires_grad == leaf.requires_grad
     with torch.no_grad():
         assert not fp8mm.lora(x.clone().requires_grad_(), down, up, ids, needs, base).requires_grad
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_lora_makes_its_inputs_dense_with_and_without_a_gradient(monkeypatch, grad):
+    """Transposed matrices, spread ids and scales: what trains runs without a gradient too."""
+    def forward(*args):
+        assert all(t is None or t.is_contiguous() for t in args)
+        return torch.zeros((4, 32), dtype=torch.bfloat16), torch.zeros(1, 4, 8)
+
+    monkeypatch.setattr(block, "lora_forward", forward)
+    x, down, up, ids, scales, base = _lora_inputs()
+
+    def spread(t):
+        wide = t.new_zeros((*t.shape[::-1], 2))[..., 0].permute(*range(t.dim())[::-1])
+        assert wide.shape == t.shape and not wide.is_contiguous()
+        return wide.requires_grad_(grad and t.dtype == torch.bfloat16)
+
+    for args in ((x, down, up, ids, scales, base), (x, down, up, ids, None, None)):
+        out = fp8mm.lora(*(None if t is None else spread(t) for t in args))
+        assert out.requires_grad == grad
