@@ -44,7 +44,8 @@ extern "C" {
  * Codes are made of bf16 rows only: q 16-byte aligned, ld_q % 16 == 0, C % 128 ==
  * 0 (FP8MM_BLOCK_1x128) or C % 16 == 0 (FP8MM_ROWWISE).
  * eps: finite, >= 0.  1 <= C <= 2^22, 0 <= R < 2^31.  Sums are float32; a row
- * whose sum of squares is past float32's range has rstd 0.
+ * whose sum of squares, or its mean and eps together, is past float32's range has
+ * rstd 0.
  * ------------------------------------------------------------------------- */
 fp8mm_status fp8mm_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, fp8mm_dtype dtype,
                             int64_t R, int64_t C, const void* weight, fp8mm_dtype param_dtype, float eps, void* h,

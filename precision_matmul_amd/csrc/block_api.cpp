@@ -108,7 +108,7 @@ fp8mm_status fp8mm_rms_norm(const void* x, int64_t ld_x, const void* residual, i
   if (st == FP8MM_OK && residual && h) st = check_ld(ld_h, C, "ld_h");
   if (st == FP8MM_OK && y) st = check_ld(ld_y, C, "ld_y");
   if (st != FP8MM_OK) return st;
-  if (!(eps >= 0.0f) || eps > 1e30f) return fail(FP8MM_EINVAL, "eps must be a finite value >= 0");
+  if (!(eps >= 0.0f && eps - eps == 0.0f)) return fail(FP8MM_EINVAL, "eps must be a finite value >= 0");
   if (q) {
     if (recipe != FP8MM_BLOCK_1x128 && recipe != FP8MM_ROWWISE) {
       if (recipe == FP8MM_TENSORWISE || recipe == FP8MM_BLOCK_128x128 || recipe == FP8MM_BLOCK_128x1 ||

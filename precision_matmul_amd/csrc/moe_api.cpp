@@ -73,7 +73,7 @@ fp8mm_status fp8mm_layer_norm(const void* x, fp8mm_dtype dtype, int64_t R, int64
   if (st == FP8MM_OK) st = check_ld(ld_x, C, "ld_x");
   if (st == FP8MM_OK) st = check_ld(ld_y, C, "ld_y");
   if (st != FP8MM_OK) return st;
-  if (!(eps >= 0.0f) || eps > 1e30f) return fail(FP8MM_EINVAL, "eps must be a finite value >= 0");
+  if (!(eps >= 0.0f && eps - eps == 0.0f)) return fail(FP8MM_EINVAL, "eps must be a finite value >= 0");
   if (R == 0) return ok();
   if (!x || !y) return fail(FP8MM_EINVAL, "x and y must not be NULL");
   if (!element_aligned(x, dtype) || !element_aligned(y, dtype) || !element_aligned(weight, param_dtype) ||

@@ -236,6 +236,21 @@ def test_rms_norm_special_rows():
     assert (q == 0).all() and (s == np.float32(1e-12)).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_norms_under_a_large_eps(dtype):
+    """Beside it the row's own size hardly counts."""
+    _, x, _, w, wv = _norm_inputs(5, 384, dtype, "fp32", False, 3)
+    for eps in (2e30, 3e38):
+        _check_forward(x, None, w, wv, dtype, eps)
+        y, mean, rstd = fp8mm.layer_norm_forward(x, w, None, eps)
+        xv = _f64(x)
+        centred = xv - xv.mean(1, keepdims=True)
+        ref = centred / np.sqrt((centred ** 2).mean(1, keepdims=True) + eps) * wv
+        # the mean's sum, up to 64 values a lane and 6 steps of the wave; difference, root, reciprocal, products
+        tol = (80 * U * np.abs(xv).mean(1, keepdims=True) / np.sqrt(eps) + 8 * U * np.abs(centred) / np.sqrt(eps)) * np.abs(wv)
+        _within(_f64(y), ref, _rounded(ref, tol, BF16 if dtype == "bf16" else U), "layer norm")
+
+
 def test_rms_norm_without_rows():
     x = torch.empty((0, 256), device=DEV, dtype=torch.bfloat16)
     w = torch.ones(256, device=DEV)

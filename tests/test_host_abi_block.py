@@ -251,3 +251,12 @@ def test_lora_makes_its_inputs_dense_with_and_without_a_gradient(monkeypatch, gr
     for args in ((x, down, up, ids, scales, base), (x, down, up, ids, None, None)):
         out = fp8mm.lora(*(None if t is None else spread(t) for t in args))
         assert out.requires_grad == grad
+
+
+def test_any_finite_eps_is_accepted(lib):
+    """Of both norms: what the headers say."""
+    from tests import test_host_abi_moe as abi
+
+    for eps, code in ((0.0, OK), (1.0000001e30, OK), (3.4028234e38, OK), (-1e-45, EINVAL), (INF, EINVAL), (NAN, EINVAL)):
+        assert _call(lib, "fp8mm_rms_norm", dict(R=0, x=None, s=None, eps=eps)) == code, eps
+        assert abi._call(lib, "fp8mm_layer_norm", abi.NORM, abi.NORM_D, dict(R=0, x=None, y=None, eps=eps)) == code, eps
