@@ -736,7 +736,8 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraProblem p, cons
   const int64_t step = int64_t(which ? blocks - split : split) * 1024;
   const int begin = a ? o.offsets[a - 1] : 0, end = o.offsets[a];
   const int64_t z0 = begin / per + a, z1 = end > begin ? (end - 1) / per + a + 1 : z0;
-  const float scale = p.scales ? p.scales[a] : 1.0f;
+  // an adapter without tokens: zeros, whatever its scale
+  const float scale = p.scales && end > begin ? p.scales[a] : 1.0f;
   for (int64_t i = first * 4; i < count; i += step) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8

@@ -669,6 +669,22 @@ def test_lora_without_tokens_and_without_adapters():
     assert (dx == 0).all() and (ddown == 0).all() and (dup == 0).all()
 
 
+def test_lora_gradients_of_adapters_without_tokens():
+    """Zeros, whatever their panels and scales hold."""
+    rng, (x, down, up, ids, scales, base), _ = _adapters(90, 64, 96, 4, 20, 1)
+    ids[ids == 1], ids[ids == 2] = 0, 3
+    v = fp8mm.lora_forward(x, down, up, ids, scales)[1]
+    for dtype in (torch.bfloat16, torch.float32):
+        want = fp8mm.lora_backward(base, x, v, down, up, ids, scales, out_dtype=dtype)
+        for value in (NAN, INF):
+            scales2, down2, up2 = scales.clone(), down.clone(), up.clone()
+            scales2[1:3], down2[1:3], up2[1:3] = value, value, value
+            dx, ddown, dup = fp8mm.lora_backward(base, x, v, down2, up2, ids, scales2, out_dtype=dtype)
+            assert torch.equal(dx, want[0])
+            for g, w in ((ddown, want[1]), (dup, want[2])):
+                assert (g[1:3] == 0).all() and torch.equal(g[[0, 3]], w[[0, 3]])
+
+
 def test_lora_parts_of_the_backward():
     rng, (x, down, up, ids, scales, base), _ = _adapters(150, 130, 200, 3, 12, 2)
     v = fp8mm.lora_forward(x, down, up, ids, scales)[1]
