@@ -25,7 +25,10 @@
 //
 // v is float32 in memory and enters the second product as two bf16 numbers, its rounding
 // and the rest, in two instructions: the matrix work is not the bound, and v keeps 16
-// bits.
+// bits.  The rest is 0 or of either sign, so that its product with an infinity is NaN, or
+// the opposite one, where v's own is an infinity.  Wherever that happens the result is NaN:
+// results are looked at before they are stored, and those of a wave that holds a NaN are
+// computed again, with the rest's products taken of the finite values alone.
 #include "block_launch.hpp"
 #include "moe_launch.hpp"
 #include "ops_common.hpp"
@@ -365,6 +368,29 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_bf16(fabsf(a) < __builtin_inff() ? ra : 0.0f, fabsf(b) < __builtin_inff() ? rb : 0.0f);
 }
 
+// The finite ones of 8 values, zeros in the place of the others.  (The empty statement keeps
+// the compiler from doing this ahead of the loop over rows, for which it spills registers.)
+__device__ __forceinline__ bf16x8 finite(const bf16x8& b) {
+  Chunk c = __builtin_bit_cast(Chunk, b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    asm volatile("" : "+v"(c.w[i]));
+    const uint32_t none = ((c.w[i] & 0x7F807F80u) + 0x00800080u) >> 15 & 0x00010001u;   // exponents of ones
+    c.w[i] &= ~(none * 0xFFFFu);
+  }
+  return as_bf16(c);
+}
+
+// t, or NaN where one of 8 packed results is NaN (or above 2^121: as float16 numbers, of which
+// one instruction looks at two, those are not finite).
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ f16x2 watch(const Chunk& v, f16x2 t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    t = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, v.w[i]), f16x2{0, 0}, t);
+  return t;
+}
+
 // -------------------------------------------------------------------- expand
 
 // v of the members (zeros in the rows behind them and in the columns up to ld - 8 behind
@@ -464,43 +490,68 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
                                             Chunk (&next)[4], int row, int by) {
   const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   for (int i = row; i < m.rows; i += by) {
-    f32x4 acc[8];                        // sums start from base
+    f32x4 acc[8];
+    const auto start = [&](const Chunk (&from)[4]) {     // sums start from base
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float f[8];
-      unpack<uint16_t>(p.base ? next[k] : Chunk{{0u, 0u, 0u, 0u}}, f);
+      for (int k = 0; k < 4; ++k) {
+        float f[8];
+        unpack<uint16_t>(p.base ? from[k] : Chunk{{0u, 0u, 0u, 0u}}, f);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc[q][k] = f[q];
-    }
-    if (p.base && i + by < m.rows) load_base<NT>(p, m, i + by, c, next);
-    const auto step = [&](int ks, const bf16x8 (&bf)[8]) {
+        for (int q = 0; q < 8; ++q) acc[q][k] = f[q];
+      }
+    };
+    const auto step = [&](int ks, const bf16x8 (&bf)[8], auto rare) {
       const int at = (i + l15) * ld + ks * 32 + g * 8;
       const bf16x8 l = *reinterpret_cast<const bf16x8*>(lo + at), h = *reinterpret_cast<const bf16x8*>(hi + at);
 #pragma unroll
-      for (int f = 0; f < 8; ++f) acc[f] = mfma(l, bf[f], acc[f]);
+      for (int f = 0; f < 8; ++f) acc[f] = mfma(l, decltype(rare)::value ? finite(bf[f]) : bf[f], acc[f]);
 #pragma unroll
       for (int f = 0; f < 8; ++f) acc[f] = mfma(h, bf[f], acc[f]);
     };
-    if constexpr (KS > 0) {
+    const auto product = [&](auto rare) {
+      if constexpr (KS > 0) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) step(ks, b[ks]);
-    } else {
-      for (int ks = 0; ks * 32 < p.r; ++ks) {
-        Chunk w[8];
-        load_panel(p, a, ks * 32, c, w);
-        clear_rows(p, ks * 32, w);
-        transpose8(w, b[0]);
-        step(ks, b[0]);
+        for (int ks = 0; ks < KS; ++ks) step(ks, b[ks], rare);
+      } else {
+        for (int ks = 0; ks * 32 < p.r; ++ks) {
+          Chunk w[8];
+          load_panel(p, a, ks * 32, c, w);
+          clear_rows(p, ks * 32, w);
+          transpose8(w, b[0]);
+          step(ks, b[0], rare);
+        }
       }
+    };
+    Chunk y[4];
+    const auto results = [&] {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float f[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] = acc[q][k];
+        y[k] = pack<uint16_t>(f);
+      }
+    };
+    start(next);
+    if (p.base && i + by < m.rows) load_base<NT>(p, m, i + by, c, next);
+    product(std::false_type{});
+    results();
+    f16x2 seen = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + g * 4 + k < m.rows) seen = watch(y[k], seen);
+    if (__any(seen.x != seen.x || seen.y != seen.y)) {   // NaN: see above
+      Chunk again[4];
+      if (p.base) load_base<NT>(p, m, i, c, again);
+      start(again);
+      product(std::true_type{});
+      results();
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int at = i + g * 4 + k;
       const int64_t row = m.at(at);
-      float y[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) y[q] = acc[q][k];
-      if (at < m.rows) c.template store<NT>(p.out + row * p.ld_out, p.C, pack<uint16_t>(y));
+      if (at < m.rows) c.template store<NT>(p.out + row * p.ld_out, p.C, y[k]);
     }
   }
 }
@@ -678,11 +729,8 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
 #pragma unroll
       for (int f = 0; f < RF; ++f) hi[f] = load_chunk(vr[f] + row0), lo[f] = load_chunk(vr[f] + row0 + to_lo);
     };
-    find(begin);
-    ask(begin);
-    if (begin + kOuterRows < end) find(begin + kOuterRows);
-    for (int row0 = begin; row0 < end; row0 += kOuterRows) {
-      bf16x8 b[8], h[RF], l[RF];
+    bf16x8 b[8], h[RF], l[RF];
+    const auto take = [&](int row0) {    // what was asked for
 #pragma unroll
       for (int i = 0; i < 8; ++i) {      // zeros past the end
         const uint32_t keep = row0 + g8 + i < end ? 0xFFFFFFFFu : 0u;
@@ -696,14 +744,43 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
         h[f] = as_bf16(left < 8 ? first_of(hi[f], left) : hi[f]);
         l[f] = as_bf16(left < 8 ? first_of(lo[f], left) : lo[f]);
       }
-      if (row0 + kOuterRows < end) ask(row0 + kOuterRows);
-      if (row0 + 2 * kOuterRows < end) find(row0 + 2 * kOuterRows);
+    };
+    const auto add = [&](auto rare) {
 #pragma unroll
       for (int f = 0; f < RF; ++f) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(l[f], b[q], acc[f][q]);
+        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(l[f], decltype(rare)::value ? finite(b[q]) : b[q], acc[f][q]);
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[f][q] = mfma(h[f], b[q], acc[f][q]);
+      }
+    };
+    find(begin);
+    ask(begin);
+    if (begin + kOuterRows < end) find(begin + kOuterRows);
+    for (int row0 = begin; row0 < end; row0 += kOuterRows) {
+      take(row0);
+      if (row0 + kOuterRows < end) ask(row0 + kOuterRows);
+      if (row0 + 2 * kOuterRows < end) find(row0 + 2 * kOuterRows);
+      add(std::false_type{});
+    }
+    float seen = 0.0f;
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) seen = fmaf(acc[f][q][k], 0.0f, seen);
+    if (__any(seen != seen)) {           // NaN (or infinite): as in the second product
+#pragma unroll
+      for (int f = 0; f < RF; ++f)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[f][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int row0 = begin; row0 < end; row0 += kOuterRows) {
+        find(row0);
+        ask(row0);
+        take(row0);
+        add(std::true_type{});
       }
     }
     float* out = side.partial + (z + a) * partial_size(p.r, C);

@@ -655,6 +655,79 @@ def test_lora_infinite_products_stay_infinite():
     assert (out == INF).all()
 
 
+def _with_infinities(t, rng, share=0.004):
+    """t with some infinities of both signs, and its float64 values."""
+    at = torch.from_numpy(rng.random(t.shape) < share).to(DEV)
+    sign = torch.from_numpy(rng.choice([-INF, INF], t.shape)).to(t.dtype).to(DEV)
+    t = torch.where(at, sign, t)
+    return t, _f64(t)
+
+
+def _same_infinities(got, ref, clean, what):
+    """Infinite and NaN where the definition is, of its sign; what no infinity reaches has
+    the bits that it has without any."""
+    value = _f64(got)
+    assert np.array_equal(np.isnan(value), np.isnan(ref)), what
+    infinite = np.isinf(ref)
+    assert np.array_equal(np.isinf(value), infinite) and np.array_equal(value[infinite], ref[infinite]), what
+    finite = torch.from_numpy(np.isfinite(ref)).to(DEV)
+    assert torch.equal(got[finite], clean[finite]), what
+
+
+INFINITE_SHAPES = [(16, 64, 300, 3, 8), (300, 72, 130, 40, 16), (200, 130, 513, 3, 64), (130, 64, 264, 2, 100),
+                   (70, 64, 96, 2, 256), (90, 100, 5, 3, 24), (90, 5, 100, 3, 24), (700, 40, 1100, 3, 32),
+                   (4200, 24, 4096, 2, 20)]
+
+
+@pytest.mark.parametrize("whole", [False, True])
+@pytest.mark.parametrize("T,K,N,n,r", INFINITE_SHAPES)
+def test_lora_of_infinite_panels_and_rows(T, K, N, n, r, whole):
+    """Times a finite number an infinity stays one, of the product's sign: the two halves of
+    that number, the second of which may be 0 or of the other sign, must not show.  whole:
+    inner products that are odd whole numbers, with no second half."""
+    say(f"lora with infinities {T}x{K}x{N} adapters {n} rank {r}")
+    if whole:
+        K, N = K // 2 * 2 + 1, N // 2 * 2 + 1        # sums of that many ones of either sign
+    rng, (x, down, up, ids, scales, base), (_, _, _, idv, sv, basev) = _adapters(T, K, N, n, r, T + r)
+    dy = _dev(rng.standard_normal((T, N)), torch.bfloat16)[0]
+    if whole:
+        x, dy, down, up = (torch.where(t < 0, -1.0, 1.0).bfloat16() for t in (x, dy, down, up))
+    xv, dyv, downv, upv = (_f64(t) for t in (x, dy, down, up))
+    out, v = fp8mm.lora_forward(x, down, up, ids, scales, base)
+    with np.errstate(all="ignore"):
+        bad, badv = _with_infinities(up, rng)
+        ref = block.lora(xv, downv, badv, idv, sv, basev)[0]
+        _same_infinities(fp8mm.lora_forward(x, down, bad, ids, scales, base)[0], ref, out, "out")
+        inplace = base.clone()
+        fp8mm.lora_forward(x, down, bad, ids, scales, inplace, out=inplace)
+        _same_infinities(inplace, ref, out, "out on base")
+        for grad in (torch.bfloat16, torch.float32):
+            clean = fp8mm.lora_backward(dy, x, v, down, up, ids, scales, out_dtype=grad)
+            bad, badv = _with_infinities(down, rng)
+            got = fp8mm.lora_backward(dy, x, v, bad, up, ids, scales, out_dtype=grad)
+            _same_infinities(got[0], block.lora_backward(dyv, xv, badv, upv, idv, sv)[0], clean[0], "dx")
+            bad, badv = _with_infinities(x, rng, 0.001)
+            got = fp8mm.lora_backward(dy, bad, None, down, up, ids, scales, False, True, False, grad)
+            _same_infinities(got[1], block.lora_backward(dyv, badv, downv, upv, idv, sv)[1], clean[1], "ddown")
+            bad, badv = _with_infinities(dy, rng, 0.001)
+            got = fp8mm.lora_backward(bad, x, v, down, up, ids, scales, False, False, True, grad)
+            _same_infinities(got[2], block.lora_backward(badv, xv, downv, upv, idv, sv)[2], clean[2], "dup")
+
+
+def test_lora_of_infinities_on_both_sides():
+    """An infinite inner product with an infinite panel."""
+    for r in (8, 40, 80):
+        x = torch.full((20, 64), 1e30, device=DEV).bfloat16()
+        down = torch.full((2, r, 64), 1e30, device=DEV).bfloat16()
+        up = torch.ones((2, r, 32), device=DEV).bfloat16()
+        up[1, :, 3], up[1, :, 4], up[1, 0, 5] = INF, -INF, -INF
+        ids = torch.arange(20, device=DEV, dtype=torch.int32) % 2
+        out, _ = fp8mm.lora_forward(x, down, up, ids)
+        want = torch.full((20, 32), INF, device=DEV)
+        want[1::2, 4], want[1::2, 5] = -INF, NAN
+        assert torch.equal(out.float().nan_to_num(7.0, 1.0, -1.0), want.nan_to_num(7.0, 1.0, -1.0))
+
+
 def test_lora_without_tokens_and_without_adapters():
     rng, (x, down, up, ids, scales, base), _ = _adapters(70, 64, 96, 3, 8, 1)
     out, v = fp8mm.lora_forward(x[:0], down, up, ids[:0], scales, base[:0])
