@@ -360,12 +360,13 @@ __device__ __forceinline__ void transpose8(const Chunk (&w)[8], bf16x8 (&b)[8]) 
 }
 
 // Two float32 values as packed bf16 and the rest of them as packed bf16 (0 where the
-// value is past bf16's range or not finite).
+// value is not finite).  Values that would round to an infinity take bf16's largest number.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16(x, y);
+  constexpr float MOST = 3.38953139e38f;
+  const bool fx = fabsf(x) < __builtin_inff(), fy = fabsf(y) < __builtin_inff();
+  hi = pack_bf16(fx ? __builtin_amdgcn_fmed3f(x, -MOST, MOST) : x, fy ? __builtin_amdgcn_fmed3f(y, -MOST, MOST) : y);
   const float a = __uint_as_float(hi << 16), b = __uint_as_float(hi & 0xFFFF0000u);
-  const float ra = x - a, rb = y - b;
-  lo = pack_bf16(fabsf(a) < __builtin_inff() ? ra : 0.0f, fabsf(b) < __builtin_inff() ? rb : 0.0f);
+  lo = pack_bf16(fx ? x - a : 0.0f, fy ? y - b : 0.0f);
 }
 
 // The finite ones of 8 values, zeros in the place of the others.  (The empty statement keeps

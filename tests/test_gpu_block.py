@@ -728,6 +728,32 @@ def test_lora_of_infinities_on_both_sides():
         assert torch.equal(out.float().nan_to_num(7.0, 1.0, -1.0), want.nan_to_num(7.0, 1.0, -1.0))
 
 
+def test_lora_of_inner_products_past_the_range_of_bf16():
+    """v is float32: between bf16's largest number and its own it is not an infinity."""
+    # bf16's largest, 2^128 - 2^120, and 0.75 of a step of it: below 2^128, where float32 ends
+    top, rest = 2.0 ** 128 - 2.0 ** 120, 1.5 * 2.0 ** 119
+    for T, r in ((20, 4), (300, 40), (70, 100)):
+        x = torch.ones((T, 2), device=DEV).bfloat16()
+        x[::2] *= -1
+        down = torch.tensor([top, rest], device=DEV).bfloat16().expand(40, r, 2).contiguous()
+        up = torch.full((40, r, 16), 2.0 ** -60, device=DEV).bfloat16()
+        ids = torch.arange(T, device=DEV, dtype=torch.int32) % 40
+        out, v = fp8mm.lora_forward(x, down, up, ids)
+        val = _f64(x), _f64(down), _f64(up), ids.cpu().numpy()
+        ref, vref = block.lora(*val)
+        assert np.array_equal(_f64(v).sum(0)[:, :r], vref) and np.isfinite(vref).all()
+        tol = (V_SPLIT + (2 * r + 24) * U) * np.abs(ref)
+        _within(_f64(out), ref, _rounded(ref, tol, BF16), "out")
+        dy = torch.full((T, 16), 2.0 ** -60, device=DEV).bfloat16()
+        for dtype, half in (("bf16", BF16), ("fp32", U)):
+            dup = fp8mm.lora_backward(dy, None, v, down, up, ids, None, False, False, True, DT[dtype])[2]
+            ref = np.zeros(dup.shape)
+            for a in range(40):
+                ref[a] = vref[val[3] == a].T @ _f64(dy)[val[3] == a]
+            size = np.array([np.abs(vref[val[3] == a]).sum() for a in range(40)])[:, None, None] * 2.0 ** -60
+            _within(_f64(dup), ref, _rounded(ref, (V_SPLIT + (2 * T + 40) * U) * size, half), "dup")
+
+
 def test_lora_without_tokens_and_without_adapters():
     rng, (x, down, up, ids, scales, base), _ = _adapters(70, 64, 96, 3, 8, 1)
     out, v = fp8mm.lora_forward(x[:0], down, up, ids[:0], scales, base[:0])
