@@ -119,7 +119,8 @@ fp8mm_status fp8mm_moe_balance_loss_backward(const float* grad_loss, const void*
  * K (their sum is v; zeros behind the rank), which the backward takes; rows of tokens
  * without an adapter are not written.
  * Sums are float32.  v enters the second product as two bf16 numbers, its
- * rounding and the rest, so that it keeps 16 bits.
+ * rounding and the rest, so that it keeps 16 bits (in the gradients of the panels too
+ * where they are bf16; all of its bits where they are float32).
  * r <= 256, else FP8MM_ENOTIMPL; 0 <= T < 2^31; 1 <= n < 2^31; 1 <= K, N <= 2^22.
  * ------------------------------------------------------------------------- */
 int64_t fp8mm_lora_splits(int64_t T, int64_t K, int64_t n, int64_t r);

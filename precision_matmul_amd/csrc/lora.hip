@@ -23,9 +23,10 @@
 // of 16 columns, whose columns it numbers so that its own 8 are neighbours again in the
 // output (16-byte loads and stores, 256 contiguous bytes of a row).
 //
-// v is float32 in memory and enters the second product as two bf16 numbers, its rounding
-// and the rest, in two instructions: the matrix work is not the bound, and v keeps 16
-// bits.  The rest is 0 or of either sign, so that its product with an infinity is NaN, or
+// v is float32 in memory and enters the second product, and panel gradients in bf16, as two
+// bf16 numbers, its rounding and the rest, in two instructions: the matrix work is not the
+// bound, and v keeps 16 bits, 8 more than the results.  Panel gradients in float32 take
+// three, which hold all of v's bits.  The rest is 0 or of either sign, so that its product with an infinity is NaN, or
 // the opposite one, where v's own is an infinity.  Wherever that happens the result is NaN:
 // results are looked at before they are stored, and those of a wave that holds a NaN are
 // computed again, with the rest's products taken of the finite values alone.
@@ -361,12 +362,15 @@ __device__ __forceinline__ void transpose8(const Chunk (&w)[8], bf16x8 (&b)[8]) 
 
 // Two float32 values as packed bf16 and the rest of them as packed bf16 (0 where the
 // value is not finite).  Values that would round to an infinity take bf16's largest number.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+// `last`: what both leave, exactly.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo, uint32_t* last = nullptr) {
   constexpr float MOST = 3.38953139e38f;
   const bool fx = fabsf(x) < __builtin_inff(), fy = fabsf(y) < __builtin_inff();
   hi = pack_bf16(fx ? __builtin_amdgcn_fmed3f(x, -MOST, MOST) : x, fy ? __builtin_amdgcn_fmed3f(y, -MOST, MOST) : y);
   const float a = __uint_as_float(hi << 16), b = __uint_as_float(hi & 0xFFFF0000u);
-  lo = pack_bf16(fx ? x - a : 0.0f, fy ? y - b : 0.0f);
+  const float ra = fx ? x - a : 0.0f, rb = fy ? y - b : 0.0f;
+  lo = pack_bf16(ra, rb);
+  if (last) *last = pack_bf16(ra - __uint_as_float(lo << 16), rb - __uint_as_float(lo & 0xFFFF0000u));
 }
 
 // The finite ones of 8 values, zeros in the place of the others.  (The empty statement keeps
@@ -613,8 +617,9 @@ __global__ __launch_bounds__(256, KS == 1 ? 3 : 2) void lora_expand_kernel(const
 // --------------------------------------------------------------------- outer
 
 // Tokens and their v in adapter order: order[row] = t, and for each of the two (v of the
-// forward, dv) its partial sums added, as two bf16 numbers each in hi and lo [r][ld], a
-// rank's tokens next to each other.  A thread takes four ranks of a token.
+// forward, dv) its partial sums added, as two bf16 numbers each (three for gradients in
+// float32) in hi, lo and last [r][ld], a rank's tokens next to each other.  A thread takes
+// four ranks of a token.
 __global__ __launch_bounds__(256) void lora_sort_kernel(const LoraProblem p, const int32_t* row_of_token, LoraOrder o) {
   const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (t >= p.T) return;
@@ -642,12 +647,15 @@ __global__ __launch_bounds__(256) void lora_sort_kernel(const LoraProblem p, con
     }
     uint16_t* hi = o.sorted[which] + j * o.ld + row;
     uint16_t* lo = hi + p.r * o.ld;
+    uint16_t* last = lo + p.r * o.ld;
 #pragma unroll
     for (int e = 0; e < 4; e += 2) {
-      uint32_t h, l;
-      split2(s[e], s[e + 1], h, l);
+      uint32_t h, l, m;
+      split2(s[e], s[e + 1], h, l, &m);
       if (j + e < p.r) hi[e * o.ld] = uint16_t(h), lo[e * o.ld] = uint16_t(l);
       if (j + e + 1 < p.r) hi[(e + 1) * o.ld] = uint16_t(h >> 16), lo[(e + 1) * o.ld] = uint16_t(l >> 16);
+      if (p.grad_fp32 && j + e < p.r) last[e * o.ld] = uint16_t(m);
+      if (p.grad_fp32 && j + e + 1 < p.r) last[(e + 1) * o.ld] = uint16_t(m >> 16);
     }
   }
 }
@@ -677,7 +685,7 @@ struct Sides {
   unsigned blocks;
 };
 
-template <int RF, bool TINY = false>
+template <int RF, int PARTS, bool TINY = false>
 __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, const LoraOrder o, const Sides sides,
                                                          int rank_blocks) {
   const int lane = threadIdx.x & 63, l15 = lane & 15, g8 = (lane >> 4) * 8;
@@ -709,7 +717,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
   const uint16_t* vr[RF];
 #pragma unroll
   for (int f = 0; f < RF; ++f) vr[f] = o.sorted[which] + min(rank0 + f * 16 + l15, p.r - 1) * o.ld + g8;
-  const int64_t to_lo = p.r * o.ld;
+  const int64_t part = p.r * o.ld;
   for (int begin = z0; begin < z1; ++a) {
     const int end = min(o.offsets[a], z1);
     if (end <= begin) continue;
@@ -718,7 +726,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
     for (int f = 0; f < RF; ++f)
 #pragma unroll
       for (int q = 0; q < 8; ++q) acc[f][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    Chunk w[8], hi[RF], lo[RF];
+    Chunk w[8], v[PARTS][RF];
     int token[8];                        // of the next turn
     const auto find = [&](int row0) {    // the last row again, past the end
 #pragma unroll
@@ -728,9 +736,11 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = c.load(side.x + int64_t(token[i]) * side.ld_x, C);
 #pragma unroll
-      for (int f = 0; f < RF; ++f) hi[f] = load_chunk(vr[f] + row0), lo[f] = load_chunk(vr[f] + row0 + to_lo);
+      for (int f = 0; f < RF; ++f)
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) v[k][f] = load_chunk(vr[f] + row0 + k * part);
     };
-    bf16x8 b[8], h[RF], l[RF];
+    bf16x8 b[8], u[PARTS][RF];
     const auto take = [&](int row0) {    // what was asked for
 #pragma unroll
       for (int i = 0; i < 8; ++i) {      // zeros past the end
@@ -742,18 +752,18 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
 #pragma unroll
       for (int f = 0; f < RF; ++f) {
         const int left = end - row0 - g8;          // the next adapter's v are not this one's
-        h[f] = as_bf16(left < 8 ? first_of(hi[f], left) : hi[f]);
-        l[f] = as_bf16(left < 8 ? first_of(lo[f], left) : lo[f]);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) u[k][f] = as_bf16(left < 8 ? first_of(v[k][f], left) : v[k][f]);
       }
     };
     const auto add = [&](auto rare) {
 #pragma unroll
-      for (int f = 0; f < RF; ++f) {
+      for (int f = 0; f < RF; ++f)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(l[f], decltype(rare)::value ? finite(b[q]) : b[q], acc[f][q]);
+        for (int k = PARTS - 1; k >= 0; --k)             // the smallest first
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[f][q] = mfma(h[f], b[q], acc[f][q]);
-      }
+          for (int q = 0; q < 8; ++q)
+            acc[f][q] = mfma(u[k][f], k && decltype(rare)::value ? finite(b[q]) : b[q], acc[f][q]);
     };
     find(begin);
     ask(begin);
@@ -897,7 +907,7 @@ OrderBytes order_bytes(int64_t T, int64_t n, int r) {
   b.rows = whole(4 * T);
   b.order = 4 * b.ld;
   b.offsets = whole(4 * n);
-  b.sorted = 2 * 2 * r * b.ld;
+  b.sorted = 3 * 2 * r * b.ld;             // three parts where gradients are float32
   b.all = b.rows + b.order + b.offsets + 2 * b.sorted + plan_workspace(T, n);
   return b;
 }
@@ -1010,10 +1020,15 @@ hipError_t launch_lora_outer(const LoraProblem& p, const LoraOrder& o, const Lor
       return hipGetLastError();
     };
     const bool tiny = (side[0].grad && side[0].C < 8) || (side[1].grad && side[1].C < 8);
-    const hipError_t e = tiny        ? run(lora_outer_kernel<4, true>)
-                         : p.r <= 16 ? run(lora_outer_kernel<1>)
-                         : p.r <= 32 ? run(lora_outer_kernel<2>)
-                                     : run(lora_outer_kernel<4>);
+    const auto parts = [&](auto n) {
+      constexpr int PARTS = decltype(n)::value;
+      return tiny        ? run(lora_outer_kernel<4, PARTS, true>)
+             : p.r <= 16 ? run(lora_outer_kernel<1, PARTS>)
+             : p.r <= 32 ? run(lora_outer_kernel<2, PARTS>)
+                         : run(lora_outer_kernel<4, PARTS>);
+    };
+    const hipError_t e =
+        p.grad_fp32 ? parts(std::integral_constant<int, 3>{}) : parts(std::integral_constant<int, 2>{});
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(lora_sum_kernel, dim3(unsigned(p.n) * (sums[0] + sums[1])), dim3(256), 0, st, p, o, sides, sums[0],

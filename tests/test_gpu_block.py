@@ -754,6 +754,39 @@ def test_lora_of_inner_products_past_the_range_of_bf16():
             _within(_f64(dup), ref, _rounded(ref, (V_SPLIT + (2 * T + 40) * U) * size, half), "dup")
 
 
+@pytest.mark.parametrize("T,K,N,n,r", [(40, 64, 40, 40, 8), (200, 100, 130, 100, 20), (90, 64, 72, 60, 33),
+                                       (70, 40, 200, 70, 100), (30, 5, 40, 30, 16)])
+def test_lora_gradients_in_float32_keep_all_bits_of_v(T, K, N, n, r):
+    """A few tokens an adapter.  v and dv enter as three bf16 numbers each, whose products
+    with bf16 are exact: what is lost are additions, three a token, at up to a step each,
+    and those of the partial sums and the scale.  (As two numbers v is off by up to 128 U.)"""
+    rng, (x, down, up, ids, scales, base), (xv, _, upv, _, sv, _) = _adapters(T, K, N, n, r, T + r)
+    idv = (np.arange(T) * 7 % n).astype(np.int32)
+    ids = torch.from_numpy(idv).to(DEV)
+    shape = fp8mm.lora_forward(x, down, up, ids, scales)[1].shape
+    v = torch.zeros(shape, device=DEV)
+    v[0, :, :r] = torch.from_numpy(rng.standard_normal((T, r)).astype(np.float32)).to(DEV)
+    dy, dyv = _dev(rng.standard_normal((T, N)), torch.bfloat16)
+    dup = fp8mm.lora_backward(dy, None, v, down, up, ids, scales, False, False, True, torch.float32)[2]
+    vv, ref, size = _f64(v)[0, :, :r], np.zeros(dup.shape), np.zeros(dup.shape)
+    most = np.bincount(idv).max()
+    for a in range(n):
+        at = idv == a
+        ref[a], size[a] = sv[a] * vv[at].T @ dyv[at], sv[a] * np.abs(vv[at]).T @ np.abs(dyv[at])
+    _within(_f64(dup), ref, (6 * most + 4) * U * size + TINY, "dup")
+    # dv = s up dy of three columns, all positive: three products and their additions
+    dy, up = dy.abs(), up.abs()
+    dy[:, 3:] = 0
+    dyv, upv = _f64(dy), _f64(up)
+    ddown = fp8mm.lora_backward(dy, x, None, down, up, ids, scales, False, True, False, torch.float32)[1]
+    ref, size = np.zeros(ddown.shape), np.zeros(ddown.shape)
+    for a in range(n):
+        at = idv == a
+        dv = sv[a] * dyv[at] @ upv[a].T
+        ref[a], size[a] = dv.T @ xv[at], dv.T @ np.abs(xv[at])
+    _within(_f64(ddown), ref, (6 * most + 4 + 6 + 4) * U * size + TINY, "ddown")
+
+
 def test_lora_without_tokens_and_without_adapters():
     rng, (x, down, up, ids, scales, base), _ = _adapters(70, 64, 96, 3, 8, 1)
     out, v = fp8mm.lora_forward(x[:0], down, up, ids[:0], scales, base[:0])
