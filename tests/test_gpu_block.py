@@ -170,6 +170,42 @@ def test_rms_norm_past_the_caches(R, C, dtype):
     test_rms_norm_of_many_rows(R, C, dtype)
 
 
+# Rows of more than 32 MiB, of each number of waves and chunks a lane.
+STREAMED = [(33000, 512, "bf16"), (16400, 1024, "bf16"), (15300, 1100, "bf16"), (11000, 1536, "bf16"), (4200, 4096, "bf16"),
+            (2100, 8192, "bf16"), (1100, 16384, "bf16"), (33000, 256, "fp32"), (16500, 511, "fp32"), (11100, 768, "fp32"),
+            (8300, 1024, "fp32")]
+
+
+@pytest.mark.parametrize("R,C,dtype", STREAMED)
+def test_rms_norm_past_the_caches_is_that_of_fewer_rows(R, C, dtype):
+    """Rows are independent: streaming accesses give the bits that parts of the rows, which
+    stay below 32 MiB, give by themselves."""
+    say(f"rms norm streamed {R}x{C} {dtype}")
+    g = torch.Generator(device=DEV).manual_seed(R)
+    x, res, dy, gh = (torch.randn((R, C), generator=g, device=DEV).to(DT[dtype]) for _ in range(4))
+    w = torch.randn(C, generator=g, device=DEV)
+    parts = [slice(0, R // 2), slice(R // 2, R)]
+    y, h, rstd = fp8mm.rms_norm_forward(x, w, res)
+    dx, dw = fp8mm.rms_norm_backward(dy, h, w, rstd, gh)
+    plain = fp8mm.rms_norm_forward(x, w)[0]
+    for p in parts:
+        for got, want in zip((y, h, rstd), fp8mm.rms_norm_forward(x[p], w, res[p])):
+            assert torch.equal(got[p], want)
+        assert torch.equal(fp8mm.rms_norm_forward(x[p], w)[0], plain[p])
+        assert torch.equal(fp8mm.rms_norm_backward(dy[p], h[p], w, rstd[p], gh[p], need_weight=False)[0], dx[p])
+    hr = h.double() * rstd.double()[:, None]
+    ref, size = (dy.double() * hr).sum(0).cpu().numpy(), (dy.double() * hr).abs().sum(0).cpu().numpy()
+    _within(_f64(dw), ref, _rounded(ref, (R + 28) * U * size, U), "dweight")
+    for recipe, group in (("1x128", 128), ("rowwise", 16)) if dtype == "bf16" else ():
+        if C % group == 0:
+            q, s, y2, h2, _ = fp8mm.fp8_rms_norm_forward(x, w, res, recipe=recipe, y=True)
+            assert torch.equal(y2, y) and torch.equal(h2, h)
+            for p in parts:
+                want = fp8mm.fp8_rms_norm_forward(x[p], w, res[p], recipe=recipe)
+                assert torch.equal(q[p], want[0])
+                assert torch.equal(s[:, p] if recipe == "1x128" else s[p], want[1])
+
+
 @pytest.mark.parametrize("recipe", ["1x128", "rowwise"])
 @pytest.mark.parametrize("R,C", [(1, 128), (3, 256), (130, 512), (5, 640), (33, 1024), (9, 1152), (40, 2048), (7, 2176),
                                  (11, 5120), (6, 6272), (5, 8192), (4, 8320), (3, 16384), (9000, 2048), (3400, 5120)])
@@ -247,7 +283,7 @@ def test_norms_under_a_large_eps(dtype):
         centred = xv - xv.mean(1, keepdims=True)
         ref = centred / np.sqrt((centred ** 2).mean(1, keepdims=True) + eps) * wv
         # the mean's sum, up to 64 values a lane and 6 steps of the wave; difference, root, reciprocal, products
-        tol = (80 * U * np.abs(xv).mean(1, keepdims=True) / np.sqrt(eps) + 8 * U * np.abs(centred) / np.sqrt(eps)) * np.abs(wv)
+        tol = (80 * U * np.abs(xv).mean(1, keepdims=True) + 8 * U * np.abs(centred)) / np.sqrt(eps) * np.abs(wv)
         _within(_f64(y), ref, _rounded(ref, tol, BF16 if dtype == "bf16" else U), "layer norm")
 
 
@@ -421,6 +457,21 @@ def test_balance_loss_of_sequences(T, E, endv, score):
             if b > a:
                 one = fp8mm.moe_balance_loss_forward(x[a:b].contiguous(), ids[a:b].contiguous(), score)
                 assert torch.equal(one[1][0], counts[s]) and torch.equal(one[2][0], tokens[s])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,E,endv", [(20000, 24, [79, 80, 5000, 5040, 12345, 19999]),
+                                      (17000, 100, [1, 66, 67, 9000, 16990]),
+                                      (17000, 200, sorted(i * 4241 % 17001 for i in range(40))),
+                                      (16600, 300, [64, 65, 8111, 16600]), (16500, 601, [16499]),
+                                      (18000, 40, sorted(i * 7919 % 18001 for i in range(300)))])
+def test_balance_loss_of_sequences_in_long_batches(T, E, endv, dtype):
+    """More than 64 tokens a chunk: ends inside its turns, several in one of them."""
+    say(f"balance loss {T}x{E} ends {endv[:8]} {dtype}")
+    _, x, xv, ids, idv = _router(T, E, 3, dtype, T + E)
+    ends = torch.tensor(endv, dtype=torch.int32, device=DEV)
+    grad = _check_balance(x, xv, ids, idv, "sigmoid" if E % 8 else "softmax", 1.0, ends, endv, strided=E < 200)[3]
+    assert (grad[endv[-1]:] == 0).all()
 
 
 def test_balance_loss_with_nothing_in_it():
@@ -603,6 +654,17 @@ def test_lora_of_packed_prompts(T, K, N, n, r, segments):
     dy, dyv = _dev(rng.standard_normal((T, N)), torch.bfloat16)
     _check_lora_backward(dev, val, v, dy, dyv)
     _check_lora_backward(dev, val, v, dy, dyv, grad="fp32")
+
+
+@pytest.mark.parametrize("T,K,N,n,r", [(4200, 64, 4096, 3, 64), (4200, 64, 4096, 3, 100), (2100, 130, 8256, 2, 40),
+                                       (100, 128, 200, 12, 100), (300, 64, 130, 40, 256), (300, 65, 131, 40, 70)])
+def test_lora_in_place_of_large_ranks(T, K, N, n, r):
+    """Results past the caches (streaming loads of base, in place too) and batches taken
+    adapter by adapter, at ranks above 32 and above 64."""
+    test_lora(T, K, N, n, r)
+    _, (x, down, up, ids, scales, base), _ = _adapters(T, K, N, n, r, T + r)
+    want, _ = fp8mm.lora_forward(x, down, up, ids, scales, base)
+    assert fp8mm.lora_forward(x, down, up, ids, scales, base, out=base)[0] is base and torch.equal(base, want)
 
 
 def test_lora_gradients_by_differences():
