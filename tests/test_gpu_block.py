@@ -1034,6 +1034,45 @@ def test_captured_training_step():
             assert not ref.isnan().any() and torch.equal(got, ref)
 
 
+def test_rows_far_apart():
+    """Row strides that put the last rows past 2^31 and 2^32 elements: the bits of dense rows."""
+    store = torch.empty(5 << 30, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+
+    def far(t, start=1):
+        flat = store.view(t.dtype)[start:]
+        view = flat.as_strided(t.shape, ((flat.numel() - t.shape[1]) // (t.shape[0] - 1), 1))
+        return view.copy_(t)
+
+    for dtype in (torch.bfloat16, torch.float32):
+        for R, C in ((5, 256), (600, 1040), (40, 20000)):
+            x, dy = (torch.randn((R, C), generator=g, device=DEV).to(dtype) for _ in range(2))
+            y, _, rstd = fp8mm.rms_norm_forward(x)
+            assert torch.equal(fp8mm.rms_norm_forward(far(x))[0], y)
+            want = fp8mm.rms_norm_backward(dy, x, None, rstd)
+            for at in range(2):
+                rows = (far(dy), x) if at == 0 else (dy, far(x))
+                assert all(torch.equal(a, b) for a, b in zip(fp8mm.rms_norm_backward(*rows, None, rstd), want))
+        for T, E in ((60, 64), (3000, 300)):
+            x = torch.randn((T, E), generator=g, device=DEV).to(dtype)
+            ids = torch.randint(0, E, (T, 3), generator=g, device=DEV, dtype=torch.int32)
+            want = fp8mm.moe_balance_loss_forward(x, ids)
+            assert all(torch.equal(a, b) for a, b in zip(fp8mm.moe_balance_loss_forward(far(x), ids), want))
+            one = torch.ones((), device=DEV)
+            assert torch.equal(fp8mm.moe_balance_loss_backward(one, far(x), *want[1:], 3),
+                               fp8mm.moe_balance_loss_backward(one, x, *want[1:], 3))
+    for T, n in ((40, 3), (300, 40), (1000, 5)):
+        _, (x, down, up, ids, scales, base), _ = _adapters(T, 200, 264, n, 16, T)
+        want, v = fp8mm.lora_forward(x, down, up, ids, scales, base)
+        assert torch.equal(fp8mm.lora_forward(far(x), down, up, ids, scales, base)[0], want)
+        inplace = far(base)
+        assert torch.equal(fp8mm.lora_forward(x, down, up, ids, scales, inplace, out=inplace)[0], want)
+        grads = fp8mm.lora_backward(want, x, v, down, up, ids, scales)
+        for at in range(2):              # one at a time: they share the memory
+            rows = (far(want), x) if at == 0 else (want, far(x))
+            assert all(torch.equal(a, b) for a, b in zip(fp8mm.lora_backward(*rows, v, down, up, ids, scales), grads))
+
+
 def test_two_streams_at_once():
     """Independent calls on two streams do not disturb each other (each has its own
     workspace)."""
