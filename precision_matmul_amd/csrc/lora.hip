@@ -387,12 +387,11 @@ __device__ __forceinline__ bf16x8 finite(const bf16x8& b) {
 }
 
 // t, or NaN where one of 8 packed results is NaN (or above 2^121: as float16 numbers, of which
-// one instruction looks at two, those are not finite).
+// one instruction looks at four, those are NaN too).
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ f16x2 watch(const Chunk& v, f16x2 t) {
+__device__ __forceinline__ f16x2 watch(f16x2 t, const Chunk& v) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    t = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, v.w[i]), f16x2{0, 0}, t);
+  for (int i = 0; i < 4; ++i) t = __builtin_elementwise_maximum(t, __builtin_bit_cast(f16x2, v.w[i]));
   return t;
 }
 
@@ -489,7 +488,7 @@ __device__ __forceinline__ void load_base(const LoraProblem& p, const Members& m
 // next ones' base in flight (`next` holds the first ones').  KS: steps of 32 rank rows whose
 // fragments stay in registers (0: any number, read again for each 16 rows: 4099 x 8192 of
 // rank 64 41 us, with two steps kept 33).
-template <int KS, bool NT, bool TINY>
+template <int KS, bool FEW, bool NT, bool TINY>
 __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const Members& m, const Columns<TINY>& c, int ld,
                                             const uint16_t* hi, const uint16_t* lo, bf16x8 (&b)[KS ? KS : 1][8],
                                             Chunk (&next)[4], int row, int by) {
@@ -541,11 +540,12 @@ __device__ __forceinline__ void expand_rows(const LoraProblem& p, int a, const M
     if (p.base && i + by < m.rows) load_base<NT>(p, m, i + by, c, next);
     product(std::false_type{});
     results();
-    f16x2 seen = {0, 0};
+    f16x2 seen[2] = {{0, 0}, {0, 0}};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + g * 4 + k < m.rows) seen = watch(y[k], seen);
-    if (__any(seen.x != seen.x || seen.y != seen.y)) {   // NaN: see above
+    for (int k = 0; k < 4; ++k)          // (rows behind the members hold anything where tokens are few)
+      if (!FEW || i + g * 4 + k < m.rows) seen[k % 2] = watch(seen[k % 2], y[k]);
+    const f16x2 both = __builtin_elementwise_maximum(seen[0], seen[1]);
+    if (__any(__builtin_isunordered(both.x, both.y))) {  // NaN: see above
       Chunk again[4];
       if (p.base) load_base<NT>(p, m, i, c, again);
       start(again);
@@ -604,7 +604,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 3 : 2) void lora_expand_kernel(const
         clear_rows(p, ks * 32, w[ks]);
         transpose8(w[ks], b[ks]);
       }
-      expand_rows<KS, NT>(p, a, m, c, ld, hi, lo, b, next, row, by);
+      expand_rows<KS, FEW, NT>(p, a, m, c, ld, hi, lo, b, next, row, by);
     }
     __syncthreads();
   };
@@ -774,14 +774,15 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraProblem p, co
       if (row0 + 2 * kOuterRows < end) find(row0 + 2 * kOuterRows);
       add(std::false_type{});
     }
-    float seen = 0.0f;
+    float seen[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int f = 0; f < RF; ++f)
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) seen = fmaf(acc[f][q][k], 0.0f, seen);
-    if (__any(seen != seen)) {           // NaN (or infinite): as in the second product
+        for (int q = 0; q < 8; ++q) seen[q] = fmaf(acc[f][q][k], 0.0f, seen[q]);
+    // NaN (or infinite): as in the second product
+    if (__any(((seen[0] + seen[1]) + (seen[2] + seen[3])) + ((seen[4] + seen[5]) + (seen[6] + seen[7])) != 0.0f)) {
 #pragma unroll
       for (int f = 0; f < RF; ++f)
 #pragma unroll
