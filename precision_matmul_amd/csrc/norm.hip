@@ -22,6 +22,18 @@ namespace {
 
 using namespace ops;
 
+// The next row's chunks.  PART: without a path for a row's last elements, for
+// which the waves that share a row would all wait where they ask for them: the
+// last chunk is loaded whole and shifted, if it has to be, when its turn comes.
+template <typename T, bool NT, bool PART>
+__device__ __forceinline__ Chunk fetch(const T* row, int64_t c, int64_t C) {
+  return PART ? fetch_row<T, NT>(row, c, C) : load_row<T, NT>(row, c, C);
+}
+template <typename T, bool PART>
+__device__ __forceinline__ Chunk settle(const Chunk& v, int64_t c, int64_t C) {
+  return PART ? fetched<T>(v, c, C) : v;
+}
+
 // ---------------------------------------------------------------------------
 // Forward, row in registers: WPR waves a row, NIT chunks a lane.  A workgroup
 // takes rows blockIdx, blockIdx + gridDim, ...; a lane's columns are the same

@@ -1,5 +1,5 @@
-// Device pieces shared by the norms: a row's sum over the waves that hold it and
-// the next row's chunks in flight.
+// Device pieces shared by the norms: a row's sum over the waves that hold it, four
+// floats as a chunk.
 #pragma once
 
 #include "ops_common.hpp"
@@ -23,18 +23,6 @@ __device__ __forceinline__ float row_sum(float v, float (&part)[2][WPR], int slo
 #pragma unroll
   for (int w = 0; w < WPR; ++w) s += part[slot][w];
   return s;
-}
-
-// The next row's chunks.  PART: without a path for a row's last elements, for
-// which the waves that share a row would all wait where they ask for them: the
-// last chunk is loaded whole and shifted, if it has to be, when its turn comes.
-template <typename T, bool NT, bool PART>
-__device__ __forceinline__ Chunk fetch(const T* row, int64_t c, int64_t C) {
-  return PART ? fetch_row<T, NT>(row, c, C) : load_row<T, NT>(row, c, C);
-}
-template <typename T, bool PART>
-__device__ __forceinline__ Chunk settle(const Chunk& v, int64_t c, int64_t C) {
-  return PART ? fetched<T>(v, c, C) : v;
 }
 
 }  // namespace ops
