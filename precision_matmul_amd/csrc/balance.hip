@@ -9,12 +9,15 @@
 //
 // HBM-bound in principle (the logits read once, their gradient written once), in
 // practice a few launches of dependent loads: 16384 x 64 float32 logits are 4 MiB, and
-// take 4.8 + 4.1 us forward and 5.1 backward; 16384 x 256 sigmoid scores in 7 sequences 14
-// + 5 + 2 and 14 us, of which the probabilities' vector instructions are most.  The forward needs
-// sums over all tokens of a sequence, so it is a pass over the tokens that leaves
-// partial sums and a sum over those.  Chunk b of the tokens and sequence s meet in at
-// most one run of tokens, and as b and s only grow from run to run, b + s names it:
-// its partial row of the workspace, written once, with no search and no atomics.
+// take 4.9 + 4.1 us forward and 5.2 backward; 16384 x 256 sigmoid scores in 7 sequences 13
+// + 4.5 + 2.0 and 14 us.  There a wave has 759 vector instructions in the forward (948 in
+// the backward), some 5 (6) us for a SIMD's four, and waits for 57 % (47 %) of its cycles:
+// each of a lane's 16 scores has a branch of the lanes around its second exponential, so
+// that they run one after the other.  The forward needs sums over all tokens of a sequence,
+// so it is a pass over the tokens that leaves partial sums and a sum over those.  Chunk b of
+// the tokens and sequence s meet in at most one run of tokens, and as b and s only grow from
+// run to run, b + s names it: its partial row of the workspace, written once, with no search
+// and no atomics.
 //
 // d_e - sum_j p_j d_j is built from differences of whole counts, c_e - c_r with r the
 // token's most probable expert: where p_r is nearly 1, the plain difference would be
@@ -32,7 +35,8 @@ using namespace ops;
 constexpr int kThreads = 1024;           // of the forward: four waves a SIMD hide each other's chains
 constexpr int kBackThreads = 256;
 
-// exp(x) for x <= 0: exp2 corrected by the rounding of its argument; 0 below 2^-150.
+// exp(x) for x <= 0: exp2 corrected by the rounding of its argument; 0 where the result is
+// below 2^-126 (the instruction gives no subnormal numbers).
 __device__ __forceinline__ float exp_down(float x) {
   const float t = x * 1.44269504f, e = __builtin_amdgcn_exp2f(t);
   const float rest = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;

@@ -7,10 +7,12 @@
 // Three products make all of them, because both panels have the rank first: shrink
 // (v = panel x), expand (out = base + s panel^T v) and outer (sum_t s v x^T).  The
 // rank is small, so all three are HBM-bound: x, base and out pass once, and the panels
-// of the adapters in use.  Of rank 16, 16640 x 5120 x 8192 takes 31 us of shrink (5.5
-// TB/s) and 92 of expand (5.9), both panels' gradients of 16384 x 2048 x 5120 40 us (5.9);
-// of rank 64, 4099 x 5120 takes 15 us (2.8: each tile reads as many bytes of panel).  Short
-// batches are bound by the latency of a few dependent loads.
+// of the adapters in use.  Of rank 16, 16640 x 5120 x 8192 takes 36 us of shrink (4.8
+// TB/s) and 97 of expand (5.6), both panels' gradients of 16384 x 2048 x 5120 41 us (5.7);
+// of rank 64, 4099 x 5120 x 8192 22 and 43 us (1.9 and 3.1: each tile reads as many bytes of
+// panel).  Short batches are bound by the latency of a few dependent loads.  (Kernels, three
+// sets of operands in turn.  Times of choices between two forms, below, are of one set again
+// and again, unless they say otherwise: there shrink of 16640 x 5120 takes 31, of 4099 15.)
 //
 // Tokens come in any order.  A workgroup takes 64 neighbouring ones and handles each
 // adapter that occurs among them in turn, its tokens gathered into the rows of 16-row
@@ -29,7 +31,9 @@
 // three, which hold all of v's bits.  The rest is 0 or of either sign, so that its product with an infinity is NaN, or
 // the opposite one, where v's own is an infinity.  Wherever that happens the result is NaN:
 // results are looked at before they are stored, and those of a wave that holds a NaN are
-// computed again, with the rest's products taken of the finite values alone.
+// computed again, with the rest's products taken of the finite values alone.  The look
+// costs runs of tokens 1 %, and 16384 of 100 adapters in any order, with a few results for
+// each look, 4 % (a training step of 1024 x 1024, rank 16, 475 us, 457 without).
 #include "block_launch.hpp"
 #include "moe_launch.hpp"
 #include "ops_common.hpp"
@@ -44,7 +48,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 64;          // tokens of a workgroup: one ballot
 constexpr int kRankBlock = 64;     // rows of a panel that a workgroup takes at once
-constexpr int kFewTokens = 512;    // batches of up to this many tokens are one tile
+// Batches of up to this many tokens are one tile.  With twice as many, single tokens would
+// gain and runs lose, and the host does not see which it has: 600 tokens of 40 adapters,
+// 2048 x 2048, 40 us by tiles and 15 adapter by adapter, 1000 tokens of 64 in 5 runs 14 and 47.
+constexpr int kFewTokens = 512;
 
 __device__ __forceinline__ bf16x8 as_bf16(const Chunk& c) { return __builtin_bit_cast(bf16x8, c); }
 

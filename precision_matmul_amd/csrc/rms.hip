@@ -7,12 +7,16 @@
 //   dx = rstd (a - hr sum(a hr) / C) + grad_h,   dw = sum over rows of dy hr
 //
 // HBM-bound: x and residual (dy, h and grad_h) are read once, h, y and the codes
-// (dx) written once: 16640 x 5120 bf16 with residual and 1x128 codes 113 us (5.3 TB/s),
-// backward of 16384 x 2048 43 + 4.8 us (6.3 TB/s in the first kernel), 8000 x 5120 59 +
-// 4.7.  A row stays in registers between its sum and its output.  The
-// norm is that of the rounded h, which is what the residual stream holds and what
+// (dx) written once: 16640 x 5120 bf16 with residual and 1x128 codes 117 us (5.1 TB/s),
+// with rowwise codes 114, backward of 16384 x 2048 47 + 4.7 us (5.7 TB/s in the first
+// kernel), 8000 x 5120 60 + 4.8.  A row stays in registers between its sum and its output.
+// The norm is that of the rounded h, which is what the residual stream holds and what
 // the backward pass reads.  All sums are float32; codes come from float32 values of
 // y with no rounding to bf16 in between.
+//
+// These times are of kernels, three sets of operands in turn; those of choices between two
+// forms, below, are of one set again and again, half of which can be in the memory's
+// cache, unless they say otherwise.
 //
 // Lanes past a row's end hold zeros.
 #include "block_launch.hpp"
@@ -154,7 +158,9 @@ __device__ __forceinline__ Turns my_rows(int64_t R, int rpb, int wave) {
 // ---------------------------------------------------------------------------
 // Forward, row in registers: WPR waves a row, NIT chunks a lane.  A lane's columns
 // are the same in all rows that a workgroup takes, so it keeps its weights in
-// registers, and the next row is loaded while this one is reduced and written.
+// registers, and the next row is loaded while this one is reduced and written.  A row has
+// a whole wave at least: of 128 bf16 columns 16 of its 64 lanes work (524288 x 128 126 us,
+// in three sets of operands; its bytes would take 50).
 // ---------------------------------------------------------------------------
 template <typename T, int FORM, int WPR, int NIT, bool NT>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void rms_kernel(const RmsProblem p) {
@@ -308,7 +314,9 @@ __global__ __launch_bounds__(256) void rms_long_kernel(const RmsProblem p) {
 // flight while this one is worked on, and keeps its share of dw in registers over
 // all of them; it then writes one partial row of the workspace, [gridDim][C], which
 // rms_column_sum_kernel adds up in workgroup order: no atomics, the same bits every
-// time.  A row by as few waves as hold it in four chunks a lane: sums across waves wait.
+// time.  A row by one wave where that holds it in four chunks a lane, since sums across
+// waves wait; longer ones by four or eight waves of two chunks (fp32 above 4096 columns: of
+// three or four), bf16 above 8192 by sixteen of two.
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;            // waves of a workgroup that takes a row with each
 
@@ -593,7 +601,7 @@ __global__ __launch_bounds__(1024) void rms_column_sum_kernel(const float* parti
 
 constexpr int64_t kForwardGrid = 1024;  // four workgroups a compute unit; whole XCDs
 constexpr int kBackwardGrid = 512;      // partial rows at most
-constexpr int64_t kRegisterCols = 8192; // longest row kept in registers (bf16: twice that)
+constexpr int64_t kRegisterCols = 8192; // longest row that is read once (bf16: twice that)
 
 // Rows that the long rows' kernels take: those, and rows of less than a chunk.
 bool long_rows(int64_t C) { return C < 8 || C > kRegisterCols; }
@@ -602,8 +610,10 @@ bool long_rows(int64_t C) { return C < 8 || C > kRegisterCols; }
 // 5120 8.0 and 8.1 + 3.1, but 512 x 5120 21 and 10.4 + 3.9).
 bool few_rows(int64_t R, int64_t C) { return R <= (C <= 2048 ? 512 : 256) && !long_rows(C); }
 
-// Long bf16 rows that 16 waves still keep in registers (4096 x 12288 70 us forward and 97
-// backward, read twice 93 and 139; the backward with grad_h a row ahead too 109).
+// Long bf16 rows by 16 waves: calls of 4096 x 12288 with a residual 73 us forward and 98
+// backward, with grad_h; read twice 93 and 139; the backward with grad_h a row ahead too 109.
+// The forward keeps rows in registers.  The backward has 128 of them a lane, and spills 66
+// more of its weights, sums and rows into 60 bytes of scratch; its bytes would take 75 us.
 template <typename T>
 bool by_sixteen(int64_t C) { return sizeof(T) == 2 && C > kRegisterCols && C <= 2 * kRegisterCols; }
 
